@@ -387,6 +387,148 @@ ds_status ds_q8_project(const ds_q8_tiled* w, int64_t rows, int32_t K, const uin
                         ds_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * Q4 projections: R rows through one Q4 matrix in the tile-major form above with groups of
+ * 1 (ds_q4_tile with group = 1), for the products of a layer outside its experts:
+ *   y[r][i] = bf16_RNE(sum_k W[i][k] * x[r][k]) for r < R.
+ * x bf16 [R][K], y bf16 [R][rows] (device, 16-byte aligned; y must not overlap x or the
+ * tiles), 1 <= R <= 8, rows a multiple of 16 up to 2^24, K a multiple of 64 up to 65536.
+ * Every weight byte is read once for all R rows; nibble x bf16 products are exact and
+ * summed in fp32 in an order that depends on rows and K alone, so an R-row call writes the
+ * same bytes as R one-row calls. No workspace. Errors: DS_ERR_INVALID_ARG, DS_ERR_CUDA. */
+ds_status ds_q4_project(const ds_q4_tiled* w, int64_t rows, int32_t K, const uint16_t* x,
+                        int32_t R, uint16_t* y, ds_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged key-value cache of one layer: n_pages pages of page_tokens tokens; a page holds,
+ * for every key-value head, page_tokens rows of head_dim values, head by head:
+ *   row of (page, head, offset): values at
+ *     page * page_stride + (head * page_tokens + offset) * head_dim,
+ *   slot of (page, offset): page * page_tokens + offset.
+ * DS_CACHE_BF16: the values as bf16. DS_CACHE_Q8: int8 codes and, per row, one fp32 scale
+ * at page * scale_page_stride + head * page_tokens + offset; value = scale * code. A row x
+ * is quantised, with a = max |x|, as
+ *   scale = a / 127,   code = rint(127 x / a)   (fp32, each operation rounded to nearest,
+ *   ties to even; for a > 2^118 x and a are halved eight times first);
+ * a row of zeros gets scale 0 and codes 0; a row that holds an infinity or a NaN gets the
+ * scale NaN, so that it reads back as NaN.
+ * Limits: page_tokens 16, 32, 64 or 128; head_dim 64 or 128 (other values from 1 to 4096:
+ * DS_ERR_UNSUPPORTED); 1 <= n_kv_heads <= 256; n_pages >= 1 and n_pages * page_tokens <
+ * 2^31; page_stride >= n_kv_heads * page_tokens * head_dim and a multiple of 16;
+ * scale_page_stride >= n_kv_heads * page_tokens and a multiple of 4; k, v, k_scale and
+ * v_scale 16-byte aligned. k and v may share one allocation (strided pages).
+ * ---------------------------------------------------------------------------------- */
+#define DS_CACHE_BF16 0
+#define DS_CACHE_Q8 1
+typedef struct {
+  int32_t n_pages, n_kv_heads, page_tokens, head_dim;
+  int32_t format;             /* DS_CACHE_BF16 or DS_CACHE_Q8                      */
+  void* k;
+  void* v;
+  int64_t page_stride;        /* values between pages of k and of v                */
+  float* k_scale;             /* DS_CACHE_Q8 only (ignored otherwise)              */
+  float* v_scale;
+  int64_t scale_page_stride;  /* floats between pages of k_scale and of v_scale    */
+} ds_paged_cache;
+
+/* Writes n_tokens (0 .. 2^24) tokens' keys and values to the cache, quantising them when it
+ * is a DS_CACHE_Q8 one. k, v: bf16 [n_tokens][n_kv_heads][head_dim], tokens k_stride and
+ * v_stride values apart (>= n_kv_heads * head_dim, multiples of 8; 16-byte aligned, so they
+ * may be parts of one projection's output). slots: int32 [n_tokens]; a token whose slot is
+ * negative or behind the last page is skipped (a padded batch), and every slot that is not
+ * named keeps its bytes. The slots of one call must be distinct: a slot named twice holds
+ * some mix of its tokens. n_tokens == 0 enqueues nothing.
+ * Errors: DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (head_dim), DS_ERR_CUDA. */
+ds_status ds_cache_write(const ds_paged_cache* cache, const uint16_t* k, int64_t k_stride,
+                         const uint16_t* v, int64_t v_stride, const int32_t* slots,
+                         int32_t n_tokens, ds_stream_t stream);
+
+/* Reads n_tokens (0 .. 2^24) tokens back: k_out, v_out bf16 [n_tokens][n_kv_heads][head_dim]
+ * (16-byte aligned). Q8 values are scale * code in fp32, rounded once to bf16. Slots may
+ * repeat; a slot that is negative or behind the last page gives a row of zeros. */
+ds_status ds_cache_read(const ds_paged_cache* cache, const int32_t* slots, int32_t n_tokens,
+                        uint16_t* k_out, uint16_t* v_out, ds_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Norms of queries and keys per head with the position rotation, in one pass. For every
+ * row x of head_dim values (one head of one token), in fp32, rounded once at the end:
+ *   with a weight w:  x[d] <- x[d] * w[d] / sqrt(mean(x^2) + eps)   (no weight: no norm);
+ *   then the first rotary_dim = n values are rotated in pairs i < n/2 by the angle
+ *   position * freqs[i] (in turns of 2^64, modulo one turn: an exact integer product, so
+ *   far positions lose nothing):  (u, v) <- (u cos - v sin, v cos + u sin), where the pair
+ *   is (x[i], x[i + n/2]), or (x[2i], x[2i + 1]) when interleaved != 0.
+ * Limits: 0 <= n_tokens <= 2^24 (0 enqueues nothing), 1 <= n_heads, n_kv_heads <= 256,
+ * head_dim 64 or 128 (else DS_ERR_UNSUPPORTED as above), rotary_dim a multiple of 16 from 0
+ * to head_dim, eps finite and >= 0; q, k 16-byte aligned with strides as for
+ * ds_cache_write; weights 16-byte aligned; positions and freqs needed when rotary_dim > 0.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t n_tokens, n_heads, n_kv_heads, head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float eps;
+  const uint16_t* q;         /* bf16 [n_tokens][n_heads][head_dim]                  */
+  int64_t q_stride;          /* values between tokens                               */
+  const uint16_t* k;         /* bf16 [n_tokens][n_kv_heads][head_dim]               */
+  int64_t k_stride;
+  const uint16_t* q_weight;  /* bf16 [head_dim], or NULL: queries are not normed    */
+  const uint16_t* k_weight;  /* bf16 [head_dim], or NULL: keys are not normed       */
+  const int32_t* positions;  /* int32 [n_tokens]; negative ones rotate backwards    */
+  const int64_t* freqs;      /* int64 [rotary_dim / 2], turns per position x 2^64   */
+} ds_norm_rope_args;
+
+/* q_out bf16 [n_tokens][n_heads][head_dim] and k_out bf16 [n_tokens][n_kv_heads][head_dim]
+ * (16-byte aligned). q_out may be q itself when q_stride == n_heads * head_dim, and k_out k
+ * likewise; other overlaps are a caller error. */
+ds_status ds_qk_norm_rope(const ds_norm_rope_args* args, uint16_t* q_out, uint16_t* k_out,
+                          ds_stream_t stream);
+
+/* The same pass with the keys, and the values v beside them, going to the cache: what
+ * ds_qk_norm_rope and ds_cache_write do together, except that the keys of a DS_CACHE_Q8
+ * cache are quantised from their fp32 values (one rounding instead of two). The cache's
+ * n_kv_heads and head_dim must be those of args; v, v_stride and slots as for
+ * ds_cache_write. A token whose slot is skipped still gets its row of q_out. */
+ds_status ds_qk_norm_rope_write(const ds_norm_rope_args* args, const uint16_t* v,
+                                int64_t v_stride, const ds_paged_cache* cache,
+                                const int32_t* slots, uint16_t* q_out, ds_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention of each sequence's last n_rows tokens over its paged cache (for one token, a
+ * plain decode step; for several, the rows of a verify step, which see one another
+ * causally). For sequence b, row r and query head h, with H = n_heads / n_kv_heads, key
+ * head g = h / H and len = lengths[b] (the new rows among them, already written):
+ *   s_t = scale * q_{b,r,h} . k_{b,g,t} over the tokens t < len - (n_rows - 1 - r),
+ *   p = softmax(s),   out_{b,r,h} = bf16_RNE(sum_t p_t v_{b,g,t}),
+ * token t in page page_table[b][t / page_tokens], offset t % page_tokens. A row with no
+ * visible token gets 0, and a score of -infinity counts as not visible; tokens that a row
+ * does not see do not reach it, whatever they hold. len is taken as 0 when negative and as
+ * max_pages * page_tokens when larger; page table entries outside 0 .. n_pages - 1 are
+ * skipped as if their tokens were not there, and entries behind the last needed page are
+ * not read. Scores, softmax and sums in fp32 on the tensor cores; p (times the value's
+ * scale in a Q8 cache) is rounded to bf16 for the product with the values.
+ * Limits: 0 <= n_seqs <= 4096 (0 enqueues nothing), 1 <= n_rows <= 8, 1 <= max_pages,
+ * max_pages * page_tokens <= 2^24, n_heads a multiple of the cache's n_kv_heads, n_rows * H
+ * <= 128 (else DS_ERR_UNSUPPORTED), scale finite; q and out 16-byte aligned.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t n_seqs, n_rows, n_heads;
+  int32_t max_pages;           /* entries of page_table per sequence                */
+  float scale;
+  const uint16_t* q;           /* bf16 [n_seqs][n_rows][n_heads][head_dim]          */
+  ds_paged_cache cache;
+  const int32_t* page_table;   /* int32 [n_seqs][max_pages]                         */
+  const int32_t* lengths;      /* int32 [n_seqs]                                    */
+} ds_paged_attn_args;
+
+/* Workspace bytes on the current device (0 when the arguments are invalid, unsupported or
+ * n_seqs == 0). It depends on the sizes alone: pointers are not examined. */
+size_t ds_paged_attn_workspace_size(const ds_paged_attn_args* args);
+/* out: bf16 [n_seqs][n_rows][n_heads][head_dim], not overlapping the inputs; workspace
+ * 256-byte aligned, its contents on entry are ignored and it must not be used by another
+ * call in flight. DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED, DS_ERR_WORKSPACE, DS_ERR_CUDA. */
+ds_status ds_paged_attention(const ds_paged_attn_args* args, uint16_t* out, void* workspace,
+                             size_t ws_bytes, ds_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Verify acceptance (page "DeepSeek V4.1F Q4 on M3 Ultra with native DSpark MTP
  * (40tps / 800tps)", paragraph "DSpark": a decode step verifies the last committed token
  * and R - 1 drafts in one pass; greedy decode gives the same output as without the

@@ -6,6 +6,7 @@ and the current CUDA stream. PyTorch provides device memory and streams.
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
 
 import torch
@@ -15,7 +16,9 @@ from . import _native as N
 __all__ = [
     "MoeLayer", "q4_tile", "moe_workspace_size", "moe_verify_forward", "select_workspace_size",
     "select_blocks", "workspace_status", "version", "DsmoeError", "verify_greedy",
-    "verify_sample", "q8_tile", "q8_project", "sparse_attention",
+    "verify_sample", "q8_tile", "q8_project", "sparse_attention", "q4_project", "PagedCache",
+    "rope_frequencies", "qk_norm_rope", "qk_norm_rope_write", "cache_write", "cache_read",
+    "paged_attention",
 ]
 
 DsmoeError = N.DsmoeError
@@ -392,6 +395,304 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, sel: tor
     _check(lib.ds_sparse_attention(args, _ptr(out), _ptr(workspace), workspace.numel(),
                                    _stream(stream)), "ds_sparse_attention")
     return out
+
+
+def _need_on(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device):
+    _need(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (got {t.device})")
+
+
+def _run(dev: torch.device, stream, call):
+    """call(stream handle) with `dev` current and its allocations made on the launch stream
+    (the current stream of `dev` when `stream` is None)."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = int(stream)
+            stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
+                      else torch.cuda.default_stream(dev))
+        if stream.device != dev:
+            raise ValueError(f"stream must be on {dev} (got {stream.device})")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def q4_project(tiles: torch.Tensor, x: torch.Tensor, *, y=None, stream=None) -> torch.Tensor:
+    """R rows (1..8) through one tile-major Q4 matrix (q4_tile with group=1): tiles uint8
+    [rows/16, K/64, 576], x bf16 [R, K] -> y bf16 [R, rows] (ds_q4_project)."""
+    lib = N.load()
+    _need(tiles, "tiles", torch.uint8)
+    if tiles.dim() != 3 or tiles.shape[2] != N.Q4_TILE_BYTES:
+        raise ValueError(f"tiles must be [rows/16, K/64, {N.Q4_TILE_BYTES}] "
+                         f"(got {tuple(tiles.shape)})")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [R, K]")
+    rows, K, R, dev = tiles.shape[0] * 16, tiles.shape[1] * 64, x.shape[0], tiles.device
+    _need_on(x, "x", torch.bfloat16, (R, K), dev)
+    if y is not None:
+        _need_on(y, "y", torch.bfloat16, (R, rows), dev)
+
+    def call(s):
+        out = torch.empty((R, rows), dtype=torch.bfloat16, device=dev) if y is None else y
+        _check(lib.ds_q4_project(N.DsQ4Tiled(_ptr(tiles)), rows, K, _ptr(x), R, _ptr(out), s),
+               "ds_q4_project")
+        return out
+
+    return _run(dev, stream, call)
+
+
+@dataclass
+class PagedCache:
+    """Paged key-value cache of one layer (include/dsmoe.h): k and v [pages, kv_heads,
+    page_tokens, head_dim], bf16, or int8 with k_scale and v_scale fp32 [pages, kv_heads,
+    page_tokens] (Q8). Pages may be strided (k and v parts of one allocation); the rest is
+    contiguous. The slot of a token is page * page_tokens + its offset in the page."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+    @staticmethod
+    def zeros(n_pages: int, n_kv_heads: int, page_tokens: int = 64, head_dim: int = 128,
+              q8: bool = False, device="cuda") -> "PagedCache":
+        shape = (n_pages, n_kv_heads, page_tokens, head_dim)
+        if not q8:
+            return PagedCache(*(torch.zeros(shape, dtype=torch.bfloat16, device=device)
+                                for _ in range(2)))
+        return PagedCache(*(torch.zeros(shape, dtype=torch.int8, device=device)
+                            for _ in range(2)),
+                          *(torch.zeros(shape[:3], dtype=torch.float32, device=device)
+                            for _ in range(2)))
+
+    @property
+    def q8(self) -> bool:
+        return self.k.dtype == torch.int8
+
+    @staticmethod
+    def _stride(t: torch.Tensor, name: str, dtype, shape, dev) -> int:
+        """Elements between the pages of t, whose pages are contiguous."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"cache.{name} must be a torch.Tensor")
+        if t.device != dev or t.device.type != "cuda" or t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"cache.{name} must be {dtype} {tuple(shape)} on {dev} "
+                             f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+        if not t[0].is_contiguous():
+            raise ValueError(f"the pages of cache.{name} must be contiguous")
+        page = t[0].numel()
+        return t.stride(0) if t.shape[0] > 1 else -(-page // 16) * 16
+
+    def struct(self) -> N.DsPagedCache:
+        if not isinstance(self.k, torch.Tensor) or self.k.dim() != 4 or self.k.numel() == 0:
+            raise ValueError("cache.k must be [pages, kv_heads, page_tokens, head_dim]")
+        if self.k.dtype not in (torch.bfloat16, torch.int8):
+            raise ValueError(f"cache.k must be bfloat16 or int8 (got {self.k.dtype})")
+        shape, dev, dt = self.k.shape, self.k.device, self.k.dtype
+        stride = self._stride(self.k, "k", dt, shape, dev)
+        if self._stride(self.v, "v", dt, shape, dev) != stride:
+            raise ValueError("cache.k and cache.v must have the same page stride")
+        scale_stride, ks, vs = 0, None, None
+        if self.q8:
+            scale_stride = self._stride(self.k_scale, "k_scale", torch.float32, shape[:3], dev)
+            if self._stride(self.v_scale, "v_scale", torch.float32, shape[:3],
+                            dev) != scale_stride:
+                raise ValueError("cache.k_scale and cache.v_scale must have the same page stride")
+            ks, vs = _ptr(self.k_scale), _ptr(self.v_scale)
+        return N.DsPagedCache(shape[0], shape[1], shape[2], shape[3],
+                              N.DS_CACHE_Q8 if self.q8 else N.DS_CACHE_BF16, _ptr(self.k),
+                              _ptr(self.v), stride, ks, vs, scale_stride)
+
+
+def rope_frequencies(rotary_dim: int | None = None, base: float = 10000.0, *, inv_freq=None,
+                     device="cuda") -> torch.Tensor:
+    """The rotation frequencies qk_norm_rope takes: int64 [rotary_dim / 2], turns per position
+    in units of 2^-64, of base^(-2i / rotary_dim) or of `inv_freq` (radians per position, one
+    per pair, any finite values). Made once per model."""
+    if inv_freq is None:
+        if rotary_dim is None or rotary_dim < 0 or rotary_dim % 2:
+            raise ValueError("rotary_dim must be even and not negative")
+        f = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+        f = float(base) ** (-f / max(rotary_dim, 1))
+    else:
+        f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").detach().reshape(-1)
+        if rotary_dim is not None and f.numel() * 2 != rotary_dim:
+            raise ValueError("inv_freq must hold rotary_dim / 2 values")
+    if not bool(torch.isfinite(f).all()):
+        raise ValueError("frequencies must be finite")
+    turns = f / (2 * math.pi)
+    turns = turns - torch.round(turns)            # whole turns per position do nothing
+    steps = [round(t * 2.0 ** 64) for t in turns.tolist()]
+    steps = [s - (1 << 64) if s >= 1 << 63 else s for s in steps]
+    return torch.tensor(steps, dtype=torch.int64, device=device)
+
+
+def _token_rows(t: torch.Tensor, name: str, shape: tuple, dev: torch.device) -> int:
+    """Values between the tokens of t [tokens, heads, head_dim]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev or t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be bfloat16 {shape} on {dev} "
+                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+    T, H, D = shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if T > 1 else -(-H * D // 8) * 8
+
+
+def _norm_rope_args(q, k, positions, freqs, q_weight, k_weight, eps, interleaved):
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.device.type != "cuda":
+        raise ValueError("q must be a CUDA tensor [tokens, heads, head_dim]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [tokens, kv_heads, head_dim]")
+    (T, Hq, D), Hkv, dev = q.shape, k.shape[1], q.device
+    qs = _token_rows(q, "q", (T, Hq, D), dev)
+    ks = _token_rows(k, "k", (T, Hkv, D), dev)
+    rot = 0
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be [rotary_dim / 2]")
+        _need_on(freqs, "freqs", torch.int64, tuple(freqs.shape), dev)
+        rot = 2 * freqs.shape[0]
+    if rot:
+        _need_on(positions, "positions", torch.int32, (T,), dev)
+    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need_on(w, nm, torch.bfloat16, (D,), dev)
+    return N.DsNormRopeArgs(T, Hq, Hkv, D, rot, int(bool(interleaved)), float(eps), _ptr(q), qs,
+                            _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
+                            _ptr(positions) if rot else None, _ptr(freqs) if rot else None)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions, freqs, *, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                 k_out=None, stream=None):
+    """Norms of queries and keys per head (where a weight is given) and the position rotation,
+    in one pass (ds_qk_norm_rope): q bf16 [T, Hq, D], k bf16 [T, Hkv, D], tokens strided as in
+    one projection's output; positions int32 [T]; freqs from rope_frequencies (None: no
+    rotation); weights bf16 [D]. Returns (q_out, k_out), contiguous; a contiguous q or k may
+    be its own output."""
+    lib = N.load()
+    a = _norm_rope_args(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
+    dev = q.device
+    for t, nm, like in ((q_out, "q_out", q), (k_out, "k_out", k)):
+        if t is not None:
+            _need_on(t, nm, torch.bfloat16, tuple(like.shape), dev)
+
+    def call(s):
+        qo = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
+        ko = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+        _check(lib.ds_qk_norm_rope(a, _ptr(qo), _ptr(ko), s), "ds_qk_norm_rope")
+        return qo, ko
+
+    return _run(dev, stream, call)
+
+
+def qk_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions, freqs,
+                       cache: PagedCache, slots: torch.Tensor, *, q_weight=None, k_weight=None,
+                       eps: float = 1e-6, interleaved: bool = False, q_out=None, stream=None):
+    """qk_norm_rope with the keys, and the values v bf16 [T, Hkv, D] beside them, going to the
+    cache at slots int32 [T] (ds_qk_norm_rope_write). Returns q_out."""
+    lib = N.load()
+    a = _norm_rope_args(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
+    dev, T = q.device, q.shape[0]
+    vs = _token_rows(v, "v", tuple(k.shape), dev)
+    _need_on(slots, "slots", torch.int32, (T,), dev)
+    c = cache.struct()
+    if cache.k.device != dev:
+        raise ValueError(f"the cache must be on {dev} (got {cache.k.device})")
+    if q_out is not None:
+        _need_on(q_out, "q_out", torch.bfloat16, tuple(q.shape), dev)
+
+    def call(s):
+        qo = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
+        _check(lib.ds_qk_norm_rope_write(a, _ptr(v), vs, c, _ptr(slots), _ptr(qo), s),
+               "ds_qk_norm_rope_write")
+        return qo
+
+    return _run(dev, stream, call)
+
+
+def cache_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *,
+                stream=None) -> None:
+    """Writes keys and values bf16 [T, kv_heads, head_dim] (tokens may be strided) to the
+    cache at slots int32 [T], quantised when it is a Q8 cache (ds_cache_write). Slots outside
+    the cache are skipped; the others must be distinct."""
+    lib = N.load()
+    c, dev = cache.struct(), cache.k.device
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [tokens, kv_heads, head_dim]")
+    shape = (k.shape[0], c.n_kv_heads, c.head_dim)
+    ks, vs = _token_rows(k, "k", shape, dev), _token_rows(v, "v", shape, dev)
+    _need_on(slots, "slots", torch.int32, shape[:1], dev)
+    _run(dev, stream, lambda s: _check(
+        lib.ds_cache_write(c, _ptr(k), ks, _ptr(v), vs, _ptr(slots), shape[0], s),
+        "ds_cache_write"))
+
+
+def cache_read(cache: PagedCache, slots: torch.Tensor, *, k_out=None, v_out=None, stream=None):
+    """The keys and values at slots int32 [T], as bf16 [T, kv_heads, head_dim] each
+    (ds_cache_read). Slots outside the cache give zeros."""
+    lib = N.load()
+    c, dev = cache.struct(), cache.k.device
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a CUDA tensor [tokens]")
+    T = slots.shape[0]
+    shape = (T, c.n_kv_heads, c.head_dim)
+    _need_on(slots, "slots", torch.int32, (T,), dev)
+    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _need_on(t, nm, torch.bfloat16, shape, dev)
+
+    def call(s):
+        ko = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+        vo = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
+        _check(lib.ds_cache_read(c, _ptr(slots), T, _ptr(ko), _ptr(vo), s), "ds_cache_read")
+        return ko, vo
+
+    return _run(dev, stream, call)
+
+
+def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
+                    lengths: torch.Tensor, *, scale: float | None = None, out=None,
+                    workspace=None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's last R tokens over its paged cache (ds_paged_attention):
+    q bf16 [B, R, Hq, D] (R 1..8, R * Hq / kv_heads <= 128), page_table int32 [B, max_pages],
+    lengths int32 [B] (tokens in the cache, the R new ones among them) -> bf16 [B, R, Hq, D].
+    scale defaults to 1 / sqrt(D)."""
+    lib = N.load()
+    c, dev = cache.struct(), cache.k.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, R, heads, head_dim]")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a CUDA tensor [B, max_pages]")
+    B, R, Hq, D = q.shape
+    if D != c.head_dim:
+        raise ValueError(f"q must have the cache's head_dim {c.head_dim} (got {D})")
+    _need_on(q, "q", torch.bfloat16, (B, R, Hq, D), dev)
+    _need_on(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    _need_on(lengths, "lengths", torch.int32, (B,), dev)
+    if out is not None:
+        _need_on(out, "out", torch.bfloat16, (B, R, Hq, D), dev)
+    args = N.DsPagedAttnArgs(B, R, Hq, page_table.shape[1],
+                             D ** -0.5 if scale is None else float(scale), _ptr(q), c,
+                             _ptr(page_table), _ptr(lengths))
+
+    def call(s):
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(1, lib.ds_paged_attn_workspace_size(args)), dtype=torch.uint8,
+                             device=dev)
+        _check(lib.ds_paged_attention(args, _ptr(o), _ptr(ws), ws.numel(), s),
+               "ds_paged_attention")
+        return o
+
+    if workspace is not None:
+        _need_on(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev)
+    return _run(dev, stream, call)
 
 
 def noalloc_status(stream=None) -> int:

@@ -24,7 +24,9 @@ EXPORTS = (
     "ds_moe_verify_forward_noalloc", "ds_noalloc_status", "ds_q4_tiled_bytes", "ds_q4_tile",
     "ds_select_workspace_offset", "ds_verify_workspace_size", "ds_verify_greedy",
     "ds_verify_sample", "ds_q8_tiled_bytes", "ds_q8_tile", "ds_q8_workspace_size",
-    "ds_q8_project", "ds_attn_workspace_size", "ds_sparse_attention",
+    "ds_q8_project", "ds_attn_workspace_size", "ds_sparse_attention", "ds_q4_project",
+    "ds_cache_write", "ds_cache_read", "ds_qk_norm_rope", "ds_qk_norm_rope_write",
+    "ds_paged_attn_workspace_size", "ds_paged_attention",
 )
 SELECT_WS_PARTS = {"union": 0, "union_count": 1, "scores": 2, "key_norms": 3, "row_scales": 4}
 
@@ -81,6 +83,37 @@ class DsAttnArgs(C.Structure):
         ("head_dim", C.c_int32), ("n_blocks", C.c_int32), ("block_tokens", C.c_int32),
         ("top_k", C.c_int32), ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
         ("kv_layer_stride", C.c_int64), ("sel", C.c_void_p),
+    ]
+
+
+DS_CACHE_BF16 = 0
+DS_CACHE_Q8 = 1
+
+
+class DsPagedCache(C.Structure):
+    _fields_ = [
+        ("n_pages", C.c_int32), ("n_kv_heads", C.c_int32), ("page_tokens", C.c_int32),
+        ("head_dim", C.c_int32), ("format", C.c_int32), ("k", C.c_void_p), ("v", C.c_void_p),
+        ("page_stride", C.c_int64), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+        ("scale_page_stride", C.c_int64),
+    ]
+
+
+class DsNormRopeArgs(C.Structure):
+    _fields_ = [
+        ("n_tokens", C.c_int32), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32),
+        ("head_dim", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32),
+        ("eps", C.c_float), ("q", C.c_void_p), ("q_stride", C.c_int64), ("k", C.c_void_p),
+        ("k_stride", C.c_int64), ("q_weight", C.c_void_p), ("k_weight", C.c_void_p),
+        ("positions", C.c_void_p), ("freqs", C.c_void_p),
+    ]
+
+
+class DsPagedAttnArgs(C.Structure):
+    _fields_ = [
+        ("n_seqs", C.c_int32), ("n_rows", C.c_int32), ("n_heads", C.c_int32),
+        ("max_pages", C.c_int32), ("scale", C.c_float), ("q", C.c_void_p),
+        ("cache", DsPagedCache), ("page_table", C.c_void_p), ("lengths", C.c_void_p),
     ]
 
 
@@ -149,6 +182,26 @@ def load() -> C.CDLL:
     lib.ds_q8_project.argtypes = [C.POINTER(DsQ8Tiled), C.c_int64, C.c_int32, C.c_void_p,
                                   C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
     lib.ds_q8_project.restype = C.c_int
+    lib.ds_q4_project.argtypes = [C.POINTER(DsQ4Tiled), C.c_int64, C.c_int32, C.c_void_p,
+                                  C.c_int32, C.c_void_p, C.c_void_p]
+    lib.ds_q4_project.restype = C.c_int
+    lib.ds_cache_write.argtypes = [C.POINTER(DsPagedCache), C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_int64, C.c_void_p, C.c_int32, C.c_void_p]
+    lib.ds_cache_write.restype = C.c_int
+    lib.ds_cache_read.argtypes = [C.POINTER(DsPagedCache), C.c_void_p, C.c_int32, C.c_void_p,
+                                  C.c_void_p, C.c_void_p]
+    lib.ds_cache_read.restype = C.c_int
+    lib.ds_qk_norm_rope.argtypes = [C.POINTER(DsNormRopeArgs), C.c_void_p, C.c_void_p, C.c_void_p]
+    lib.ds_qk_norm_rope.restype = C.c_int
+    lib.ds_qk_norm_rope_write.argtypes = [C.POINTER(DsNormRopeArgs), C.c_void_p, C.c_int64,
+                                          C.POINTER(DsPagedCache), C.c_void_p, C.c_void_p,
+                                          C.c_void_p]
+    lib.ds_qk_norm_rope_write.restype = C.c_int
+    lib.ds_paged_attn_workspace_size.argtypes = [C.POINTER(DsPagedAttnArgs)]
+    lib.ds_paged_attn_workspace_size.restype = C.c_size_t
+    lib.ds_paged_attention.argtypes = [C.POINTER(DsPagedAttnArgs), C.c_void_p, C.c_void_p,
+                                       C.c_size_t, C.c_void_p]
+    lib.ds_paged_attention.restype = C.c_int
     lib.ds_verify_workspace_size.argtypes = [C.c_int32, C.c_int32, C.c_int32]
     lib.ds_verify_workspace_size.restype = C.c_size_t
     lib.ds_verify_greedy.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,

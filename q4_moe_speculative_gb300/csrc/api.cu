@@ -341,6 +341,255 @@ ds_status ds_q8_project(const ds_q8_tiled* w, int64_t rows, int32_t K, const uin
              : DS_ERR_CUDA;
 }
 
+ds_status ds_q4_project(const ds_q4_tiled* w, int64_t rows, int32_t K, const uint16_t* x,
+                        int32_t R, uint16_t* y, ds_stream_t stream) {
+  if (!w || !w->tiles || !x || !y) return DS_ERR_INVALID_ARG;
+  if (rows < 16 || rows > (1 << 24) || rows % 16 || K < 64 || K > 65536 || K % 64)
+    return DS_ERR_INVALID_ARG;
+  if (R < 1 || R > 8) return DS_ERR_INVALID_ARG;
+  if (!aligned(w->tiles, 16) || !aligned(x, 16) || !aligned(y, 16)) return DS_ERR_INVALID_ARG;
+  return launch_q4_project(w->tiles, (int)rows, K, x, R, y,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? DS_OK
+             : DS_ERR_CUDA;
+}
+
+namespace {
+
+ds_status check_head_dim(int32_t D) {
+  if (D < 1 || D > 4096) return DS_ERR_INVALID_ARG;
+  return D == 64 || D == 128 ? DS_OK : DS_ERR_UNSUPPORTED;
+}
+
+// Sizes only (no pointers).
+ds_status check_cache_sizes(const ds_paged_cache* c) {
+  if (!c) return DS_ERR_INVALID_ARG;
+  if (c->format != DS_CACHE_BF16 && c->format != DS_CACHE_Q8) return DS_ERR_INVALID_ARG;
+  const int32_t pt = c->page_tokens;
+  if (!(pt == 16 || pt == 32 || pt == 64 || pt == 128)) return DS_ERR_INVALID_ARG;
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 256) return DS_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || (int64_t)c->n_pages * pt > INT32_MAX) return DS_ERR_INVALID_ARG;
+  const ds_status st = check_head_dim(c->head_dim);
+  if (st != DS_OK) return st;
+  const int64_t rows = (int64_t)c->n_kv_heads * pt;
+  if (c->page_stride < rows * c->head_dim || c->page_stride % 16) return DS_ERR_INVALID_ARG;
+  if (c->format == DS_CACHE_Q8 && (c->scale_page_stride < rows || c->scale_page_stride % 4))
+    return DS_ERR_INVALID_ARG;
+  // (the last row's byte offset stays far inside 63 bits)
+  if (c->page_stride > ((int64_t)1 << 31) || c->scale_page_stride > ((int64_t)1 << 31))
+    return DS_ERR_INVALID_ARG;
+  return DS_OK;
+}
+
+ds_status check_cache(const ds_paged_cache* c) {
+  const ds_status st = check_cache_sizes(c);
+  if (st != DS_OK) return st;
+  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return DS_ERR_INVALID_ARG;
+  if (c->format == DS_CACHE_Q8 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) ||
+                                   !aligned(c->v_scale, 16)))
+    return DS_ERR_INVALID_ARG;
+  return DS_OK;
+}
+
+CacheView view_of(const ds_paged_cache* c) {
+  CacheView v{};
+  v.pages = c->n_pages;
+  v.heads = c->n_kv_heads;
+  while ((1 << v.page_shift) < c->page_tokens) ++v.page_shift;
+  v.q8 = c->format == DS_CACHE_Q8;
+  v.k = static_cast<uint8_t*>(c->k);
+  v.v = static_cast<uint8_t*>(c->v);
+  v.stride = c->page_stride;
+  v.k_scale = c->k_scale;
+  v.v_scale = c->v_scale;
+  v.scale_stride = c->scale_page_stride;
+  return v;
+}
+
+constexpr int32_t kMaxTokens = 1 << 24;
+
+// bf16 rows of `heads` heads per token, tokens `stride` values apart.
+bool token_rows_ok(const uint16_t* x, int64_t stride, int32_t heads, int32_t D) {
+  return x && aligned(x, 16) && stride >= (int64_t)heads * D && stride % 8 == 0 &&
+         stride <= ((int64_t)1 << 31);
+}
+
+ds_status check_norm_rope(const ds_norm_rope_args* a) {
+  if (!a) return DS_ERR_INVALID_ARG;
+  if (a->n_tokens < 0 || a->n_tokens > kMaxTokens) return DS_ERR_INVALID_ARG;
+  if (a->n_heads < 1 || a->n_heads > 256 || a->n_kv_heads < 1 || a->n_kv_heads > 256)
+    return DS_ERR_INVALID_ARG;
+  const ds_status st = check_head_dim(a->head_dim);
+  if (st != DS_OK) return st;
+  if (a->rotary_dim < 0 || a->rotary_dim > a->head_dim || a->rotary_dim % 16)
+    return DS_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.f) || !(a->eps < HUGE_VALF)) return DS_ERR_INVALID_ARG;
+  if (a->n_tokens == 0) return DS_OK;   // (an empty tensor has no storage)
+  if (!token_rows_ok(a->q, a->q_stride, a->n_heads, a->head_dim) ||
+      !token_rows_ok(a->k, a->k_stride, a->n_kv_heads, a->head_dim))
+    return DS_ERR_INVALID_ARG;
+  if ((a->q_weight && !aligned(a->q_weight, 16)) || (a->k_weight && !aligned(a->k_weight, 16)))
+    return DS_ERR_INVALID_ARG;
+  if (a->rotary_dim > 0 && (!a->positions || !a->freqs || !aligned(a->positions, 4) ||
+                            !aligned(a->freqs, 8)))
+    return DS_ERR_INVALID_ARG;
+  return DS_OK;
+}
+
+RowsProblem rows_of(const ds_norm_rope_args* a) {
+  RowsProblem p{};
+  p.T = a->n_tokens;
+  p.Hq = a->n_heads;
+  p.Hkv = a->n_kv_heads;
+  p.D = a->head_dim;
+  p.rot = a->rotary_dim;
+  p.interleaved = a->interleaved != 0;
+  p.eps = a->eps;
+  p.q = a->q;
+  p.q_stride = a->q_stride;
+  p.k = a->k;
+  p.k_stride = a->k_stride;
+  p.q_weight = a->q_weight;
+  p.k_weight = a->k_weight;
+  p.positions = a->positions;
+  p.freqs = a->freqs;
+  return p;
+}
+
+}  // namespace
+
+ds_status ds_cache_write(const ds_paged_cache* cache, const uint16_t* k, int64_t k_stride,
+                         const uint16_t* v, int64_t v_stride, const int32_t* slots,
+                         int32_t n_tokens, ds_stream_t stream) {
+  const ds_status st = check_cache(cache);
+  if (st != DS_OK) return st;
+  if (n_tokens < 0 || n_tokens > kMaxTokens) return DS_ERR_INVALID_ARG;
+  if (n_tokens == 0) return DS_OK;
+  if (!token_rows_ok(k, k_stride, cache->n_kv_heads, cache->head_dim) ||
+      !token_rows_ok(v, v_stride, cache->n_kv_heads, cache->head_dim) || !slots ||
+      !aligned(slots, 4))
+    return DS_ERR_INVALID_ARG;
+  RowsProblem p{};
+  p.T = n_tokens;
+  p.Hkv = cache->n_kv_heads;
+  p.D = cache->head_dim;
+  p.k = k;
+  p.k_stride = k_stride;
+  p.v = v;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  const CacheView c = view_of(cache);
+  return launch_rows(p, &c, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DS_OK
+                                                                                  : DS_ERR_CUDA;
+}
+
+ds_status ds_cache_read(const ds_paged_cache* cache, const int32_t* slots, int32_t n_tokens,
+                        uint16_t* k_out, uint16_t* v_out, ds_stream_t stream) {
+  const ds_status st = check_cache(cache);
+  if (st != DS_OK) return st;
+  if (n_tokens < 0 || n_tokens > kMaxTokens) return DS_ERR_INVALID_ARG;
+  if (n_tokens == 0) return DS_OK;
+  if (!slots || !aligned(slots, 4) || !k_out || !v_out || !aligned(k_out, 16) ||
+      !aligned(v_out, 16))
+    return DS_ERR_INVALID_ARG;
+  return launch_cache_read(view_of(cache), cache->head_dim, slots, n_tokens, k_out, v_out,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? DS_OK
+             : DS_ERR_CUDA;
+}
+
+ds_status ds_qk_norm_rope(const ds_norm_rope_args* a, uint16_t* q_out, uint16_t* k_out,
+                          ds_stream_t stream) {
+  const ds_status st = check_norm_rope(a);
+  if (st != DS_OK) return st;
+  if (a->n_tokens == 0) return DS_OK;
+  if (!q_out || !k_out || !aligned(q_out, 16) || !aligned(k_out, 16)) return DS_ERR_INVALID_ARG;
+  if ((q_out == a->q && a->q_stride != (int64_t)a->n_heads * a->head_dim) ||
+      (k_out == a->k && a->k_stride != (int64_t)a->n_kv_heads * a->head_dim))
+    return DS_ERR_INVALID_ARG;
+  RowsProblem p = rows_of(a);
+  p.q_out = q_out;
+  p.k_out = k_out;
+  return launch_rows(p, nullptr, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? DS_OK
+             : DS_ERR_CUDA;
+}
+
+ds_status ds_qk_norm_rope_write(const ds_norm_rope_args* a, const uint16_t* v,
+                                int64_t v_stride, const ds_paged_cache* cache,
+                                const int32_t* slots, uint16_t* q_out, ds_stream_t stream) {
+  ds_status st = check_norm_rope(a);
+  if (st != DS_OK) return st;
+  st = check_cache(cache);
+  if (st != DS_OK) return st;
+  if (cache->n_kv_heads != a->n_kv_heads || cache->head_dim != a->head_dim)
+    return DS_ERR_INVALID_ARG;
+  if (a->n_tokens == 0) return DS_OK;
+  if (!token_rows_ok(v, v_stride, a->n_kv_heads, a->head_dim) || !slots || !aligned(slots, 4) ||
+      !q_out || !aligned(q_out, 16))
+    return DS_ERR_INVALID_ARG;
+  if (q_out == a->q && a->q_stride != (int64_t)a->n_heads * a->head_dim)
+    return DS_ERR_INVALID_ARG;
+  RowsProblem p = rows_of(a);
+  p.v = v;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.q_out = q_out;
+  const CacheView c = view_of(cache);
+  return launch_rows(p, &c, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DS_OK
+                                                                                  : DS_ERR_CUDA;
+}
+
+namespace {
+
+// Sizes only (no pointers).
+ds_status check_paged_sizes(const ds_paged_attn_args* a) {
+  if (!a) return DS_ERR_INVALID_ARG;
+  const ds_status st = check_cache_sizes(&a->cache);
+  if (st != DS_OK) return st;
+  if (a->n_seqs < 0 || a->n_seqs > 4096 || a->n_rows < 1 || a->n_rows > 8)
+    return DS_ERR_INVALID_ARG;
+  if (a->max_pages < 1 || (int64_t)a->max_pages * a->cache.page_tokens > (1 << 24))
+    return DS_ERR_INVALID_ARG;
+  if (a->n_heads < 1 || a->n_heads % a->cache.n_kv_heads) return DS_ERR_INVALID_ARG;
+  // (also finite in units of log2)
+  if (!std::isfinite(a->scale) || !std::isfinite(a->scale * 1.5f)) return DS_ERR_INVALID_ARG;
+  if ((int64_t)a->n_rows * (a->n_heads / a->cache.n_kv_heads) > kPagedMaxRows)
+    return DS_ERR_UNSUPPORTED;
+  return DS_OK;
+}
+
+PagedAttnProblem paged_of(const ds_paged_attn_args* a, uint16_t* out) {
+  return PagedAttnProblem{a->n_seqs, a->n_rows, a->n_heads, a->cache.head_dim, a->max_pages,
+                          a->scale, a->q, view_of(&a->cache), a->page_table, a->lengths, out};
+}
+
+}  // namespace
+
+size_t ds_paged_attn_workspace_size(const ds_paged_attn_args* a) {
+  if (check_paged_sizes(a) != DS_OK || a->n_seqs == 0) return 0;
+  return paged_attn_workspace(paged_of(a, nullptr));
+}
+
+ds_status ds_paged_attention(const ds_paged_attn_args* a, uint16_t* out, void* workspace,
+                             size_t ws_bytes, ds_stream_t stream) {
+  ds_status st = check_paged_sizes(a);
+  if (st != DS_OK) return st;
+  st = check_cache(&a->cache);
+  if (st != DS_OK) return st;
+  if (a->n_seqs == 0) return DS_OK;
+  if (!a->q || !out || !a->page_table || !a->lengths || !aligned(a->q, 16) ||
+      !aligned(out, 16) || !aligned(a->page_table, 4) || !aligned(a->lengths, 4))
+    return DS_ERR_INVALID_ARG;
+  const PagedAttnProblem p = paged_of(a, out);
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < paged_attn_workspace(p))
+    return DS_ERR_WORKSPACE;
+  return launch_paged_attn(p, static_cast<uint8_t*>(workspace),
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? DS_OK
+             : DS_ERR_CUDA;
+}
+
 namespace {
 
 bool verify_sizes_ok(int32_t B, int32_t R, int32_t V) {

@@ -145,6 +145,58 @@ int attn_splits(int L, int R);
 AttnLayout attn_layout(int L, int R, int splits);
 cudaError_t launch_attn(const AttnProblem& p, uint8_t* ws, cudaStream_t s);
 
+// ---- Q4 projections (q4.cu)
+cudaError_t launch_q4_project(const void* tiles, int rows, int K, const uint16_t* x, int R,
+                              uint16_t* y, cudaStream_t s);
+
+// ---- paged cache, norms and rotation of its rows (cache.cu)
+struct CacheView {
+  int pages, heads, page_shift;   // page_tokens = 1 << page_shift
+  bool q8;
+  uint8_t* k;
+  uint8_t* v;
+  int64_t stride;                 // values between pages
+  float* k_scale;
+  float* v_scale;
+  int64_t scale_stride;
+};
+struct RowsProblem {              // queries and keys of T tokens (Hq == 0: keys and values only)
+  int T, Hq, Hkv, D, rot;
+  bool interleaved;
+  float eps;
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint16_t* k;
+  int64_t k_stride;
+  const uint16_t* v;              // with a cache only
+  int64_t v_stride;
+  const uint16_t* q_weight;
+  const uint16_t* k_weight;
+  const int32_t* positions;
+  const int64_t* freqs;
+  const int32_t* slots;           // with a cache only
+  uint16_t* q_out;
+  uint16_t* k_out;                // without a cache only
+};
+cudaError_t launch_rows(const RowsProblem& p, const CacheView* cache, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheView& c, int D, const int32_t* slots, int n,
+                              uint16_t* k_out, uint16_t* v_out, cudaStream_t s);
+
+// ---- attention over the paged cache (paged_attn.cu)
+constexpr int kPagedMaxRows = 128;   // query rows per key head: n_rows * n_heads / n_kv_heads
+struct PagedAttnProblem {
+  int B, R, Hq, D, max_pages;
+  float scale;
+  const uint16_t* q;
+  CacheView cache;
+  const int32_t* table;
+  const int32_t* lengths;
+  uint16_t* out;
+};
+// Workspace bytes, from the sizes in p alone.
+size_t paged_attn_workspace(const PagedAttnProblem& p);
+cudaError_t launch_paged_attn(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s);
+
 // ---- verify acceptance (accept.cu)
 constexpr int kAcceptChunk = 4096;    // tokens of a row per CTA
 constexpr int kAcceptChunkSmall = 1024;   // the same for batches of few steps
