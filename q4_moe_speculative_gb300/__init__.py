@@ -398,19 +398,34 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, sel: tor
 
 
 def _need_on(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device):
-    _need(t, name, dtype, shape)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev} (got {t.device})")
+    """A contiguous tensor of this type and shape on `dev`, a CUDA device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, contiguous, on {dev} (got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device})")
+
+
+def _cuda_tensor(t: torch.Tensor, name: str, dims: int) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dim() != dims:
+        raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions "
+                         f"(got {tuple(t.shape)} on {t.device})")
+    return t.device
 
 
 def _run(dev: torch.device, stream, call):
     """call(stream handle) with `dev` current and its allocations made on the launch stream
     (the current stream of `dev` when `stream` is None)."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+    if stream is None:
+        # (the handle of torch.cuda.current_stream(dev), without making the object)
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        if dev.index == torch._C._cuda_getDevice():
+            return call(handle)
+        with torch.cuda.device(dev):
+            return call(handle)
     with torch.cuda.device(dev):
-        if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
         if not isinstance(stream, torch.cuda.Stream):
             handle = int(stream)
             stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
@@ -425,21 +440,19 @@ def q4_project(tiles: torch.Tensor, x: torch.Tensor, *, y=None, stream=None) -> 
     """R rows (1..8) through one tile-major Q4 matrix (q4_tile with group=1): tiles uint8
     [rows/16, K/64, 576], x bf16 [R, K] -> y bf16 [R, rows] (ds_q4_project)."""
     lib = N.load()
-    _need(tiles, "tiles", torch.uint8)
-    if tiles.dim() != 3 or tiles.shape[2] != N.Q4_TILE_BYTES:
-        raise ValueError(f"tiles must be [rows/16, K/64, {N.Q4_TILE_BYTES}] "
-                         f"(got {tuple(tiles.shape)})")
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be a tensor [R, K]")
-    rows, K, R, dev = tiles.shape[0] * 16, tiles.shape[1] * 64, x.shape[0], tiles.device
-    _need_on(x, "x", torch.bfloat16, (R, K), dev)
+    dev = _cuda_tensor(tiles, "tiles", 3)
+    units, Tk, _ = tiles.shape
+    _need_on(tiles, "tiles", torch.uint8, (units, Tk, N.Q4_TILE_BYTES), dev)
+    _cuda_tensor(x, "x", 2)
+    R = x.shape[0]
+    _need_on(x, "x", torch.bfloat16, (R, 64 * Tk), dev)
     if y is not None:
-        _need_on(y, "y", torch.bfloat16, (R, rows), dev)
+        _need_on(y, "y", torch.bfloat16, (R, 16 * units), dev)
 
     def call(s):
-        out = torch.empty((R, rows), dtype=torch.bfloat16, device=dev) if y is None else y
-        _check(lib.ds_q4_project(N.DsQ4Tiled(_ptr(tiles)), rows, K, _ptr(x), R, _ptr(out), s),
-               "ds_q4_project")
+        out = torch.empty((R, 16 * units), dtype=torch.bfloat16, device=dev) if y is None else y
+        _check(lib.ds_q4_project(N.DsQ4Tiled(tiles.data_ptr()), 16 * units, 64 * Tk, x.data_ptr(),
+                                 R, out.data_ptr(), s), "ds_q4_project")
         return out
 
     return _run(dev, stream, call)
@@ -477,33 +490,34 @@ class PagedCache:
         """Elements between the pages of t, whose pages are contiguous."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"cache.{name} must be a torch.Tensor")
-        if t.device != dev or t.device.type != "cuda" or t.dtype != dtype or t.shape != shape:
+        if not t.is_cuda or t.dtype is not dtype or t.shape != shape or t.device != dev:
             raise ValueError(f"cache.{name} must be {dtype} {tuple(shape)} on {dev} "
                              f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
-        if not t[0].is_contiguous():
-            raise ValueError(f"the pages of cache.{name} must be contiguous")
-        page = t[0].numel()
-        return t.stride(0) if t.shape[0] > 1 else -(-page // 16) * 16
+        strides = t.stride()
+        inner = 1
+        for n, st in zip(reversed(shape[1:]), reversed(strides[1:])):
+            if n > 1 and st != inner:
+                raise ValueError(f"the pages of cache.{name} must be contiguous")
+            inner *= n
+        return strides[0] if shape[0] > 1 else -(-inner // 16) * 16
 
     def struct(self) -> N.DsPagedCache:
-        if not isinstance(self.k, torch.Tensor) or self.k.dim() != 4 or self.k.numel() == 0:
-            raise ValueError("cache.k must be [pages, kv_heads, page_tokens, head_dim]")
-        if self.k.dtype not in (torch.bfloat16, torch.int8):
-            raise ValueError(f"cache.k must be bfloat16 or int8 (got {self.k.dtype})")
-        shape, dev, dt = self.k.shape, self.k.device, self.k.dtype
-        stride = self._stride(self.k, "k", dt, shape, dev)
-        if self._stride(self.v, "v", dt, shape, dev) != stride:
+        k, v = self.k, self.v
+        dev = _cuda_tensor(k, "cache.k", 4)
+        dt, shape = k.dtype, k.shape
+        stride = self._stride(k, "k", dt, shape, dev)
+        if self._stride(v, "v", dt, shape, dev) != stride:
             raise ValueError("cache.k and cache.v must have the same page stride")
-        scale_stride, ks, vs = 0, None, None
-        if self.q8:
-            scale_stride = self._stride(self.k_scale, "k_scale", torch.float32, shape[:3], dev)
-            if self._stride(self.v_scale, "v_scale", torch.float32, shape[:3],
-                            dev) != scale_stride:
-                raise ValueError("cache.k_scale and cache.v_scale must have the same page stride")
-            ks, vs = _ptr(self.k_scale), _ptr(self.v_scale)
-        return N.DsPagedCache(shape[0], shape[1], shape[2], shape[3],
-                              N.DS_CACHE_Q8 if self.q8 else N.DS_CACHE_BF16, _ptr(self.k),
-                              _ptr(self.v), stride, ks, vs, scale_stride)
+        if dt is torch.bfloat16:
+            return N.DsPagedCache(*shape, N.DS_CACHE_BF16, k.data_ptr(), v.data_ptr(), stride)
+        if dt is not torch.int8:
+            raise ValueError(f"cache.k must be bfloat16 or int8 (got {dt})")
+        rows, ks, vs = shape[:3], self.k_scale, self.v_scale
+        scale_stride = self._stride(ks, "k_scale", torch.float32, rows, dev)
+        if self._stride(vs, "v_scale", torch.float32, rows, dev) != scale_stride:
+            raise ValueError("cache.k_scale and cache.v_scale must have the same page stride")
+        return N.DsPagedCache(*shape, N.DS_CACHE_Q8, k.data_ptr(), v.data_ptr(), stride,
+                              ks.data_ptr(), vs.data_ptr(), scale_stride)
 
 
 def rope_frequencies(rotary_dim: int | None = None, base: float = 10000.0, *, inv_freq=None,
@@ -533,37 +547,39 @@ def _token_rows(t: torch.Tensor, name: str, shape: tuple, dev: torch.device) -> 
     """Values between the tokens of t [tokens, heads, head_dim]."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev or t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be bfloat16 {shape} on {dev} "
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} must be bfloat16 {tuple(shape)} on {dev} "
                          f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
     T, H, D = shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    per_token, per_head, per_value = t.stride()
+    if (D > 1 and per_value != 1) or (H > 1 and per_head != D):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if T > 1 else -(-H * D // 8) * 8
+    return per_token if T > 1 else -(-H * D // 8) * 8
 
 
 def _norm_rope_args(q, k, positions, freqs, q_weight, k_weight, eps, interleaved):
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.device.type != "cuda":
-        raise ValueError("q must be a CUDA tensor [tokens, heads, head_dim]")
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a CUDA tensor [tokens, kv_heads, head_dim]")
-    (T, Hq, D), Hkv, dev = q.shape, k.shape[1], q.device
+    dev = _cuda_tensor(q, "q", 3)
+    _cuda_tensor(k, "k", 3)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
     qs = _token_rows(q, "q", (T, Hq, D), dev)
     ks = _token_rows(k, "k", (T, Hkv, D), dev)
-    rot = 0
+    rot, pos_p, freq_p, qw_p, kw_p = 0, None, None, None, None
     if freqs is not None:
-        if freqs.dim() != 1:
-            raise ValueError("freqs must be [rotary_dim / 2]")
-        _need_on(freqs, "freqs", torch.int64, tuple(freqs.shape), dev)
-        rot = 2 * freqs.shape[0]
-    if rot:
-        _need_on(positions, "positions", torch.int32, (T,), dev)
-    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need_on(w, nm, torch.bfloat16, (D,), dev)
-    return N.DsNormRopeArgs(T, Hq, Hkv, D, rot, int(bool(interleaved)), float(eps), _ptr(q), qs,
-                            _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
-                            _ptr(positions) if rot else None, _ptr(freqs) if rot else None)
+        _cuda_tensor(freqs, "freqs", 1)
+        pairs = freqs.shape[0]
+        _need_on(freqs, "freqs", torch.int64, (pairs,), dev)
+        if pairs:
+            _need_on(positions, "positions", torch.int32, (T,), dev)
+            rot, pos_p, freq_p = 2 * pairs, positions.data_ptr(), freqs.data_ptr()
+    if q_weight is not None:
+        _need_on(q_weight, "q_weight", torch.bfloat16, (D,), dev)
+        qw_p = q_weight.data_ptr()
+    if k_weight is not None:
+        _need_on(k_weight, "k_weight", torch.bfloat16, (D,), dev)
+        kw_p = k_weight.data_ptr()
+    return N.DsNormRopeArgs(T, Hq, Hkv, D, rot, 1 if interleaved else 0, eps, q.data_ptr(), qs,
+                            k.data_ptr(), ks, qw_p, kw_p, pos_p, freq_p)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions, freqs, *, q_weight=None,
@@ -577,14 +593,15 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions, freqs, *, q_weight
     lib = N.load()
     a = _norm_rope_args(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
     dev = q.device
-    for t, nm, like in ((q_out, "q_out", q), (k_out, "k_out", k)):
-        if t is not None:
-            _need_on(t, nm, torch.bfloat16, tuple(like.shape), dev)
+    if q_out is not None:
+        _need_on(q_out, "q_out", torch.bfloat16, q.shape, dev)
+    if k_out is not None:
+        _need_on(k_out, "k_out", torch.bfloat16, k.shape, dev)
 
     def call(s):
         qo = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
         ko = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-        _check(lib.ds_qk_norm_rope(a, _ptr(qo), _ptr(ko), s), "ds_qk_norm_rope")
+        _check(lib.ds_qk_norm_rope(a, qo.data_ptr(), ko.data_ptr(), s), "ds_qk_norm_rope")
         return qo, ko
 
     return _run(dev, stream, call)
@@ -597,19 +614,19 @@ def qk_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     cache at slots int32 [T] (ds_qk_norm_rope_write). Returns q_out."""
     lib = N.load()
     a = _norm_rope_args(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
-    dev, T = q.device, q.shape[0]
-    vs = _token_rows(v, "v", tuple(k.shape), dev)
-    _need_on(slots, "slots", torch.int32, (T,), dev)
+    dev = q.device
+    vs = _token_rows(v, "v", k.shape, dev)
+    _need_on(slots, "slots", torch.int32, q.shape[:1], dev)
     c = cache.struct()
     if cache.k.device != dev:
         raise ValueError(f"the cache must be on {dev} (got {cache.k.device})")
     if q_out is not None:
-        _need_on(q_out, "q_out", torch.bfloat16, tuple(q.shape), dev)
+        _need_on(q_out, "q_out", torch.bfloat16, q.shape, dev)
 
     def call(s):
         qo = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-        _check(lib.ds_qk_norm_rope_write(a, _ptr(v), vs, c, _ptr(slots), _ptr(qo), s),
-               "ds_qk_norm_rope_write")
+        _check(lib.ds_qk_norm_rope_write(a, v.data_ptr(), vs, c, slots.data_ptr(), qo.data_ptr(),
+                                         s), "ds_qk_norm_rope_write")
         return qo
 
     return _run(dev, stream, call)
@@ -622,13 +639,13 @@ def cache_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     the cache are skipped; the others must be distinct."""
     lib = N.load()
     c, dev = cache.struct(), cache.k.device
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a CUDA tensor [tokens, kv_heads, head_dim]")
-    shape = (k.shape[0], c.n_kv_heads, c.head_dim)
+    _cuda_tensor(k, "k", 3)
+    T = k.shape[0]
+    shape = (T, c.n_kv_heads, c.head_dim)
     ks, vs = _token_rows(k, "k", shape, dev), _token_rows(v, "v", shape, dev)
-    _need_on(slots, "slots", torch.int32, shape[:1], dev)
+    _need_on(slots, "slots", torch.int32, (T,), dev)
     _run(dev, stream, lambda s: _check(
-        lib.ds_cache_write(c, _ptr(k), ks, _ptr(v), vs, _ptr(slots), shape[0], s),
+        lib.ds_cache_write(c, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, s),
         "ds_cache_write"))
 
 
@@ -637,19 +654,20 @@ def cache_read(cache: PagedCache, slots: torch.Tensor, *, k_out=None, v_out=None
     (ds_cache_read). Slots outside the cache give zeros."""
     lib = N.load()
     c, dev = cache.struct(), cache.k.device
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-        raise ValueError("slots must be a CUDA tensor [tokens]")
+    _cuda_tensor(slots, "slots", 1)
     T = slots.shape[0]
     shape = (T, c.n_kv_heads, c.head_dim)
     _need_on(slots, "slots", torch.int32, (T,), dev)
-    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None:
-            _need_on(t, nm, torch.bfloat16, shape, dev)
+    if k_out is not None:
+        _need_on(k_out, "k_out", torch.bfloat16, shape, dev)
+    if v_out is not None:
+        _need_on(v_out, "v_out", torch.bfloat16, shape, dev)
 
     def call(s):
         ko = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
         vo = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
-        _check(lib.ds_cache_read(c, _ptr(slots), T, _ptr(ko), _ptr(vo), s), "ds_cache_read")
+        _check(lib.ds_cache_read(c, slots.data_ptr(), T, ko.data_ptr(), vo.data_ptr(), s),
+               "ds_cache_read")
         return ko, vo
 
     return _run(dev, stream, call)
@@ -664,34 +682,32 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     scale defaults to 1 / sqrt(D)."""
     lib = N.load()
     c, dev = cache.struct(), cache.k.device
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a CUDA tensor [B, R, heads, head_dim]")
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be a CUDA tensor [B, max_pages]")
+    _cuda_tensor(q, "q", 4)
+    _cuda_tensor(page_table, "page_table", 2)
     B, R, Hq, D = q.shape
     if D != c.head_dim:
         raise ValueError(f"q must have the cache's head_dim {c.head_dim} (got {D})")
+    max_pages = page_table.shape[1]
     _need_on(q, "q", torch.bfloat16, (B, R, Hq, D), dev)
-    _need_on(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    _need_on(page_table, "page_table", torch.int32, (B, max_pages), dev)
     _need_on(lengths, "lengths", torch.int32, (B,), dev)
     if out is not None:
         _need_on(out, "out", torch.bfloat16, (B, R, Hq, D), dev)
-    args = N.DsPagedAttnArgs(B, R, Hq, page_table.shape[1],
-                             D ** -0.5 if scale is None else float(scale), _ptr(q), c,
-                             _ptr(page_table), _ptr(lengths))
+    if workspace is not None:
+        _need_on(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    args = N.DsPagedAttnArgs(B, R, Hq, max_pages, D ** -0.5 if scale is None else scale,
+                             q.data_ptr(), c, page_table.data_ptr(), lengths.data_ptr())
 
     def call(s):
-        o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        o = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
         ws = workspace
         if ws is None:
-            ws = torch.empty(max(1, lib.ds_paged_attn_workspace_size(args)), dtype=torch.uint8,
+            ws = torch.empty(lib.ds_paged_attn_workspace_size(args), dtype=torch.uint8,
                              device=dev)
-        _check(lib.ds_paged_attention(args, _ptr(o), _ptr(ws), ws.numel(), s),
+        _check(lib.ds_paged_attention(args, o.data_ptr(), ws.data_ptr(), ws.numel(), s),
                "ds_paged_attention")
         return o
 
-    if workspace is not None:
-        _need_on(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev)
     return _run(dev, stream, call)
 
 
