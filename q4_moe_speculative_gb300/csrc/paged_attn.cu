@@ -22,6 +22,9 @@
 // maxima and no rescaling: the CTA votes on it at the barrier that publishes P anyway.
 // P is rounded once to bf16, half a step of 2^-8 relative per term; for a bf16 cache the
 // normaliser sums the rounded values, so that the weights add up to one.
+#include <atomic>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -186,18 +189,23 @@ struct Shape {
   static constexpr int RB = D * (kQ8 ? 1 : 2);          // bytes of a cached row
   static constexpr int kMat = kTile * RB;
   static constexpr int kStage = 2 * kMat + (kQ8 ? 2 * kTile * 4 : 0);
+  static constexpr bool kSplit = kQ8 || kRows <= 32;    // P as a high and a low part
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kP = kRows * kTile * 2;
   static constexpr int kRed = 4 * kRows * 4;
-  static constexpr int kFixed = kQ + kP + kRed;
-  // two CTAs per SM while three stages fit beside the rest, else one with a deeper ring
-  static constexpr int kHalf = 113 * 1024, kWhole = 226 * 1024;
-  static constexpr bool kTwo = MH == 1 && kFixed + 3 * kStage <= kHalf;
-  static constexpr int kFit = ((kTwo ? kHalf : kWhole) - kFixed) / kStage;
+  static constexpr int kFixed = kQ + kP * (kSplit ? 2 : 1) + kRed + 64;
+  // CTAs per SM: as many as the registers allow (65,536 over the threads at 128, 168 or 255
+  // each) with at least two stages each
+  static constexpr int kWant = MH == 2 ? 1 : (MT == 1 ? 4 : MT == 2 ? 3 : 2);
+  static constexpr int room(int n) { return 228 * 1024 / n - 1024; }
+  static constexpr int fit(int n) {
+    return n > 1 && kFixed + 2 * kStage > room(n) ? fit(n - 1) : n;
+  }
+  static constexpr int kPerSm = fit(kWant);
+  static constexpr int kFit = (room(kPerSm) - kFixed) / kStage;
   static constexpr int kStages = kFit > 5 ? 5 : kFit;
-  static constexpr int kPerSm = kTwo ? 2 : 1;
   static constexpr int kSmem = kFixed + kStages * kStage;
-  static_assert(kStages >= 2, "a ring of at least two stages");
+  static_assert(kStages >= 2 && kStages <= 8, "a ring of two to eight stages");
 };
 
 template <int D, bool kQ8, int MT, int MH>
@@ -208,7 +216,8 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* sQ = sm + S * C::kStage;
   uint8_t* sP = sQ + C::kQ;
-  float* red = reinterpret_cast<float*>(sP + C::kP);   // [4][kRows]
+  float* red = reinterpret_cast<float*>(sP + C::kP * (C::kSplit ? 2 : 1));   // [4][kRows]
+  bool* there = reinterpret_cast<bool*>(red + 4 * C::kRows);   // [stage][4] 16-token groups
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w4 = warp & 3, row0 = (warp >> 2) * MT * 16;
   const int g = lane >> 2, q = lane & 3;
@@ -228,44 +237,58 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
     const int p = a.table[(int64_t)b * a.max_pages + (t >> a.c.page_shift)];
     return p >= 0 && p < a.c.pages ? p : -1;
   };
+  // Each run of 16 tokens lies in one page. Lane x of every warp holds where run x & 3 of the
+  // tile to be fetched next starts (in values, -1: nowhere), looked up a tile ahead.
+  int64_t run_at, run_scale;
+  auto look_up = [&](const Cursor& at) {
+    const int t = at.tile * kTile + 16 * (lane & 3), page = page_of(at.b, t, at.len);
+    const int64_t in_page = ((int64_t)at.h << a.c.page_shift) + (t & page_mask);
+    run_at = page < 0 ? -1 : page * a.c.stride + in_page * D;
+    if (kQ8) run_scale = page < 0 ? -1 : page * a.c.scale_stride + in_page;
+  };
+  constexpr int kChunks = RB / 16, kStep = C::kThreads / kChunks;   // rows per iteration
+  const int my_row = tid / kChunks, my_chunk = tid % kChunks;
+  const uint32_t my_dst = swz<RB>(my_row, my_chunk);   // (kStep is a multiple of 8 rows)
   auto load_tile = [&](const Cursor& at, int stage) {
-    const uint32_t k0 = smem_u32(sm + stage * C::kStage), v0 = k0 + C::kMat;
-    constexpr int kChunks = RB / 16, kIters = kTile * kChunks / C::kThreads;
+    const uint32_t k0 = smem_u32(sm + stage * C::kStage) + my_dst, v0 = k0 + C::kMat;
+    const int left = at.len - at.tile * kTile;   // tokens from the tile's first on
+    int64_t run = 0;
 #pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      const int idx = it * C::kThreads + tid, r = idx / kChunks, ch = idx % kChunks;
-      const int t = at.tile * kTile + r, page = page_of(at.b, t, at.len);
-      const bool ok = page >= 0;
-      const int64_t off =
-          ok ? (page * a.c.stride + (((int64_t)at.h << a.c.page_shift) + (t & page_mask)) * D) *
-                       (kQ8 ? 1 : 2) + ch * 16
-             : 0;
-      cp_async16(k0 + swz<RB>(r, ch), a.c.k + off, ok);
-      cp_async16(v0 + swz<RB>(r, ch), a.c.v + off, ok);
+    for (int it = 0; it < kTile / kStep; ++it) {
+      const int r = it * kStep + my_row;
+      if (it * kStep % 16 == 0 || kStep > 16) run = __shfl_sync(0xffffffffu, run_at, (r >> 4) & 3);
+      const bool ok = run >= 0 && r < left;
+      const int64_t off = ok ? (run + (r & 15) * D) * (kQ8 ? 1 : 2) + my_chunk * 16 : 0;
+      cp_async16(k0 + it * kStep * RB, a.c.k + off, ok);
+      cp_async16(v0 + it * kStep * RB, a.c.v + off, ok);
     }
-    if constexpr (kQ8) {
-      if (tid < 32) {   // 4 scales per copy: 16 of the keys, 16 of the values
-        const int t = at.tile * kTile + 4 * (tid & 15), page = page_of(at.b, t, at.len);
-        const int64_t off =
-            page >= 0 ? page * a.c.scale_stride + ((int64_t)at.h << a.c.page_shift) + (t & page_mask)
-                      : 0;
-        cp_async16(v0 + C::kMat + 16 * tid, (tid < 16 ? a.c.k_scale : a.c.v_scale) + off,
-                   page >= 0);
+    if (warp == 0) {
+      if constexpr (kQ8) {   // 4 scales per copy: 16 of the keys, 16 of the values
+        const int r = 4 * (lane & 15);
+        const int64_t at_s = __shfl_sync(0xffffffffu, run_scale, r >> 4);
+        const bool ok = at_s >= 0 && r < left;
+        cp_async16(smem_u32(sm + stage * C::kStage) + 2 * C::kMat + 16 * lane,
+                   (lane < 16 ? a.c.k_scale : a.c.v_scale) + (ok ? at_s + (r & 15) : 0), ok);
       }
+      if (lane < 4) there[4 * stage + lane] = run_at >= 0;
     }
   };
 
   const int n = (int)(hi - lo);   // tiles of this CTA
   int fetched = 0;
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) {
+  auto fetch = [&](int stage) {
     if (fetched < n) {
-      load_tile(ahead, s);
-      ahead.next(a);
-      ++fetched;
+      load_tile(ahead, stage);
+      if (++fetched < n) {
+        ahead.next(a);
+        look_up(ahead);
+      }
     }
     cp_async_commit();
-  }
+  };
+  look_up(ahead);
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(s);
 
   int rr[MT][2];   // verify row of this lane's query rows
 #pragma unroll
@@ -316,20 +339,22 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
     }
     cp_async_wait<S - 2>();
     __syncthreads();   // the tile and the queries are there; the tile before is done with
-    if (fetched < n) {
-      load_tile(ahead, refill);
-      ahead.next(a);
-      ++fetched;
-    }
-    cp_async_commit();
+    fetch(refill);
 
     const int t0 = cur.tile * kTile, seen0 = cur.len - (a.R - 1);   // row r sees t < seen0 + r
     // ------------------------------------------------------------ S = Q K^T ---------
-    float s[MT][2][4];
+    // (few rows: even and odd steps in accumulators of their own, for shorter chains)
+    constexpr int kSets = MT <= 2 ? 2 : 1;
+    float s[MT][2][4], s_odd[kSets == 2 ? MT : 1][2][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[mt][nt][e] = 0.f;
+          if constexpr (kSets == 2) s_odd[mt][nt][e] = 0.f;
+        }
     {
       const uint32_t kb = smem_u32(sK), qb = smem_u32(sQ);
       constexpr int kSteps = D / 16, kPer = kQ8 ? 4 : 2;   // 16-value steps per ldmatrix.x4
@@ -357,15 +382,33 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t qf[4];
             ldsm_x4(qb + swz<2 * D>(row0 + 16 * mt + (lane & 15), 2 * ks + (lane >> 4)), qf);
-            mma16816(s[mt][0], qf, b[0][0], b[0][1]);
-            mma16816(s[mt][1], qf, b[1][0], b[1][1]);
+            if (kSets == 2 && (ks & 1)) {
+              mma16816(s_odd[kSets == 2 ? mt : 0][0], qf, b[0][0], b[0][1]);
+              mma16816(s_odd[kSets == 2 ? mt : 0][1], qf, b[1][0], b[1][1]);
+            } else {
+              mma16816(s[mt][0], qf, b[0][0], b[0][1]);
+              mma16816(s[mt][1], qf, b[1][0], b[1][1]);
+            }
           }
         }
+      }
+      if constexpr (kSets == 2) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][nt][e] = __fadd_rn(s[mt][nt][e], s_odd[mt][nt][e]);
       }
     }
     // -------------------------------------------------- scale, mask, P = 2^(S - m) ---
     // this lane: rows g (s[.][.][0, 1]) and g + 8 (2, 3), tokens 8 nt + 2q, 2q + 1 of the warp's
-    float vs[2][2];
+    float vs[2][2], ref[MT][2], top[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      ref[mt][0] = m[mt][0] == kNegInf ? 0.f : m[mt][0];
+      ref[mt][1] = m[mt][1] == kNegInf ? 0.f : m[mt][1];
+    }
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       float f0 = a.scale_log2, f1 = f0;
@@ -378,15 +421,15 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
         vs[nt][1] = vq.y;
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        s[mt][nt][0] = __fmul_rn(s[mt][nt][0], f0);
-        s[mt][nt][1] = __fmul_rn(s[mt][nt][1], f1);
-        s[mt][nt][2] = __fmul_rn(s[mt][nt][2], f0);
-        s[mt][nt][3] = __fmul_rn(s[mt][nt][3], f1);
+      for (int mt = 0; mt < MT; ++mt) {   // s: log2 of p, before any mask
+        s[mt][nt][0] = __fmaf_rn(s[mt][nt][0], f0, -ref[mt][0]);
+        s[mt][nt][1] = __fmaf_rn(s[mt][nt][1], f1, -ref[mt][0]);
+        s[mt][nt][2] = __fmaf_rn(s[mt][nt][2], f0, -ref[mt][1]);
+        s[mt][nt][3] = __fmaf_rn(s[mt][nt][3], f1, -ref[mt][1]);
       }
     }
-    const int wt0 = t0 + 16 * w4;   // the warp's first token; its 16 lie in one page
-    const bool gone = page_of(cur.b, wt0, cur.len) < 0;
+    const int wt0 = t0 + 16 * w4;   // the warp's first token
+    const bool gone = !there[4 * stage + w4];
     const bool edge = gone || wt0 + 16 > seen0;
     if (edge) {
 #pragma unroll
@@ -405,28 +448,29 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float ref = m[mt][e] == kNegInf ? 0.f : m[mt][e];
           const int row = row0 + 16 * mt + g + 8 * e;
           float sum = 0.f;
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             const float s0 = s[mt][nt][2 * e], s1 = s[mt][nt][2 * e + 1];
-            float p0 = exp2_fast(__fsub_rn(s0, ref)), p1 = exp2_fast(__fsub_rn(s1, ref));
-            uint32_t w;
+            float p0 = exp2_fast(s0), p1 = exp2_fast(s1);
+            uint8_t* dst = sP + swz<2 * kTile>(row, 2 * w4 + nt) + 4 * q;
+            if constexpr (C::kSplit) sum = __fadd_rn(sum, __fadd_rn(p0, p1));
             if constexpr (kQ8) {
-              sum = __fadd_rn(sum, __fadd_rn(p0, p1));
               p0 = __fmul_rn(p0, vs[nt][0]);
               p1 = __fmul_rn(p1, vs[nt][1]);
               if (edge) {   // a masked token's scale may be anything
                 p0 = s0 == kNegInf ? 0.f : p0;
                 p1 = s1 == kNegInf ? 0.f : p1;
               }
-              w = pack2(p0, p1);
-            } else {
-              w = pack2(p0, p1);
-              sum = __fadd_rn(sum, __fadd_rn(bf16_lo(w), bf16_hi(w)));
             }
-            *reinterpret_cast<uint32_t*>(sP + swz<2 * kTile>(row, 2 * w4 + nt) + 4 * q) = w;
+            const uint32_t w = pack2(p0, p1);
+            *reinterpret_cast<uint32_t*>(dst) = w;
+            if constexpr (C::kSplit)
+              *reinterpret_cast<uint32_t*>(dst + C::kP) =
+                  pack2(__fsub_rn(p0, bf16_lo(w)), __fsub_rn(p1, bf16_hi(w)));
+            else
+              sum = __fadd_rn(sum, __fadd_rn(bf16_lo(w), bf16_hi(w)));
           }
           lt[mt][e] = sum;
         }
@@ -436,9 +480,11 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) over |= s[mt][nt][e] > __fadd_rn(m[mt][e >> 1], kSlack);
+      for (int e = 0; e < 2; ++e) {
+        top[mt][e] = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]),
+                           fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
+        over |= top[mt][e] > (m[mt][e] == kNegInf ? kNegInf : kSlack);
+      }
     make_p();
     if (__syncthreads_or(over)) {
       // some row's reference moves: exchange the tile's maxima, rescale, and make P again
@@ -446,11 +492,10 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]),
-                            fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          if (q == 0) red[w4 * C::kRows + row0 + 16 * mt + g + 8 * e] = top;
+          float x = __fadd_rn(top[mt][e], ref[mt][e]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          if (q == 0) red[w4 * C::kRows + row0 + 16 * mt + g + 8 * e] = x;
         }
       __syncthreads();
 #pragma unroll
@@ -458,16 +503,21 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float* rp = red + row0 + 16 * mt + g + 8 * e;
-          const float top = fmaxf(fmaxf(rp[0], rp[C::kRows]),
-                                  fmaxf(rp[2 * C::kRows], rp[3 * C::kRows]));
-          const float mn = fmaxf(m[mt][e], top);
+          const float mn = fmaxf(m[mt][e], fmaxf(fmaxf(rp[0], rp[C::kRows]),
+                                                 fmaxf(rp[2 * C::kRows], rp[3 * C::kRows])));
           const float f = m[mt][e] == kNegInf ? 0.f : exp2_fast(__fsub_rn(m[mt][e], mn));
+          const float move = __fsub_rn(ref[mt][e], mn == kNegInf ? 0.f : mn);
           m[mt][e] = mn;
           l[mt][e] = __fmul_rn(l[mt][e], f);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             o[mt][nt][2 * e] = __fmul_rn(o[mt][nt][2 * e], f);
             o[mt][nt][2 * e + 1] = __fmul_rn(o[mt][nt][2 * e + 1], f);
+          }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            s[mt][nt][2 * e] = __fadd_rn(s[mt][nt][2 * e], move);
+            s[mt][nt][2 * e + 1] = __fadd_rn(s[mt][nt][2 * e + 1], move);
           }
         }
       make_p();
@@ -526,6 +576,12 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
           ldsm_x4(pb + swz<2 * kTile>(row0 + 16 * mt + (lane & 15), 2 * ks + (lane >> 4)), pf);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816(o[mt][nt], pf, b[nt][0], b[nt][1]);
+          if constexpr (C::kSplit) {
+            ldsm_x4(pb + C::kP + swz<2 * kTile>(row0 + 16 * mt + (lane & 15), 2 * ks + (lane >> 4)),
+                    pf);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[mt][nt], pf, b[nt][0], b[nt][1]);
+          }
         }
       }
     }
@@ -544,8 +600,10 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
             for (int e = 0; e < 2; ++e) {
               if (t0 + t >= seen0 + rr[mt][e]) continue;
               const int row = row0 + 16 * mt + g + 8 * e;
-              const float p = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(
-                  sP + swz<2 * kTile>(row, t >> 3) + 2 * (t & 7)));
+              const uint8_t* ps = sP + swz<2 * kTile>(row, t >> 3) + 2 * (t & 7);
+              float p = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(ps));
+              if constexpr (C::kSplit)
+                p = __fadd_rn(p, bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(ps + C::kP)));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 o[mt][nt][2 * e] = __fmaf_rn(p, bf16_lo(v[nt]), o[mt][nt][2 * e]);
@@ -765,9 +823,17 @@ cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   cudaError_t err = with_rows<D, kQ8>(a.M, [&](auto mt, auto mh) {
     using C = Shape<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
     const auto kernel = k_paged<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    // (the attribute belongs to the kernel on a device and lasts: set once on each)
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      if (e != cudaSuccess) return e;
+      ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch_pdl(kernel, dim3(pl.grid), C::kThreads, C::kSmem, s, a);
   });
   if (err != cudaSuccess) return err;
