@@ -160,6 +160,11 @@ struct CacheView {
   float* v_scale;
   int64_t scale_stride;
 };
+// TMA tensor map of bf16 pages [pages][rows][D] (page_stride values apart, a multiple of 8) in
+// boxes of 64 values x box_rows rows of one page, 128-byte swizzle. Encoded at every call.
+cudaError_t page_tile_map(CUtensorMap* out, const void* base, int D, int rows, int pages,
+                          int64_t page_stride, int box_rows);
+
 struct RowsProblem {              // queries and keys of T tokens (Hq == 0: keys and values only)
   int T, Hq, Hkv, D, rot;
   bool interleaved;

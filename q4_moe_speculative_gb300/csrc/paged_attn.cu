@@ -22,47 +22,17 @@
 // maxima and no rescaling: the CTA votes on it at the barrier that publishes P anyway.
 // P is rounded once to bf16, half a step of 2^-8 relative per term; for a bf16 cache the
 // normaliser sums the rounded values, so that the weights add up to one.
-#include <atomic>
 #include <type_traits>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "paged.cuh"
 
 namespace dsmoe {
 namespace {
 
+using namespace paged;
+
 constexpr int kTile = 64;
-constexpr float kNegInf = -INFINITY;
-constexpr float kSlack = 8.f;   // log2 by which a score may exceed the row's reference
 
-struct PagedArgs {
-  int B, R, Hq, G, M, max_pages;
-  float scale_log2;
-  const uint16_t* q;
-  CacheView c;
-  const int32_t* table;
-  const int32_t* lengths;
-  uint16_t* out;
-  float* part_o;    // [2 grid][M][D]
-  float* part_ml;   // [2 grid][M][2]
-  int grid;         // CTAs of k_paged
-};
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -88,97 +58,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// The int8 values at bytes 0 and 2 of w as a bf16 pair, exactly: (128 + low 7 bits) minus
-// 128 or, with the sign bit, 256.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  uint32_t m, c, d;
-  asm("lop3.b32 %0, %1, 0x007F007F, 0x43004300, 0xEA;" : "=r"(m) : "r"(w));
-  asm("lop3.b32 %0, %1, 0x00800080, 0x43004300, 0xEA;" : "=r"(c) : "r"(w));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
 // Byte offset of 16-byte chunk c of row r in a tile of rows of RB bytes: the eight rows of
 // an ldmatrix meet eight different bank groups.
 template <int RB>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   if constexpr (RB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   return r * RB + ((c ^ (r & 7)) << 4);
-}
-
-__device__ __forceinline__ int seq_len(const PagedArgs& a, int b) {
-  const int n = a.lengths[b], cap = a.max_pages << a.c.page_shift;
-  return n < 0 ? 0 : (n > cap ? cap : n);
-}
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
-
-// Tiles of all sequences, per key head (every lane of the warp gets the sum).
-__device__ __forceinline__ int64_t all_tiles(const PagedArgs& a, int lane) {
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32)
-    sum += b0 + lane < a.B ? tiles_of(seq_len(a, b0 + lane)) : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
-}
-
-// The place of a tile in the list: sequences, then key heads, then tiles along the length.
-struct Cursor {
-  int b, h, tile, tiles, len;
-  __device__ __forceinline__ void open(const PagedArgs& a) {   // first non-empty from b on
-    for (; b < a.B; ++b) {
-      len = seq_len(a, b);
-      tiles = tiles_of(len);
-      if (tiles) break;
-    }
-  }
-  __device__ __forceinline__ void next(const PagedArgs& a) {
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++h < a.c.heads) return;
-    h = 0;
-    ++b;
-    open(a);
-  }
-};
-
-// The cursor of tile `at` (warp-wide search; at is inside the list).
-__device__ __forceinline__ Cursor find_tile(const PagedArgs& a, int64_t at, int lane) {
-  Cursor cur{};
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 + lane < a.B ? tiles_of(seq_len(a, b0 + lane)) : 0;
-    int64_t upto = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, (before + upto) * a.c.heads > at);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      const int64_t first =
-          (before + __shfl_sync(0xffffffffu, upto - n, l)) * a.c.heads;   // of sequence b0 + l
-      cur.b = b0 + l;
-      cur.len = seq_len(a, cur.b);
-      cur.tiles = tiles_of(cur.len);
-      cur.h = (int)((at - first) / cur.tiles);
-      cur.tile = (int)((at - first) % cur.tiles);
-      return cur;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  cur.b = a.B;
-  return cur;
 }
 
 // Shapes of one instantiation: MT m16 tiles of rows per warp, MH groups of four warps.
@@ -224,24 +109,18 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
   pdl_trigger();
   pdl_wait();
 
-  const int64_t total = all_tiles(a, lane) * a.c.heads;
-  const int64_t ctas = total < a.grid ? total : a.grid;   // every one has a tile
-  if (blockIdx.x >= ctas) return;
-  const int64_t lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
-  Cursor cur = find_tile(a, lo, lane), ahead = cur;
+  if (blockIdx.x == 0 && tid == 0) *a.status = 0u;
+  Cursor cur{};
+  const int n = cta_run(a, blockIdx.x, lane, &cur);   // tiles of this CTA
+  if (n == 0) return;
+  Cursor ahead = cur;
 
   const int page_mask = (1 << a.c.page_shift) - 1;
-  // page of token t of sequence b, or -1: no such token, or a bad page table entry
-  auto page_of = [&](int b, int t, int len) {
-    if (t >= len) return -1;
-    const int p = a.table[(int64_t)b * a.max_pages + (t >> a.c.page_shift)];
-    return p >= 0 && p < a.c.pages ? p : -1;
-  };
   // Each run of 16 tokens lies in one page. Lane x of every warp holds where run x & 3 of the
   // tile to be fetched next starts (in values, -1: nowhere), looked up a tile ahead.
   int64_t run_at, run_scale;
   auto look_up = [&](const Cursor& at) {
-    const int t = at.tile * kTile + 16 * (lane & 3), page = page_of(at.b, t, at.len);
+    const int t = at.tile * kTile + 16 * (lane & 3), page = page_of(a, at.b, t, at.len);
     const int64_t in_page = ((int64_t)at.h << a.c.page_shift) + (t & page_mask);
     run_at = page < 0 ? -1 : page * a.c.stride + in_page * D;
     if (kQ8) run_scale = page < 0 ? -1 : page * a.c.scale_stride + in_page;
@@ -250,7 +129,7 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
   const int my_row = tid / kChunks, my_chunk = tid % kChunks;
   const uint32_t my_dst = swz<RB>(my_row, my_chunk);   // (kStep is a multiple of 8 rows)
   auto load_tile = [&](const Cursor& at, int stage) {
-    const uint32_t k0 = smem_u32(sm + stage * C::kStage) + my_dst, v0 = k0 + C::kMat;
+    const uint32_t k0 = smem_at(sm + stage * C::kStage) + my_dst, v0 = k0 + C::kMat;
     const int left = at.len - at.tile * kTile;   // tokens from the tile's first on
     int64_t run = 0;
 #pragma unroll
@@ -267,14 +146,13 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
         const int r = 4 * (lane & 15);
         const int64_t at_s = __shfl_sync(0xffffffffu, run_scale, r >> 4);
         const bool ok = at_s >= 0 && r < left;
-        cp_async16(smem_u32(sm + stage * C::kStage) + 2 * C::kMat + 16 * lane,
+        cp_async16(smem_at(sm + stage * C::kStage) + 2 * C::kMat + 16 * lane,
                    (lane < 16 ? a.c.k_scale : a.c.v_scale) + (ok ? at_s + (r & 15) : 0), ok);
       }
       if (lane < 4) there[4 * stage + lane] = run_at >= 0;
     }
   };
 
-  const int n = (int)(hi - lo);   // tiles of this CTA
   int fetched = 0;
   auto fetch = [&](int stage) {
     if (fetched < n) {
@@ -356,7 +234,7 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
           if constexpr (kSets == 2) s_odd[mt][nt][e] = 0.f;
         }
     {
-      const uint32_t kb = smem_u32(sK), qb = smem_u32(sQ);
+      const uint32_t kb = smem_at(sK), qb = smem_at(sQ);
       constexpr int kSteps = D / 16, kPer = kQ8 ? 4 : 2;   // 16-value steps per ldmatrix.x4
 #pragma unroll
       for (int kk = 0; kk < kSteps / kPer; ++kk) {
@@ -533,7 +411,7 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
     // (at most 7) tokens from seen0 on are left out of the product and added row by row.
     const bool part_seen = !kQ8 && a.R > 1 && t0 + kTile > seen0;
     {
-      const uint32_t vb = smem_u32(sV), pb = smem_u32(sP);
+      const uint32_t vb = smem_at(sV), pb = smem_at(sP);
       const int vrow = (lane & 7) + 8 * ((lane >> 3) & 1);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -682,24 +560,39 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
 }
 
 // k_paged_join: block x = (sequence, key head). Those that crossed a CTA boundary are merged
-// in CTA order; empty sequences get zeros; the others are already written. 8 warps: a row
-// each, or (many CTAs per head) all on one row.
-template <int D>
-__global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ PagedArgs a,
-                                                    int rows_per_block) {
+// in CTA order; empty sequences get zeros; the others are already written. kShared: all 32
+// warps on one row (a head is cut into many pieces), else a row for each of 8 warps.
+constexpr int kJoinWarps = 32;
+// (top, norm, acc) += (m, l, x): sums relative to 2^reference.
+template <int V>
+__device__ __forceinline__ void merge(float& top, float& norm, float (&acc)[V], float m, float l,
+                                      const float (&x)[V]) {
+  const float now = fmaxf(top, m);
+  const float f = top == kNegInf ? 0.f : exp2_fast(__fsub_rn(top, now));
+  const float g = m == kNegInf ? 0.f : exp2_fast(__fsub_rn(m, now));
+  top = now;
+  norm = __fmaf_rn(l, g, __fmul_rn(norm, f));
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = __fmaf_rn(x[e], g, __fmul_rn(acc[e], f));
+}
+template <int D, bool kShared>
+__global__ void __launch_bounds__(32 * (kShared ? kJoinWarps : 8))
+    k_paged_join(const __grid_constant__ PagedArgs a) {
   constexpr int V = D / 32;   // values per lane
-  __shared__ float acc_s[8][D], l_s[8];
+  constexpr int kWarps = kShared ? kJoinWarps : 1;
+  __shared__ float acc_s[kWarps][D];
+  __shared__ float2 l_s[kWarps];   // reference, normaliser
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
   pdl_trigger();
   pdl_wait();
-  const bool shared_row = rows_per_block == 1;
-  const int row = blockIdx.y * rows_per_block + (shared_row ? 0 : warp);
+  const int row = kShared ? blockIdx.y : blockIdx.y * 8 + warp;
+  const int n = tiles_of(a, seq_len(a, b));
   int64_t before = 0, total = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 + lane < a.B ? tiles_of(seq_len(a, b0 + lane)) : 0;
-    total += n;
-    before += b0 + lane < b ? n : 0;
+    const int p = b0 + lane < a.B ? places_of(tiles_of(a, seq_len(a, b0 + lane))) : 0;
+    total += p;
+    before += b0 + lane < b ? p : 0;
   }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) {
@@ -707,27 +600,22 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
     before += __shfl_xor_sync(0xffffffffu, before, x);
   }
   total *= a.c.heads;
-  const int n = tiles_of(seq_len(a, b));
-  const int64_t first = before * a.c.heads + (int64_t)h * n;
   int c0 = 0, c1 = -1;   // CTAs that hold a piece
   if (n) {
-    const int64_t ctas = total < a.grid ? total : a.grid;   // as in k_paged
-    c0 = (int)(((first + 1) * ctas - 1) / total);
-    c1 = (int)(((first + n) * ctas - 1) / total);
+    const int64_t first = before * a.c.heads + (int64_t)h * places_of(n) + kBegin;
+    const int64_t ctas = cta_count(a, total);
+    c0 = cta_of(first, ctas, total);
+    c1 = cta_of(first + n - 1, ctas, total);
     if (c0 == c1) return;
   }
   if (row >= a.M) return;   // (all warps of the block, when they share the row)
   auto piece = [&](int c) { return (2 * (int64_t)c + (c == c0 ? 1 : 0)) * a.M + row; };
-  float top = kNegInf;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(a.part_ml + 2 * piece(c)));
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  float acc[V], norm = 0.f;
+  // a warp's pieces, the reference moving up as it goes
+  float top = kNegInf, acc[V], norm = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  const int step = shared_row ? 8 : 1;
-#pragma unroll 4
-  for (int c = c0 + (shared_row ? warp : 0); c <= c1; c += step) {
+#pragma unroll 8
+  for (int c = c0 + (kShared ? warp : 0); c <= c1; c += kWarps) {
     const int64_t at = piece(c);
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
     float x[V];
@@ -738,22 +626,20 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
       const float2 f2 = __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D) + lane);
       x[0] = f2.x, x[1] = f2.y;
     }
-    const float f = ml.x == kNegInf ? 0.f : exp2_fast(__fsub_rn(ml.x, top));
-    norm = __fmaf_rn(ml.y, f, norm);
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = __fmaf_rn(x[e], f, acc[e]);
+    merge<V>(top, norm, acc, ml.x, ml.y, x);
   }
-  if (shared_row) {
+  if constexpr (kShared) {
 #pragma unroll
     for (int e = 0; e < V; ++e) acc_s[warp][V * lane + e] = acc[e];
-    if (lane == 0) l_s[warp] = norm;
+    if (lane == 0) l_s[warp] = make_float2(top, norm);
     __syncthreads();
     if (warp) return;
-    norm = l_s[0];
-    for (int w = 1; w < 8; ++w) {
-      norm = __fadd_rn(norm, l_s[w]);
+#pragma unroll 8
+    for (int w = 1; w < kWarps; ++w) {
+      float x[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = __fadd_rn(acc[e], acc_s[w][V * lane + e]);
+      for (int e = 0; e < V; ++e) x[e] = acc_s[w][V * lane + e];
+      merge<V>(top, norm, acc, l_s[w].x, l_s[w].y, x);
     }
   }
   uint16_t* dst = a.out + (((int64_t)b * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * D + V * lane;
@@ -768,7 +654,8 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
 
 // ------------------------------------------------------------------------------- host ----
 struct Plan {
-  int grid, per_sm;
+  bool tc;
+  int grid;
   size_t ml, po, total;
 };
 
@@ -782,21 +669,28 @@ auto with_rows(int M, F&& f) {
   return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
 }
 
+bool use_tc(int M, bool q8, int64_t most_tokens) {
+  return M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) && most_tokens > 0;
+}
+
 template <int D, bool kQ8>
 Plan make_plan(const PagedAttnProblem& p) {
   const int M = p.R * (p.Hq / p.cache.heads);
   Plan pl{};
-  pl.per_sm = with_rows<D, kQ8>(M, [](auto mt, auto mh) {
+  const int64_t cap = (int64_t)p.max_pages << p.cache.page_shift;
+  const int64_t runs = (int64_t)p.B * p.cache.heads;
+  pl.tc = use_tc(M, kQ8, runs * cap);
+  const int per_sm = pl.tc ? 1 : with_rows<D, kQ8>(M, [](auto mt, auto mh) {
     return Shape<D, kQ8, decltype(mt)::value, decltype(mh)::value>::kPerSm;
   });
-  // no more CTAs than tiles there can be
-  const int64_t cap = (int64_t)p.max_pages << p.cache.page_shift;
-  const int64_t most = (int64_t)p.B * p.cache.heads * ((cap + kTile - 1) / kTile);
-  const int64_t all = (int64_t)pl.per_sm * device_sm_count();
+  // no more CTAs than positions in the list of tiles there can be
+  const int tile = pl.tc ? 128 : kTile;
+  const int64_t most = runs * ((cap + tile - 1) / tile + kBegin);
+  const int64_t all = (int64_t)per_sm * device_sm_count();
   pl.grid = (int)(most < all ? most : all);
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-  pl.ml = 0;
-  pl.po = up((size_t)2 * pl.grid * M * 2 * sizeof(float));
+  pl.ml = 256;   // behind the status word
+  pl.po = pl.ml + up((size_t)2 * pl.grid * M * 2 * sizeof(float));
   pl.total = pl.po + up((size_t)2 * pl.grid * M * D * sizeof(float));
   return pl;
 }
@@ -811,36 +705,37 @@ cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   a.G = p.Hq / p.cache.heads;
   a.M = p.R * a.G;
   a.max_pages = p.max_pages;
+  a.tile_log = pl.tc ? 7 : 6;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   a.q = p.q;
   a.c = p.cache;
   a.table = p.table;
   a.lengths = p.lengths;
   a.out = p.out;
+  a.status = reinterpret_cast<uint32_t*>(ws);
   a.part_ml = reinterpret_cast<float*>(ws + pl.ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.po);
   a.grid = pl.grid;
-  cudaError_t err = with_rows<D, kQ8>(a.M, [&](auto mt, auto mh) {
-    using C = Shape<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
-    const auto kernel = k_paged<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
-    // (the attribute belongs to the kernel on a device and lasts: set once on each)
-    static std::atomic<uint64_t> ready{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t err;
+  if (pl.tc) {
+    err = launch_tc(a, D, s);
+  } else {
+    err = with_rows<D, kQ8>(a.M, [&](auto mt, auto mh) {
+      using C = Shape<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
+      const auto kernel = k_paged<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
+      static OncePerDevice ready;
+      const cudaError_t e = ready.run([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      });
       if (e != cudaSuccess) return e;
-      ready.fetch_or(bit, std::memory_order_relaxed);
-    }
-    return launch_pdl(kernel, dim3(pl.grid), C::kThreads, C::kSmem, s, a);
-  });
+      return launch_pdl(kernel, dim3(pl.grid), C::kThreads, C::kSmem, s, a);
+    });
+  }
   if (err != cudaSuccess) return err;
-  // rows of a head over its pieces: all warps on one row when a head is cut into many
   const int heads = p.B * p.cache.heads;
-  const int rows = pl.grid > 8 * heads ? 1 : 8;
-  return launch_pdl(k_paged_join<D>, dim3(heads, (a.M + rows - 1) / rows), 256, 0, s, a, rows);
+  if (pl.grid > 8 * heads)   // many pieces per head
+    return launch_pdl(k_paged_join<D, true>, dim3(heads, a.M), 32 * kJoinWarps, 0, s, a);
+  return launch_pdl(k_paged_join<D, false>, dim3(heads, (a.M + 7) / 8), 256, 0, s, a);
 }
 
 }  // namespace

@@ -1,0 +1,893 @@
+// paged_tc.cu — the attention over the paged cache on the 5th-generation tensor cores, for the
+// calls whose work pays for it (choice and figures in paged_attn.cu). The list of tiles, the
+// split over CTAs and the join are those of paged_attn.cu, with tiles of 128 tokens.
+//
+// Tokens are the M = 128 rows of both products, so every thread of the softmax owns one token
+// and its scales are scalars:
+//   S^T = K Q^T      A = the key tile [128 tokens][D], B = the queries [N rows][D], both
+//                    K-major; TMEM lane = token, column = query row (N = M up to a multiple
+//                    of 32);
+//   O^T += V^T P^T   A = the value tile, read MN-major (its rows are tokens, the MMA's K),
+//                    B = P [128 tokens][N rows], also MN-major, a high bf16 part and,
+//                    up to 64 rows, a low one in columns of its own; TMEM lane = value
+//                    dimension, column = query row (of either part).
+// Roles: warps 0-7 turn scores into P (a row's reference maximum moves only when a score
+// exceeds it by 2^8, agreed by one barrier vote per tile), keep the normaliser of their
+// token in registers or TMEM, and write the results; two warps copy tiles page by page, by TMA
+// straight into the swizzled operand layout (bf16) or as raw codes that eight more warps widen
+// to bf16 (Q8); one thread each of the last two warps issues the MMAs of S and of O. S is double-buffered: the next
+// tile's scores are computed while this tile's are exponentiated.
+// A token of a bf16 cache that only some rows see may hold infinities, and 0 x infinity is
+// not 0: its values are cleared before the product, and the (at most 7) such tokens are added
+// row by row when the run ends. Every wait is bounded; a give-up sets the status word.
+#include "paged.cuh"
+#include "sm100.cuh"
+
+namespace dsmoe {
+namespace paged_tc {
+
+using namespace paged;
+
+constexpr int kTok = 128;
+constexpr int kScore = 256;               // softmax threads: two per token, half of the rows each
+constexpr int kMaxN = kTcMaxRows;                 // query rows, as a multiple of 32
+constexpr int kMaxRing = 4;
+constexpr int kInfo = 8;                  // tiles whose pages and scales are at hand
+constexpr float kNothing = -1e30f;        // reference of a row that has seen no token yet
+constexpr uint32_t kWaitPolls = 1u << 20;
+
+struct TcArgs {
+  PagedArgs p;
+  int N;            // query rows, padded to a multiple of 32
+  int parts;        // parts of P side by side: a high and a low one, or 1
+  int k_ring, v_ring;   // stages of the key and of the value operand tiles
+  int raw;          // stages of raw codes (Q8)
+  int p_bufs;       // 2: P of one tile is multiplied while the next is formed
+  uint32_t tmem_cols;
+};
+
+template <int D, bool kQ8>
+struct Tc {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kMat = kTok * D * 2;             // bytes of an operand tile
+  static constexpr int kRawMat = kQ8 ? kTok * D : 0;
+  static constexpr int kWiden = kQ8 ? 128 : 0;          // threads per matrix that widen codes
+  static constexpr int kThreads = kScore + 2 * kWiden + 128;
+  static constexpr int kFetchWarp = kThreads / 32 - 4;  // keys; the next one: values
+  static constexpr int kMmaWarp = kThreads / 32 - 2;    // scores; the next one: values
+};
+
+struct alignas(16) TcSmem {   // small arrays in front of the tiles
+  uint64_t kfull[kMaxRing], vfull[kMaxRing], kfree[kMaxRing], vfree[kMaxRing];
+  uint64_t sfull[2], pfull[2], odone[2], qfull;
+  uint64_t raw_full[2][kMaxRing], raw_free[2][kMaxRing];   // Q8: codes of keys, of values
+  uint64_t info[kInfo], vedge;
+  uint32_t tmem;
+  int abort;
+  alignas(16) float ref[kMaxN];   // (read four at a time)
+  float fac[kMaxN], red[4 * kMaxN], norm[kMaxN];
+  int row_r[kMaxN];           // verify row of a query row
+  int row_at[kMaxN];          // and where its values start in a sequence's queries or results
+  alignas(16) float pe[7][kMaxN];   // P of the tokens that only some rows see
+  unsigned runs[kInfo];       // which pages of a tile are there
+};
+constexpr int kSmallBytes = (sizeof(TcSmem) + 1023) / 1024 * 1024;
+static_assert(kSmallBytes <= 10240, "the largest call fills the SM's shared memory");
+
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Copies bytes (a multiple of 16, both addresses 16-byte aligned), counted by `bar`.
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(smem_at(dst)), "l"(src), "r"(bytes), "r"(smem_at(bar))
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(bar)) : "memory");
+}
+// One arrival for the whole warp, after what its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) arrive(bar);
+}
+// Whether three phases are complete: one round trip when they are.
+__device__ __forceinline__ bool ready3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                       uint64_t* c, uint32_t pc) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q, s;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 s, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\tand.pred p, p, s;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(smem_at(a)), "r"(pa), "r"(smem_at(b)), "r"(pb), "r"(smem_at(c)), "r"(pc)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool score_any(bool x) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((int)x)
+      : "memory");
+  return r != 0;
+}
+// An operand stored with its K (tokens) as rows of 128 bytes of 64 M or N values, 128-byte
+// swizzle: groups of 8 tokens are 1024 bytes apart, the next 64 values `next` bytes further.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t next) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(next >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kMajorMN = (1u << 15) | (1u << 16);   // instruction descriptor: A and B
+
+// To 16 columns; tmem_wait_st() waits for it.
+__device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Twice 16 columns, one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t at0, float (&v)[16], uint32_t at1,
+                                            float (&w)[16]) {
+  uint32_t r[16], x[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]),
+        "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]),
+        "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+      : "r"(at0), "r"(at1)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]), w[i] = __uint_as_float(x[i]);
+}
+
+// Combines 16 columns over the warp's lanes: lanes j and j + 16 end up with column j.
+template <typename Op>
+__device__ __forceinline__ float over_lanes(float (&v)[16], int lane, Op op) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+}
+
+// kOne: N is 32. kSplit: P in two parts.
+template <int D, bool kQ8, bool kOne, bool kSplit>
+__global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
+    k_paged_tc(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap k_map,
+               const __grid_constant__ CUtensorMap v_map) {
+  using T = Tc<D, kQ8>;
+  extern __shared__ uint8_t smem_raw[];
+  const PagedArgs& a = ta.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t pad = (1024u - (smem_at(smem_raw) & 1023u)) & 1023u;
+  uint8_t* const base = smem_raw + pad;
+  TcSmem& sh = *reinterpret_cast<TcSmem*>(base);
+  const int N = ta.N, NP = ta.N * ta.parts;   // columns of S, of P and O
+  uint8_t* const sQ = base + kSmallBytes;                       // [halves][N][128 B]
+  const uint32_t p_size = (uint32_t)((NP + 63) / 64) * kTok * 128;
+  uint8_t* const sP = sQ + T::kHalves * N * 128;                // [buffers][NP / 64][tokens][128 B]
+  uint8_t* const sK = sP + ta.p_bufs * p_size;                  // [ring][halves][tokens][128 B]
+  uint8_t* const sV = sK + ta.k_ring * T::kMat;
+  uint8_t* const sRaw = sV + ta.v_ring * T::kMat;               // Q8: [2][raw][tokens][D]
+  float* const sScale = reinterpret_cast<float*>(sRaw + 2 * ta.raw * T::kRawMat);  // [kInfo][2][tokens]
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxRing; ++i) {
+      sm100::mbar_init(&sh.kfull[i], kQ8 ? T::kWiden / 32 : 1);
+      sm100::mbar_init(&sh.vfull[i], kQ8 ? T::kWiden / 32 : 1);
+      sm100::mbar_init(&sh.kfree[i], 1);
+      sm100::mbar_init(&sh.vfree[i], 1);
+      for (int x = 0; kQ8 && x < 2; ++x) {
+        sm100::mbar_init(&sh.raw_full[x][i], 1);
+        sm100::mbar_init(&sh.raw_free[x][i], T::kWiden / 32);
+      }
+    }
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&sh.sfull[i], 1);
+      sm100::mbar_init(&sh.pfull[i], kScore / 32);
+      sm100::mbar_init(&sh.odone[i], 1);
+    }
+    sm100::mbar_init(&sh.qfull, kScore / 32);
+    for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&sh.info[i], 1);
+    sm100::mbar_init(&sh.vedge, 1);
+    sh.abort = 0;
+    sm100::fence_mbar_init();
+  }
+  if (tid < kMaxN) {
+    sh.row_r[tid] = tid / a.G;
+    sh.row_at[tid] = (tid / a.G * a.Hq + tid % a.G) * D;
+  }
+  if (warp == 0) {
+    sm100::tmem_alloc(&sh.tmem, ta.tmem_cols);
+    sm100::tmem_relinquish();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0 && tid == 0) *a.status = 0u;
+
+  Cursor cur{};
+  const int n = cta_run(a, blockIdx.x, lane, &cur);   // tiles of this CTA
+
+  volatile int* const abort_flag = &sh.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+      if (sm100::mbar_try_wait(bar, parity)) return true;
+      if ((i & 63u) == 63u && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    flag_status(a.status, kStatusTimeout);
+    return false;
+  };
+  const int page_mask = (1 << a.c.page_shift) - 1;
+
+  if (n == 0) {
+    // nothing to do
+  } else if (warp < kScore / 32) {
+    // ------------------------------------------------------------ softmax, results ------
+    // thread = token tk (TMEM lane) x the query rows col0 .. col0 + N / 2 - 1, 16 at a time
+    const int quad = warp & 3, tk = 32 * quad + lane, half = N / 2, col0 = (warp >> 2) * half;
+    const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
+    const uint32_t tO = tmem + lane_at + 2 * N;
+    const uint16_t* const q0 = a.q;
+    auto seq_at = [&](const Cursor& c) {   // of its queries and results for the key head
+      return ((int64_t)c.b * a.R * a.Hq + c.h * a.G) * D;
+    };
+    auto stage_q = [&](const Cursor& c) {
+      constexpr int kChunks = D / 8;
+      const int64_t at = seq_at(c);
+      constexpr int kMost = (kMaxN * kChunks + kScore - 1) / kScore;
+      uint4 in[kMost];   // (all loads before the first store)
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) {
+        const int idx = tid + u * kScore, r = idx / kChunks;
+        in[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < a.M) in[u] = reinterpret_cast<const uint4*>(q0 + at + sh.row_at[r])[idx % kChunks];
+      }
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) {
+        const int idx = tid + u * kScore, r = idx / kChunks, ch = idx % kChunks;
+        if (r >= N) break;
+        uint4 x = in[u];
+        if constexpr (kQ8) {   // each four values as (0, 2, 1, 3), the order of widened codes
+          x.x = __byte_perm(in[u].x, in[u].y, 0x5410);
+          x.y = __byte_perm(in[u].x, in[u].y, 0x7632);
+          x.z = __byte_perm(in[u].z, in[u].w, 0x5410);
+          x.w = __byte_perm(in[u].z, in[u].w, 0x7632);
+        }
+        *reinterpret_cast<uint4*>(sQ + (ch >> 3) * N * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+      }
+      fence_async();
+      warp_arrive(&sh.qfull, lane);
+    };
+    Cursor n1 = cur;                   // the next tile
+    stage_q(cur);
+    float l_keep[16];                  // (N = 32: the sums stay in registers)
+    bool alive = true;
+    for (int i = 0; i < n && alive; ++i) {
+      if (i + 1 < n) n1.next(a);
+      const bool first = i == 0 || cur.tile == 0;
+      const bool ends = cur.tile + 1 == cur.tiles;      // of the (sequence, head)
+      const bool last = ends || i + 1 == n;             // of this run
+      const int t0 = cur.tile * kTok, tok = t0 + tk;
+      const int seen0 = cur.len - (a.R - 1);            // row r sees t < seen0 + r
+      const uint32_t tS = tmem + lane_at + (i & 1) * N;
+      const uint32_t tL = tmem + lane_at + 2 * N + NP + (i & 1) * N;
+      const uint32_t tLnew = tmem + lane_at + 2 * N + NP + (~i & 1) * N;
+      uint8_t* const p_at = sP + (i & (ta.p_bufs - 1)) * p_size + tk * 128;
+      const int slot = i % kInfo;
+      // what is known of the tile, its scores, and P's buffer (free after the tile p_bufs before)
+      const int before = i - ta.p_bufs;
+      uint64_t* const p_free = before >= 0 ? &sh.odone[before & 1] : &sh.sfull[i & 1];
+      const uint32_t p_par = before >= 0 ? (before >> 1) & 1 : (i >> 1) & 1;
+      if (!ready3(&sh.info[slot], (i / kInfo) & 1, &sh.sfull[i & 1], (i >> 1) & 1, p_free, p_par))
+        alive = wait(&sh.info[slot], (i / kInfo) & 1) && wait(&sh.sfull[i & 1], (i >> 1) & 1) &&
+                wait(p_free, p_par);
+      sm100::tc_fence_after();
+      if (last && i + 1 < n) {   // the scores with these queries are done
+        alive = !score_any(!alive);
+        if (!alive) break;
+        stage_q(n1);
+      }
+      const bool ok = tok < cur.len && (sh.runs[slot] >> (tk >> a.c.page_shift) & 1u);
+      const bool edge = __any_sync(0xffffffffu, !ok || tok >= seen0);
+      const bool partly = !kQ8 && tok >= seen0 && tok < cur.len;   // some rows may not see it
+      const float fk = kQ8 ? __fmul_rn(a.scale_log2, sScale[2 * slot * kTok + tk]) : a.scale_log2;
+      const float vs0 = kQ8 ? sScale[(2 * slot + 1) * kTok + tk] : 1.f;
+      auto mask = [&](int c, float (&t)[16]) {
+        if (!edge) return;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (!ok || tok - seen0 >= sh.row_r[c + j]) t[j] = kNegInf;
+      };
+      // Moves the references up to what this tile needs, and the sums with them. False: a wait
+      // gave up (the same for all threads).
+      auto move = [&] {
+        if (alive && !first) alive = wait(&sh.odone[(i - 1) & 1], ((i - 1) >> 1) & 1);   // O rests
+        if (score_any(!alive)) return false;
+        sm100::tc_fence_after();
+        float t[16];
+#pragma unroll 1
+        for (int c = col0; c < col0 + half; c += 16) {
+          __syncwarp();
+          sm100::tmem_ld16(tS + c, t);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) t[j] = __fmul_rn(t[j], fk);
+          mask(c, t);
+          const float top = over_lanes(t, lane, [](float x, float y) { return fmaxf(x, y); });
+          if (lane < 16) sh.red[kMaxN * quad + c + lane] = top;
+        }
+        score_sync();
+        if (tid < N) {
+          const float was = first ? kNothing : sh.ref[tid];
+          const float now = fmaxf(was, fmaxf(fmaxf(sh.red[tid], sh.red[kMaxN + tid]),
+                                             fmaxf(sh.red[2 * kMaxN + tid], sh.red[3 * kMaxN + tid])));
+          sh.ref[tid] = now;
+          sh.fac[tid] = exp2_fast(__fsub_rn(was, now));
+        }
+        score_sync();
+        if (first) return true;
+        if constexpr (kOne) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) l_keep[j] = __fmul_rn(l_keep[j], sh.fac[col0 + j]);
+        }
+#pragma unroll 1
+        for (int c = col0; c < col0 + half; c += 16) {
+#pragma unroll 1
+          for (int x = 0; x < (kOne ? 2 : 3); ++x) {    // O, its low part, the sums
+            if (x == 1 && !kSplit) continue;
+            const uint32_t at = (x == 2 ? tL : tO + x * N) + c;
+            __syncwarp();
+            sm100::tmem_ld16(at, t);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) t[j] = __fmul_rn(t[j], sh.fac[c + j]);
+            tmem_st(at, t);
+          }
+        }
+        if (!kQ8)
+          for (int x = tid; x < 7 * N; x += kScore)
+            if (seen0 + x / N < t0) {
+              float& pe = sh.pe[x / N][x % N];
+              pe = __fmul_rn(pe, sh.fac[x % N]);
+            }
+        tmem_wait_st();
+        return true;
+      };
+      float l[16];
+      for (bool settled = first;; settled = true) {   // P of the tile, at most twice
+        if (settled) alive = move();
+        if (settled && !alive) break;
+        bool over = !alive;
+#pragma unroll 1
+        for (int c = col0; c < (kOne ? col0 + 1 : col0 + half); c += 16) {
+          float t[16];
+          float4 r4[4];
+#pragma unroll
+          for (int j4 = 0; j4 < 4; ++j4)
+            r4[j4] = *reinterpret_cast<const float4*>(sh.ref + c + 4 * j4);
+          __syncwarp();
+          if constexpr (kOne) {
+            sm100::tmem_ld16(tS + c, t);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) l[j] = first ? 0.f : l_keep[j];
+          } else {
+            tmem_ld16x2(tS + c, t, tL + c, l);
+            if (first) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) l[j] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int j4 = 0; j4 < 4; ++j4) {
+            const float4 r = r4[j4];
+            t[4 * j4] = __fmaf_rn(t[4 * j4], fk, -r.x);
+            t[4 * j4 + 1] = __fmaf_rn(t[4 * j4 + 1], fk, -r.y);
+            t[4 * j4 + 2] = __fmaf_rn(t[4 * j4 + 2], fk, -r.z);
+            t[4 * j4 + 3] = __fmaf_rn(t[4 * j4 + 3], fk, -r.w);
+          }
+          mask(c, t);
+          float top[4] = {t[0], t[1], t[2], t[3]};
+#pragma unroll
+          for (int j = 4; j < 16; ++j) top[j & 3] = fmaxf(top[j & 3], t[j]);
+          over |= fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack;
+          // P, and its sum per row over this thread's tokens
+#pragma unroll
+          for (int c8 = 0; c8 < 2; ++c8) {
+            uint32_t hi4[4], lo4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = 8 * c8 + 2 * e;
+              float p0 = exp2_fast(t[j]), p1 = exp2_fast(t[j + 1]);
+              if (!kSplit) {   // (the sums of what is multiplied, so that weights add up to 1)
+                hi4[e] = pack2(p0, p1);
+                p0 = bf16_lo(hi4[e]);
+                p1 = bf16_hi(hi4[e]);
+              }
+              l[j] = __fadd_rn(l[j], p0);
+              l[j + 1] = __fadd_rn(l[j + 1], p1);
+              if constexpr (kQ8) {
+                p0 = __fmul_rn(p0, vs0);
+                p1 = __fmul_rn(p1, vs0);
+                if (edge) {   // a masked token's scale may be anything
+                  p0 = t[j] == kNegInf ? 0.f : p0;
+                  p1 = t[j + 1] == kNegInf ? 0.f : p1;
+                }
+              } else if (partly) {
+                sh.pe[tok - seen0][c + j] = p0;
+                sh.pe[tok - seen0][c + j + 1] = p1;
+              }
+              if (kSplit) {
+                hi4[e] = pack2(p0, p1);
+                lo4[e] = pack2(__fsub_rn(p0, bf16_lo(hi4[e])), __fsub_rn(p1, bf16_hi(hi4[e])));
+              }
+            }
+            auto put = [&](int ch, const uint32_t(&x)[4]) {
+              *reinterpret_cast<uint4*>(p_at + (ch >> 3) * kTok * 128 +
+                                        (((ch & 7) ^ (tk & 7)) << 4)) =
+                  make_uint4(x[0], x[1], x[2], x[3]);
+            };
+            put(c / 8 + c8, hi4);
+            if (kSplit) put((N + c) / 8 + c8, lo4);
+          }
+          if constexpr (!kOne) {
+            __syncwarp();
+            tmem_st(tLnew + c, l);
+          }
+        }
+        if (settled || !score_any(over)) break;
+      }
+      if (!alive) break;
+      if constexpr (kOne) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) l_keep[j] = l[j];
+      } else {
+        tmem_wait_st();
+      }
+      sm100::tc_fence_before();
+      fence_async();
+      warp_arrive(&sh.pfull[i & 1], lane);
+      if (last) {
+        // ------------------------------------------------------------ results -------------
+        const int run = i < cur.tile ? i : cur.tile;    // tiles before this one in the run
+        const bool whole = ends && cur.tile == run;
+        // this thread's dimension of the values (codes are widened as (0, 2, 1, 3))
+        const int dim = kQ8 ? (tk & ~3) | ((tk & 1) << 1) | ((tk >> 1) & 1) : tk;
+        // the partly seen tokens of this run, e0 .. e1 - 1 behind seen0
+        const int e0 = max(max((cur.tile - run) * kTok, 0) - seen0, 0);
+        const int e1 = min(cur.len, t0 + kTok) - seen0;
+        float v[7];
+        if (!kQ8) {
+#pragma unroll
+          for (int e = 0; e < 7; ++e) {   // (their loads overlap)
+            v[e] = 0.f;
+            if (e < e0 || e >= e1 || tk >= D) continue;
+            const int t = seen0 + e, page = page_of(a, cur.b, t, cur.len);
+            if (page >= 0)
+              v[e] = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(
+                  a.c.v)[page * a.c.stride +
+                         (((int64_t)cur.h << a.c.page_shift) + (t & page_mask)) * D + dim]);
+          }
+        }
+#pragma unroll 1
+        for (int c = col0; c < col0 + half; c += 16) {
+          __syncwarp();
+          if (!kOne) sm100::tmem_ld16(tLnew + c, l);
+          const float sum =
+              over_lanes(l, lane, [](float x, float y) { return __fadd_rn(x, y); });
+          if (lane < 16) sh.red[kMaxN * quad + c + lane] = sum;
+        }
+        score_sync();
+        const int64_t piece = 2 * (int64_t)blockIdx.x + (cur.tile == run ? 1 : 0);
+        if (tid < N) {
+          const float norm = __fadd_rn(__fadd_rn(sh.red[tid], sh.red[kMaxN + tid]),
+                                       __fadd_rn(sh.red[2 * kMaxN + tid], sh.red[3 * kMaxN + tid]));
+          sh.norm[tid] = norm == 0.f ? 0.f : __frcp_rn(norm);
+          if (!whole && tid < a.M)
+            *reinterpret_cast<float2*>(a.part_ml + 2 * (piece * a.M + tid)) =
+                make_float2(sh.ref[tid] == kNothing ? kNegInf : sh.ref[tid], norm);
+        }
+        alive = wait(&sh.odone[i & 1], (i >> 1) & 1);
+        alive = !score_any(!alive);
+        if (!alive) break;
+        sm100::tc_fence_after();
+        uint16_t* const out = a.out + seq_at(cur) + dim;
+        float* const po = a.part_o + piece * a.M * D + dim;
+        // (this thread's column goes through its own words of P's buffers, which nothing else
+        // uses now, so that the rows can be walked in a loop: this code runs once per run)
+        float* const mine = reinterpret_cast<float*>(sP) + tk;
+        float* const mine_v = mine + (N + 7 * (col0 != 0)) * kTok;
+        if (!kQ8) {
+#pragma unroll
+          for (int e = 0; e < 7; ++e) mine_v[e * kTok] = v[e];
+        }
+#pragma unroll 1
+        for (int c = col0; c < col0 + half; c += 16) {
+          float o[16];
+          __syncwarp();
+          sm100::tmem_ld16(tO + c, o);
+          if (kSplit) {
+            sm100::tmem_ld16(tO + N + c, l);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __fadd_rn(o[j], l[j]);
+          }
+          if (!kQ8) {
+#pragma unroll 1
+            for (int e = e0; e < e1; ++e) {
+              const float ve = mine_v[e * kTok];
+              const bool plain = fabsf(ve) < INFINITY;   // P of a row that does not see it is 0
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (plain || e < sh.row_r[c + j]) o[j] = __fmaf_rn(sh.pe[e][c + j], ve, o[j]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) mine[(c + j) * kTok] = o[j];
+        }
+        if (tk < D) {                                   // (D = 64: the upper lanes repeat)
+          const int rows = min(a.M, col0 + half);
+#pragma unroll 4
+          for (int row = col0; row < rows; ++row) {
+            const float o = mine[row * kTok];
+            // (a normaliser of 0 is a row that sees nothing; its sums may hold a token's NaN)
+            if (whole)
+              out[sh.row_at[row]] =
+                  f32_to_bf16_rne(sh.norm[row] == 0.f ? 0.f : __fmul_rn(o, sh.norm[row]));
+            else
+              po[row * D] = o;
+          }
+        }
+        score_sync();   // (sh is free for the next run)
+      }
+      cur = n1;
+    }
+  } else if (warp < T::kFetchWarp) {
+    // ----------------------------------------------------- Q8: codes widened to operands ---
+    if constexpr (kQ8) {
+      const bool values = warp >= (kScore + T::kWiden) / 32;
+      const int lt = tid - kScore - (values ? T::kWiden : 0);
+      uint64_t* const full = values ? sh.vfull : sh.kfull;
+      uint64_t* const free_bar = values ? sh.vfree : sh.kfree;
+      const int ring = values ? ta.v_ring : ta.k_ring;
+      constexpr int kChunks = D / 16, kStep = T::kWiden / kChunks, kIters = kTok / kStep;
+      // (eight lanes take 4 chunks of 2 rows, so that a quarter warp's stores meet all banks)
+      const int my_row = D == 128 ? (lt >> 4) * 2 + ((lt >> 2) & 1) : lt / kChunks;
+      const int my_chunk = D == 128 ? (lt & 3) + ((lt >> 1) & 4) : lt % kChunks;
+      const uint8_t* const raw0 =
+          sRaw + (values ? ta.raw * T::kRawMat : 0) + my_row * D + my_chunk * 16;
+      uint8_t* const dst0 = (values ? sV : sK) + (my_chunk >> 2) * (kTok * 128) + my_row * 128;
+      const int c0 = ((2 * my_chunk & 7) ^ (my_row & 7)) << 4;   // (kStep: a multiple of 8 rows)
+      int st = 0, rst = 0;            // stages of the operand tile, of the codes
+      uint32_t par = 1, rpar = 0;     // and parities: of the phase before, of this one
+      for (int i = 0; i < n; ++i) {
+        bool alive = wait(&sh.raw_full[values][rst], rpar);
+        if (i >= ring) alive = alive && wait(&free_bar[st], par);
+        if (!__all_sync(0xffffffffu, alive)) break;
+        uint4 w[kIters];   // (all loads before the first store)
+#pragma unroll
+        for (int it = 0; it < kIters; ++it)
+          w[it] = *reinterpret_cast<const uint4*>(raw0 + rst * T::kRawMat + it * (kStep * D));
+        warp_arrive(&sh.raw_free[values][rst], lane);
+        uint8_t* const dst = dst0 + st * T::kMat;
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          const uint4 v = w[it];
+          *reinterpret_cast<uint4*>(dst + it * (kStep * 128) + c0) = make_uint4(
+              code_pair(v.x), code_pair(v.x >> 8), code_pair(v.y), code_pair(v.y >> 8));
+          *reinterpret_cast<uint4*>(dst + it * (kStep * 128) + (c0 ^ 16)) = make_uint4(
+              code_pair(v.z), code_pair(v.z >> 8), code_pair(v.w), code_pair(v.w >> 8));
+        }
+        fence_async();
+        warp_arrive(&full[st], lane);
+        if (++st == ring) st = 0, par ^= 1;
+        if (++rst == ta.raw) rst = 0, rpar ^= 1;
+      }
+    }
+  } else if (warp < T::kMmaWarp) {
+    // ------------------------------------------------------------- copies from the pages ---
+    // A page's tokens of one head are one stretch of memory: lane x copies the x-th page of a
+    // tile, by TMA into the swizzled operand tile (bf16) or as raw codes (Q8). What no copy
+    // brings is left as it is: its scores are masked, and its values either count as codes
+    // (finite) times 0 or are cleared below.
+    const bool values = warp == T::kFetchWarp + 1;
+    const int pt = 1 << a.c.page_shift, pages = kTok >> a.c.page_shift;
+    const int ring = kQ8 ? ta.raw : (values ? ta.v_ring : ta.k_ring);
+    uint64_t* const full = kQ8 ? sh.raw_full[values] : (values ? sh.vfull : sh.kfull);
+    uint64_t* const free_bar = kQ8 ? sh.raw_free[values] : (values ? sh.vfree : sh.kfree);
+    uint8_t* const tiles = kQ8 ? sRaw + (values ? ta.raw * T::kRawMat : 0) : (values ? sV : sK);
+    int page = lane < pages ? page_of(a, cur.b, cur.tile * kTok + lane * pt, cur.len) : -1;
+    // The ring holds too little to cover the memory's latency at full rate: the tiles after it
+    // are brought into L2 ahead of time (kAhead tiles, 39 MB over all SMs at most).
+    constexpr int kAhead = 4;
+    Cursor pre = cur;
+    int pre_page = page, pre_done = 0;
+    auto prefetch = [&] {
+      if (pre_page >= 0 && pre_page < a.c.pages)
+        prefetch_l2((values ? a.c.v : a.c.k) +
+                        (pre_page * a.c.stride + (((int64_t)pre.h << a.c.page_shift)) * D) *
+                            (kQ8 ? 1 : 2),
+                    pt * D * (kQ8 ? 1 : 2));
+      if (++pre_done >= n) return;
+      pre.next(a);
+      const int t = pre.tile * kTok + lane * pt;
+      pre_page = -1;
+      if (lane < pages && t < pre.len)
+        pre_page = a.table[(int64_t)pre.b * a.max_pages + (t >> a.c.page_shift)];
+    };
+    int st = 0, done = 0, edges = 0;
+    uint32_t par = 1;
+    bool alive = true;
+    for (int i = 0; i < n; ++i) {
+      for (int x = 0; x < 2 && pre_done < n && pre_done < i + ring + kAhead; ++x) prefetch();
+      if (i >= ring) alive = wait(&free_bar[st], par);
+      if (!__all_sync(0xffffffffu, alive)) break;
+      const bool ok = page >= 0 && page < a.c.pages;
+      const unsigned there = __ballot_sync(0xffffffffu, ok);
+      const int count = __popc(there), t0 = cur.tile * kTok, seen0 = cur.len - (a.R - 1);
+      if (!values) {   // what the softmax needs to know (its slot is free: see kInfo's use)
+        const int slot = i % kInfo;
+        if (lane == 0) {
+          sh.runs[slot] = there;
+          sm100::mbar_arrive_expect_tx(&sh.info[slot], kQ8 ? count * pt * 8 : 0);
+        }
+        __syncwarp();
+        if (kQ8 && ok) {
+          const int64_t at = page * a.c.scale_stride + ((int64_t)cur.h << a.c.page_shift);
+          float* const dst = sScale + 2 * slot * kTok + lane * pt;
+          bulk_copy(dst, a.c.k_scale + at, pt * 4, &sh.info[slot]);
+          bulk_copy(dst + kTok, a.c.v_scale + at, pt * 4, &sh.info[slot]);
+        }
+      }
+      const bool edge = !kQ8 && values && (t0 + kTok > seen0 || count < pages);
+      uint64_t* const bar = edge ? &sh.vedge : &full[st];
+      if (lane == 0) sm100::mbar_arrive_expect_tx(bar, count * pt * (kQ8 ? D : 2 * D));
+      __syncwarp();
+      if (ok) {
+        if constexpr (kQ8) {
+          bulk_copy(tiles + st * T::kRawMat + lane * pt * D,
+                    (values ? a.c.v : a.c.k) + page * a.c.stride +
+                        (((int64_t)cur.h << a.c.page_shift)) * D,
+                    pt * D, bar);
+        } else {
+#pragma unroll
+          for (int hf = 0; hf < T::kHalves; ++hf)
+            sm100::tma_load_3d(tiles + st * T::kMat + hf * (kTok * 128) + lane * pt * 128,
+                               values ? &v_map : &k_map, 64 * hf, cur.h << a.c.page_shift, page, bar);
+        }
+      }
+      if (edge) {   // clear the values that not every row sees
+        alive = wait(&sh.vedge, edges++ & 1);
+        if (!__all_sync(0xffffffffu, alive)) break;
+        for (int r = lane; r < kTok; r += 32)
+          if (t0 + r >= seen0 || !(there >> (r >> a.c.page_shift) & 1u))
+            for (int x = 0; x < 8 * T::kHalves; ++x)
+              *reinterpret_cast<uint4*>(tiles + st * T::kMat + (x >> 3) * (kTok * 128) + r * 128 +
+                                        (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) arrive(&full[st]);
+      }
+      done = i + 1;
+      if (++st == ring) st = 0, par ^= 1;
+      if (done < n) {
+        cur.next(a);
+        const int t = cur.tile * kTok + lane * pt;
+        page = -1;
+        if (lane < pages && t < cur.len)
+          page = a.table[(int64_t)cur.b * a.max_pages + (t >> a.c.page_shift)];
+      }
+    }
+    if (*abort_flag) {   // copies in flight end (bounded) before the CTA does
+      for (int j = done - ring < 0 ? 0 : done - ring; j < done; ++j)
+        sm100::mbar_wait(&full[j % ring], (j / ring) & 1, kWaitPolls);
+      if (!values)
+        for (int j = done - kInfo < 0 ? 0 : done - kInfo; j < done; ++j)
+          sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
+    }
+  } else if (warp == T::kMmaWarp) {
+    // ---------------------------------------------------------------- MMAs of the scores ---
+    // (the whole warp walks the loop, so that descriptors stay in uniform registers; one lane
+    // issues)
+    const bool leader = elect_one();
+    const uint32_t idesc = sm100::idesc_bf16_f32(kTok, N);
+    const uint64_t q_desc = sm100::desc_k_sw128(smem_at(sQ));
+    const uint64_t k_desc = sm100::desc_k_sw128(smem_at(sK));
+    int segs = 0, done = 0, st = 0;
+    uint32_t par = 0;
+    for (int j = 0; j < n; ++j) {
+      const bool new_q = j == 0 || cur.tile == 0;
+      // the buffer of S is free once P of the tile before the last is there
+      bool ok = j < 2 || wait(&sh.pfull[j & 1], ((j - 2) >> 1) & 1);
+      if (new_q) ok = ok && wait(&sh.qfull, segs++ & 1);
+      ok = ok && wait(&sh.kfull[st], par);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      sm100::tc_fence_after();
+      fence_async();
+      const uint64_t kd = k_desc + (uint32_t)st * (T::kMat >> 4);
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)   // 16 values: 32 bytes, or the next 64 values
+          sm100::mma_bf16(tmem + (j & 1) * N, kd + (ks >> 2) * (kTok * 8) + (ks & 3) * 2,
+                          q_desc + (uint32_t)((ks >> 2) * N * 8 + (ks & 3) * 2), idesc, ks > 0);
+        sm100::mma_commit(&sh.sfull[j & 1]);
+        sm100::mma_commit(&sh.kfree[st]);
+      }
+      __syncwarp();
+      if (++st == ta.k_ring) st = 0, par ^= 1;
+      done = j + 1;
+      if (done < n) cur.next(a);
+    }
+    // MMAs issued but maybe not observed complete: wait (bounded) before TMEM is freed
+    if (done) sm100::mbar_wait(&sh.sfull[(done - 1) & 1], ((done - 1) >> 1) & 1, kWaitPolls);
+  } else {
+    // ---------------------------------------------------------------- MMAs of the values ---
+    const bool leader = elect_one();
+    const uint32_t idesc = sm100::idesc_bf16_f32(kTok, NP) | kMajorMN;
+    // (D = 64: the upper half of the M rows repeats the lower one)
+    const uint64_t v_desc = desc_mn_sw128(smem_at(sV), D == 128 ? kTok * 128 : 0);
+    const uint64_t p_desc = desc_mn_sw128(smem_at(sP), kTok * 128);
+    int done = 0, st = 0;
+    uint32_t par = 0;
+    for (int i = 0; i < n; ++i) {
+      bool ok = wait(&sh.vfull[st], par);
+      ok = ok && wait(&sh.pfull[i & 1], (i >> 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      sm100::tc_fence_after();
+      fence_async();
+      const uint64_t vd = v_desc + (uint32_t)st * (T::kMat >> 4);
+      const uint64_t pd = p_desc + (uint32_t)(i & (ta.p_bufs - 1)) * (p_size >> 4);
+      const bool fresh = i == 0 || cur.tile == 0;
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < kTok / 16; ++ks)   // 16 tokens: 2 KB
+          sm100::mma_bf16(tmem + 2 * N, vd + ks * 128, pd + ks * 128, idesc, !(fresh && ks == 0));
+        sm100::mma_commit(&sh.odone[i & 1]);
+        sm100::mma_commit(&sh.vfree[st]);
+      }
+      __syncwarp();
+      if (++st == ta.v_ring) st = 0, par ^= 1;
+      done = i + 1;
+      if (done < n) cur.next(a);
+    }
+    if (done) sm100::mbar_wait(&sh.odone[(done - 1) & 1], ((done - 1) >> 1) & 1, kWaitPolls);
+  }
+  __syncwarp();
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) sm100::tmem_dealloc(tmem, ta.tmem_cols);
+}
+
+// Shared memory of a call.
+template <int D, bool kQ8>
+int smem_bytes(const TcArgs& a) {
+  using T = Tc<D, kQ8>;
+  return 1024 + kSmallBytes + T::kHalves * a.N * 128 +
+         a.p_bufs * ((a.N * a.parts + 63) / 64) * kTok * 128 + (a.k_ring + a.v_ring) * T::kMat +
+         2 * a.raw * T::kRawMat + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
+}
+
+template <int D, bool kQ8, bool kOne, bool kSplit>
+cudaError_t start_as(const TcArgs& a, int room, int smem, cudaStream_t s) {
+  const auto kernel = k_paged_tc<D, kQ8, kOne, kSplit>;
+  static OncePerDevice ready;
+  const cudaError_t e = ready.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
+  });
+  if (e != cudaSuccess) return e;
+  CUtensorMap k_map = {}, v_map = {};
+  if (!kQ8) {
+    const CacheView& c = a.p.c;
+    const int pt = 1 << c.page_shift;
+    cudaError_t m = page_tile_map(&k_map, c.k, D, c.heads * pt, c.pages, c.stride, pt);
+    if (m == cudaSuccess) m = page_tile_map(&v_map, c.v, D, c.heads * pt, c.pages, c.stride, pt);
+    if (m != cudaSuccess) return m;
+  }
+  return launch_pdl(kernel, dim3(a.p.grid), Tc<D, kQ8>::kThreads, smem, s, a, k_map, v_map);
+}
+
+template <int D, bool kQ8>
+cudaError_t start(const PagedArgs& p, cudaStream_t s) {
+  TcArgs a{};
+  a.p = p;
+  a.N = (p.M + 31) / 32 * 32;
+  a.parts = a.N <= 64 ? 2 : 1;
+  const int room = 227 * 1024;
+  // The least first, then what fits: a second buffer of P, a second value tile, deeper rings.
+  a.p_bufs = 1;
+  a.k_ring = a.v_ring = kQ8 ? 1 : 2;
+  a.raw = kQ8 ? 2 : 0;
+  auto grow = [&](int TcArgs::*what, int most) {
+    while (a.*what < most) {
+      ++(a.*what);
+      if (smem_bytes<D, kQ8>(a) <= room) continue;
+      --(a.*what);
+      break;
+    }
+  };
+  if (kQ8) grow(&TcArgs::v_ring, 2);
+  grow(&TcArgs::p_bufs, 2);
+  if (kQ8) {
+    grow(&TcArgs::k_ring, 2);
+    grow(&TcArgs::raw, kMaxRing);
+  } else {
+    grow(&TcArgs::k_ring, kMaxRing);
+    grow(&TcArgs::v_ring, kMaxRing);
+  }
+  // Page flags and scales of a tile are overwritten kInfo tiles later. The keys of that tile
+  // are fetched once the codes of the tile `raw` before it are widened, so k_ring further
+  // back the scores are done, and two further back P (the two buffers of S).
+  static_assert(kMaxRing + 2 + 2 <= kInfo, "slots of the tile information");
+  a.tmem_cols = 128;
+  while ((int)a.tmem_cols < (4 + a.parts) * a.N) a.tmem_cols *= 2;
+  // (the results of a run pass through P's buffers)
+  if (a.p_bufs * ((a.N * a.parts + 63) / 64) * 128 < (a.N + (kQ8 ? 0 : 14)) * 4)
+    return cudaErrorInvalidValue;
+  // (at least half of the SM's shared memory, so that one CTA has the SM's tensor memory)
+  int smem = smem_bytes<D, kQ8>(a);
+  smem = smem < 120 * 1024 ? 120 * 1024 : smem;
+  if (a.N == 32) return start_as<D, kQ8, true, true>(a, room, smem, s);
+  if (a.N == 64) return start_as<D, kQ8, false, true>(a, room, smem, s);
+  if constexpr (kQ8) return cudaErrorInvalidValue;   // (kTcMaxRowsQ8)
+  else return start_as<D, kQ8, false, false>(a, room, smem, s);
+}
+
+}  // namespace paged_tc
+
+namespace paged {
+
+using paged_tc::start;
+
+cudaError_t launch_tc(const PagedArgs& p, int D, cudaStream_t s) {
+  if (D == 128) return p.c.q8 ? start<128, true>(p, s) : start<128, false>(p, s);
+  return p.c.q8 ? start<64, true>(p, s) : start<64, false>(p, s);
+}
+
+}  // namespace paged
+}  // namespace dsmoe

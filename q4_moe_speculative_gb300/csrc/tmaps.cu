@@ -84,4 +84,20 @@ cudaError_t key_tile_map(CUtensorMap* out, const uint16_t* keys, int N, int L,
   return cached_map(out, k);
 }
 
+cudaError_t page_tile_map(CUtensorMap* out, const void* base, int D, int rows, int pages,
+                          int64_t page_stride, int box_rows) {
+  const EncodeTiledFn f = encode_tiled();
+  if (!f) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)page_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return f(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 }  // namespace dsmoe
