@@ -81,7 +81,7 @@ struct Shape {
   static constexpr int kFixed = kQ + kP * (kSplit ? 2 : 1) + kRed + 64;
   // CTAs per SM: as many as the registers allow (65,536 over the threads at 128, 168 or 255
   // each) with at least two stages each
-  static constexpr int kWant = MH == 2 ? 1 : (MT == 1 ? 4 : MT == 2 ? 3 : 2);
+  static constexpr int kWant = MH == 2 ? 1 : (MT == 1 ? 4 : 3);
   static constexpr int room(int n) { return 228 * 1024 / n - 1024; }
   static constexpr int fit(int n) {
     return n > 1 && kFixed + 2 * kStage > room(n) ? fit(n - 1) : n;
@@ -664,13 +664,20 @@ template <int D, bool kQ8, typename F>
 auto with_rows(int M, F&& f) {
   if (M <= 16) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
   if (M <= 32) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
-  if (M <= 64) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  if (M <= 64) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
   if (M <= 96) return f(std::integral_constant<int, 3>{}, std::integral_constant<int, 2>{});
   return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
 }
 
-bool use_tc(int M, bool q8, int64_t most_tokens) {
-  return M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) && most_tokens > 0;
+// The tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and end. Up to
+// 32 rows this file's kernel is as fast at any length (6 rows x 4 heads, 32 sequences of up to
+// 8k, bf16 121 against 154 us, Q8 109 against 108); with more, the other one is ahead from
+// several tiles per SM on: 6 x 16 rows at 300k tokens 59 against 73 us, 4 sequences x 8 heads
+// at 64k bf16 247 against 405 us, Q8 (64 rows) 242 against 342 us, but at 500 tokens of one
+// head 29 against 13 us. `places`: tokens x key heads there can be (lengths are not known here).
+bool use_tc(int M, bool q8, int64_t places) {
+  return M > 32 && M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) &&
+         places >= (int64_t)(q8 ? 3 : 8) * 128 * device_sm_count();
 }
 
 template <int D, bool kQ8>

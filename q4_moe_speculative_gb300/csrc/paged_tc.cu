@@ -13,7 +13,7 @@
 //                    dimension, column = query row (of either part).
 // Roles: warps 0-7 turn scores into P (a row's reference maximum moves only when a score
 // exceeds it by 2^8, agreed by one barrier vote per tile), keep the normaliser of their
-// token in registers or TMEM, and write the results; two warps copy tiles page by page, by TMA
+// token in TMEM, and write the results; two warps copy tiles page by page, by TMA
 // straight into the swizzled operand layout (bf16) or as raw codes that eight more warps widen
 // to bf16 (Q8); one thread each of the last two warps issues the MMAs of S and of O. S is double-buffered: the next
 // tile's scores are computed while this tile's are exponentiated.
@@ -195,8 +195,8 @@ __device__ __forceinline__ float over_lanes(float (&v)[16], int lane, Op op) {
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// kOne: N is 32. kSplit: P in two parts.
-template <int D, bool kQ8, bool kOne, bool kSplit>
+// kSplit: P in two parts.
+template <int D, bool kQ8, bool kSplit>
 __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     k_paged_tc(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap k_map,
                const __grid_constant__ CUtensorMap v_map) {
@@ -310,7 +310,6 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     };
     Cursor n1 = cur;                   // the next tile
     stage_q(cur);
-    float l_keep[16];                  // (N = 32: the sums stay in registers)
     bool alive = true;
     for (int i = 0; i < n && alive; ++i) {
       if (i + 1 < n) n1.next(a);
@@ -375,14 +374,10 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         }
         score_sync();
         if (first) return true;
-        if constexpr (kOne) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) l_keep[j] = __fmul_rn(l_keep[j], sh.fac[col0 + j]);
-        }
 #pragma unroll 1
         for (int c = col0; c < col0 + half; c += 16) {
 #pragma unroll 1
-          for (int x = 0; x < (kOne ? 2 : 3); ++x) {    // O, its low part, the sums
+          for (int x = 0; x < 3; ++x) {    // O, its low part, the sums
             if (x == 1 && !kSplit) continue;
             const uint32_t at = (x == 2 ? tL : tO + x * N) + c;
             __syncwarp();
@@ -407,23 +402,17 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         if (settled && !alive) break;
         bool over = !alive;
 #pragma unroll 1
-        for (int c = col0; c < (kOne ? col0 + 1 : col0 + half); c += 16) {
+        for (int c = col0; c < col0 + half; c += 16) {
           float t[16];
           float4 r4[4];
 #pragma unroll
           for (int j4 = 0; j4 < 4; ++j4)
             r4[j4] = *reinterpret_cast<const float4*>(sh.ref + c + 4 * j4);
           __syncwarp();
-          if constexpr (kOne) {
-            sm100::tmem_ld16(tS + c, t);
+          tmem_ld16x2(tS + c, t, tL + c, l);
+          if (first) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) l[j] = first ? 0.f : l_keep[j];
-          } else {
-            tmem_ld16x2(tS + c, t, tL + c, l);
-            if (first) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) l[j] = 0.f;
-            }
+            for (int j = 0; j < 16; ++j) l[j] = 0.f;
           }
 #pragma unroll
           for (int j4 = 0; j4 < 4; ++j4) {
@@ -477,20 +466,13 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             put(c / 8 + c8, hi4);
             if (kSplit) put((N + c) / 8 + c8, lo4);
           }
-          if constexpr (!kOne) {
-            __syncwarp();
-            tmem_st(tLnew + c, l);
-          }
+          __syncwarp();
+          tmem_st(tLnew + c, l);
         }
         if (settled || !score_any(over)) break;
       }
       if (!alive) break;
-      if constexpr (kOne) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) l_keep[j] = l[j];
-      } else {
-        tmem_wait_st();
-      }
+      tmem_wait_st();
       sm100::tc_fence_before();
       fence_async();
       warp_arrive(&sh.pfull[i & 1], lane);
@@ -519,7 +501,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
 #pragma unroll 1
         for (int c = col0; c < col0 + half; c += 16) {
           __syncwarp();
-          if (!kOne) sm100::tmem_ld16(tLnew + c, l);
+          sm100::tmem_ld16(tLnew + c, l);
           const float sum =
               over_lanes(l, lane, [](float x, float y) { return __fadd_rn(x, y); });
           if (lane < 16) sh.red[kMaxN * quad + c + lane] = sum;
@@ -813,9 +795,9 @@ int smem_bytes(const TcArgs& a) {
          2 * a.raw * T::kRawMat + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
 }
 
-template <int D, bool kQ8, bool kOne, bool kSplit>
+template <int D, bool kQ8, bool kSplit>
 cudaError_t start_as(const TcArgs& a, int room, int smem, cudaStream_t s) {
-  const auto kernel = k_paged_tc<D, kQ8, kOne, kSplit>;
+  const auto kernel = k_paged_tc<D, kQ8, kSplit>;
   static OncePerDevice ready;
   const cudaError_t e = ready.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
@@ -836,7 +818,7 @@ template <int D, bool kQ8>
 cudaError_t start(const PagedArgs& p, cudaStream_t s) {
   TcArgs a{};
   a.p = p;
-  a.N = (p.M + 31) / 32 * 32;
+  a.N = p.M <= 64 ? 64 : 96;   // (smaller problems take the kernel of paged_attn.cu)
   a.parts = a.N <= 64 ? 2 : 1;
   const int room = 227 * 1024;
   // The least first, then what fits: a second buffer of P, a second value tile, deeper rings.
@@ -872,10 +854,9 @@ cudaError_t start(const PagedArgs& p, cudaStream_t s) {
   // (at least half of the SM's shared memory, so that one CTA has the SM's tensor memory)
   int smem = smem_bytes<D, kQ8>(a);
   smem = smem < 120 * 1024 ? 120 * 1024 : smem;
-  if (a.N == 32) return start_as<D, kQ8, true, true>(a, room, smem, s);
-  if (a.N == 64) return start_as<D, kQ8, false, true>(a, room, smem, s);
+  if (a.N <= 64) return start_as<D, kQ8, true>(a, room, smem, s);
   if constexpr (kQ8) return cudaErrorInvalidValue;   // (kTcMaxRowsQ8)
-  else return start_as<D, kQ8, false, false>(a, room, smem, s);
+  else return start_as<D, kQ8, false>(a, room, smem, s);
 }
 
 }  // namespace paged_tc

@@ -1,6 +1,10 @@
 """Attention over the paged cache (ds_paged_attention) against a plain implementation in 64
 bits, tolerances as derived in paged_ref.check_attention; and the operators of a decode step
-run together."""
+run together.
+
+The kernel is chosen by the query rows per key head and by the tokens that the page table has
+room for: `wide` tables have room for more than 200,000 tokens, most of it unused, so that
+33 to 96 rows (64 for Q8) take the tensor-memory kernel at short lengths too."""
 import pytest
 import torch
 
@@ -13,7 +17,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 
 
-def problem(lens, R, Hq, kv, D, page, q8, seed, strided=False, sigma=1.0, spare=2):
+def problem(lens, R, Hq, kv, D, page, q8, seed, strided=False, sigma=1.0, spare=2, wide=False):
     g = torch.Generator()
     g.manual_seed(seed)
     need = [-(-max(n, 0) // page) for n in lens]
@@ -28,7 +32,10 @@ def problem(lens, R, Hq, kv, D, page, q8, seed, strided=False, sigma=1.0, spare=
         parts = [pool[:, 0], pool[:, 1]]
     cache = dsm.PagedCache(*(p if strided else p.contiguous() for p in parts))
     order = torch.randperm(pages, generator=g).to(torch.int32)
-    table = torch.full((len(lens), max(1, max(need))), -1, dtype=torch.int32)
+    columns = max(1, max(need))
+    if wide:
+        columns = max(columns, 200_000 // (page * len(lens) * kv) + 1)
+    table = torch.full((len(lens), columns), -1, dtype=torch.int32)
     at = 0
     for b, n in enumerate(need):
         table[b, :n] = order[at:at + n]
@@ -46,6 +53,7 @@ def check(q, cache, table, lengths, scale=None, got=None):
     return got
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("lens,R,Hq,kv,D,page", [
     ([1], 1, 1, 1, 128, 16),                       # one token, one head
@@ -55,6 +63,9 @@ def check(q, cache, table, lengths, scale=None, got=None):
     ([300, 7], 6, 16, 1, 128, 64),                 # M = 96
     ([257], 8, 16, 1, 64, 32),                     # M = 128
     ([190, 191, 64, 66], 8, 16, 2, 128, 32),       # M = 64
+    ([1, 0, 129, 2, 256, 640, 127], 5, 16, 2, 128, 16),   # M = 40
+    ([400, 3, 128, 257], 7, 14, 2, 64, 64),        # M = 49
+    ([1000, 128, 5], 5, 16, 1, 128, 128),          # M = 80
     ([130, 5, 70], 3, 6, 2, 64, 128),              # M = 9
     ([77, 200], 4, 14, 2, 128, 16),                # M = 28
     ([2, 0, 1, 5, 0], 8, 2, 1, 128, 16),           # rows that see nothing, empty sequences
@@ -63,22 +74,27 @@ def check(q, cache, table, lengths, scale=None, got=None):
     ([5000, 40], 2, 4, 2, 64, 128),
     ([1 + 13 * i % 150 for i in range(70)], 2, 3, 3, 64, 16),
 ])
-def test_attention_matches_64_bits(lens, R, Hq, kv, D, page, q8):
-    check(*problem(lens, R, Hq, kv, D, page, q8, seed=sum(lens) + R + D, strided=R % 2 == 0))
+def test_attention_matches_64_bits(lens, R, Hq, kv, D, page, q8, wide):
+    check(*problem(lens, R, Hq, kv, D, page, q8, seed=sum(lens) + R + D, strided=R % 2 == 0,
+                   wide=wide))
 
 
 @pytest.mark.parametrize("M", [1, 15, 16, 17, 31, 32, 33, 48, 64, 65, 80, 96, 97, 112, 127, 128])
-@pytest.mark.parametrize("D,q8", [(128, False), (64, True)])
+@pytest.mark.parametrize("D,q8", [(128, False), (64, True), (128, True), (64, False)])
 def test_every_count_of_rows(M, D, q8):
     R = 1 if M % 2 else (8 if M % 8 == 0 and M <= 64 else 2)
     check(*problem([150, 65], R, M // R, 1, D, 32, q8, seed=M))
+    if 32 < M <= 96:
+        check(*problem([150, 65], R, M // R, 1, D, 32, q8, seed=M, wide=True))
 
 
+@pytest.mark.parametrize("Hq,wide", [(4, False), (10, True)])
 @pytest.mark.parametrize("q8", [False, True])
-def test_peaked_and_rising_scores(q8):
+def test_peaked_and_rising_scores(q8, Hq, wide):
     # scores of hundreds, growing along the length: the reference of every row moves again
     # and again
-    q, cache, table, lengths = problem([700, 333], 4, 4, 1, 128, 16, q8, seed=3, sigma=12.0)
+    q, cache, table, lengths = problem([700, 333], 4, Hq, 1, 128, 16, q8, seed=3, sigma=12.0,
+                                       wide=wide)
     check(q, cache, table, lengths)
     ramp = torch.linspace(0.01, 4, 700)
     slots = table[0].cpu().long()[torch.arange(700) // 16] * 16 + torch.arange(700) % 16
@@ -100,17 +116,19 @@ def test_scale_argument():
         check(*p, scale=scale)
 
 
+@pytest.mark.parametrize("Hq,wide", [(4, False), (20, True)])
 @pytest.mark.parametrize("q8", [False, True])
-def test_what_is_not_visible_does_not_matter(q8):
+def test_what_is_not_visible_does_not_matter(q8, Hq, wide):
     # everything behind the lengths, in other pages, and in new tokens that a row does not
     # see holds infinities and NaN
     lens, R, page = [37, 64, 129, 6, 3], 4, 16
-    q, cache, table, lengths = problem(lens, R, 4, 2, 128, page, q8, seed=8)
+    q, cache, table, lengths = problem(lens, R, Hq, 2, 128, page, q8, seed=8, wide=wide)
     clean = dsm.paged_attention(q, cache, table, lengths)
     seen = torch.zeros(cache.k.shape[0] * page, dtype=torch.bool)
     for b, n in enumerate(lens):
         t = torch.arange(n - (R - 1) if n > R - 1 else 0)
         seen[table[b].cpu().long()[t // page] * page + t % page] = True
+    one_q = q[:, :1].contiguous()
     for bad in (float("inf"), float("nan"), -float("inf")):
         parts = {}
         for n in ("k", "v", "k_scale", "v_scale"):
@@ -127,31 +145,35 @@ def test_what_is_not_visible_does_not_matter(q8):
         assert torch.equal(out[:, 0], clean[:, 0])
         # longer sequences in the cache than asked for: all rows clean when one fewer is new
         short = (lengths - (R - 1)).clamp(min=0)
-        one = dsm.paged_attention(q[:, :1].contiguous(), dirty, table, short)
-        want = dsm.paged_attention(q[:, :1].contiguous(), cache, table, short)
+        one = dsm.paged_attention(one_q, dirty, table, short)
+        want = dsm.paged_attention(one_q, cache, table, short)
         assert torch.equal(one, want)
         assert bool(torch.isfinite(one).all())
 
 
-def test_bad_pages_are_skipped():
+@pytest.mark.parametrize("Hq,wide", [(4, False), (40, True)])
+@pytest.mark.parametrize("q8", [False, True])
+def test_bad_pages_are_skipped(q8, Hq, wide):
     page = 16
-    q, cache, table, lengths = problem([100, 64, 40], 2, 4, 2, 128, page, False, seed=9)
+    q, cache, table, lengths = problem([100, 64, 40], 2, Hq, 2, 128, page, q8, seed=9, wide=wide)
     table[0, 2], table[1, 0], table[1, 3], table[2, :] = -1, cache.k.shape[0], 2**31 - 1, -5
     out = check(q, cache, table, lengths)
     assert bool((out[2] == 0).all())
 
 
-def test_lengths_are_clamped():
-    q, cache, table, lengths = problem([64, 64], 1, 2, 1, 64, 16, True, seed=10)
+@pytest.mark.parametrize("Hq,wide", [(2, False), (40, True)])
+def test_lengths_are_clamped(Hq, wide):
+    q, cache, table, lengths = problem([64, 64], 1, Hq, 1, 64, 16, True, seed=10, wide=wide)
     want = dsm.paged_attention(q, cache, table, lengths)
     odd = torch.tensor([2**31 - 1, -3], dtype=torch.int32, device=DEV)
     out = dsm.paged_attention(q, cache, table, odd)
     assert torch.equal(out[0], want[0]) and bool((out[1] == 0).all())
 
 
-def test_shared_pages_and_repeated_rows():
+@pytest.mark.parametrize("Hq,wide", [(8, False), (32, True)])
+def test_shared_pages_and_repeated_rows(Hq, wide):
     # two sequences on the same pages give the same bytes, and so do two calls
-    q, cache, table, lengths = problem([900, 900], 2, 8, 1, 128, 32, True, seed=11)
+    q, cache, table, lengths = problem([900, 900], 2, Hq, 1, 128, 32, True, seed=11, wide=wide)
     table[1], q[1] = table[0], q[0]
     out = dsm.paged_attention(q, cache, table, lengths)
     again = dsm.paged_attention(q, cache, table, lengths)
@@ -166,11 +188,13 @@ def test_no_sequences():
     assert out.shape == (0, 1, 2, 64)
 
 
+@pytest.mark.parametrize("Hq", [5, 20])
 @pytest.mark.parametrize("q8", [False, True])
-def test_a_long_context_over_every_cta(q8):
+def test_a_long_context_over_every_cta(q8, Hq):
     # 70,000 tokens of one head: pieces on every CTA, joined; against fp64 on the device
     n, page = 70_001, 64
-    q, cache, table, lengths = problem([n], 3, 5, 1, 128, page, q8, seed=12, sigma=2.0)
+    q, cache, table, lengths = problem([n], 3, Hq, 1, 128, page, q8, seed=12, sigma=2.0,
+                                       wide=Hq > 5)
     out = dsm.paged_attention(q, cache, table, lengths)
     t = torch.arange(n, device=DEV)
     slots = table[0].long()[t // page] * page + t % page
@@ -275,9 +299,11 @@ def test_decode_steps_eager_and_captured(q8):
             assert torch.equal(getattr(cache, n), getattr(eager, n)), n
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("Hq,q8", [(8, True), (40, False)])
+def test_two_streams_at_once(Hq, q8):
     # two calls in flight, each with its own workspace (allocated on its own stream)
-    ps = [problem([4000, 100], 2, 8, 2, 128, 32, True, seed=40 + i) for i in range(2)]
+    ps = [problem([4000, 100], 2, Hq, 2, 128, 32, q8, seed=40 + i, wide=Hq > 8)
+          for i in range(2)]
     wants = [dsm.paged_attention(*p) for p in ps]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in ps]
@@ -298,6 +324,7 @@ def test_given_workspace_and_output():
     ws = torch.full((64 << 20,), 0xA5, dtype=torch.uint8, device=DEV)
     assert dsm.paged_attention(q, cache, table, lengths, out=out, workspace=ws) is out
     assert torch.equal(out, want)
+    assert dsm.workspace_status(ws) == 0
     with pytest.raises(dsm.DsmoeError) as e:
         dsm.paged_attention(q, cache, table, lengths, workspace=ws[:256])
     assert e.value.status == 3
