@@ -3,15 +3,16 @@
 // cache is written, and reading it back (arithmetic and layouts in include/dsmoe.h).
 //
 // k_rows: a row (one head of one token) belongs to D / 8 lanes of 8 values each, one 16-byte
-// load and one store per lane, so a warp takes 2 (D = 128) or 4 (D = 64) rows at a time and
+// load and one store per lane, so a warp takes 2 (D = 128) or 4 (D = 64) tokens at a time and
 // no shared memory is needed: the norm's sum and the quantiser's maximum are butterfly
-// shuffles inside the row's lanes, and the rotation's partner values (n / 2 values away) one
-// shuffle from a fixed lane, because n / 2 is a multiple of a lane's 8 values.
+// shuffles inside the row's lanes, and the rotation's partner values (n / 2 values away) come
+// as bf16 from one fixed lane, because n / 2 is a multiple of a lane's 8 values. A warp's rows
+// are of the same head, so what is done to queries, keys and values branches for whole warps.
 // The angle of a pair is position * freq modulo one turn, with freq in units of 2^-64 turn:
 // a 64-bit integer product that wraps, exact at any position, of which the upper 32 bits go
-// to sincospif. Each lane computes the angles of its own 8 values once per token and keeps
-// them in registers over the heads of its chunk. Memory-bound: every value is read once and
-// written once.
+// to sincospif. Each lane computes the angles of its own 8 values once per token, times the
+// weights, and keeps them in registers over the heads of its chunk. Memory-bound by bytes,
+// by instruction issue in practice: fp32 arithmetic is done two values at a time (f32x2).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -23,9 +24,38 @@ constexpr int kThreads = 256;
 struct RowsArgs {
   RowsProblem p;
   CacheView c;
+  int groups;              // warps per chunk of heads: 32 * 8 / D tokens each
   int chunks, per_chunk;   // the heads of a token in chunks of per_chunk
 };
 
+// Pairs of fp32 values.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 parts(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void pairs_of(const uint4& w, f2 (&x)[4]) {
+  x[0] = pair(bf16_lo(w.x), bf16_hi(w.x));
+  x[1] = pair(bf16_lo(w.y), bf16_hi(w.y));
+  x[2] = pair(bf16_lo(w.z), bf16_hi(w.z));
+  x[3] = pair(bf16_lo(w.w), bf16_hi(w.w));
+}
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
   x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
@@ -51,147 +81,234 @@ __device__ __forceinline__ bool slot_ok(const CacheView& c, int slot) {
   return slot >= 0 && (slot >> c.page_shift) < c.pages;
 }
 
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The larger of two bf16 pairs of magnitudes, NaN above all.
+__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Writes the codes and the scale of a row of the cache: code = 127 x / a rounded to nearest,
+// ties to even, a the row's largest magnitude (its bits in `top`, already the maximum over the
+// row's lanes). The quotient is the product with 1 / a and one correction by its remainder
+// (Markstein, IBM J. Res. Dev. 34, 1990), which makes a half-integer exactly that: for bf16
+// values 127 x / a is a ratio of small integers, so no other value comes near one. Rounding is
+// the addition of 1.5 * 2^23, whose low byte is the code.
+template <int D>
+__device__ __forceinline__ void put_codes(const f2 (&x)[4], uint32_t top, uint8_t* dst,
+                                          float* scale, int j, bool store) {
+  const bool bad = top >= 0x7F800000u, none = top == 0u || bad;
+  const float amax = __uint_as_float(top);
+  // 127 x and 1 / a stay finite: both sides by 2^-8 or 2^64 where they would not (exact)
+  const float pre = amax > 3.3230699e35f ? 0.00390625f : (amax < 7.8886091e-31f ? 1.8446744e19f : 1.f);
+  const float den = __fmul_rn(amax, pre), inv = none ? 0.f : __frcp_rn(den);
+  const float mult = __fmul_rn(127.f, pre);
+  const f2 mult2 = pair(mult, mult), inv2 = pair(inv, inv), den2 = pair(-den, -den);
+  const f2 magic = pair(12582912.f, 12582912.f);
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 t = mul2(x[i], mult2), u = mul2(t, inv2);
+    const float2 m = parts(add2(fma2(fma2(u, den2, t), inv2, u), magic));
+    q[2 * i] = __float_as_uint(m.x);
+    q[2 * i + 1] = __float_as_uint(m.y);
+  }
+  if (!store) return;
+  const uint32_t lo =
+      __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+  const uint32_t hi =
+      __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+  reinterpret_cast<uint2*>(dst)[j] = make_uint2(none ? 0u : lo, none ? 0u : hi);
+  if (j == 0) *scale = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 127.f);
+}
+// Bits of the largest magnitude of a row: of bf16 values, and of fp32 ones (as integers they
+// order as the values do, NaN above all).
+template <int LPH>
+__device__ __forceinline__ uint32_t top_of(const uint4& x) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t m = max_bf2(max_bf2(x.x & kAbs, x.y & kAbs), max_bf2(x.z & kAbs, x.w & kAbs));
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) m = max_bf2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return max_bf2(m, m << 16) & 0xFFFF0000u;
+}
+template <int LPH>
+__device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
 // kCache: 0 keys to k_out, 1 keys and values to a bf16 cache, 2 to a Q8 cache.
-// kTurn: norms and rotation (false: rows are stored as they are).
-template <int D, int kCache, bool kTurn>
-__global__ void __launch_bounds__(kThreads) k_rows(const __grid_constant__ RowsArgs a) {
-  constexpr int LPH = D / 8;         // lanes per row
-  constexpr int kBatch = 4;          // rows whose loads are in flight together
+// kTurn: 0 rows are stored as they are; norms and rotation of halves (1) or neighbours (2).
+template <int D, int kCache, int kTurn>
+__global__ void __launch_bounds__(kThreads, kTurn && kCache == 2 ? 2 : 4) k_rows(const __grid_constant__ RowsArgs a) {
+  constexpr int LPH = D / 8, kTokens = 32 / LPH;   // lanes per row, tokens per warp
+  constexpr int kBatch = 4;                        // rows whose loads are in flight together
   pdl_trigger();
   pdl_wait();
   const RowsProblem& p = a.p;
-  const int64_t sub = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / LPH;
-  const int j = threadIdx.x % LPH;
-  const bool live = sub < (int64_t)p.T * a.chunks;
-  const int t = live ? (int)(sub / a.chunks) : 0;
-  const int h_begin = live ? (int)(sub % a.chunks) * a.per_chunk : 0;
-  const int heads = p.Hq + (kCache ? 2 : 1) * p.Hkv;
-  const int h_end = !live ? 0 : min(heads, h_begin + a.per_chunk);
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int chunk = (int)(w / a.groups);
+  if (chunk >= a.chunks) return;                   // (a whole warp)
+  const int lane = threadIdx.x & 31, j = lane % LPH;
+  const int t_mine = (int)(w % a.groups) * kTokens + lane / LPH;
+  const bool live = t_mine < p.T;
+  const int t = live ? t_mine : p.T - 1;           // (every lane takes part in the shuffles)
 
   int slot = -1;
   if (kCache) slot = p.slots[t];
-  const bool keep = kCache == 0 || slot_ok(a.c, slot);
+  const bool keep = live && (kCache == 0 || slot_ok(a.c, slot));
 
-  // this lane's 8 angles: value e is x[e] * co[e] + partner[e] * si[e]
-  const bool turned = kTurn && j < p.rot / 8;
+  // this lane's 8 angles: value e becomes x[e] * co[e] + partner[e] * si[e]
+  const int half = p.rot / 16;                     // lanes per half of the rotated values
+  const bool turned = kTurn && j < 2 * half;
+  const int partner = kTurn != 1 || !turned ? j : (j < half ? j + half : j - half);
   float co[8], si[8];
-  if constexpr (kTurn) {
+  if constexpr (kTurn != 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) co[e] = 1.f, si[e] = 0.f;
     if (turned) {
       const uint64_t pos = (uint64_t)(int64_t)p.positions[t];
-      const int half = p.rot / 16;   // lanes per half
-      const int first = p.interleaved ? 4 * j : 8 * (j < half ? j : j - half);
+      const int64_t* f = p.freqs + (kTurn == 2 ? 4 * j : 8 * (j < half ? j : j - half));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (p.interleaved && (e & 1)) continue;
-        const uint64_t turn = pos * (uint64_t)p.freqs[first + (p.interleaved ? e / 2 : e)];
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-        co[e] = c;
-        si[e] = (p.interleaved || j < half) ? -s : s;
-        if (p.interleaved) co[e + 1] = c, si[e + 1] = s;
-      }
-    }
-  }
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if constexpr (kTurn) {
-    if (p.q_weight) wq = reinterpret_cast<const uint4*>(p.q_weight)[j];
-    if (p.k_weight) wk = reinterpret_cast<const uint4*>(p.k_weight)[j];
-  }
-  const int partner = j < p.rot / 16 ? j + p.rot / 16 : (j < p.rot / 8 ? j - p.rot / 16 : j);
-
-  for (int i0 = 0; i0 < a.per_chunk; i0 += kBatch) {
-    uint4 in[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int h = h_begin + i0 + b;
-      in[b] = make_uint4(0, 0, 0, 0);
-      if (i0 + b >= a.per_chunk || h >= h_end) continue;
-      const uint16_t* src;
-      if (h < p.Hq) src = p.q + t * p.q_stride + (int64_t)h * D;
-      else if (h < p.Hq + p.Hkv) src = p.k + t * p.k_stride + (int64_t)(h - p.Hq) * D;
-      else src = p.v + t * p.v_stride + (int64_t)(h - p.Hq - p.Hkv) * D;
-      in[b] = reinterpret_cast<const uint4*>(src)[j];
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (i0 + b >= a.per_chunk) break;   // the same for the whole grid
-      const int h = h_begin + i0 + b;
-      const bool store = h < h_end;
-      const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-      float x[8];
-      unpack8(in[b], x);
-      if constexpr (kTurn) {
-        // (every lane shuffles, whatever its row: rows of one warp may be of different kinds)
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = __fmaf_rn(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1)
-          ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-        const bool normed = is_q ? p.q_weight != nullptr : (is_k && p.k_weight != nullptr);
-        const uint4 w4 = is_q ? wq : wk;
-        float w[8], y[8];
-        unpack8(w4, w);
-        const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.f / D), p.eps));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = normed ? __fmul_rn(__fmul_rn(x[e], r), w[e]) : x[e];
-        if (p.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+      for (int e = 0; e < (kTurn == 2 ? 4 : 8); ++e) {
+        const uint64_t turn = pos * (uint64_t)f[e];
+        float sn, cs;
+        sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31
+        if constexpr (kTurn == 2) {
+          co[2 * e] = co[2 * e + 1] = cs;
+          si[2 * e] = -sn, si[2 * e + 1] = sn;
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner, LPH);
+          co[e] = cs;
+          si[e] = j < half ? -sn : sn;
         }
-        if (turned && (is_q || is_k)) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __fmaf_rn(y[e], si[e], __fmul_rn(x[e], co[e]));
-        }
-      }
-      if constexpr (kCache == 2) {
-        // the largest magnitude, by its bits: they order as the values do, NaN above all
-        uint32_t top = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1)
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (store && !is_q && keep) {
-          const int head = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
-          const bool bad = top >= 0x7F800000u;
-          const float amax = __uint_as_float(top);
-          // 127 x stays finite: both sides down by 2^-8 where it could not
-          const float pre = amax > 3.3230699e35f ? 0.00390625f : 1.f;   // 2^118
-          const float den = __fmul_rn(amax, pre);
-          uint32_t q[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            q[e] = top == 0u || bad
-                       ? 0u
-                       : (uint32_t)__float2int_rn(
-                             __fdiv_rn(__fmul_rn(127.f, __fmul_rn(x[e], pre)), den)) & 0xFFu;
-          const uint2 code = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
-                                        q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
-          uint8_t* dst = (is_k ? a.c.k : a.c.v) + cache_row(a.c, slot, head, D);
-          reinterpret_cast<uint2*>(dst)[j] = code;
-          if (j == 0)
-            (is_k ? a.c.k_scale : a.c.v_scale)[scale_at(a.c, slot, head)] =
-                bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 127.f);
-        }
-      }
-      if (store && is_q)
-        reinterpret_cast<uint4*>(p.q_out + ((int64_t)t * p.Hq + h) * D)[j] = pack8(x);
-      if (kCache == 0 && store && is_k)
-        reinterpret_cast<uint4*>(p.k_out + ((int64_t)t * p.Hkv + h - p.Hq) * D)[j] = pack8(x);
-      if (kCache == 1 && store && !is_q && keep) {
-        const int head = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(is_k ? a.c.k : a.c.v) +
-                        cache_row(a.c, slot, head, D);
-        reinterpret_cast<uint4*>(dst)[j] = pack8(x);
       }
     }
   }
+  const uint32_t other = turned ? 0xFFFFFFFFu : 0u;   // (0 x infinity is not 0)
+
+  // heads [from, to) of one kind, rows `stride` values apart per token
+  auto rows = [&](const uint16_t* src, int64_t stride, int from, int to, const uint16_t* weight,
+                  bool turn, auto&& emit) {
+    f2 c2[4], s2[4];
+    if (kTurn && turn) {
+      float c[8], s[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = co[e], s[e] = si[e];
+      if (weight) {
+        float wo[8], wp[8];
+        unpack8(reinterpret_cast<const uint4*>(weight)[j], wo);
+        unpack8(reinterpret_cast<const uint4*>(weight)[partner], wp);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c[e] = __fmul_rn(c[e], wo[e]);
+          s[e] = __fmul_rn(s[e], wp[kTurn == 2 ? e ^ 1 : e]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c2[i] = pair(c[2 * i], c[2 * i + 1]), s2[i] = pair(s[2 * i], s[2 * i + 1]);
+    }
+    const uint4* row = reinterpret_cast<const uint4*>(src + t * stride) + j;
+    for (int h0 = from; h0 < to; h0 += kBatch) {
+      uint4 in[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        in[b] = h0 + b < to ? row[(h0 + b) * LPH] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (h0 + b >= to) break;
+        float x[8];
+        f2 x2[4];
+        if (kTurn && turn) {
+          f2 y2[4];
+          pairs_of(in[b], x2);
+          if constexpr (kTurn == 1) {
+            uint4 y;
+            y.x = __shfl_sync(0xffffffffu, in[b].x, partner, LPH) & other;
+            y.y = __shfl_sync(0xffffffffu, in[b].y, partner, LPH) & other;
+            y.z = __shfl_sync(0xffffffffu, in[b].z, partner, LPH) & other;
+            y.w = __shfl_sync(0xffffffffu, in[b].w, partner, LPH) & other;
+            pairs_of(y, y2);
+          } else {
+            const uint4 y = make_uint4(__byte_perm(in[b].x, 0u, 0x1032) & other,
+                                       __byte_perm(in[b].y, 0u, 0x1032) & other,
+                                       __byte_perm(in[b].z, 0u, 0x1032) & other,
+                                       __byte_perm(in[b].w, 0u, 0x1032) & other);
+            pairs_of(y, y2);
+          }
+          if (weight) {
+            f2 sum = mul2(x2[0], x2[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) sum = fma2(x2[i], x2[i], sum);
+            const float2 two = parts(sum);
+            float ss = __fadd_rn(two.x, two.y);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1)
+              ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+            const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.f / D), p.eps));
+            const f2 r2 = pair(r, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x2[i] = mul2(x2[i], r2), y2[i] = mul2(y2[i], r2);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x2[i] = fma2(y2[i], s2[i], mul2(x2[i], c2[i]));
+            const float2 o = parts(x2[i]);
+            x[2 * i] = o.x;
+            x[2 * i + 1] = o.y;
+          }
+        } else {
+          pairs_of(in[b], x2);
+        }
+        emit(h0 + b, x, x2, in[b]);
+      }
+    }
+  };
+  // the row of head 0 in the cache; heads are head_rows rows apart
+  const int64_t row0 = keep && kCache ? cache_row(a.c, slot, 0, D) : 0;
+  const int64_t scale0 = keep && kCache == 2 ? scale_at(a.c, slot, 0) : 0;
+  const int begin = chunk * a.per_chunk, end = begin + a.per_chunk;
+  if constexpr (kTurn != 0)
+    rows(p.q, p.q_stride, begin, min(end, p.Hq), p.q_weight, true,
+         [&](int h, const float(&x)[8], const f2(&)[4], const uint4&) {
+           if (live) reinterpret_cast<uint4*>(p.q_out + ((int64_t)t * p.Hq + h) * D)[j] = pack8(x);
+         });
+  rows(p.k, p.k_stride, max(begin - p.Hq, 0), min(end - p.Hq, p.Hkv), p.k_weight, true,
+       [&](int h, const float(&x)[8], const f2(&x2)[4], const uint4& in) {
+         const int64_t at = row0 + ((int64_t)h << a.c.page_shift) * D;
+         if constexpr (kCache == 0) {
+           if (live) reinterpret_cast<uint4*>(p.k_out + ((int64_t)t * p.Hkv + h) * D)[j] = pack8(x);
+         } else if constexpr (kCache == 1) {
+           if (keep)
+             reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.c.k) + at)[j] =
+                 kTurn ? pack8(x) : in;
+         } else {
+           uint32_t top;
+           if constexpr (kTurn != 0) top = top_of<LPH>(x);
+           else top = top_of<LPH>(in);
+           put_codes<D>(x2, top, a.c.k + at, a.c.k_scale + scale0 + ((int64_t)h << a.c.page_shift), j,
+                        keep);
+         }
+       });
+  if constexpr (kCache != 0)
+    rows(p.v, p.v_stride, max(begin - p.Hq - p.Hkv, 0), min(end - p.Hq - p.Hkv, p.Hkv), nullptr,
+         false, [&](int h, const float(&)[8], const f2(&x2)[4], const uint4& in) {
+           const int64_t at = row0 + ((int64_t)h << a.c.page_shift) * D;
+           if constexpr (kCache == 1) {
+             if (keep) reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.c.v) + at)[j] = in;
+           } else {
+             put_codes<D>(x2, top_of<LPH>(in), a.c.v + at,
+                          a.c.v_scale + scale0 + ((int64_t)h << a.c.page_shift), j, keep);
+           }
+         });
 }
 
 // k_cache_read: one thread per 8 values of a (token, head), keys and values.
@@ -234,30 +351,36 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const CacheView c, cons
   reinterpret_cast<uint4*>(v_out)[i] = v;
 }
 
-template <int D, int kCache, bool kTurn>
+template <int D, int kCache, int kTurn>
 cudaError_t start_rows(const RowsProblem& p, const CacheView* c, cudaStream_t s) {
+  constexpr int kTokens = 256 / D;
   RowsArgs a{};
   a.p = p;
   if (c) a.c = *c;
   const int heads = p.Hq + (c ? 2 : 1) * p.Hkv;
-  // Few tokens: a row per group of lanes, so that the call is one short wave. Many: a token's
-  // heads share its angles, as long as every SM keeps its lanes busy.
-  const int64_t groups = (int64_t)device_sm_count() * 2048 / (D / 8);
-  int64_t chunks = (groups + p.T - 1) / p.T;
+  a.groups = (p.T + kTokens - 1) / kTokens;
+  // Few tokens: a head per warp, so that the call is one short wave. Many: a token's heads
+  // share its angles, as long as every SM keeps its warps busy.
+  const int64_t warps = (int64_t)device_sm_count() * 64;
+  int64_t chunks = (warps + a.groups - 1) / a.groups;
   chunks = chunks > heads ? heads : chunks;
   a.per_chunk = (int)((heads + chunks - 1) / chunks);
   a.chunks = (heads + a.per_chunk - 1) / a.per_chunk;
-  const int64_t threads = (int64_t)p.T * a.chunks * (D / 8);
-  const int64_t grid = (threads + kThreads - 1) / kThreads;
+  const int64_t grid = ((int64_t)a.groups * a.chunks + kThreads / 32 - 1) / (kThreads / 32);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   return launch_pdl(k_rows<D, kCache, kTurn>, dim3((unsigned)grid), kThreads, 0, s, a);
 }
 
+template <int D, int kCache>
+cudaError_t pick_turn(const RowsProblem& p, const CacheView* c, cudaStream_t s) {
+  return p.interleaved ? start_rows<D, kCache, 2>(p, c, s) : start_rows<D, kCache, 1>(p, c, s);
+}
+
 template <int D>
 cudaError_t pick_rows(const RowsProblem& p, const CacheView* c, cudaStream_t s) {
-  if (p.Hq == 0) return c->q8 ? start_rows<D, 2, false>(p, c, s) : start_rows<D, 1, false>(p, c, s);
-  if (!c) return start_rows<D, 0, true>(p, c, s);
-  return c->q8 ? start_rows<D, 2, true>(p, c, s) : start_rows<D, 1, true>(p, c, s);
+  if (p.Hq == 0) return c->q8 ? start_rows<D, 2, 0>(p, c, s) : start_rows<D, 1, 0>(p, c, s);
+  if (!c) return pick_turn<D, 0>(p, c, s);
+  return c->q8 ? pick_turn<D, 2>(p, c, s) : pick_turn<D, 1>(p, c, s);
 }
 
 template <int D>

@@ -1,5 +1,6 @@
 // common.cuh — device helpers shared by the kernels of libdsmoe.so (sm_103a).
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <utility>
 #include <cuda_runtime.h>
@@ -47,6 +48,26 @@ cudaError_t launch_pdl(void (*kernel)(Exp...), dim3 grid, int block, size_t smem
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Act>(args)...);
 }
+
+// A call that succeeds once on each device (a kernel's attributes last as long as the device's
+// context); on devices from the 65th on it is made every time.
+class OncePerDevice {
+ public:
+  template <typename F>
+  cudaError_t run(F&& f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done_.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = f();
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
 
 __device__ __forceinline__ void flag_status(uint32_t* status, uint32_t bit) {
   atomicOr(status, bit);

@@ -1,8 +1,6 @@
 // paged.cuh — what the kernels of the attention over the paged cache share: the list of tiles
 // that the CTAs divide among themselves, look-ups in the page table, and small helpers.
 #pragma once
-#include <atomic>
-
 #include "common.cuh"
 #include "kernels.h"
 
@@ -33,26 +31,6 @@ struct PagedArgs {
 // the normaliser).
 constexpr int kTcMaxRows = 96, kTcMaxRowsQ8 = 64;
 cudaError_t launch_tc(const PagedArgs& p, int D, cudaStream_t s);
-
-// A call that succeeds once on each device (a kernel's attributes last as long as the device's
-// context); on devices from the 65th on it is made every time.
-class OncePerDevice {
- public:
-  template <typename F>
-  cudaError_t run(F&& f) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done_.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = f();
-    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-  }
-
- private:
-  std::atomic<uint64_t> done_{0};
-};
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -8,12 +8,14 @@
 // once by its fp16 scale. Weights go from global memory to registers in 16-byte loads, a
 // batch of tiles ahead of the arithmetic, without shared memory: no other warp needs them.
 //
-// k_q4_proj: 16 warps; kWk of them split a unit's (16 rows') K tiles, tile kt to warp
-// kt mod kWk, and 16 / kWk units run side by side (short K). A warp's tiles of a unit come in
-// batches of kTiles. When one batch is all of them the activation fragments stay in
+// k_q4_proj: 16 warps; 2^wk_log of them split a unit's (16 rows') K tiles, tile kt to warp
+// kt mod 2^wk_log, and the others run units side by side (short K). A warp's tiles of a unit
+// come in batches of kTiles. When one batch is all of them the activation fragments stay in
 // registers for the whole call (kKeepX); else they are read again through L1. The warps'
-// partials meet in shared memory, added in warp order, rounded once. Nothing depends on R.
-// Memory-bound: rows x K x 9/16 bytes.
+// partials meet in shared memory, kGroup units at a time (every thread then adds one or two
+// outputs, and the barrier is paid once per group), in warp order, rounded once. Nothing
+// depends on R. Bound: rows x K x 9/16 bytes; in practice the issue of about 80 instructions
+// per tile, of which 44 widen nibbles.
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -23,6 +25,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kGroup = 4;   // rounds per barrier
 
 struct Q4Args {
   const uint8_t* tiles;
@@ -56,23 +59,28 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t w) {
   return d;
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+                                         uint32_t a3, uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
 }
 
 // acc += scales x (block of 16 rows x 32 values) x X: the K order of the two MMAs is
-// (8w + {0, 4} | 8w + {1, 5}) and (8w + {2, 6} | 8w + {3, 7}) for lane w of a row.
+// (8w + {0, 4} | 8w + {1, 5}) and (8w + {2, 6} | 8w + {3, 7}) for lane w of a row. acc: row g
+// columns 2w and 2w + 1, then row g + 8.
 __device__ __forceinline__ void block_mma(uint32_t lo, uint32_t hi, uint32_t scales,
                                           const uint4& X, float (&acc)[4]) {
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
+  const float z[4] = {0.f, 0.f, 0.f, 0.f};
+  float d[4];
   mma16816(d, nibble_pair(lo), nibble_pair(hi), nibble_pair(lo >> 4), nibble_pair(hi >> 4), X.x,
-           X.y);
+           X.y, z);
   mma16816(d, nibble_pair(lo >> 8), nibble_pair(hi >> 8), nibble_pair(lo >> 12),
-           nibble_pair(hi >> 12), X.z, X.w);
-  const float s0 = f16_bits_to_f32((uint16_t)scales), s1 = f16_bits_to_f32((uint16_t)(scales >> 16));
+           nibble_pair(hi >> 12), X.z, X.w, d);
+  const __half2 s2 = *reinterpret_cast<const __half2*>(&scales);
+  const float s0 = __low2float(s2), s1 = __high2float(s2);
   acc[0] = __fmaf_rn(s0, d[0], acc[0]);
   acc[1] = __fmaf_rn(s0, d[1], acc[1]);
   acc[2] = __fmaf_rn(s1, d[2], acc[2]);
@@ -85,13 +93,15 @@ __device__ __forceinline__ uint4 x_pairs(const uint4& r) {
                     __byte_perm(r.y, r.w, 0x5410), __byte_perm(r.y, r.w, 0x7632));
 }
 
-template <int kTiles, bool kKeepX>
+// kFull: all 16 warps along K (K >= 1024), so that tiles lie at fixed distances.
+template <int kTiles, bool kKeepX, bool kFull>
 __global__ void __launch_bounds__(kThreads, 1) k_q4_proj(const __grid_constant__ Q4Args a) {
-  __shared__ float4 part[2][kWarps][32];
+  extern __shared__ float4 part[];   // [2][kGroup][warps][32 lanes]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int wk = 1 << a.wk_log, wu = kWarps >> a.wk_log;      // warps along K, units side by side
-  const int my_k = warp & (wk - 1), my_u = warp >> a.wk_log;
+  const int wk_log = kFull ? 4 : a.wk_log;
+  const int wk = 1 << wk_log, wu = kWarps >> wk_log;   // warps along K, units side by side
+  const int my_k = warp & (wk - 1), my_u = warp >> wk_log;
   const int rounds = (a.units + wu - 1) / wu;
   const int r0 = (int)((int64_t)blockIdx.x * rounds / gridDim.x);
   const int r1 = (int)((int64_t)(blockIdx.x + 1) * rounds / gridDim.x);
@@ -99,25 +109,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_q4_proj(const __grid_constant__
   pdl_wait();
 
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  uint4 W[kTiles], Wn[kTiles];
-  uint2 S[kTiles], Sn[kTiles];
-  // batch b of round r into (w, s): tiles behind the row's end have scale 0
-  auto load = [&](int r, int b, uint4(&w)[kTiles], uint2(&s)[kTiles]) {
-    const int unit = r * wu + my_u;
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int kt = ((b * kTiles + i) << a.wk_log) + my_k;
-      w[i] = none;
-      s[i] = make_uint2(0u, 0u);
-      if (r < r1 && unit < a.units && kt < a.Tk) {
-        const uint8_t* t = a.tiles + ((int64_t)unit * a.Tk + kt) * kQ4TileBytes;
-        w[i] = ldg_once(t + 16 * lane);
-        s[i] = ldg_once8(t + 512 + 8 * g);
-      }
+  const int64_t round_bytes = (int64_t)wu * a.Tk * kQ4TileBytes;
+  const int tile_step = wk * kQ4TileBytes;
+  const uint8_t* const lane0 =
+      a.tiles + ((int64_t)my_u * a.Tk + my_k) * kQ4TileBytes + r0 * round_bytes + 16 * lane;
+  const int scales_at = 512 + 8 * g - 16 * lane;
+  const int mine = (a.Tk - my_k + wk - 1) >> wk_log;   // K tiles of a unit that are this warp's
+  // The batch to be loaded next, and where its first tile is. Tiles behind the row's end have
+  // scale 0.
+  int rl = r0, bl = 0;
+  const uint8_t* next = lane0;
+  auto load = [&](int i, uint4& w, uint2& s) {
+    w = none;
+    s = make_uint2(0u, 0u);
+    if (bl * kTiles + i < mine && rl < r1 && (kFull || rl * wu + my_u < a.units)) {
+      w = ldg_once(next + i * tile_step);
+      s = ldg_once8(next + i * tile_step + scales_at);
+    }
+  };
+  auto advance = [&] {
+    next += kTiles * tile_step;
+    if (kKeepX || ++bl == a.batches) {
+      bl = 0;
+      ++rl;
+      next += round_bytes - (int64_t)(kKeepX ? 1 : a.batches) * kTiles * tile_step;
     }
   };
   auto load_x = [&](int b, int i, uint4& x0, uint4& x1) {
-    const int kt = ((b * kTiles + i) << a.wk_log) + my_k;
+    const int kt = ((b * kTiles + i) << wk_log) + my_k;
     x0 = x1 = none;
     if (g < a.R && kt < a.Tk) {
       const uint4* src =
@@ -127,46 +146,74 @@ __global__ void __launch_bounds__(kThreads, 1) k_q4_proj(const __grid_constant__
     }
   };
   uint4 X[kKeepX ? kTiles : 1][2];
-  load(r0, 0, W, S);
-  if constexpr (kKeepX) {
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) load_x(0, i, X[i][0], X[i][1]);
-  }
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  int r = r0, b = 0, par = 0;
-  while (r < r1) {
-    const bool unit_ends = b + 1 == a.batches;
+  int r = r0, b = 0, filled = 0, buf = 0;   // rounds whose partials are in this buffer
+  // Multiplies a batch; each of its registers is loaded again, two batches ahead, as soon as
+  // it is used. False after the last.
+  auto step = [&](uint4(&w)[kTiles], uint2(&s)[kTiles]) {
+    const bool unit_ends = kKeepX || b + 1 == a.batches;
     const int rn = unit_ends ? r + 1 : r, bn = unit_ends ? 0 : b + 1;
-    load(rn, bn, Wn, Sn);
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       uint4 x0, x1;
       if constexpr (kKeepX) x0 = X[i][0], x1 = X[i][1];
       else load_x(b, i, x0, x1);
-      block_mma(W[i].x, W[i].y, S[i].x, x0, acc);
-      block_mma(W[i].z, W[i].w, S[i].y, x1, acc);
+      block_mma(w[i].x, w[i].y, s[i].x, x0, acc);
+      block_mma(w[i].z, w[i].w, s[i].y, x1, acc);
+      load(i, w[i], s[i]);
     }
+    advance();
     if (unit_ends) {
-      part[par][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      float4* const group = part + buf * kGroup * kWarps * 32;
+      group[(filled * kWarps + warp) * 32 + lane] =
+          make_float4(acc[0], acc[1], acc[2], acc[3]);   // rows g and g + 8, columns 2q, 2q + 1
       acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-      // (the slots written two rounds ago were read before the last barrier)
-      __syncthreads();
-      for (int o = tid; o < wu * 128; o += kThreads) {
-        const int row = o & 15, col = (o >> 4) & 7, u = o >> 7, unit = r * wu + u;
-        const int at = ((row & 7) * 4 + (col >> 1)) * 4 + (row >> 3) * 2 + (col & 1);
-        if (col >= a.R || unit >= a.units) continue;
-        float sum = 0.f;
-        for (int w = 0; w < wk; ++w)
-          sum = __fadd_rn(sum, reinterpret_cast<const float*>(part[par][u * wk + w])[at]);
-        a.y[(int64_t)col * a.units * 16 + unit * 16 + row] = f32_to_bf16_rne(sum);
+      if (++filled == kGroup || rn == r1) {
+        __syncthreads();   // (the other buffer was read before the last one)
+        for (int o = tid; o < filled * wu * 128; o += kThreads) {
+          const int at = o & 127, u = (o >> 7) & (wu - 1), f = o >> 7 >> (4 - wk_log);
+          const int row = (at >> 4) + 8 * ((at >> 1) & 1), col = 2 * ((at >> 2) & 3) + (at & 1);
+          const int unit = (rn - filled + f) * wu + u;
+          if (col >= a.R || unit >= a.units) continue;
+          const float* p = reinterpret_cast<const float*>(group + (f * kWarps + u * wk) * 32) + at;
+          float sum = 0.f;
+          for (int k = 0; k < wk; ++k) sum = __fadd_rn(sum, p[k * 128]);
+          a.y[(int64_t)col * a.units * 16 + unit * 16 + row] = f32_to_bf16_rne(sum);
+        }
+        buf ^= 1;
+        filled = 0;
       }
-      par ^= 1;
     }
     r = rn;
     b = bn;
+    return r < r1;
+  };
+  uint4 W0[kTiles], W1[kTiles];
+  uint2 S0[kTiles], S1[kTiles];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) W[i] = Wn[i], S[i] = Sn[i];
+  for (int i = 0; i < kTiles; ++i) load(i, W0[i], S0[i]);
+  advance();
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) load(i, W1[i], S1[i]);
+  advance();
+  if constexpr (kKeepX) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) load_x(0, i, X[i][0], X[i][1]);
   }
+  while (step(W0, S0) && step(W1, S1)) {
+  }
+}
+
+template <int kTiles, bool kKeepX, bool kFull>
+cudaError_t start(const Q4Args& a, int grid, cudaStream_t s) {
+  constexpr int kSmem = 2 * kGroup * kWarps * 32 * (int)sizeof(float4);
+  static OncePerDevice ready;
+  const cudaError_t e = ready.run([] {
+    return cudaFuncSetAttribute(k_q4_proj<kTiles, kKeepX, kFull>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_q4_proj<kTiles, kKeepX, kFull>, dim3(grid), kThreads, kSmem, s, a);
 }
 
 }  // namespace
@@ -186,12 +233,10 @@ cudaError_t launch_q4_project(const void* tiles, int rows, int K, const uint16_t
   const int rounds = (a.units + wu - 1) / wu;
   const int grid = rounds < device_sm_count() ? rounds : device_sm_count();
   a.batches = (per_warp + 3) / 4;
-  if (per_warp <= 2) {
-    a.batches = 1;
-    return launch_pdl(k_q4_proj<2, true>, dim3(grid), kThreads, 0, s, a);
-  }
-  if (per_warp <= 4) return launch_pdl(k_q4_proj<4, true>, dim3(grid), kThreads, 0, s, a);
-  return launch_pdl(k_q4_proj<4, false>, dim3(grid), kThreads, 0, s, a);
+  if (a.wk_log < 4) return start<2, true, false>(a, grid, s);   // (at most two tiles per warp)
+  if (per_warp <= 2) return start<2, true, true>(a, grid, s);
+  if (per_warp <= 4) return start<4, true, true>(a, grid, s);
+  return start<4, false, true>(a, grid, s);
 }
 
 }  // namespace dsmoe
