@@ -414,7 +414,8 @@ ds_status ds_q4_project(const ds_q4_tiled* w, int64_t rows, int32_t K, const uin
  * Limits: page_tokens 16, 32, 64 or 128; head_dim 64 or 128 (other values from 1 to 4096:
  * DS_ERR_UNSUPPORTED); 1 <= n_kv_heads <= 256; n_pages >= 1 and n_pages * page_tokens <
  * 2^31; page_stride >= n_kv_heads * page_tokens * head_dim and a multiple of 16;
- * scale_page_stride >= n_kv_heads * page_tokens and a multiple of 4; k, v, k_scale and
+ * scale_page_stride >= n_kv_heads * page_tokens and a multiple of 4 (both and token strides at
+ * most 2^31); k, v, k_scale and
  * v_scale 16-byte aligned. k and v may share one allocation (strided pages).
  * ---------------------------------------------------------------------------------- */
 #define DS_CACHE_BF16 0
@@ -500,11 +501,15 @@ ds_status ds_qk_norm_rope_write(const ds_norm_rope_args* args, const uint16_t* v
  *   p = softmax(s),   out_{b,r,h} = bf16_RNE(sum_t p_t v_{b,g,t}),
  * token t in page page_table[b][t / page_tokens], offset t % page_tokens. A row with no
  * visible token gets 0, and a score of -infinity counts as not visible; tokens that a row
- * does not see do not reach it, whatever they hold. len is taken as 0 when negative and as
+ * does not see do not reach it, whatever they hold (an infinity among the values that it
+ * does see gives infinities or NaN). len is taken as 0 when negative and as
  * max_pages * page_tokens when larger; page table entries outside 0 .. n_pages - 1 are
  * skipped as if their tokens were not there, and entries behind the last needed page are
- * not read. Scores, softmax and sums in fp32 on the tensor cores; p (times the value's
- * scale in a Q8 cache) is rounded to bf16 for the product with the values.
+ * not read. Scores, softmax and sums in fp32 on the tensor cores; for the product with the
+ * values, p (times the value's scale in a Q8 cache) is a high and a low bf16 part, or, over a
+ * bf16 cache with more than 32 or 64 rows per key head, one bf16 value that the softmax's sum
+ * is taken of as well. The result does not depend on timing, but it may in its last bits on
+ * the other sequences of the call and on max_pages, which decide how the work is cut.
  * Limits: 0 <= n_seqs <= 4096 (0 enqueues nothing), 1 <= n_rows <= 8, 1 <= max_pages,
  * max_pages * page_tokens <= 2^24, n_heads a multiple of the cache's n_kv_heads, n_rows * H
  * <= 128 (else DS_ERR_UNSUPPORTED), scale finite; q and out 16-byte aligned.
@@ -524,7 +529,8 @@ typedef struct {
 size_t ds_paged_attn_workspace_size(const ds_paged_attn_args* args);
 /* out: bf16 [n_seqs][n_rows][n_heads][head_dim], not overlapping the inputs; workspace
  * 256-byte aligned, its contents on entry are ignored and it must not be used by another
- * call in flight. DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED, DS_ERR_WORKSPACE, DS_ERR_CUDA. */
+ * call in flight; ds_workspace_status() reads the call's device status from it.
+ * DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED, DS_ERR_WORKSPACE, DS_ERR_CUDA. */
 ds_status ds_paged_attention(const ds_paged_attn_args* args, uint16_t* out, void* workspace,
                              size_t ws_bytes, ds_stream_t stream);
 

@@ -7,6 +7,7 @@ and the current CUDA stream. PyTorch provides device memory and streams.
 from __future__ import annotations
 
 import math
+from contextlib import ExitStack
 from dataclasses import dataclass
 
 import torch
@@ -415,25 +416,32 @@ def _cuda_tensor(t: torch.Tensor, name: str, dims: int) -> torch.device:
     return t.device
 
 
-def _run(dev: torch.device, stream, call):
-    """call(stream handle) with `dev` current and its allocations made on the launch stream
-    (the current stream of `dev` when `stream` is None)."""
+def _enter(dev: torch.device, stream):
+    """(stream handle, what to close afterwards or None): makes `dev` current, and `stream`
+    current on it, so that what the call allocates belongs to the stream it is launched on.
+    Nothing changes when `dev` is current already and no stream is given."""
     if stream is None:
         # (the handle of torch.cuda.current_stream(dev), without making the object)
         handle = torch._C._cuda_getCurrentRawStream(dev.index)
         if dev.index == torch._C._cuda_getDevice():
-            return call(handle)
-        with torch.cuda.device(dev):
-            return call(handle)
-    with torch.cuda.device(dev):
+            return handle, None
+        undo = ExitStack()
+        undo.enter_context(torch.cuda.device(dev))
+        return handle, undo
+    undo = ExitStack()
+    try:
+        undo.enter_context(torch.cuda.device(dev))
         if not isinstance(stream, torch.cuda.Stream):
             handle = int(stream)
             stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
                       else torch.cuda.default_stream(dev))
         if stream.device != dev:
             raise ValueError(f"stream must be on {dev} (got {stream.device})")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+        undo.enter_context(torch.cuda.stream(stream))
+    except BaseException:
+        undo.close()
+        raise
+    return stream.cuda_stream, undo
 
 
 def q4_project(tiles: torch.Tensor, x: torch.Tensor, *, y=None, stream=None) -> torch.Tensor:
@@ -449,13 +457,16 @@ def q4_project(tiles: torch.Tensor, x: torch.Tensor, *, y=None, stream=None) -> 
     if y is not None:
         _need_on(y, "y", torch.bfloat16, (R, 16 * units), dev)
 
-    def call(s):
-        out = torch.empty((R, 16 * units), dtype=torch.bfloat16, device=dev) if y is None else y
+    s, undo = _enter(dev, stream)
+    try:
+        if y is None:
+            y = torch.empty((R, 16 * units), dtype=torch.bfloat16, device=dev)
         _check(lib.ds_q4_project(N.DsQ4Tiled(tiles.data_ptr()), 16 * units, 64 * Tk, x.data_ptr(),
-                                 R, out.data_ptr(), s), "ds_q4_project")
-        return out
-
-    return _run(dev, stream, call)
+                                 R, y.data_ptr(), s), "ds_q4_project")
+    finally:
+        if undo:
+            undo.close()
+    return y
 
 
 @dataclass
@@ -493,13 +504,15 @@ class PagedCache:
         if not t.is_cuda or t.dtype is not dtype or t.shape != shape or t.device != dev:
             raise ValueError(f"cache.{name} must be {dtype} {tuple(shape)} on {dev} "
                              f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
-        strides = t.stride()
-        inner = 1
-        for n, st in zip(reversed(shape[1:]), reversed(strides[1:])):
-            if n > 1 and st != inner:
+        inner = t.numel() // max(1, shape[0])
+        if t.is_contiguous():
+            return inner
+        at = 1
+        for n, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+            if n > 1 and stride != at:
                 raise ValueError(f"the pages of cache.{name} must be contiguous")
-            inner *= n
-        return strides[0] if shape[0] > 1 else -(-inner // 16) * 16
+            at *= n
+        return t.stride(0) if shape[0] > 1 else inner
 
     def struct(self) -> N.DsPagedCache:
         k, v = self.k, self.v
@@ -598,13 +611,17 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions, freqs, *, q_weight
     if k_out is not None:
         _need_on(k_out, "k_out", torch.bfloat16, k.shape, dev)
 
-    def call(s):
-        qo = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-        ko = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-        _check(lib.ds_qk_norm_rope(a, qo.data_ptr(), ko.data_ptr(), s), "ds_qk_norm_rope")
-        return qo, ko
-
-    return _run(dev, stream, call)
+    s, undo = _enter(dev, stream)
+    try:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+        _check(lib.ds_qk_norm_rope(a, q_out.data_ptr(), k_out.data_ptr(), s), "ds_qk_norm_rope")
+    finally:
+        if undo:
+            undo.close()
+    return q_out, k_out
 
 
 def qk_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions, freqs,
@@ -623,13 +640,16 @@ def qk_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     if q_out is not None:
         _need_on(q_out, "q_out", torch.bfloat16, q.shape, dev)
 
-    def call(s):
-        qo = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-        _check(lib.ds_qk_norm_rope_write(a, v.data_ptr(), vs, c, slots.data_ptr(), qo.data_ptr(),
-                                         s), "ds_qk_norm_rope_write")
-        return qo
-
-    return _run(dev, stream, call)
+    s, undo = _enter(dev, stream)
+    try:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        _check(lib.ds_qk_norm_rope_write(a, v.data_ptr(), vs, c, slots.data_ptr(),
+                                         q_out.data_ptr(), s), "ds_qk_norm_rope_write")
+    finally:
+        if undo:
+            undo.close()
+    return q_out
 
 
 def cache_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *,
@@ -644,9 +664,13 @@ def cache_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     shape = (T, c.n_kv_heads, c.head_dim)
     ks, vs = _token_rows(k, "k", shape, dev), _token_rows(v, "v", shape, dev)
     _need_on(slots, "slots", torch.int32, (T,), dev)
-    _run(dev, stream, lambda s: _check(
-        lib.ds_cache_write(c, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, s),
-        "ds_cache_write"))
+    s, undo = _enter(dev, stream)
+    try:
+        _check(lib.ds_cache_write(c, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, s),
+               "ds_cache_write")
+    finally:
+        if undo:
+            undo.close()
 
 
 def cache_read(cache: PagedCache, slots: torch.Tensor, *, k_out=None, v_out=None, stream=None):
@@ -663,14 +687,18 @@ def cache_read(cache: PagedCache, slots: torch.Tensor, *, k_out=None, v_out=None
     if v_out is not None:
         _need_on(v_out, "v_out", torch.bfloat16, shape, dev)
 
-    def call(s):
-        ko = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-        vo = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
-        _check(lib.ds_cache_read(c, slots.data_ptr(), T, ko.data_ptr(), vo.data_ptr(), s),
+    s, undo = _enter(dev, stream)
+    try:
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        _check(lib.ds_cache_read(c, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(), s),
                "ds_cache_read")
-        return ko, vo
-
-    return _run(dev, stream, call)
+    finally:
+        if undo:
+            undo.close()
+    return k_out, v_out
 
 
 def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
@@ -698,17 +726,19 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     args = N.DsPagedAttnArgs(B, R, Hq, max_pages, D ** -0.5 if scale is None else scale,
                              q.data_ptr(), c, page_table.data_ptr(), lengths.data_ptr())
 
-    def call(s):
-        o = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib.ds_paged_attn_workspace_size(args), dtype=torch.uint8,
-                             device=dev)
-        _check(lib.ds_paged_attention(args, o.data_ptr(), ws.data_ptr(), ws.numel(), s),
-               "ds_paged_attention")
-        return o
-
-    return _run(dev, stream, call)
+    s, undo = _enter(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = torch.empty(lib.ds_paged_attn_workspace_size(args), dtype=torch.uint8,
+                                    device=dev)
+        _check(lib.ds_paged_attention(args, out.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel(), s), "ds_paged_attention")
+    finally:
+        if undo:
+            undo.close()
+    return out
 
 
 def noalloc_status(stream=None) -> int:
