@@ -13,6 +13,7 @@ constexpr float kSlack = 8.f;   // log2 by which a score may exceed the row's re
 struct PagedArgs {
   int B, R, Hq, G, M, max_pages;
   int tile_log;     // log2 of the tokens of a tile
+  int begin;        // places in the list before a (sequence, key head)'s tiles
   float scale_log2;
   const uint16_t* q;
   CacheView c;
@@ -22,8 +23,14 @@ struct PagedArgs {
   uint32_t* status;
   float* part_o;    // [2 grid][M][D]
   float* part_ml;   // [2 grid][M][2]
+  int* span;        // [B][key heads][2]: the CTAs that begin and end a (sequence, head)
   int grid;         // CTAs that share the tiles
 };
+
+// paged_few.cu: tiles of 64 tokens, up to 32 query rows per key head.
+constexpr int kFewMaxRows = 32;
+int few_ctas_per_sm(int M, int D, bool q8);
+cudaError_t launch_few(const PagedArgs& p, int D, cudaStream_t s);
 
 // paged_tc.cu: tiles of 128 tokens, one CTA per SM. The most query rows per key head: tensor
 // memory holds two buffers of S, O and two of the sums, 5 N columns of 512, or 6 N where P
@@ -66,6 +73,39 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x2_t(uint32_t addr, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Byte offset of 16-byte chunk c of row r in a tile of rows of RB bytes: the eight rows of
+// an ldmatrix meet eight different bank groups.
+template <int RB>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  if constexpr (RB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  return r * RB + ((c ^ (r & 7)) << 4);
+}
+
 __device__ __forceinline__ int seq_len(const PagedArgs& a, int b) {
   const int n = a.lengths[b], cap = a.max_pages << a.c.page_shift;
   return n < 0 ? 0 : (n > cap ? cap : n);
@@ -75,10 +115,11 @@ __device__ __forceinline__ int tiles_of(const PagedArgs& a, int len) {
 }
 
 // The list of tiles: sequences, then key heads, then tiles along the length. Beginning and
-// ending a (sequence, key head) costs about as much as kBegin tiles, so each non-empty one
-// takes kBegin positions before its tiles, and the CTAs share the positions evenly.
-constexpr int kBegin = 2;
-__device__ __forceinline__ int places_of(int tiles) { return tiles ? tiles + kBegin : 0; }
+// ending a (sequence, key head) costs about as much as `begin` tiles, so each non-empty one
+// takes that many positions before its tiles, and the CTAs share the positions evenly.
+__device__ __forceinline__ int places_of(const PagedArgs& a, int tiles) {
+  return tiles ? tiles + a.begin : 0;
+}
 
 // The place of a tile in the list.
 struct Cursor {
@@ -104,9 +145,12 @@ struct Cursor {
 __device__ __forceinline__ int64_t cta_count(const PagedArgs& a, int64_t total) {
   return total < a.grid ? total : a.grid;
 }
-// The CTA that holds a position.
-__device__ __forceinline__ int cta_of(int64_t at, int64_t ctas, int64_t total) {
-  return (int)(((at + 1) * ctas - 1) / total);
+// Notes that this CTA has the first or the last tile of a (sequence, key head).
+__device__ __forceinline__ void note_span(const PagedArgs& a, const Cursor& at, bool begins,
+                                          bool ends) {
+  int* const span = a.span + 2 * ((int64_t)at.b * a.c.heads + at.h);
+  if (begins) span[0] = blockIdx.x;
+  if (ends) span[1] = blockIdx.x;
 }
 
 // The run of tiles of CTA `cta`: its first tile's cursor and the number of tiles (0: none).
@@ -114,9 +158,9 @@ __device__ __forceinline__ int cta_of(int64_t at, int64_t ctas, int64_t total) {
 __device__ __forceinline__ int cta_run(const PagedArgs& a, int cta, int lane, Cursor* cur) {
   // lengths of the first 32 sequences stay in registers, the others are read again
   const int len0 = lane < a.B ? seq_len(a, lane) : 0;
-  int64_t sum = places_of(tiles_of(a, len0));
+  int64_t sum = places_of(a, tiles_of(a, len0));
   for (int b0 = 32; b0 < a.B; b0 += 32)
-    sum += b0 + lane < a.B ? places_of(tiles_of(a, seq_len(a, b0 + lane))) : 0;
+    sum += b0 + lane < a.B ? places_of(a, tiles_of(a, seq_len(a, b0 + lane))) : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const int64_t total = sum * a.c.heads, ctas = cta_count(a, total);
@@ -128,7 +172,7 @@ __device__ __forceinline__ int cta_run(const PagedArgs& a, int cta, int lane, Cu
   bool found[2] = {false, false};
   for (int b0 = 0; b0 < a.B && !(found[0] && found[1]); b0 += 32) {
     const int len = b0 == 0 ? len0 : (b0 + lane < a.B ? seq_len(a, b0 + lane) : 0);
-    const int tiles = tiles_of(a, len), mine = places_of(tiles);
+    const int tiles = tiles_of(a, len), mine = places_of(a, tiles);
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -146,14 +190,14 @@ __device__ __forceinline__ int cta_run(const PagedArgs& a, int cta, int lane, Cu
       const int64_t first = (before + __shfl_sync(0xffffffffu, upto, l) - places) * a.c.heads;
       const int h = (int)((ends[e] - first) / places), pos = (int)((ends[e] - first) % places);
       const int64_t begun = (pairs + __popc(filled & ((1u << l) - 1))) * a.c.heads + h;
-      tiles_before[e] = ends[e] - begun * kBegin - (pos < kBegin ? pos : kBegin);
+      tiles_before[e] = ends[e] - begun * a.begin - (pos < a.begin ? pos : a.begin);
       const int n = __shfl_sync(0xffffffffu, tiles, l), ln = __shfl_sync(0xffffffffu, len, l);
-      if (e == 0) *cur = Cursor{b0 + l, h, pos > kBegin ? pos - kBegin : 0, n, ln};
+      if (e == 0) *cur = Cursor{b0 + l, h, pos > a.begin ? pos - a.begin : 0, n, ln};
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
     pairs += __popc(filled);
   }
-  if (!found[1]) tiles_before[1] = total - pairs * a.c.heads * kBegin;   // the end of the list
+  if (!found[1]) tiles_before[1] = total - pairs * a.c.heads * a.begin;   // the end of the list
   return (int)(tiles_before[1] - tiles_before[0]);
 }
 // Page of token t of sequence b of `len` tokens, or -1: no such token, or a bad table entry.

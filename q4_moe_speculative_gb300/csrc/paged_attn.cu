@@ -3,25 +3,33 @@
 //
 // All query rows of one key head, M = R x heads per key head (row m = r * G + j), read the
 // same keys and values, so they are the M dimension of one problem whose cost is the bytes
-// of the cache. Tokens come in tiles of 64. The tiles of all sequences and key heads form one
-// list that is cut into equal runs, one per CTA: a long sequence is split over many CTAs, a
-// batch of ragged ones is balanced, and no CTA waits for another. A (sequence, head) that
-// lies inside one run is finished there; one that crosses a boundary leaves its running
-// maximum, normaliser and sums per CTA in the workspace, and k_paged_join merges those in
-// CTA order, so results do not depend on timing.
+// of the cache. Tokens come in tiles. The tiles of all sequences and key heads form one list
+// that is cut into equal runs, one per CTA: a long sequence is split over many CTAs, a batch
+// of ragged ones is balanced, and no CTA waits for another. A (sequence, head) that lies
+// inside one run is finished there; one that crosses a boundary leaves its running maximum,
+// normaliser and sums per CTA in the workspace, and k_paged_join merges those in CTA order, so
+// results do not depend on timing.
 //
-// k_paged (4 or 8 warps): tiles are copied by cp.async into a ring of stages (rows swizzled
-// in 16-byte chunks, so that ldmatrix is free of bank conflicts). Per tile, warp w scores
-// tokens 16 w .. 16 w + 15 for its rows (S = Q K^T, mma.sync m16n8k16), P = 2^(S - m) goes
-// to shared memory as bf16, and then warp w accumulates its quarter of the head's values for
-// all 64 tokens (O += P V): a key or value byte is read from shared memory (and an int8 one
-// widened) once per CTA, and the accumulators are a quarter of M x D per warp. Codes of a Q8
-// cache are widened exactly to bf16; the key's scale multiplies the score, the value's scale
-// P. The reference m of a row moves only when a score exceeds it by 2^8 (P stays in range and
-// bf16's relative precision does not depend on it), so the usual tile needs no exchange of
-// maxima and no rescaling: the CTA votes on it at the barrier that publishes P anyway.
-// P is rounded once to bf16, half a step of 2^-8 relative per term; for a bf16 cache the
-// normaliser sums the rounded values, so that the weights add up to one.
+// Three kernels do the runs: paged_few.cu up to 32 rows, k_paged here for more, paged_tc.cu
+// for more rows and long contexts (rules and figures at which()). None of them lets the next
+// kernel start early: waiting CTAs of the join took room from this kernel's and of the next
+// kernel from the join's (16 rows, 8 sequences x 8 heads at 4k, Q8: 32 against 27 us).
+//
+// k_paged (8 warps, one CTA per SM): tiles of 64 tokens are copied by cp.async into a ring of
+// stages (rows swizzled in 16-byte chunks, so that ldmatrix is free of bank conflicts). Per
+// tile, warp w of each group of four scores tokens 16 w .. 16 w + 15 for its group's rows
+// (S = Q K^T, mma.sync m16n8k16), P = 2^(S - m) goes to shared memory as bf16, and then the
+// warp accumulates its quarter of the head's values for all 64 tokens (O += P V): a key or
+// value byte is read from shared memory (and an int8 one widened) once per group, and the
+// accumulators are a quarter of M x D per warp. Codes of a Q8 cache are widened exactly to
+// bf16; the key's scale multiplies the score, the value's scale P. The reference m of a row
+// moves only when a score exceeds it by 2^8 (P stays in range and bf16's relative precision
+// does not depend on it), so the usual tile needs no exchange of maxima and no rescaling: the
+// CTA votes on it at the barrier that publishes P anyway. P is rounded once to bf16, half a
+// step of 2^-8 relative per term, and the normaliser sums the rounded values, so that the
+// weights add up to one; with a Q8 cache, where the value's scale is part of P, P goes in as a
+// high and a low part instead. Its bound is the issue of instructions: 4 sequences x 8 heads
+// of 8k tokens, 64 rows, 52 us for 132 MB of bf16 and 58 us for 68 MB of Q8.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -33,70 +41,28 @@ using namespace paged;
 
 constexpr int kTile = 64;
 
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x2_t(uint32_t addr, uint32_t& r0, uint32_t& r1) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-               : "=r"(r0), "=r"(r1)
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Byte offset of 16-byte chunk c of row r in a tile of rows of RB bytes: the eight rows of
-// an ldmatrix meet eight different bank groups.
-template <int RB>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  if constexpr (RB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  return r * RB + ((c ^ (r & 7)) << 4);
-}
-
-// Shapes of one instantiation: MT m16 tiles of rows per warp, MH groups of four warps.
-template <int D, bool kQ8, int MT, int MH>
+// Shapes of one instantiation: MT m16 tiles of rows per warp, two groups of four warps.
+template <int D, bool kQ8, int MT>
 struct Shape {
-  static constexpr int kThreads = 128 * MH;
-  static constexpr int kRows = 16 * MT * MH;
+  static constexpr int kThreads = 256;
+  static constexpr int kRows = 32 * MT;
   static constexpr int RB = D * (kQ8 ? 1 : 2);          // bytes of a cached row
   static constexpr int kMat = kTile * RB;
   static constexpr int kStage = 2 * kMat + (kQ8 ? 2 * kTile * 4 : 0);
-  static constexpr bool kSplit = kQ8 || kRows <= 32;    // P as a high and a low part
+  static constexpr bool kSplit = kQ8;                   // P as a high and a low part
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kP = kRows * kTile * 2;
   static constexpr int kRed = 4 * kRows * 4;
   static constexpr int kFixed = kQ + kP * (kSplit ? 2 : 1) + kRed + 64;
-  // CTAs per SM: as many as the registers allow (65,536 over the threads at 128, 168 or 255
-  // each) with at least two stages each
-  static constexpr int kWant = MH == 2 ? 1 : (MT == 1 ? 4 : 3);
-  static constexpr int room(int n) { return 228 * 1024 / n - 1024; }
-  static constexpr int fit(int n) {
-    return n > 1 && kFixed + 2 * kStage > room(n) ? fit(n - 1) : n;
-  }
-  static constexpr int kPerSm = fit(kWant);
-  static constexpr int kFit = (room(kPerSm) - kFixed) / kStage;
+  static constexpr int kFit = (227 * 1024 - kFixed) / kStage;
   static constexpr int kStages = kFit > 5 ? 5 : kFit;
   static constexpr int kSmem = kFixed + kStages * kStage;
   static_assert(kStages >= 2 && kStages <= 8, "a ring of two to eight stages");
 };
 
-template <int D, bool kQ8, int MT, int MH>
-__global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
-    k_paged(const __grid_constant__ PagedArgs a) {
-  using C = Shape<D, kQ8, MT, MH>;
+template <int D, bool kQ8, int MT>
+__global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedArgs a) {
+  using C = Shape<D, kQ8, MT>;
   constexpr int RB = C::RB, S = C::kStages, NT = D / 32;
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* sQ = sm + S * C::kStage;
@@ -106,7 +72,6 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w4 = warp & 3, row0 = (warp >> 2) * MT * 16;
   const int g = lane >> 2, q = lane & 3;
-  pdl_trigger();
   pdl_wait();
 
   if (blockIdx.x == 0 && tid == 0) *a.status = 0u;
@@ -509,6 +474,7 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
       const bool whole = whole_end && cur.tile == run;
       // slot 0: the run began before this CTA; slot 1: it begins here and goes on in the next
       const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.tile == run ? 1 : 0);
+      if (tid == 0) note_span(a, cur, cur.tile == run, whole_end);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -560,26 +526,36 @@ __global__ void __launch_bounds__(128 * MH, (Shape<D, kQ8, MT, MH>::kPerSm))
 }
 
 // k_paged_join: block x = (sequence, key head). Those that crossed a CTA boundary are merged
-// in CTA order; empty sequences get zeros; the others are already written. kShared: all 32
-// warps on one row (a head is cut into many pieces), else a row for each of 8 warps.
-constexpr int kJoinWarps = 32;
-// (top, norm, acc) += (m, l, x): sums relative to 2^reference.
-template <int V>
-__device__ __forceinline__ void merge(float& top, float& norm, float (&acc)[V], float m, float l,
-                                      const float (&x)[V]) {
-  const float now = fmaxf(top, m);
-  const float f = top == kNegInf ? 0.f : exp2_fast(__fsub_rn(top, now));
-  const float g = m == kNegInf ? 0.f : exp2_fast(__fsub_rn(m, now));
-  top = now;
-  norm = __fmaf_rn(l, g, __fmul_rn(norm, f));
+// in CTA order; empty sequences get zeros; the others are already written. kWarps: the warps
+// that share a row (a head is cut into many pieces); with 1, a row for each of 8 warps. Its
+// time is latency, so pieces are read several at a time (one after the other: 41 against 32 us
+// for the whole call of 16 rows, 8 sequences x 8 heads at 4k). One head of 64 pieces or fewer
+// takes 8 warps: 24 rows, 8 heads of 38 pieces, 16 us for the call against 19 with 32.
+// (top, norm, acc) += the N (m, l, x), in order: sums relative to 2^reference.
+template <int V, int N>
+__device__ __forceinline__ void merge(float& top, float& norm, float (&acc)[V],
+                                      const float2 (&ml)[N], const float (&x)[N][V]) {
+  float now = top;
 #pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = __fmaf_rn(x[e], g, __fmul_rn(acc[e], f));
+  for (int j = 0; j < N; ++j) now = fmaxf(now, ml[j].x);
+  const float f = top == kNegInf ? 0.f : exp2_fast(__fsub_rn(top, now));
+  top = now;
+  norm = __fmul_rn(norm, f);
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = __fmul_rn(acc[e], f);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float g = ml[j].x == kNegInf ? 0.f : exp2_fast(__fsub_rn(ml[j].x, now));
+    norm = __fmaf_rn(ml[j].y, g, norm);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = __fmaf_rn(x[j][e], g, acc[e]);
+  }
 }
-template <int D, bool kShared>
-__global__ void __launch_bounds__(32 * (kShared ? kJoinWarps : 8))
+template <int D, int kWarps>
+__global__ void __launch_bounds__(kWarps == 1 ? 256 : 32 * kWarps)
     k_paged_join(const __grid_constant__ PagedArgs a) {
   constexpr int V = D / 32;   // values per lane
-  constexpr int kWarps = kShared ? kJoinWarps : 1;
+  constexpr bool kShared = kWarps > 1;
   __shared__ float acc_s[kWarps][D];
   __shared__ float2 l_s[kWarps];   // reference, normaliser
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -587,46 +563,39 @@ __global__ void __launch_bounds__(32 * (kShared ? kJoinWarps : 8))
   pdl_trigger();
   pdl_wait();
   const int row = kShared ? blockIdx.y : blockIdx.y * 8 + warp;
-  const int n = tiles_of(a, seq_len(a, b));
-  int64_t before = 0, total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int p = b0 + lane < a.B ? places_of(tiles_of(a, seq_len(a, b0 + lane))) : 0;
-    total += p;
-    before += b0 + lane < b ? p : 0;
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, x);
-    before += __shfl_xor_sync(0xffffffffu, before, x);
-  }
-  total *= a.c.heads;
-  int c0 = 0, c1 = -1;   // CTAs that hold a piece
-  if (n) {
-    const int64_t first = before * a.c.heads + (int64_t)h * places_of(n) + kBegin;
-    const int64_t ctas = cta_count(a, total);
-    c0 = cta_of(first, ctas, total);
-    c1 = cta_of(first + n - 1, ctas, total);
-    if (c0 == c1) return;
-  }
+  const int2 span = __ldcg(reinterpret_cast<const int2*>(a.span) + blockIdx.x);
+  const bool empty = seq_len(a, b) == 0;
+  const int c0 = empty ? 0 : span.x, c1 = empty ? -1 : span.y;
+  // (in one CTA: already written; not noted: the kernel gave up, and the status says so)
+  if (!empty && (c0 < 0 || c1 <= c0 || c1 >= a.grid)) return;
   if (row >= a.M) return;   // (all warps of the block, when they share the row)
   auto piece = [&](int c) { return (2 * (int64_t)c + (c == c0 ? 1 : 0)) * a.M + row; };
-  // a warp's pieces, the reference moving up as it goes
+  // a warp's pieces, as many at a time as keep memory's latency down, the reference moving up
+  constexpr int kAt = kWarps == 32 ? 5 : 8;
   float top = kNegInf, acc[V], norm = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 8
-  for (int c = c0 + (kShared ? warp : 0); c <= c1; c += kWarps) {
-    const int64_t at = piece(c);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
-    float x[V];
-    if constexpr (V == 4) {
-      const float4 f4 = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
-      x[0] = f4.x, x[1] = f4.y, x[2] = f4.z, x[3] = f4.w;
-    } else {
-      const float2 f2 = __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D) + lane);
-      x[0] = f2.x, x[1] = f2.y;
+  for (int first = c0 + (kShared ? warp : 0); first <= c1; first += kAt * kWarps) {
+    float2 ml[kAt];
+    float x[kAt][V];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const int c = first + j * kWarps;
+      ml[j] = make_float2(kNegInf, 0.f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[j][e] = 0.f;
+      if (c > c1) continue;
+      const int64_t at = (2 * (int64_t)c + (c == c0 ? 1 : 0)) * a.M + row;
+      ml[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
+      if constexpr (V == 4) {
+        const float4 f4 = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
+        x[j][0] = f4.x, x[j][1] = f4.y, x[j][2] = f4.z, x[j][3] = f4.w;
+      } else {
+        const float2 f2 = __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D) + lane);
+        x[j][0] = f2.x, x[j][1] = f2.y;
+      }
     }
-    merge<V>(top, norm, acc, ml.x, ml.y, x);
+    merge<V, kAt>(top, norm, acc, ml, x);
   }
   if constexpr (kShared) {
 #pragma unroll
@@ -634,12 +603,16 @@ __global__ void __launch_bounds__(32 * (kShared ? kJoinWarps : 8))
     if (lane == 0) l_s[warp] = make_float2(top, norm);
     __syncthreads();
     if (warp) return;
-#pragma unroll 8
-    for (int w = 1; w < kWarps; ++w) {
-      float x[V];
+    for (int w = 1; w < kWarps; w += kAt) {
+      float2 ml[kAt];
+      float x[kAt][V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) x[e] = acc_s[w][V * lane + e];
-      merge<V>(top, norm, acc, l_s[w].x, l_s[w].y, x);
+      for (int j = 0; j < kAt; ++j) {
+        ml[j] = w + j < kWarps ? l_s[w + j] : make_float2(kNegInf, 0.f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[j][e] = w + j < kWarps ? acc_s[w + j][V * lane + e] : 0.f;
+      }
+      merge<V, kAt>(top, norm, acc, ml, x);
     }
   }
   uint16_t* dst = a.out + (((int64_t)b * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * D + V * lane;
@@ -653,58 +626,66 @@ __global__ void __launch_bounds__(32 * (kShared ? kJoinWarps : 8))
 }
 
 // ------------------------------------------------------------------------------- host ----
+enum class Kernel { kFew, kRows, kTensor };
+
 struct Plan {
-  bool tc;
+  Kernel kernel;
   int grid;
-  size_t ml, po, total;
+  size_t span, ml, po, total;
 };
 
-// Calls f with the instantiation for these rows: m16 tiles per warp x warp groups.
-template <int D, bool kQ8, typename F>
+// Calls f with the m16 tiles per warp for these rows.
+template <typename F>
 auto with_rows(int M, F&& f) {
-  if (M <= 16) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-  if (M <= 32) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
-  if (M <= 64) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
-  if (M <= 96) return f(std::integral_constant<int, 3>{}, std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  if (M <= 64) return f(std::integral_constant<int, 2>{});
+  if (M <= 96) return f(std::integral_constant<int, 3>{});
+  return f(std::integral_constant<int, 4>{});
 }
 
-// The tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and end. Up to
-// 32 rows this file's kernel is as fast at any length (6 rows x 4 heads, 32 sequences of up to
-// 8k, bf16 121 against 154 us, Q8 109 against 108); with more, the other one is ahead from
-// several tiles per SM on: 6 x 16 rows at 300k tokens 59 against 73 us, 4 sequences x 8 heads
-// at 64k bf16 247 against 405 us, Q8 (64 rows) 242 against 342 us, but at 500 tokens of one
-// head 29 against 13 us. `places`: tokens x key heads there can be (lengths are not known here).
-bool use_tc(int M, bool q8, int64_t places) {
-  return M > 32 && M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) &&
-         places >= (int64_t)(q8 ? 3 : 8) * 128 * device_sm_count();
+// Up to 32 rows: paged_few.cu, which costs no more for 1 row than it has to (24 rows, 32
+// sequences x 8 heads at 8k, bf16 169 us, Q8 165; k_paged's design with 16-row tiles: 207, 186).
+// More rows: the tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and
+// end, and is ahead from several tiles per SM on. k_paged against it, 4 sequences x 8 heads:
+// bf16, 64 rows, 32 against 38 us at 4k tokens, 52 against 51 at 8k, 171 against 130 at 32k; 96
+// rows 38 against 42, 63 against 56, 209 against 135; one head of 64k 24 against 32. Q8, 64
+// rows: 22 against 24 us at 2k, 34 against 30 at 4k, 201 against 127 at 32k; one head of 32k 16
+// against 17, of 64k 21 against 21. `places`: tokens x key heads there can be (lengths are not
+// known here).
+Kernel which(int M, bool q8, int64_t places) {
+  if (M <= kFewMaxRows) return Kernel::kFew;
+  return M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) &&
+                 places >= (int64_t)(q8 ? 4 : 10) * 128 * device_sm_count()
+             ? Kernel::kTensor
+             : Kernel::kRows;
 }
 
-template <int D, bool kQ8>
+// What a (sequence, key head) costs beside its tiles, in tiles (24 rows, 32 sequences of up to
+// 8k tokens, 8 heads, Q8: 99 us with 2 in paged_few.cu, 95 with 3, 97 with 6).
+int begin_of(Kernel k) { return k == Kernel::kFew ? 3 : 2; }
+
 Plan make_plan(const PagedAttnProblem& p) {
   const int M = p.R * (p.Hq / p.cache.heads);
   Plan pl{};
   const int64_t cap = (int64_t)p.max_pages << p.cache.page_shift;
   const int64_t runs = (int64_t)p.B * p.cache.heads;
-  pl.tc = use_tc(M, kQ8, runs * cap);
-  const int per_sm = pl.tc ? 1 : with_rows<D, kQ8>(M, [](auto mt, auto mh) {
-    return Shape<D, kQ8, decltype(mt)::value, decltype(mh)::value>::kPerSm;
-  });
+  pl.kernel = which(M, p.cache.q8, runs * cap);
+  const int per_sm = pl.kernel == Kernel::kFew ? few_ctas_per_sm(M, p.D, p.cache.q8) : 1;
   // no more CTAs than positions in the list of tiles there can be
-  const int tile = pl.tc ? 128 : kTile;
-  const int64_t most = runs * ((cap + tile - 1) / tile + kBegin);
+  const int tile = pl.kernel == Kernel::kTensor ? 128 : kTile;
+  const int64_t most = runs * ((cap + tile - 1) / tile + begin_of(pl.kernel));
   const int64_t all = (int64_t)per_sm * device_sm_count();
   pl.grid = (int)(most < all ? most : all);
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-  pl.ml = 256;   // behind the status word
+  pl.span = 256;   // behind the status word
+  pl.ml = pl.span + up((size_t)runs * 2 * sizeof(int));
   pl.po = pl.ml + up((size_t)2 * pl.grid * M * 2 * sizeof(float));
-  pl.total = pl.po + up((size_t)2 * pl.grid * M * D * sizeof(float));
+  pl.total = pl.po + up((size_t)2 * pl.grid * M * p.D * sizeof(float));
   return pl;
 }
 
 template <int D, bool kQ8>
 cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
-  const Plan pl = make_plan<D, kQ8>(p);
+  const Plan pl = make_plan(p);
   PagedArgs a{};
   a.B = p.B;
   a.R = p.R;
@@ -712,7 +693,8 @@ cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   a.G = p.Hq / p.cache.heads;
   a.M = p.R * a.G;
   a.max_pages = p.max_pages;
-  a.tile_log = pl.tc ? 7 : 6;
+  a.tile_log = pl.kernel == Kernel::kTensor ? 7 : 6;
+  a.begin = begin_of(pl.kernel);
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   a.q = p.q;
   a.c = p.cache;
@@ -720,16 +702,19 @@ cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   a.lengths = p.lengths;
   a.out = p.out;
   a.status = reinterpret_cast<uint32_t*>(ws);
+  a.span = reinterpret_cast<int*>(ws + pl.span);
   a.part_ml = reinterpret_cast<float*>(ws + pl.ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.po);
   a.grid = pl.grid;
   cudaError_t err;
-  if (pl.tc) {
+  if (pl.kernel == Kernel::kFew) {
+    err = launch_few(a, D, s);
+  } else if (pl.kernel == Kernel::kTensor) {
     err = launch_tc(a, D, s);
   } else {
-    err = with_rows<D, kQ8>(a.M, [&](auto mt, auto mh) {
-      using C = Shape<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
-      const auto kernel = k_paged<D, kQ8, decltype(mt)::value, decltype(mh)::value>;
+    err = with_rows(a.M, [&](auto mt) {
+      using C = Shape<D, kQ8, decltype(mt)::value>;
+      const auto kernel = k_paged<D, kQ8, decltype(mt)::value>;
       static OncePerDevice ready;
       const cudaError_t e = ready.run([&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -740,17 +725,15 @@ cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   }
   if (err != cudaSuccess) return err;
   const int heads = p.B * p.cache.heads;
-  if (pl.grid > 8 * heads)   // many pieces per head
-    return launch_pdl(k_paged_join<D, true>, dim3(heads, a.M), 32 * kJoinWarps, 0, s, a);
-  return launch_pdl(k_paged_join<D, false>, dim3(heads, (a.M + 7) / 8), 256, 0, s, a);
+  if (pl.grid > 64 * heads)   // pieces per head
+    return launch_pdl(k_paged_join<D, 32>, dim3(heads, a.M), 1024, 0, s, a);
+  if (pl.grid > 8 * heads) return launch_pdl(k_paged_join<D, 8>, dim3(heads, a.M), 256, 0, s, a);
+  return launch_pdl(k_paged_join<D, 1>, dim3(heads, (a.M + 7) / 8), 256, 0, s, a);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(const PagedAttnProblem& p) {
-  if (p.D == 128) return (p.cache.q8 ? make_plan<128, true>(p) : make_plan<128, false>(p)).total;
-  return (p.cache.q8 ? make_plan<64, true>(p) : make_plan<64, false>(p)).total;
-}
+size_t paged_attn_workspace(const PagedAttnProblem& p) { return make_plan(p).total; }
 
 cudaError_t launch_paged_attn(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   if (p.D == 128) return p.cache.q8 ? run<128, true>(p, ws, s) : run<128, false>(p, ws, s);
