@@ -643,7 +643,7 @@ auto with_rows(int M, F&& f) {
 }
 
 // Up to 32 rows: paged_few.cu, which costs no more for 1 row than it has to (24 rows, 32
-// sequences x 8 heads at 8k, bf16 169 us, Q8 165; k_paged's design with 16-row tiles: 207, 186).
+// sequences x 8 heads at 8k, bf16 169 us, Q8 158; k_paged's design with 16-row tiles: 207, 186).
 // More rows: the tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and
 // end, and is ahead from several tiles per SM on. k_paged against it, 4 sequences x 8 heads:
 // bf16, 64 rows, 32 against 38 us at 4k tokens, 52 against 51 at 8k, 171 against 130 at 32k; 96

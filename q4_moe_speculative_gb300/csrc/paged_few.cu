@@ -16,7 +16,7 @@
 // reference of a row moves only when a score exceeds it by 2^8.
 //
 // Measured on 32 sequences x 8 heads of 8k tokens, D = 128: bf16 (1.05 GB) 160 us for 1 to 8
-// rows, 6.6 TB/s, bound by memory, and 177 us for 32 rows; Q8 (0.54 GB) 101, 125, 165 and 195 us
+// rows, 6.6 TB/s, bound by memory, and 177 us for 32 rows; Q8 (0.54 GB) 102, 127, 158 and 196 us
 // for 8, 16, 24 and 32 rows, bound by the issue of instructions (700 per 16 tokens and warp at 16
 // rows, of which 224 widen codes and 48 are products). A single head of 500 tokens: 6.3 us, of
 // which launching the two kernels is most.
@@ -45,6 +45,9 @@ struct Few {
   static constexpr int kMat = kTok * RB;
   static constexpr int kStage = 2 * kMat + (kQ8 ? 2 * kTok * 4 : 0);
   static constexpr int kPart = kQ8 || NT <= 2 ? D : 64;   // values that are added up at a time
+  // The next queries wait in registers while results are added up, where the loop has the
+  // registers for it: Q8, 24 rows 158 against 163 us, but 32 rows 222 against 196.
+  static constexpr bool kHold = NT % 2 == 1;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSum = kRows * kPart * 4;
   static constexpr int kStat = kWarps * kRows * 4;
@@ -435,6 +438,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Few<D, kQ8, NT>::kPerSm))
       if (i + 1 < n) {
         cur.next(a);
         load_queries(cur);
+        if (!C::kHold) store_queries();
       }
       auto top_of = [&](int row) {
         return fmaxf(fmaxf(top_s[row], top_s[C::kRows + row]),
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Few<D, kQ8, NT>::kPerSm))
               }
           __syncthreads();
         }
-        if (part == 0) store_queries();
+        if (C::kHold && part == 0) store_queries();
         for (int idx = tid; idx < a.M * (C::kPart / 2); idx += 32 * kWarps) {
           const int row = idx / (C::kPart / 2), d = 2 * (idx % (C::kPart / 2));
           const int p0 = kQ8 ? (d & ~15) + (d & 15) / 2 : d, p1 = kQ8 ? p0 + 8 : d + 1;

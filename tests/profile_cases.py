@@ -5,6 +5,11 @@
     python tests/profile_cases.py q8       # paired Q8 projection, 16384 x 4096, R 6
     python tests/profile_cases.py attn     # sparse attention, 43 layers x 6 rows x 512 blocks
     python tests/profile_cases.py accept   # acceptance, 8 steps x 6 rows x 129,280 tokens
+    python tests/profile_cases.py paged_few   # paged attention, 8 x 6 rows x 32/8 heads, 16k, Q8
+    python tests/profile_cases.py paged_long  # paged attention, 1 x 6 rows x 16/1 heads, 300k, bf16
+    python tests/profile_cases.py rows     # norms and rotation of 16,384 tokens x 32 + 8 heads,
+                                           # then a Q8 cache's write and read of 32,768 x 8 heads
+    python tests/profile_cases.py q4       # Q4 projection, 129,280 x 4096, R 6
 
 Each case holds a few GB on the device at most, with weights / keys larger than L2, and
 runs its call `--reps` times (default 4) on synthetic inputs, then checks the workspace
@@ -66,6 +71,45 @@ def run(case: str, reps: int) -> None:
         for _ in range(reps):
             dsm.verify_greedy(t["logits"], t["draft"])
             dsm.verify_sample(t["logits"], 1.0, t["qd"], t["draft"], t["u_acc"], t["u_res"])
+    elif case in ("paged_few", "paged_long"):
+        B, R, Hq, Hkv, n, q8 = (8, 6, 32, 8, 16000, True) if case == "paged_few" else (
+            1, 6, 16, 1, 300000, False)
+        pages = -(-n // 64)
+        cache = dsm.PagedCache.zeros(B * pages, Hkv, 64, 128, q8=q8, device=dev)
+        rows = B * pages * 64
+        for at in range(0, rows, 1 << 16):   # keys and values by the cache's own write
+            slots = torch.arange(at, min(at + (1 << 16), rows), dtype=torch.int32, device=dev)
+            dsm.cache_write(cache, *(torch.randn(len(slots), Hkv, 128, device=dev).bfloat16()
+                                     for _ in range(2)), slots)
+        table = torch.randperm(B * pages, device=dev).to(torch.int32).reshape(B, pages)
+        lengths = torch.full((B,), n, dtype=torch.int32, device=dev)
+        q = torch.randn(B, R, Hq, 128, device=dev).bfloat16()
+        ws = torch.zeros(1 << 26, dtype=torch.uint8, device=dev)
+        for _ in range(reps):
+            dsm.paged_attention(q, cache, table, lengths, workspace=ws)
+    elif case == "rows":
+        T = 16384
+        q, k = (torch.randn(T, h, 128, device=dev).bfloat16() for h in (32, 8))
+        w = torch.ones(128, dtype=torch.bfloat16, device=dev)
+        pos = torch.arange(T, dtype=torch.int32, device=dev)
+        freqs = dsm.rope_frequencies(128, device=dev)
+        cache = dsm.PagedCache.zeros(512, 8, 64, 128, q8=True, device=dev)
+        kv = torch.randn(2, 2 * T, 8, 128, device=dev).bfloat16()
+        slots = torch.randperm(2 * T, device=dev).to(torch.int32)
+        ws = None
+        for _ in range(reps):
+            dsm.qk_norm_rope(q, k, pos, freqs, q_weight=w, k_weight=w)
+            dsm.cache_write(cache, kv[0], kv[1], slots)
+            dsm.cache_read(cache, slots)
+    elif case == "q4":
+        rows, K = 129280, 4096
+        tiles = dsm.q4_tile(
+            torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device=dev),
+            (torch.rand(rows, K // 32, device=dev) * 0.01).half())
+        x = synth.activations(6, K, seed=2, device=dev)
+        ws = None
+        for _ in range(reps):
+            dsm.q4_project(tiles, x)
     else:
         raise SystemExit(f"unknown case {case}")
     torch.cuda.synchronize()
