@@ -88,7 +88,7 @@ def test_every_count_of_rows(M, D, q8):
         check(*problem([150, 65], R, M // R, 1, D, 32, q8, seed=M, wide=True))
 
 
-@pytest.mark.parametrize("Hq,wide", [(4, False), (10, True)])
+@pytest.mark.parametrize("Hq,wide", [(4, False), (8, False), (10, False), (10, True)])
 @pytest.mark.parametrize("q8", [False, True])
 def test_peaked_and_rising_scores(q8, Hq, wide):
     # scores of hundreds, growing along the length: the reference of every row moves again
@@ -116,7 +116,7 @@ def test_scale_argument():
         check(*p, scale=scale)
 
 
-@pytest.mark.parametrize("Hq,wide", [(4, False), (20, True)])
+@pytest.mark.parametrize("Hq,wide", [(4, False), (16, False), (20, False), (20, True)])
 @pytest.mark.parametrize("q8", [False, True])
 def test_what_is_not_visible_does_not_matter(q8, Hq, wide):
     # everything behind the lengths, in other pages, and in new tokens that a row does not
@@ -151,7 +151,7 @@ def test_what_is_not_visible_does_not_matter(q8, Hq, wide):
         assert bool(torch.isfinite(one).all())
 
 
-@pytest.mark.parametrize("Hq,wide", [(4, False), (40, True)])
+@pytest.mark.parametrize("Hq,wide", [(4, False), (40, False), (40, True)])
 @pytest.mark.parametrize("q8", [False, True])
 def test_bad_pages_are_skipped(q8, Hq, wide):
     page = 16
@@ -161,7 +161,7 @@ def test_bad_pages_are_skipped(q8, Hq, wide):
     assert bool((out[2] == 0).all())
 
 
-@pytest.mark.parametrize("Hq,wide", [(2, False), (40, True)])
+@pytest.mark.parametrize("Hq,wide", [(2, False), (40, False), (40, True)])
 def test_lengths_are_clamped(Hq, wide):
     q, cache, table, lengths = problem([64, 64], 1, Hq, 1, 64, 16, True, seed=10, wide=wide)
     want = dsm.paged_attention(q, cache, table, lengths)
@@ -170,7 +170,7 @@ def test_lengths_are_clamped(Hq, wide):
     assert torch.equal(out[0], want[0]) and bool((out[1] == 0).all())
 
 
-@pytest.mark.parametrize("Hq,wide", [(8, False), (32, True)])
+@pytest.mark.parametrize("Hq,wide", [(8, False), (32, False), (32, True)])
 def test_shared_pages_and_repeated_rows(Hq, wide):
     # two sequences on the same pages give the same bytes, and so do two calls
     q, cache, table, lengths = problem([900, 900], 2, Hq, 1, 128, 32, True, seed=11, wide=wide)
@@ -188,13 +188,13 @@ def test_no_sequences():
     assert out.shape == (0, 1, 2, 64)
 
 
-@pytest.mark.parametrize("Hq", [5, 20])
+@pytest.mark.parametrize("Hq", [1, 5, 10, 20, 40])
 @pytest.mark.parametrize("q8", [False, True])
 def test_a_long_context_over_every_cta(q8, Hq):
     # 70,000 tokens of one head: pieces on every CTA, joined; against fp64 on the device
     n, page = 70_001, 64
     q, cache, table, lengths = problem([n], 3, Hq, 1, 128, page, q8, seed=12, sigma=2.0,
-                                       wide=Hq > 5)
+                                       wide=Hq in (20, 40))
     out = dsm.paged_attention(q, cache, table, lengths)
     t = torch.arange(n, device=DEV)
     slots = table[0].long()[t // page] * page + t % page
@@ -317,14 +317,37 @@ def test_two_streams_at_once(Hq, q8):
             assert torch.equal(o, want)
 
 
-def test_given_workspace_and_output():
-    q, cache, table, lengths = problem([2000], 6, 8, 1, 128, 64, False, seed=44)
+@pytest.mark.parametrize("Hq,lens,wide", [(8, [2000], False), (8, [2000], True), (3, [2000], False),
+                                          (4, [700, 90, 333] * 4, False)])
+def test_given_workspace_and_output(Hq, lens, wide):
+    # whatever the workspace holds
+    q, cache, table, lengths = problem(lens, 6, Hq, 1, 128, 64, False, seed=44, wide=wide)
     want = dsm.paged_attention(q, cache, table, lengths)
     out = torch.empty_like(q)
-    ws = torch.full((64 << 20,), 0xA5, dtype=torch.uint8, device=DEV)
-    assert dsm.paged_attention(q, cache, table, lengths, out=out, workspace=ws) is out
-    assert torch.equal(out, want)
-    assert dsm.workspace_status(ws) == 0
+    for fill in (0xA5, 0x00, 0x01, 0xFF):
+        ws = torch.full((64 << 20,), fill, dtype=torch.uint8, device=DEV)
+        assert dsm.paged_attention(q, cache, table, lengths, out=out, workspace=ws) is out
+        assert torch.equal(out, want)
+        assert dsm.workspace_status(ws) == 0
     with pytest.raises(dsm.DsmoeError) as e:
         dsm.paged_attention(q, cache, table, lengths, workspace=ws[:256])
     assert e.value.status == 3
+
+
+@pytest.mark.parametrize("Hq,q8,wide", [(3, True, False), (4, False, False), (10, False, False),
+                                        (10, True, True)])
+def test_replays_with_other_lengths(Hq, q8, wide):
+    # one captured call (the first of its sizes in this process or not) whose lengths, table and
+    # queries change between replays; the workspace keeps what the longer calls left in it
+    q, cache, table, lengths = problem([900, 130, 64, 700], 4, Hq, 1, 64, 32, q8, seed=21,
+                                       wide=wide)
+    out = torch.empty_like(q)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dsm.paged_attention(q, cache, table, lengths, out=out, workspace=ws)
+    for lens in ([900, 130, 64, 700], [1, 0, 64, 3], [0, 0, 0, 0], [64, 130, 2, 512], [900, 130, 0, 1]):
+        lengths.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.copy_(q.flip(0))
+        g.replay()
+        check(q, cache, table, lengths, got=out)
