@@ -12,7 +12,9 @@
 // a 64-bit integer product that wraps, exact at any position, of which the upper 32 bits go
 // to sincospif. Each lane computes the angles of its own 8 values once per token, times the
 // weights, and keeps them in registers over the heads of its chunk. Memory-bound by bytes,
-// by instruction issue in practice: fp32 arithmetic is done two values at a time (f32x2).
+// by instruction issue in practice (59 to 68% of the slots): fp32 arithmetic is done two values
+// at a time (f32x2). 16,384 tokens x 20 heads of 128, rotated: 31.8 us, 5.3 TB/s; 32,768 tokens x
+// 8 heads into a Q8 cache: 45 us, 4.5 TB/s.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -148,10 +150,12 @@ __device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
 
 // kCache: 0 keys to k_out, 1 keys and values to a bf16 cache, 2 to a Q8 cache.
 // kTurn: 0 rows are stored as they are; norms and rotation of halves (1) or neighbours (2).
-template <int D, int kCache, int kTurn>
-__global__ void __launch_bounds__(kThreads, kTurn && kCache == 2 ? 2 : 4) k_rows(const __grid_constant__ RowsArgs a) {
+// kPerSm: CTAs per SM the registers are limited for.
+template <int D, int kCache, int kTurn, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm)
+    k_rows(const __grid_constant__ RowsArgs a) {
   constexpr int LPH = D / 8, kTokens = 32 / LPH;   // lanes per row, tokens per warp
-  constexpr int kBatch = 4;                        // rows whose loads are in flight together
+  constexpr int kBatch = 4;   // rows whose loads are in flight together (2: the write above 52 us)
   pdl_trigger();
   pdl_wait();
   const RowsProblem& p = a.p;
@@ -311,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, kTurn && kCache == 2 ? 2 : 4) k_rows
          });
 }
 
-// k_cache_read: one thread per 8 values of a (token, head), keys and values.
+// k_cache_read: one thread per 8 values of a (token, head), keys and values. Bound by memory's
+// latency over scattered rows: 32,768 tokens x 8 heads from a Q8 cache 33 us, 6.1 TB/s.
 template <int D, bool kQ8>
 __global__ void __launch_bounds__(kThreads) k_cache_read(const CacheView c, const int32_t* slots,
                                                          int n, uint16_t* k_out,
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const CacheView c, cons
   reinterpret_cast<uint4*>(v_out)[i] = v;
 }
 
-template <int D, int kCache, int kTurn>
+template <int D, int kCache, int kTurn, int kPerSm>
 cudaError_t start_rows(const RowsProblem& p, const CacheView* c, cudaStream_t s) {
   constexpr int kTokens = 256 / D;
   RowsArgs a{};
@@ -359,28 +364,41 @@ cudaError_t start_rows(const RowsProblem& p, const CacheView* c, cudaStream_t s)
   if (c) a.c = *c;
   const int heads = p.Hq + (c ? 2 : 1) * p.Hkv;
   a.groups = (p.T + kTokens - 1) / kTokens;
-  // Few tokens: a head per warp, so that the call is one short wave. Many: a token's heads
-  // share its angles, as long as every SM keeps its warps busy.
-  const int64_t warps = (int64_t)device_sm_count() * 64;
-  int64_t chunks = (warps + a.groups - 1) / a.groups;
-  chunks = chunks > heads ? heads : chunks;
-  a.per_chunk = (int)((heads + chunks - 1) / chunks);
+  // A token's heads go to one warp after another in chunks. Long chunks share the angles (which
+  // cost about as much as 6 heads), short ones keep every SM's warps busy: the fewest steps over
+  // the waves of resident warps. (384 tokens x 40 heads, a wave of warps at all costs: 8.8 us,
+  // this 5.0; 2048 tokens 14.7 and 10.8.)
+  const int64_t resident = (int64_t)device_sm_count() * kPerSm * (kThreads / 32);
+  constexpr int kAngles = kTurn ? 6 : 1;
+  int64_t best = INT64_MAX;
+  for (int chunks = 1; chunks <= heads; chunks += (chunks + 3) / 4) {
+    const int per = (heads + chunks - 1) / chunks;
+    const int64_t warps = (int64_t)a.groups * ((heads + per - 1) / per);
+    const int64_t cost = (warps + resident - 1) / resident * (per + kAngles);
+    if (cost < best) best = cost, a.per_chunk = per;
+  }
   a.chunks = (heads + a.per_chunk - 1) / a.per_chunk;
   const int64_t grid = ((int64_t)a.groups * a.chunks + kThreads / 32 - 1) / (kThreads / 32);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(k_rows<D, kCache, kTurn>, dim3((unsigned)grid), kThreads, 0, s, a);
+  return launch_pdl(k_rows<D, kCache, kTurn, kPerSm>, dim3((unsigned)grid), kThreads, 0, s, a);
 }
 
-template <int D, int kCache>
+template <int D, int kCache, int kPerSm>
 cudaError_t pick_turn(const RowsProblem& p, const CacheView* c, cudaStream_t s) {
-  return p.interleaved ? start_rows<D, kCache, 2>(p, c, s) : start_rows<D, kCache, 1>(p, c, s);
+  return p.interleaved ? start_rows<D, kCache, 2, kPerSm>(p, c, s)
+                       : start_rows<D, kCache, 1, kPerSm>(p, c, s);
 }
 
 template <int D>
 cudaError_t pick_rows(const RowsProblem& p, const CacheView* c, cudaStream_t s) {
-  if (p.Hq == 0) return c->q8 ? start_rows<D, 2, 0>(p, c, s) : start_rows<D, 1, 0>(p, c, s);
-  if (!c) return pick_turn<D, 0>(p, c, s);
-  return c->q8 ? pick_turn<D, 2>(p, c, s) : pick_turn<D, 1>(p, c, s);
+  if (p.Hq == 0) return c->q8 ? start_rows<D, 2, 0, 4>(p, c, s) : start_rows<D, 1, 0, 4>(p, c, s);
+  // CTAs per SM: four have 64 registers a thread. Into a Q8 cache that is too few (8192 tokens x
+  // 48 heads 58.6 us, with four 60.1, with two 62.0); without a cache three are faster while all
+  // tokens fit the SMs at once (384 tokens x 40 heads 5.0 against 6.4 us, 2048 10.8 against 13.0),
+  // four beyond (16,384 tokens x 20 heads 31.8 against 34.8).
+  if (c) return c->q8 ? pick_turn<D, 2, 3>(p, c, s) : pick_turn<D, 1, 4>(p, c, s);
+  const bool many = (int64_t)p.T * D / 256 > (int64_t)device_sm_count() * 4 * (kThreads / 32);
+  return many ? pick_turn<D, 0, 4>(p, c, s) : pick_turn<D, 0, 3>(p, c, s);
 }
 
 template <int D>
