@@ -364,12 +364,12 @@ cudaError_t start_rows(const RowsProblem& p, const CacheView* c, cudaStream_t s)
   if (c) a.c = *c;
   const int heads = p.Hq + (c ? 2 : 1) * p.Hkv;
   a.groups = (p.T + kTokens - 1) / kTokens;
-  // A token's heads go to one warp after another in chunks. Long chunks share the angles (which
-  // cost about as much as 6 heads), short ones keep every SM's warps busy: the fewest steps over
-  // the waves of resident warps. (384 tokens x 40 heads, a wave of warps at all costs: 8.8 us,
-  // this 5.0; 2048 tokens 14.7 and 10.8.)
+  // A token's heads go to one warp after another in chunks. Long chunks share what a warp does
+  // once (the angles: about as long as 6 heads; else addresses, 3), short ones keep every SM's
+  // warps busy: the fewest steps over the waves of resident warps. (384 tokens x 40 heads, as
+  // many warps as two waves have: 8.8 us, this 5.0; 2048 tokens 14.7 and 10.8.)
   const int64_t resident = (int64_t)device_sm_count() * kPerSm * (kThreads / 32);
-  constexpr int kAngles = kTurn ? 6 : 1;
+  constexpr int kAngles = kTurn ? 6 : 3;
   int64_t best = INT64_MAX;
   for (int chunks = 1; chunks <= heads; chunks += (chunks + 3) / 4) {
     const int per = (heads + chunks - 1) / chunks;
