@@ -646,15 +646,15 @@ auto with_rows(int M, F&& f) {
 // sequences x 8 heads at 8k, bf16 169 us, Q8 158; k_paged's design with 16-row tiles: 207, 186).
 // More rows: the tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and
 // end, and is ahead from several tiles per SM on. k_paged against it, 4 sequences x 8 heads:
-// bf16, 64 rows, 32 against 38 us at 4k tokens, 52 against 51 at 8k, 171 against 130 at 32k; 96
-// rows 38 against 42, 63 against 56, 209 against 135; one head of 64k 24 against 32. Q8, 64
+// bf16, 64 rows, 32 against 36 us at 4k tokens, 52 against 46 at 8k, 336 against 170 at 64k; 96
+// rows 38 against 40, 63 against 51, 403 against 176; one head of 64k 25 against 31. Q8, 64
 // rows: 22 against 24 us at 2k, 34 against 30 at 4k, 201 against 127 at 32k; one head of 32k 16
 // against 17, of 64k 21 against 21. `places`: tokens x key heads there can be (lengths are not
 // known here).
 Kernel which(int M, bool q8, int64_t places) {
   if (M <= kFewMaxRows) return Kernel::kFew;
   return M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) &&
-                 places >= (int64_t)(q8 ? 4 : 10) * 128 * device_sm_count()
+                 places >= (int64_t)(q8 ? 4 : 8) * 128 * device_sm_count()
              ? Kernel::kTensor
              : Kernel::kRows;
 }

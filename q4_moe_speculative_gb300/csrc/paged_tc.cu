@@ -17,9 +17,11 @@
 // into the swizzled operand layout (bf16) or as raw codes that eight more warps widen to bf16
 // (Q8); one thread each of the last two warps issues the MMAs of S and of O. S is
 // double-buffered: the next tile's scores are computed while this tile's are exponentiated.
-// Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 55 us with the join,
-// which takes 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 rows 232 us, 96 rows
-// 242 (4.3 TB/s); Q8 (0.54 GB) 231. The softmax warps bound it: they turn 128 x M scores per tile.
+// Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 48 us with the join,
+// which takes 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 rows 165 us, 96 rows
+// 176 (6.0 TB/s, bound by memory); Q8 (0.54 GB) 233, bound by the chain of a tile through
+// widening, scores and P. (Bringing the tiles behind the ring into L2 ahead of time costs: 96
+// rows 176 us without, 190 two tiles ahead, 241 with four, 297 with eight.)
 // A token of a bf16 cache that only some rows see may hold infinities, and 0 x infinity is
 // not 0: its values are cleared before the product, and the (at most 7) such tokens are added
 // row by row when the run ends. Every wait is bounded; a give-up sets the status word.
@@ -87,9 +89,6 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
       ::"r"(smem_at(dst)), "l"(src), "r"(bytes), "r"(smem_at(bar))
       : "memory");
-}
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 // One lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one() {
@@ -628,29 +627,10 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     uint64_t* const free_bar = kQ8 ? sh.raw_free[values] : (values ? sh.vfree : sh.kfree);
     uint8_t* const tiles = kQ8 ? sRaw + (values ? ta.raw * T::kRawMat : 0) : (values ? sV : sK);
     int page = lane < pages ? page_of(a, cur.b, cur.tile * kTok + lane * pt, cur.len) : -1;
-    // The ring holds too little to cover the memory's latency at full rate: the tiles after it
-    // are brought into L2 ahead of time (kAhead tiles, 39 MB over all SMs at most).
-    constexpr int kAhead = 4;
-    Cursor pre = cur;
-    int pre_page = page, pre_done = 0;
-    auto prefetch = [&] {
-      if (pre_page >= 0 && pre_page < a.c.pages)
-        prefetch_l2((values ? a.c.v : a.c.k) +
-                        (pre_page * a.c.stride + (((int64_t)pre.h << a.c.page_shift)) * D) *
-                            (kQ8 ? 1 : 2),
-                    pt * D * (kQ8 ? 1 : 2));
-      if (++pre_done >= n) return;
-      pre.next(a);
-      const int t = pre.tile * kTok + lane * pt;
-      pre_page = -1;
-      if (lane < pages && t < pre.len)
-        pre_page = a.table[(int64_t)pre.b * a.max_pages + (t >> a.c.page_shift)];
-    };
     int st = 0, done = 0, edges = 0;
     uint32_t par = 1;
     bool alive = true;
     for (int i = 0; i < n; ++i) {
-      for (int x = 0; x < 2 && pre_done < n && pre_done < i + ring + kAhead; ++x) prefetch();
       if (i >= ring) alive = wait(&free_bar[st], par);
       if (!__all_sync(0xffffffffu, alive)) break;
       const bool ok = page >= 0 && page < a.c.pages;
