@@ -23,8 +23,8 @@
 // widening, scores and P. (Bringing the tiles behind the ring into L2 ahead of time costs: 96
 // rows 176 us without, 190 two tiles ahead, 241 with four, 297 with eight.)
 // A token of a bf16 cache that only some rows see may hold infinities, and 0 x infinity is
-// not 0: its values are cleared before the product, and the (at most 7) such tokens are added
-// row by row when the run ends. Every wait is bounded; a give-up sets the status word.
+// not 0: where one of its values is not finite they are cleared before the product, and the
+// (at most 7) such tokens are added row by row when the run ends. Every wait is bounded; a give-up sets the status word.
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -75,6 +75,7 @@ struct alignas(16) TcSmem {   // small arrays in front of the tiles
   int row_at[kMaxN];          // and where its values start in a sequence's queries or results
   alignas(16) float pe[7][kMaxN];   // P of the tokens that only some rows see
   unsigned runs[kInfo];       // which pages of a tile are there
+  unsigned apart[kInfo];      // tokens behind seen0 whose values are not finite, and cleared
 };
 constexpr int kSmallBytes = (sizeof(TcSmem) + 1023) / 1024 * 1024;
 static_assert(kSmallBytes <= 10240, "the largest call fills the SM's shared memory");
@@ -89,6 +90,10 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
       ::"r"(smem_at(dst)), "l"(src), "r"(bytes), "r"(smem_at(bar))
       : "memory");
+}
+// Whether one of two bf16 values is infinite or NaN.
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 // One lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one() {
@@ -252,6 +257,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   __syncthreads();
   sm100::tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  if (!kQ8 && tid < 2)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &v_map : &k_map) : "memory");
   pdl_wait();
   if (blockIdx.x == 0 && tid == 0) *a.status = 0u;
 
@@ -483,22 +490,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         const bool whole = ends && cur.tile == run;
         // this thread's dimension of the values (codes are widened as (0, 2, 1, 3))
         const int dim = kQ8 ? (tk & ~3) | ((tk & 1) << 1) | ((tk >> 1) & 1) : tk;
-        // the partly seen tokens of this run, e0 .. e1 - 1 behind seen0
-        const int e0 = max(max((cur.tile - run) * kTok, 0) - seen0, 0);
-        const int e1 = min(cur.len, t0 + kTok) - seen0;
         float v[7];
-        if (!kQ8) {
-#pragma unroll
-          for (int e = 0; e < 7; ++e) {   // (their loads overlap)
-            v[e] = 0.f;
-            if (e < e0 || e >= e1 || tk >= D) continue;
-            const int t = seen0 + e, page = page_of(a, cur.b, t, cur.len);
-            if (page >= 0)
-              v[e] = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(
-                  a.c.v)[page * a.c.stride +
-                         (((int64_t)cur.h << a.c.page_shift) + (t & page_mask)) * D + dim]);
-          }
-        }
 #pragma unroll 1
         for (int c = col0; c < col0 + half; c += 16) {
           __syncwarp();
@@ -522,13 +514,31 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         alive = !score_any(!alive);
         if (!alive) break;
         sm100::tc_fence_after();
+        // the partly seen tokens of this run that were left out of the products (they are among
+        // its last 7, so in its last two tiles)
+        unsigned apart = 0;
+        if (!kQ8) {
+          volatile unsigned* const left_out = sh.apart;
+          apart = left_out[i % kInfo];
+          if (run > 0) apart |= left_out[(i + kInfo - 1) % kInfo];
+#pragma unroll
+          for (int e = 0; e < 7; ++e) {   // (their loads overlap)
+            v[e] = 0.f;
+            if (!(apart >> e & 1u) || tk >= D) continue;
+            const int t = seen0 + e, page = page_of(a, cur.b, t, cur.len);
+            if (page >= 0)
+              v[e] = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(
+                  a.c.v)[page * a.c.stride +
+                         (((int64_t)cur.h << a.c.page_shift) + (t & page_mask)) * D + dim]);
+          }
+        }
         uint16_t* const out = a.out + seq_at(cur) + dim;
         float* const po = a.part_o + piece * a.M * D + dim;
         // (this thread's column goes through its own words of P's buffers, which nothing else
         // uses now, so that the rows can be walked in a loop: this code runs once per run)
         float* const mine = reinterpret_cast<float*>(sP) + tk;
         float* const mine_v = mine + (N + 7 * (col0 != 0)) * kTok;
-        if (!kQ8) {
+        if (apart) {
 #pragma unroll
           for (int e = 0; e < 7; ++e) mine_v[e * kTok] = v[e];
         }
@@ -544,7 +554,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           }
           if (!kQ8) {
 #pragma unroll 1
-            for (int e = e0; e < e1; ++e) {
+            for (unsigned rest = apart; rest; rest &= rest - 1) {
+              const int e = __ffs(rest) - 1;
               const float ve = mine_v[e * kTok];
               const bool plain = fabsf(ve) < INFINITY;   // P of a row that does not see it is 0
 #pragma unroll
@@ -651,6 +662,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         }
       }
       const bool edge = !kQ8 && values && (t0 + kTok > seen0 || count < pages);
+      // (read when the results of tile i or i + 1 are written: at most the ring ahead of here)
+      if (!kQ8 && values && !edge && lane == 0) sh.apart[i % kInfo] = 0u;
       uint64_t* const bar = edge ? &sh.vedge : &full[st];
       if (lane == 0) sm100::mbar_arrive_expect_tx(bar, count * pt * (kQ8 ? D : 2 * D));
       __syncwarp();
@@ -667,14 +680,28 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
                                values ? &v_map : &k_map, 64 * hf, cur.h << a.c.page_shift, page, bar);
         }
       }
-      if (edge) {   // clear the values that not every row sees
+      if (edge) {   // clear what is no value, and the partly seen values that are not finite
         alive = wait(&sh.vedge, edges++ & 1);
         if (!__all_sync(0xffffffffu, alive)) break;
-        for (int r = lane; r < kTok; r += 32)
-          if (t0 + r >= seen0 || !(there >> (r >> a.c.page_shift) & 1u))
-            for (int x = 0; x < 8 * T::kHalves; ++x)
-              *reinterpret_cast<uint4*>(tiles + st * T::kMat + (x >> 3) * (kTok * 128) + r * 128 +
-                                        (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        unsigned apart = 0;
+        for (int r = lane; r < kTok; r += 32) {
+          bool none = t0 + r >= cur.len || !(there >> (r >> a.c.page_shift) & 1u);
+          auto at = [&](int x) {
+            return reinterpret_cast<uint4*>(tiles + st * T::kMat + (x >> 3) * (kTok * 128) +
+                                            r * 128 + (x & 7) * 16);
+          };
+          if (!none && t0 + r >= seen0) {
+            for (int x = 0; x < 8 * T::kHalves; ++x) {
+              const uint4 v = *at(x);
+              none |= not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
+            }
+            if (none) apart |= 1u << (t0 + r - seen0);
+          }
+          if (none)
+            for (int x = 0; x < 8 * T::kHalves; ++x) *at(x) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        apart = __reduce_or_sync(0xffffffffu, apart);
+        if (lane == 0) sh.apart[i % kInfo] = apart;
         fence_async();
         __syncwarp();
         if (lane == 0) arrive(&full[st]);
