@@ -645,16 +645,17 @@ auto with_rows(int M, F&& f) {
 // Up to 32 rows: paged_few.cu, which costs no more for 1 row than it has to (24 rows, 32
 // sequences x 8 heads at 8k, bf16 169 us, Q8 158; k_paged's design with 16-row tiles: 207, 186).
 // More rows: the tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and
-// end, and is ahead from several tiles per SM on. k_paged against it, 4 sequences x 8 heads:
-// bf16, 64 rows, 32 against 36 us at 4k tokens, 52 against 46 at 8k, 336 against 170 at 64k; 96
-// rows 38 against 40, 63 against 51, 403 against 176; one head of 64k 25 against 31. Q8, 64
-// rows: 22 against 24 us at 2k, 34 against 30 at 4k, 201 against 127 at 32k; one head of 32k 16
-// against 17, of 64k 21 against 21. `places`: tokens x key heads there can be (lengths are not
-// known here).
-Kernel which(int M, bool q8, int64_t places) {
+// end, and is ahead from several tiles per SM on. k_paged against it, in us: bf16, D = 128, 4
+// sequences x 8 heads, 40 rows 12 against 16 at 500 tokens, 21 against 19 at 2k, 51 against 34 at
+// 8k, 335 against 158 at 64k, 96 rows 15 against 20, 26 against 23, 63 against 39, 403 against
+// 166; one head of 32k, 96 rows, 17 against 17; Q8, 64 rows, 22 against 24 at 2k, 34 against 30 at
+// 4k, 389 against 234 at 64k. D = 64, 64 rows: bf16 16.4 against 16.8 at 2k, 40 against 31 at 8k,
+// 257 against 137 at 64k; Q8 16.8 against 18.7, 43 against 39, 282 against 189. `places`: tokens x
+// key heads there can be (lengths are not known here).
+Kernel which(int M, int D, bool q8, int64_t places) {
   if (M <= kFewMaxRows) return Kernel::kFew;
   return M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) &&
-                 places >= (int64_t)(q8 ? 4 : 8) * 128 * device_sm_count()
+                 places >= (int64_t)(q8 ? 4 : 2) * (128 / D) * 128 * device_sm_count()
              ? Kernel::kTensor
              : Kernel::kRows;
 }
@@ -668,7 +669,7 @@ Plan make_plan(const PagedAttnProblem& p) {
   Plan pl{};
   const int64_t cap = (int64_t)p.max_pages << p.cache.page_shift;
   const int64_t runs = (int64_t)p.B * p.cache.heads;
-  pl.kernel = which(M, p.cache.q8, runs * cap);
+  pl.kernel = which(M, p.D, p.cache.q8, runs * cap);
   const int per_sm = pl.kernel == Kernel::kFew ? few_ctas_per_sm(M, p.D, p.cache.q8) : 1;
   // no more CTAs than positions in the list of tiles there can be
   const int tile = pl.kernel == Kernel::kTensor ? 128 : kTile;

@@ -17,11 +17,11 @@
 // into the swizzled operand layout (bf16) or as raw codes that eight more warps widen to bf16
 // (Q8); one thread each of the last two warps issues the MMAs of S and of O. S is
 // double-buffered: the next tile's scores are computed while this tile's are exponentiated.
-// Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 48 us with the join,
-// which takes 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 rows 165 us, 96 rows
-// 176 (6.0 TB/s, bound by memory); Q8 (0.54 GB) 233, bound by the chain of a tile through
-// widening, scores and P. (Bringing the tiles behind the ring into L2 ahead of time costs: 96
-// rows 176 us without, 190 two tiles ahead, 241 with four, 297 with eight.)
+// Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 38.5 us with the join,
+// which takes 6 to 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 rows 158 us, 96
+// rows 166 (6.3 TB/s, bound by memory); Q8 (0.54 GB) 234, and D = 64, bf16, 137 (0.52 GB), bound
+// by the chain of a tile through widening, scores and P. (Bringing the tiles behind the ring
+// into L2 ahead of time costs: 96 rows 176 us without, 190 two tiles ahead, 241 with four.)
 // A token of a bf16 cache that only some rows see may hold infinities, and 0 x infinity is
 // not 0: where one of its values is not finite they are cleared before the product, and the
 // (at most 7) such tokens are added row by row when the run ends. Every wait is bounded; a give-up sets the status word.
