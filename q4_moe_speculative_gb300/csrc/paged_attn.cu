@@ -11,7 +11,7 @@
 // results do not depend on timing.
 //
 // Three kernels do the runs: paged_few.cu up to 32 rows, k_paged here for more, paged_tc.cu
-// for more rows and long contexts (rules and figures at which()). None of them lets the next
+// for 25 rows and more of long contexts (rules and figures at which()). None of them lets the next
 // kernel start early: waiting CTAs of the join took room from this kernel's and of the next
 // kernel from the join's (16 rows, 8 sequences x 8 heads at 4k, Q8: 32 against 27 us).
 //
@@ -648,16 +648,19 @@ auto with_rows(int M, F&& f) {
 // end, and is ahead from several tiles per SM on. k_paged against it, in us: bf16, D = 128, 4
 // sequences x 8 heads, 40 rows 12 against 16 at 500 tokens, 21 against 19 at 2k, 51 against 34 at
 // 8k, 335 against 158 at 64k, 96 rows 15 against 20, 26 against 23, 63 against 39, 403 against
-// 166; one head of 32k, 96 rows, 17 against 17; Q8, 64 rows, 22 against 24 at 2k, 34 against 30 at
-// 4k, 389 against 234 at 64k. D = 64, 64 rows: bf16 16.4 against 16.8 at 2k, 40 against 31 at 8k,
+// 166; one head of 32k, 96 rows, 17 against 17; Q8, 64 rows, 22 against 24 at 2k, 34 against 29 at
+// 4k, 389 against 207 at 64k. D = 64, 64 rows: bf16 16.4 against 16.8 at 2k, 40 against 31 at 8k,
 // 257 against 137 at 64k; Q8 16.8 against 18.7, 43 against 39, 282 against 189. `places`: tokens x
-// key heads there can be (lengths are not known here).
+// key heads there can be (lengths are not known here). From 25 rows on at D = 128 it is ahead of
+// paged_few.cu as well: 32 rows, 32 sequences x 8 heads at 8k, bf16 177 against 164 us, Q8 196
+// against 167; 8 x 8 heads at 2k, 24.3 against 21.5 and 24.5 against 23.4; at 1k, 16.9 against 16.9
+// and 16.3 against 18.8; 24 rows 170 against 163 and 158 against 166 (D = 64: 91 and 109, 103 and
+// 153).
 Kernel which(int M, int D, bool q8, int64_t places) {
-  if (M <= kFewMaxRows) return Kernel::kFew;
-  return M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows) &&
-                 places >= (int64_t)(q8 ? 4 : 2) * (128 / D) * 128 * device_sm_count()
-             ? Kernel::kTensor
-             : Kernel::kRows;
+  const bool lengthy = places >= (int64_t)(q8 ? 4 : 2) * (128 / D) * 128 * device_sm_count();
+  if (lengthy && M > (D == 128 ? 24 : kFewMaxRows) && M <= (q8 ? kTcMaxRowsQ8 : kTcMaxRows))
+    return Kernel::kTensor;
+  return M <= kFewMaxRows ? Kernel::kFew : Kernel::kRows;
 }
 
 // What a (sequence, key head) costs beside its tiles, in tiles (24 rows, 32 sequences of up to

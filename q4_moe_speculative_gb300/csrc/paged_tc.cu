@@ -19,7 +19,7 @@
 // double-buffered: the next tile's scores are computed while this tile's are exponentiated.
 // Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 38.5 us with the join,
 // which takes 6 to 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 rows 158 us, 96
-// rows 166 (6.3 TB/s, bound by memory); Q8 (0.54 GB) 234, and D = 64, bf16, 137 (0.52 GB), bound
+// rows 166 (6.3 TB/s, bound by memory); Q8 (0.54 GB) 207, and D = 64, bf16, 137 (0.52 GB), bound
 // by the chain of a tile through widening, scores and P. (Bringing the tiles behind the ring
 // into L2 ahead of time costs: 96 rows 176 us without, 190 two tiles ahead, 241 with four.)
 // A token of a bf16 cache that only some rows see may hold infinities, and 0 x infinity is
@@ -828,10 +828,11 @@ template <int D, bool kQ8>
 cudaError_t start(const PagedArgs& p, cudaStream_t s) {
   TcArgs a{};
   a.p = p;
-  a.N = p.M <= 64 ? 64 : 96;   // (smaller problems take the kernel of paged_attn.cu)
+  a.N = p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 96);
   a.parts = a.N <= 64 ? 2 : 1;
   const int room = 227 * 1024;
-  // The least first, then what fits: a second buffer of P, a second value tile, deeper rings.
+  // The least first, then what fits: a second buffer of P (Q8, 64 rows, D = 128: 207 us with two,
+  // 234 with one and a second value tile), a second value tile, deeper rings.
   a.p_bufs = 1;
   a.k_ring = a.v_ring = kQ8 ? 1 : 2;
   a.raw = kQ8 ? 2 : 0;
@@ -843,8 +844,8 @@ cudaError_t start(const PagedArgs& p, cudaStream_t s) {
       break;
     }
   };
-  if (kQ8) grow(&TcArgs::v_ring, 2);
   grow(&TcArgs::p_bufs, 2);
+  if (kQ8) grow(&TcArgs::v_ring, 2);
   if (kQ8) {
     grow(&TcArgs::k_ring, 2);
     grow(&TcArgs::raw, kMaxRing);
