@@ -95,12 +95,20 @@ __device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// 1 / x to an ulp, x normal and not near the largest.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Writes the codes and the scale of a row of the cache: code = 127 x / a rounded to nearest,
 // ties to even, a the row's largest magnitude (its bits in `top`, already the maximum over the
-// row's lanes). The quotient is the product with 1 / a and one correction by its remainder
-// (Markstein, IBM J. Res. Dev. 34, 1990), which makes a half-integer exactly that: for bf16
-// values 127 x / a is a ratio of small integers, so no other value comes near one. Rounding is
-// the addition of 1.5 * 2^23, whose low byte is the code.
+// row's lanes). The quotient is the product with 1 / a (to an ulp) and one correction by its
+// remainder (Markstein, IBM J. Res. Dev. 34, 1990), which makes a half-integer exactly that: for
+// bf16 values 127 x / a is a ratio of small integers, so no other value comes near one. Rounding
+// is the addition of 1.5 * 2^23, whose low byte is the code. a / 127 by the same theorem, with
+// 1 / 127 rounded correctly, is the correctly rounded quotient where it is normal.
 template <int D>
 __device__ __forceinline__ void put_codes(const f2 (&x)[4], uint32_t top, uint8_t* dst,
                                           float* scale, int j, bool store) {
@@ -108,7 +116,7 @@ __device__ __forceinline__ void put_codes(const f2 (&x)[4], uint32_t top, uint8_
   const float amax = __uint_as_float(top);
   // 127 x and 1 / a stay finite: both sides by 2^-8 or 2^64 where they would not (exact)
   const float pre = amax > 3.3230699e35f ? 0.00390625f : (amax < 7.8886091e-31f ? 1.8446744e19f : 1.f);
-  const float den = __fmul_rn(amax, pre), inv = none ? 0.f : __frcp_rn(den);
+  const float den = __fmul_rn(amax, pre), inv = none ? 0.f : rcp(den);
   const float mult = __fmul_rn(127.f, pre);
   const f2 mult2 = pair(mult, mult), inv2 = pair(inv, inv), den2 = pair(-den, -den);
   const f2 magic = pair(12582912.f, 12582912.f);
@@ -126,7 +134,13 @@ __device__ __forceinline__ void put_codes(const f2 (&x)[4], uint32_t top, uint8_
   const uint32_t hi =
       __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
   reinterpret_cast<uint2*>(dst)[j] = make_uint2(none ? 0u : lo, none ? 0u : hi);
-  if (j == 0) *scale = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 127.f);
+  if (j == 0) {
+    constexpr float k127 = 1.f / 127.f;
+    const float t = __fmul_rn(amax, k127);
+    float q127 = __fmaf_rn(__fmaf_rn(-127.f, t, amax), k127, t);
+    if (amax < 7.8886091e-31f) q127 = __fdiv_rn(amax, 127.f);
+    *scale = bad ? __uint_as_float(0x7FC00000u) : q127;
+  }
 }
 // Bits of the largest magnitude of a row: of bf16 values, and of fp32 ones (as integers they
 // order as the values do, NaN above all).
