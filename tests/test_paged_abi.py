@@ -197,6 +197,18 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes(lib):
         dsm.q4_project(torch.zeros(1, 576, dtype=torch.uint8), bf(1, 64))
 
 
+def test_the_binding_refuses_what_is_no_tensor():
+    import q4_moe_speculative_gb300 as dsm
+    dev, bf = torch.device("cpu"), torch.bfloat16
+    for bad in (None, [1, 2], 3):
+        with pytest.raises(TypeError):
+            dsm._need_on(bad, "lengths", torch.int32, (2,), dev)
+        with pytest.raises(TypeError):
+            dsm._token_rows(bad, "k", (2, 1, 64), dev)
+        with pytest.raises(TypeError):
+            dsm.q4_project(bad, torch.zeros(1, 64, dtype=bf))
+
+
 def test_page_strides_of_a_cache():
     from q4_moe_speculative_gb300 import PagedCache
     st = PagedCache._stride

@@ -352,3 +352,33 @@ def test_replays_with_other_lengths(Hq, q8, wide):
         q.copy_(q.flip(0))
         g.replay()
         check(q, cache, table, lengths, got=out)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_caches_beyond_32_bits(q8):
+    # pages more than 2^32 bytes and 2^31 values apart give what the same pages side by side give
+    page, kv, D, R, lens = 64, 8, 128, 5, [250, 129]
+    n = 70_000 if q8 else 40_000
+    big = dsm.PagedCache.zeros(1, kv, page, D, q8=q8)
+    big = dsm.PagedCache(*(torch.empty((n, *t.shape[1:]), dtype=t.dtype, device=DEV)
+                           for t in (big.k, big.v, big.k_scale, big.v_scale) if t is not None))
+    small = dsm.PagedCache.zeros(8, kv, page, D, q8=q8)
+    near = torch.arange(8, dtype=torch.int32).view(2, 4)
+    pages = torch.tensor([n - 1, 0, n - 2, 1, n // 2, n - 3, 3, n - 4], dtype=torch.int32)
+    far = pages.view(2, 4)
+    T = sum(lens)
+    k, v = (ref.normal(T, kv, D, seed=50 + i).to(DEV) for i in range(2))
+    at = {}
+    for name, table, cache in (("near", near, small), ("far", far, big)):
+        slots = torch.cat([table[b].long()[torch.arange(m) // page] * page + torch.arange(m) % page
+                           for b, m in enumerate(lens)]).to(torch.int32).to(DEV)
+        dsm.cache_write(cache, k, v, slots)
+        at[name] = [dsm.cache_read(cache, slots)]
+        for G, room in ((1, 4), (8, 4), (8, 12000)):
+            q = ref.normal(2, R, G * kv, D, seed=60 + G).to(DEV)
+            wide = torch.full((2, room), -1, dtype=torch.int32)
+            wide[:, :4] = table
+            at[name].append((dsm.paged_attention(
+                q, cache, wide.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)),))
+    for a, b in zip(at["near"], at["far"]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
