@@ -407,16 +407,16 @@ ds_status ds_q4_project(const ds_q4_tiled* w, int64_t rows, int32_t K, const uin
  * DS_CACHE_BF16: the values as bf16. DS_CACHE_Q8: int8 codes and, per row, one fp32 scale
  * at page * scale_page_stride + head * page_tokens + offset; value = scale * code. A row x
  * is quantised, with a = max |x|, as
- *   scale = a / 127,   code = rint(127 x / a)   (fp32, each operation rounded to nearest,
- *   ties to even; for a > 2^118 x and a are halved eight times first);
+ *   scale = a / 127 (fp32),   code = 127 x / a rounded to the nearest integer, ties to even
+ *   (exactly so for bf16 values; an fp32 x may go either way within 2^-21 of a tie);
  * a row of zeros gets scale 0 and codes 0; a row that holds an infinity or a NaN gets the
  * scale NaN, so that it reads back as NaN.
  * Limits: page_tokens 16, 32, 64 or 128; head_dim 64 or 128 (other values from 1 to 4096:
  * DS_ERR_UNSUPPORTED); 1 <= n_kv_heads <= 256; n_pages >= 1 and n_pages * page_tokens <
  * 2^31; page_stride >= n_kv_heads * page_tokens * head_dim and a multiple of 16;
- * scale_page_stride >= n_kv_heads * page_tokens and a multiple of 4 (both and token strides at
- * most 2^31); k, v, k_scale and
- * v_scale 16-byte aligned. k and v may share one allocation (strided pages).
+ * scale_page_stride >= n_kv_heads * page_tokens and a multiple of 4 (all strides at most
+ * 2^31); k, v, k_scale and v_scale 16-byte aligned. k and v may share one allocation
+ * (strided pages).
  * ---------------------------------------------------------------------------------- */
 #define DS_CACHE_BF16 0
 #define DS_CACHE_Q8 1
@@ -512,7 +512,8 @@ ds_status ds_qk_norm_rope_write(const ds_norm_rope_args* args, const uint16_t* v
  * the other sequences of the call and on max_pages, which decide how the work is cut.
  * Limits: 0 <= n_seqs <= 4096 (0 enqueues nothing), 1 <= n_rows <= 8, 1 <= max_pages,
  * max_pages * page_tokens <= 2^24, n_heads a multiple of the cache's n_kv_heads, n_rows * H
- * <= 128 (else DS_ERR_UNSUPPORTED), scale finite; q and out 16-byte aligned.
+ * <= 128 (else DS_ERR_UNSUPPORTED), scale and scale * 1.5 finite; q and out 16-byte
+ * aligned.
  * ---------------------------------------------------------------------------------- */
 typedef struct {
   int32_t n_seqs, n_rows, n_heads;
