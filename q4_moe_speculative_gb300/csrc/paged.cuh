@@ -34,9 +34,8 @@ cudaError_t launch_few(const PagedArgs& p, int D, cudaStream_t s);
 
 // paged_tc.cu: tiles of 128 tokens, one CTA per SM. The most query rows per key head: tensor
 // memory holds two buffers of S, O and two of the sums, 5 N columns of 512, or 6 N where P
-// has two parts (Q8 always: a value's scale is part of P, which then cannot be made up for by
-// the normaliser).
-constexpr int kTcMaxRows = 96, kTcMaxRowsQ8 = 64;
+// has two parts.
+constexpr int kTcMaxRows = 96;
 cudaError_t launch_tc(const PagedArgs& p, int D, cudaStream_t s);
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {

@@ -10,7 +10,9 @@
 //   O^T += V^T P^T   A = the value tile, read MN-major (its rows are tokens, the MMA's K),
 //                    B = P [128 tokens][N rows], also MN-major, a high bf16 part and,
 //                    up to 64 rows, a low one in columns of its own; TMEM lane = value
-//                    dimension, column = query row (of either part).
+//                    dimension, column = query row (of either part). With one part a weight
+//                    is off by half a step of bf16, as the results are; over a bf16 cache
+//                    the normaliser sums what is multiplied.
 // Roles: warps 0-7 turn scores into P (a row's reference maximum moves only when a score
 // exceeds it by 2^8, agreed by one barrier vote per tile), keep the normaliser of their
 // token in TMEM, and write the results; two warps copy tiles page by page, by TMA straight
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             for (int e = 0; e < 4; ++e) {
               const int j = 8 * c8 + 2 * e;
               float p0 = exp2_fast(t[j]), p1 = exp2_fast(t[j + 1]);
-              if (!kSplit) {   // (the sums of what is multiplied, so that weights add up to 1)
+              if (!kSplit && !kQ8) {   // (the sums of what is multiplied: weights add up to 1)
                 hi4[e] = pack2(p0, p1);
                 p0 = bf16_lo(hi4[e]);
                 p1 = bf16_hi(hi4[e]);
@@ -461,8 +463,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
                 sh.pe[tok - seen0][c + j] = p0;
                 sh.pe[tok - seen0][c + j + 1] = p1;
               }
+              if (kSplit || kQ8) hi4[e] = pack2(p0, p1);
               if (kSplit) {
-                hi4[e] = pack2(p0, p1);
                 lo4[e] = pack2(__fsub_rn(p0, bf16_lo(hi4[e])), __fsub_rn(p1, bf16_hi(hi4[e])));
               }
             }
@@ -534,10 +536,11 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         }
         uint16_t* const out = a.out + seq_at(cur) + dim;
         float* const po = a.part_o + piece * a.M * D + dim;
-        // (this thread's column goes through its own words of P's buffers, which nothing else
-        // uses now, so that the rows can be walked in a loop: this code runs once per run)
-        float* const mine = reinterpret_cast<float*>(sP) + tk;
-        float* const mine_v = mine + (N + 7 * (col0 != 0)) * kTok;
+        // (16 rows at a time go through this thread's own words of P's buffers, which nothing else
+        // uses now, so that they can be walked in a loop: this code runs once per run)
+        float* const words = reinterpret_cast<float*>(sP) + tk;
+        float* const mine = words + (col0 ? 16 : 0) * kTok;
+        float* const mine_v = words + (col0 ? 39 : 32) * kTok;
         if (apart) {
 #pragma unroll
           for (int e = 0; e < 7; ++e) mine_v[e * kTok] = v[e];
@@ -564,13 +567,11 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             }
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) mine[(c + j) * kTok] = o[j];
-        }
-        if (tk < D) {                                   // (D = 64: the upper lanes repeat)
-          const int rows = min(a.M, col0 + half);
+          for (int j = 0; j < 16; ++j) mine[j * kTok] = o[j];
+          const int rows = tk < D ? min(a.M, c + 16) : 0;   // (D = 64: the upper lanes repeat)
 #pragma unroll 4
-          for (int row = col0; row < rows; ++row) {
-            const float o = mine[row * kTok];
+          for (int row = c; row < rows; ++row) {
+            const float o = mine[(row - c) * kTok];
             // (a normaliser of 0 is a row that sees nothing; its sums may hold a token's NaN)
             if (whole)
               out[sh.row_at[row]] =
@@ -860,14 +861,13 @@ cudaError_t start(const PagedArgs& p, cudaStream_t s) {
   a.tmem_cols = 128;
   while ((int)a.tmem_cols < (4 + a.parts) * a.N) a.tmem_cols *= 2;
   // (the results of a run pass through P's buffers)
-  if (a.p_bufs * ((a.N * a.parts + 63) / 64) * 128 < (a.N + (kQ8 ? 0 : 14)) * 4)
+  if (a.p_bufs * ((a.N * a.parts + 63) / 64) * 128 < (32 + (kQ8 ? 0 : 14)) * 4)
     return cudaErrorInvalidValue;
   // (at least half of the SM's shared memory, so that one CTA has the SM's tensor memory)
   int smem = smem_bytes<D, kQ8>(a);
   smem = smem < 120 * 1024 ? 120 * 1024 : smem;
   if (a.N <= 64) return start_as<D, kQ8, true>(a, room, smem, s);
-  if constexpr (kQ8) return cudaErrorInvalidValue;   // (kTcMaxRowsQ8)
-  else return start_as<D, kQ8, false>(a, room, smem, s);
+  return start_as<D, kQ8, false>(a, room, smem, s);
 }
 
 }  // namespace paged_tc

@@ -4,8 +4,7 @@ run together.
 
 The kernel is chosen by the query rows per key head and by the tokens that the page table has
 room for: `wide` tables have room for more than 200,000 tokens, most of it unused, so that
-33 (25 at head_dim 128) to 96 rows (64 for Q8) take the tensor-memory kernel at short lengths
-too."""
+33 (25 at head_dim 128) to 96 rows take the tensor-memory kernel at short lengths too."""
 import pytest
 import torch
 
