@@ -33,9 +33,9 @@ int few_ctas_per_sm(int M, int D, bool q8);
 cudaError_t launch_few(const PagedArgs& p, int D, cudaStream_t s);
 
 // paged_tc.cu: tiles of 128 tokens, one CTA per SM. The most query rows per key head: tensor
-// memory holds two buffers of S, O and two of the sums, 5 N columns of 512, or 6 N where P
-// has two parts.
-constexpr int kTcMaxRows = 96;
+// memory holds S, O and two buffers of the sums, 4 N columns of 512 (and up to 96 rows a second
+// buffer of S, up to 64 the second part of O).
+constexpr int kTcMaxRows = 128;
 cudaError_t launch_tc(const PagedArgs& p, int D, cudaStream_t s);
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {

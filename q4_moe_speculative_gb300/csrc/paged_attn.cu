@@ -650,7 +650,8 @@ auto with_rows(int M, F&& f) {
 // 8k, 335 against 158 at 64k, 96 rows 15 against 20, 26 against 23, 63 against 39, 403 against
 // 166; one head of 32k, 96 rows, 17 against 17; Q8, 64 rows, 22 against 24 at 2k, 34 against 29 at
 // 4k, 389 against 207 at 64k, 96 rows 28 against 29, 45 against 35 and, of one head, at 300k 86
-// against 53. D = 64, 64 rows: bf16 16.4 against 16.8 at 2k, 40 against 31 at 8k,
+// against 53; 128 rows, bf16, 22 against 25 at 1k, 32 against 29 at 2k, 134 against 77 at 16k, Q8
+// 35 against 40 at 2k, 54 against 42 at 4k, 172 against 96 at 16k. D = 64, 64 rows: bf16 16.4 against 16.8 at 2k, 40 against 31 at 8k,
 // 257 against 137 at 64k; Q8 16.8 against 18.7, 43 against 39, 282 against 189. `places`: tokens x
 // key heads there can be (lengths are not known here). From 25 rows on at D = 128 it is ahead of
 // paged_few.cu as well: 32 rows, 32 sequences x 8 heads at 8k, bf16 177 against 164 us, Q8 196
@@ -659,8 +660,8 @@ auto with_rows(int M, F&& f) {
 // 153).
 Kernel which(int M, int D, bool q8, int64_t places) {
   const bool lengthy = places >= (int64_t)(q8 ? 4 : 2) * (128 / D) * 128 * device_sm_count();
-  if (lengthy && M > (D == 128 ? 24 : kFewMaxRows) && M <= kTcMaxRows)
-    return Kernel::kTensor;
+  static_assert(kPagedMaxRows <= kTcMaxRows, "it takes any rows");
+  if (lengthy && M > (D == 128 ? 24 : kFewMaxRows)) return Kernel::kTensor;
   return M <= kFewMaxRows ? Kernel::kFew : Kernel::kRows;
 }
 

@@ -17,7 +17,7 @@
 // exceeds it by 2^8, agreed by one barrier vote per tile), keep the normaliser of their
 // token in TMEM, and write the results; two warps copy tiles page by page, by TMA straight
 // into the swizzled operand layout (bf16) or as raw codes that eight more warps widen to bf16
-// (Q8); one thread each of the last two warps issues the MMAs of S and of O. S is
+// (Q8); one thread each of the last two warps issues the MMAs of S and of O. Up to 96 rows S is
 // double-buffered: the next tile's scores are computed while this tile's are exponentiated.
 // Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 38.5 us with the join,
 // which takes 6 to 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 rows 158 us, 96
@@ -50,6 +50,7 @@ struct TcArgs {
   int k_ring, v_ring;   // stages of the key and of the value operand tiles
   int raw;          // stages of raw codes (Q8)
   int p_bufs;       // 2: P of one tile is multiplied while the next is formed
+  int s_bufs;       // 2: the next tile's scores are computed while this tile's are read
   uint32_t tmem_cols;
 };
 
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     // thread = token tk (TMEM lane) x the query rows col0 .. col0 + N / 2 - 1, 16 at a time
     const int quad = warp & 3, tk = 32 * quad + lane, half = N / 2, col0 = (warp >> 2) * half;
     const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
-    const uint32_t tO = tmem + lane_at + 2 * N;
+    const uint32_t tO = tmem + lane_at + ta.s_bufs * N;
     const uint16_t* const q0 = a.q;
     auto seq_at = [&](const Cursor& c) {   // of its queries and results for the key head
       return ((int64_t)c.b * a.R * a.Hq + c.h * a.G) * D;
@@ -328,9 +329,9 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       const bool last = ends || i + 1 == n;             // of this run
       const int t0 = cur.tile * kTok, tok = t0 + tk;
       const int seen0 = cur.len - (a.R - 1);            // row r sees t < seen0 + r
-      const uint32_t tS = tmem + lane_at + (i & 1) * N;
-      const uint32_t tL = tmem + lane_at + 2 * N + NP + (i & 1) * N;
-      const uint32_t tLnew = tmem + lane_at + 2 * N + NP + (~i & 1) * N;
+      const uint32_t tS = tmem + lane_at + (i & (ta.s_bufs - 1)) * N;
+      const uint32_t tL = tO + NP + (i & 1) * N;
+      const uint32_t tLnew = tO + NP + (~i & 1) * N;
       uint8_t* const p_at = sP + (i & (ta.p_bufs - 1)) * p_size + tk * 128;
       const int slot = i % kInfo;
       // what is known of the tile, its scores, and P's buffer (free after the tile p_bufs before)
@@ -736,8 +737,9 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     uint32_t par = 0;
     for (int j = 0; j < n; ++j) {
       const bool new_q = j == 0 || cur.tile == 0;
-      // the buffer of S is free once P of the tile before the last is there
-      bool ok = j < 2 || wait(&sh.pfull[j & 1], ((j - 2) >> 1) & 1);
+      // the buffer of S is free once P of the tile s_bufs before is there
+      const int before = j - ta.s_bufs;
+      bool ok = before < 0 || wait(&sh.pfull[before & 1], (before >> 1) & 1);
       if (new_q) ok = ok && wait(&sh.qfull, segs++ & 1);
       ok = ok && wait(&sh.kfull[st], par);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       if (leader) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)   // 16 values: 32 bytes, or the next 64 values
-          sm100::mma_bf16(tmem + (j & 1) * N, kd + (ks >> 2) * (kTok * 8) + (ks & 3) * 2,
+          sm100::mma_bf16(tmem + (j & (ta.s_bufs - 1)) * N, kd + (ks >> 2) * (kTok * 8) + (ks & 3) * 2,
                           q_desc + (uint32_t)((ks >> 2) * N * 8 + (ks & 3) * 2), idesc, ks > 0);
         sm100::mma_commit(&sh.sfull[j & 1]);
         sm100::mma_commit(&sh.kfree[st]);
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       if (leader) {
 #pragma unroll
         for (int ks = 0; ks < kTok / 16; ++ks)   // 16 tokens: 2 KB
-          sm100::mma_bf16(tmem + 2 * N, vd + ks * 128, pd + ks * 128, idesc, !(fresh && ks == 0));
+          sm100::mma_bf16(tmem + ta.s_bufs * N, vd + ks * 128, pd + ks * 128, idesc, !(fresh && ks == 0));
         sm100::mma_commit(&sh.odone[i & 1]);
         sm100::mma_commit(&sh.vfree[st]);
       }
@@ -829,8 +831,9 @@ template <int D, bool kQ8>
 cudaError_t start(const PagedArgs& p, cudaStream_t s) {
   TcArgs a{};
   a.p = p;
-  a.N = p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 96);
+  a.N = p.M <= 32 ? 32 : (p.M <= 64 ? 64 : (p.M <= 96 ? 96 : 128));
   a.parts = a.N <= 64 ? 2 : 1;
+  a.s_bufs = a.N <= 96 ? 2 : 1;   // (tensor memory has 512 columns)
   const int room = 227 * 1024;
   // The least first, then what fits: a second buffer of P (Q8, 64 rows, D = 128: 207 us with two,
   // 234 with one and a second value tile), a second value tile, deeper rings.
@@ -859,7 +862,7 @@ cudaError_t start(const PagedArgs& p, cudaStream_t s) {
   // back the scores are done, and two further back P (the two buffers of S).
   static_assert(kMaxRing + 2 + 2 <= kInfo, "slots of the tile information");
   a.tmem_cols = 128;
-  while ((int)a.tmem_cols < (4 + a.parts) * a.N) a.tmem_cols *= 2;
+  while ((int)a.tmem_cols < (a.s_bufs + 2 + a.parts) * a.N) a.tmem_cols *= 2;
   // (the results of a run pass through P's buffers)
   if (a.p_bufs * ((a.N * a.parts + 63) / 64) * 128 < (32 + (kQ8 ? 0 : 14)) * 4)
     return cudaErrorInvalidValue;
