@@ -645,19 +645,21 @@ auto with_rows(int M, F&& f) {
 // Up to 32 rows: paged_few.cu, which costs no more for 1 row than it has to (24 rows, 32
 // sequences x 8 heads at 8k, bf16 169 us, Q8 158; k_paged's design with 16-row tiles: 207, 186).
 // More rows: the tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and
-// end, and is ahead from several tiles per SM on. k_paged against it, in us: bf16, D = 128, 4
-// sequences x 8 heads, 40 rows 12 against 16 at 500 tokens, 21 against 19 at 2k, 51 against 34 at
-// 8k, 335 against 158 at 64k, 96 rows 15 against 20, 26 against 23, 63 against 39, 403 against
-// 166; one head of 32k, 96 rows, 17 against 17; Q8, 64 rows, 22 against 24 at 2k, 34 against 29 at
-// 4k, 389 against 207 at 64k, 96 rows 28 against 29, 45 against 35 and, of one head, at 300k 86
-// against 53; 128 rows, bf16, 22 against 25 at 1k, 32 against 29 at 2k, 134 against 77 at 16k, Q8
-// 35 against 40 at 2k, 54 against 42 at 4k, 172 against 96 at 16k. D = 64, 64 rows: bf16 16.4 against 16.8 at 2k, 40 against 31 at 8k,
-// 257 against 137 at 64k; Q8 16.8 against 18.7, 43 against 39, 282 against 189. `places`: tokens x
-// key heads there can be (lengths are not known here). From 25 rows on at D = 128 it is ahead of
-// paged_few.cu as well: 32 rows, 32 sequences x 8 heads at 8k, bf16 177 against 164 us, Q8 196
-// against 167; 8 x 8 heads at 2k, 24.3 against 21.5 and 24.5 against 23.4; at 1k, 16.9 against 16.9
-// and 16.3 against 18.8; 24 rows 170 against 163 and 158 against 166 (D = 64: 91 and 109, 103 and
-// 153).
+// end, and is ahead from several tiles per SM on. k_paged | paged_tc, us, 4 sequences x 8 heads:
+//   tokens per sequence        500      1k       2k       4k        8k       64k
+//   bf16, D = 128, 40 rows   12 | 16           21 | 19  31 | 25   51 | 34  335 | 158
+//                  96 rows   15 | 20           26 | 23  38 | 29   63 | 39  403 | 166
+//                 128 rows   19 | 25  22 | 25  32 | 29  46 | 36   (16k: 134 | 77)
+//   Q8,   D = 128, 64 rows   13 | 19           22 | 24  34 | 29   58 | 42  389 | 207
+//                  96 rows            19 | 24  28 | 29  45 | 35   76 | 52
+//   bf16, D = 64,  64 rows                     16 | 17            40 | 31  257 | 137
+//   Q8,   D = 64,  64 rows                     17 | 19            43 | 39  282 | 189
+// One head of 32k, D = 128, 96 rows: bf16 17 | 17, Q8 19 | 19. From 25 rows on it is ahead of
+// paged_few.cu as well at D = 128: 32 rows, 32 sequences x 8 heads at 8k, bf16 177 against 164,
+// Q8 196 against 167; 8 x 8 heads at 2k, 24.3 against 21.5 and 24.5 against 23.4; at 1k, 16.9
+// against 16.9 and 16.3 against 18.8; but 24 rows at 8k 170 against 163 and 158 against 166, and 32
+// rows at D = 64 111 against 110 and 126 against 153. `places`: tokens x key heads there can be
+// (lengths are not known here).
 Kernel which(int M, int D, bool q8, int64_t places) {
   const bool lengthy = places >= (int64_t)(q8 ? 4 : 2) * (128 / D) * 128 * device_sm_count();
   static_assert(kPagedMaxRows <= kTcMaxRows, "it takes any rows");

@@ -26,7 +26,8 @@
 // into L2 ahead of time costs: 96 rows 176 us without, 190 two tiles ahead, 241 with four.)
 // A token of a bf16 cache that only some rows see may hold infinities, and 0 x infinity is
 // not 0: where one of its values is not finite they are cleared before the product, and the
-// (at most 7) such tokens are added row by row when the run ends. Every wait is bounded; a give-up sets the status word.
+// (at most 7) such tokens are added row by row when the run ends. Every wait is bounded; a
+// give-up sets the status word.
 #include "paged.cuh"
 #include "sm100.cuh"
 
