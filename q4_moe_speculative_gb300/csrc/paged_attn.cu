@@ -667,9 +667,12 @@ Kernel which(int M, int D, bool q8, int64_t places) {
   return M <= kFewMaxRows ? Kernel::kFew : Kernel::kRows;
 }
 
-// What a (sequence, key head) costs beside its tiles, in tiles (24 rows, 32 sequences of up to
-// 8k tokens, 8 heads, Q8: 99 us with 2 in paged_few.cu, 95 with 3, 97 with 6).
-int begin_of(Kernel k) { return k == Kernel::kFew ? 3 : 2; }
+// What a (sequence, key head) costs beside its tiles, in tiles. 32 sequences of up to 8k tokens,
+// 8 heads: paged_few.cu, 24 rows, Q8: 99 us with 2, 95 with 3, 97 with 6; paged_tc.cu, 48 rows,
+// bf16: 121 with 2, 101.6 with 5, 103 with 8; Q8: 140 with 2, 134 with 4, 139 with 8.
+int begin_of(Kernel k, bool q8) {
+  return k == Kernel::kFew ? 3 : (k == Kernel::kTensor ? (q8 ? 4 : 5) : 2);
+}
 
 Plan make_plan(const PagedAttnProblem& p) {
   const int M = p.R * (p.Hq / p.cache.heads);
@@ -680,7 +683,7 @@ Plan make_plan(const PagedAttnProblem& p) {
   const int per_sm = pl.kernel == Kernel::kFew ? few_ctas_per_sm(M, p.D, p.cache.q8) : 1;
   // no more CTAs than positions in the list of tiles there can be
   const int tile = pl.kernel == Kernel::kTensor ? 128 : kTile;
-  const int64_t most = runs * ((cap + tile - 1) / tile + begin_of(pl.kernel));
+  const int64_t most = runs * ((cap + tile - 1) / tile + begin_of(pl.kernel, p.cache.q8));
   const int64_t all = (int64_t)per_sm * device_sm_count();
   pl.grid = (int)(most < all ? most : all);
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
@@ -702,7 +705,7 @@ cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   a.M = p.R * a.G;
   a.max_pages = p.max_pages;
   a.tile_log = pl.kernel == Kernel::kTensor ? 7 : 6;
-  a.begin = begin_of(pl.kernel);
+  a.begin = begin_of(pl.kernel, p.cache.q8);
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   a.q = p.q;
   a.c = p.cache;
