@@ -14,7 +14,7 @@
 // weights, and keeps them in registers over the heads of its chunk. Memory-bound by bytes,
 // by instruction issue in practice (59 to 68% of the slots): fp32 arithmetic is done two values
 // at a time (f32x2). 16,384 tokens x 20 heads of 128, rotated: 31.8 us, 5.3 TB/s; 32,768 tokens x
-// 8 heads into a Q8 cache: 43 us, 4.7 TB/s.
+// 8 heads into a Q8 cache: 40 us, 5.1 TB/s.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -169,7 +169,10 @@ template <int D, int kCache, int kTurn, int kPerSm>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     k_rows(const __grid_constant__ RowsArgs a) {
   constexpr int LPH = D / 8, kTokens = 32 / LPH;   // lanes per row, tokens per warp
-  constexpr int kBatch = 4;   // rows whose loads are in flight together (2: the write above 7 us more)
+  // rows whose loads are in flight together (the write above: 2 50 us, 4 43, 8 40, but of one
+  // head, 16,384 tokens with the reading back, 4 8.2 and 8 8.6; the rotation: 4 31.9 us, 5, which
+  // spills, 36.4)
+  constexpr int kBatch = kTurn ? 4 : 8;
   pdl_trigger();
   pdl_wait();
   const RowsProblem& p = a.p;
