@@ -656,7 +656,7 @@ auto with_rows(int M, F&& f) {
 //   Q8,   D = 64,  64 rows                     17 | 19            43 | 39  282 | 189
 // One head of 32k, D = 128, 96 rows: bf16 17 | 17, Q8 19 | 19. From 25 rows on it is ahead of
 // paged_few.cu as well at D = 128: 32 rows, 32 sequences x 8 heads at 8k, bf16 177 against 164,
-// Q8 196 against 167; 8 x 8 heads at 2k, 24.3 against 21.5 and 24.5 against 23.4; at 1k, 16.9
+// Q8 196 against 169; 8 x 8 heads at 2k, 24.3 against 21.5 and 24.5 against 23.4; at 1k, 16.9
 // against 16.9 and 16.3 against 18.8; but 24 rows at 8k 170 against 163 and 158 against 166, and 32
 // rows at D = 64 111 against 110 and 126 against 153. `places`: tokens x key heads there can be
 // (lengths are not known here).

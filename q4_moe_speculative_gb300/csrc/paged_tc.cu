@@ -296,26 +296,33 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     auto stage_q = [&](const Cursor& c) {
       constexpr int kChunks = D / 8;
       const int64_t at = seq_at(c);
-      constexpr int kMost = (kMaxN * kChunks + kScore - 1) / kScore;
-      uint4 in[kMost];   // (all loads before the first store)
+      // (all loads of a batch before its first store; the Q8 kernel has 96 registers: 32 rows, 32
+      // sequences x 8 heads at 8k, 169 us with batches of 2, 179 with 4, 183 with 8)
+      constexpr int kMost = (kMaxN * kChunks + kScore - 1) / kScore, kBatch = kQ8 ? 2 : kMost;
+#pragma unroll 1
+      for (int u0 = 0; u0 < kMost && (tid + u0 * kScore) / kChunks < N; u0 += kBatch) {
+        uint4 in[kBatch];
 #pragma unroll
-      for (int u = 0; u < kMost; ++u) {
-        const int idx = tid + u * kScore, r = idx / kChunks;
-        in[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < a.M) in[u] = reinterpret_cast<const uint4*>(q0 + at + sh.row_at[r])[idx % kChunks];
-      }
-#pragma unroll
-      for (int u = 0; u < kMost; ++u) {
-        const int idx = tid + u * kScore, r = idx / kChunks, ch = idx % kChunks;
-        if (r >= N) break;
-        uint4 x = in[u];
-        if constexpr (kQ8) {   // each four values as (0, 2, 1, 3), the order of widened codes
-          x.x = __byte_perm(in[u].x, in[u].y, 0x5410);
-          x.y = __byte_perm(in[u].x, in[u].y, 0x7632);
-          x.z = __byte_perm(in[u].z, in[u].w, 0x5410);
-          x.w = __byte_perm(in[u].z, in[u].w, 0x7632);
+        for (int u = 0; u < kBatch; ++u) {
+          const int idx = tid + (u0 + u) * kScore, r = idx / kChunks;
+          in[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < a.M)
+            in[u] = reinterpret_cast<const uint4*>(q0 + at + sh.row_at[r])[idx % kChunks];
         }
-        *reinterpret_cast<uint4*>(sQ + (ch >> 3) * N * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int idx = tid + (u0 + u) * kScore, r = idx / kChunks, ch = idx % kChunks;
+          if (r >= N) break;
+          uint4 x = in[u];
+          if constexpr (kQ8) {   // each four values as (0, 2, 1, 3), the order of widened codes
+            x.x = __byte_perm(in[u].x, in[u].y, 0x5410);
+            x.y = __byte_perm(in[u].x, in[u].y, 0x7632);
+            x.z = __byte_perm(in[u].z, in[u].w, 0x5410);
+            x.w = __byte_perm(in[u].z, in[u].w, 0x7632);
+          }
+          *reinterpret_cast<uint4*>(sQ + (ch >> 3) * N * 128 + r * 128 +
+                                    (((ch & 7) ^ (r & 7)) << 4)) = x;
+        }
       }
       fence_async();
       warp_arrive(&sh.qfull, lane);
