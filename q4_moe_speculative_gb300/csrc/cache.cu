@@ -30,28 +30,6 @@ struct RowsArgs {
   int chunks, per_chunk;   // the heads of a token in chunks of per_chunk
 };
 
-// Pairs of fp32 values.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pair(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 parts(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ void pairs_of(const uint4& w, f2 (&x)[4]) {
   x[0] = pair(bf16_lo(w.x), bf16_hi(w.x));
   x[1] = pair(bf16_lo(w.y), bf16_hi(w.y));

@@ -264,11 +264,11 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
         vs[nt][1] = vq.y;
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {   // s: log2 of p, before any mask
-        s[mt][nt][0] = __fmaf_rn(s[mt][nt][0], f0, -ref[mt][0]);
-        s[mt][nt][1] = __fmaf_rn(s[mt][nt][1], f1, -ref[mt][0]);
-        s[mt][nt][2] = __fmaf_rn(s[mt][nt][2], f0, -ref[mt][1]);
-        s[mt][nt][3] = __fmaf_rn(s[mt][nt][3], f1, -ref[mt][1]);
+      for (int mt = 0; mt < MT; ++mt) {   // s: scores in log2, before any mask
+        s[mt][nt][0] = __fmul_rn(s[mt][nt][0], f0);
+        s[mt][nt][1] = __fmul_rn(s[mt][nt][1], f1);
+        s[mt][nt][2] = __fmul_rn(s[mt][nt][2], f0);
+        s[mt][nt][3] = __fmul_rn(s[mt][nt][3], f1);
       }
     }
     const int wt0 = t0 + 16 * w4;   // the warp's first token
@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             const float s0 = s[mt][nt][2 * e], s1 = s[mt][nt][2 * e + 1];
-            float p0 = exp2_fast(s0), p1 = exp2_fast(s1);
+            float p0 = exp2_fast(__fsub_rn(s0, ref[mt][e]));
+            float p1 = exp2_fast(__fsub_rn(s1, ref[mt][e]));
             uint8_t* dst = sP + swz<2 * kTile>(row, 2 * w4 + nt) + 4 * q;
             if constexpr (C::kSplit) sum = __fadd_rn(sum, __fadd_rn(p0, p1));
             if constexpr (kQ8) {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
       for (int e = 0; e < 2; ++e) {
         top[mt][e] = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]),
                            fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
-        over |= top[mt][e] > (m[mt][e] == kNegInf ? kNegInf : kSlack);
+        over |= top[mt][e] > __fadd_rn(m[mt][e], kSlack);   // (-infinity: nothing seen yet)
       }
     make_p();
     if (__syncthreads_or(over)) {
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = __fadd_rn(top[mt][e], ref[mt][e]);
+          float x = top[mt][e];
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
           if (q == 0) red[w4 * C::kRows + row0 + 16 * mt + g + 8 * e] = x;
@@ -349,18 +350,13 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
           const float mn = fmaxf(m[mt][e], fmaxf(fmaxf(rp[0], rp[C::kRows]),
                                                  fmaxf(rp[2 * C::kRows], rp[3 * C::kRows])));
           const float f = m[mt][e] == kNegInf ? 0.f : exp2_fast(__fsub_rn(m[mt][e], mn));
-          const float move = __fsub_rn(ref[mt][e], mn == kNegInf ? 0.f : mn);
           m[mt][e] = mn;
+          ref[mt][e] = mn == kNegInf ? 0.f : mn;
           l[mt][e] = __fmul_rn(l[mt][e], f);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             o[mt][nt][2 * e] = __fmul_rn(o[mt][nt][2 * e], f);
             o[mt][nt][2 * e + 1] = __fmul_rn(o[mt][nt][2 * e + 1], f);
-          }
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            s[mt][nt][2 * e] = __fadd_rn(s[mt][nt][2 * e], move);
-            s[mt][nt][2 * e + 1] = __fadd_rn(s[mt][nt][2 * e + 1], move);
           }
         }
       make_p();

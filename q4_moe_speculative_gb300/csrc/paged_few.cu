@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Few<D, kQ8, NT>::kPerSm))
 #pragma unroll
     for (int e = 0; e < 2; ++e) rr[nt][e] = (8 * nt + 2 * q + e) / a.G;
 
-  // per query row: the reference (log2), what a score minus it may be before it has to move
-  // (-infinity: nothing seen yet), the lanes' shares of the normaliser, and the sums
+  // per query row: the reference (log2), what a score may be before it has to move (-infinity:
+  // nothing seen yet), the lanes' shares of the normaliser, and the sums
   float m[NT][2], lim[NT][2], l[NT][2], o[DT][NT][4];
   bool starts = true;
   int stage = 0;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Few<D, kQ8, NT>::kPerSm))
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = __fmaf_rn(s[nt][e], f[e >> 1], -m[nt][e & 1]);
+        for (int e = 0; e < 4; ++e) s[nt][e] = __fmul_rn(s[nt][e], f[e >> 1]);
         if (edge) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -294,13 +294,11 @@ __global__ void __launch_bounds__(32 * kWarps, (Few<D, kQ8, NT>::kPerSm))
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
             // up to the row's largest score so far, or down to the first ones
             const bool first = lim[nt][e] == kNegInf;
-            const float up = first ? (x == kNegInf ? 0.f : x) : fmaxf(x, 0.f);
-            const float c = first ? 0.f : exp2_fast(-up), move = -up;
-            m[nt][e] = __fadd_rn(m[nt][e], up);
-            if (x > kNegInf) lim[nt][e] = kSlack;
+            const float now = first ? (x == kNegInf ? 0.f : x) : fmaxf(x, m[nt][e]);
+            const float c = first ? 0.f : exp2_fast(__fsub_rn(m[nt][e], now));
+            m[nt][e] = now;
+            if (x > kNegInf) lim[nt][e] = __fadd_rn(now, kSlack);
             l[nt][e] = __fmul_rn(l[nt][e], c);
-            s[nt][e] = __fadd_rn(s[nt][e], move);
-            s[nt][2 + e] = __fadd_rn(s[nt][2 + e], move);
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) {
               o[dt][nt][e] = __fmul_rn(o[dt][nt][e], c);
@@ -313,7 +311,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Few<D, kQ8, NT>::kPerSm))
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float p0 = exp2_fast(s[nt][2 * h]), p1 = exp2_fast(s[nt][2 * h + 1]);
+          float p0 = exp2_fast(__fsub_rn(s[nt][2 * h], m[nt][0]));
+          float p1 = exp2_fast(__fsub_rn(s[nt][2 * h + 1], m[nt][1]));
           l[nt][0] = __fadd_rn(l[nt][0], p0);
           l[nt][1] = __fadd_rn(l[nt][1], p1);
           if constexpr (kQ8) {

@@ -41,7 +41,9 @@ constexpr int kScore = 256;               // softmax threads: two per token, hal
 constexpr int kMaxN = kTcMaxRows;                 // query rows, as a multiple of 32
 constexpr int kMaxRing = 4;
 constexpr int kInfo = 8;                  // tiles whose pages and scales are at hand
-constexpr float kNothing = -1e30f;        // reference of a row that has seen no token yet
+// Reference of a row that has seen no token yet: the least finite value, so that any score that
+// counts is above it by more than kSlack, or is equal to it and has the weight 1.
+constexpr float kNothing = -3.402823466e38f;
 constexpr uint32_t kWaitPolls = 1u << 20;
 
 struct TcArgs {
@@ -415,6 +417,14 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         tmem_wait_st();
         return true;
       };
+      // (the score is rounded as it was for the reference, so that the largest one is off by
+      // nothing from it whatever its size)
+      const f2 fk2 = pair(fk, fk), less = pair(-1.f, -1.f);
+      auto minus = [&](float& x, float& y, float rx, float ry) {
+        const float2 d = parts(fma2(pair(rx, ry), less, mul2(pair(x, y), fk2)));
+        x = d.x;
+        y = d.y;
+      };
       float l[16];
       for (bool settled = first;; settled = true) {   // P of the tile, at most twice
         if (settled) alive = move();
@@ -436,10 +446,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
 #pragma unroll
           for (int j4 = 0; j4 < 4; ++j4) {
             const float4 r = r4[j4];
-            t[4 * j4] = __fmaf_rn(t[4 * j4], fk, -r.x);
-            t[4 * j4 + 1] = __fmaf_rn(t[4 * j4 + 1], fk, -r.y);
-            t[4 * j4 + 2] = __fmaf_rn(t[4 * j4 + 2], fk, -r.z);
-            t[4 * j4 + 3] = __fmaf_rn(t[4 * j4 + 3], fk, -r.w);
+            minus(t[4 * j4], t[4 * j4 + 1], r.x, r.y);
+            minus(t[4 * j4 + 2], t[4 * j4 + 3], r.z, r.w);
           }
           mask(c, t);
           float top[4] = {t[0], t[1], t[2], t[3]};
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           sh.norm[tid] = norm == 0.f ? 0.f : __frcp_rn(norm);
           if (!whole && tid < a.M)
             *reinterpret_cast<float2*>(a.part_ml + 2 * (piece * a.M + tid)) =
-                make_float2(sh.ref[tid] == kNothing ? kNegInf : sh.ref[tid], norm);
+                make_float2(norm == 0.f ? kNegInf : sh.ref[tid], norm);
         }
         alive = wait(&sh.odone[i & 1], (i >> 1) & 1);
         alive = !score_any(!alive);
