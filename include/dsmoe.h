@@ -506,11 +506,9 @@ ds_status ds_qk_norm_rope_write(const ds_norm_rope_args* args, const uint16_t* v
  * max_pages * page_tokens when larger; page table entries outside 0 .. n_pages - 1 are
  * skipped as if their tokens were not there, and entries behind the last needed page are
  * not read. Scores, softmax and sums in fp32 on the tensor cores; for the product with the
- * values, p (times the value's scale in a Q8 cache) is a high and a low bf16 part, or, with
- * more than 64 rows per key head (more than 32 over a bf16 cache), may be one bf16 value, of
- * which the softmax's sum over a bf16 cache is taken as well. The result does not depend on
- * timing, but it may in its last bits on the other sequences of the call and on max_pages,
- * which decide how the work is cut.
+ * values, p (times the value's scale in a Q8 cache) is a high and a low bf16 part, off by at
+ * most 2^-16 relative. The result does not depend on timing, but it may in its last bits on
+ * the other sequences of the call and on max_pages, which decide how the work is cut.
  * Limits: 0 <= n_seqs <= 4096 (0 enqueues nothing), 1 <= n_rows <= 8, 1 <= max_pages,
  * max_pages * page_tokens <= 2^24, n_heads a multiple of the cache's n_kv_heads, n_rows * H
  * <= 128 (else DS_ERR_UNSUPPORTED), scale and scale * 1.5 finite; q and out 16-byte

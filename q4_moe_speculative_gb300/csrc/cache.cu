@@ -61,11 +61,6 @@ __device__ __forceinline__ bool slot_ok(const CacheView& c, int slot) {
   return slot >= 0 && (slot >> c.page_shift) < c.pages;
 }
 
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // The larger of two bf16 pairs of magnitudes, NaN above all.
 __device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
   uint32_t r;

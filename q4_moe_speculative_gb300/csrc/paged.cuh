@@ -34,7 +34,7 @@ cudaError_t launch_few(const PagedArgs& p, int D, cudaStream_t s);
 
 // paged_tc.cu: tiles of 128 tokens, one CTA per SM. The most query rows per key head: tensor
 // memory holds S, O and two buffers of the sums, 4 N columns of 512 (and up to 96 rows a second
-// buffer of S, up to 64 the second part of O).
+// buffer of S, up to 64 columns of O for either part of P).
 constexpr int kTcMaxRows = 128;
 cudaError_t launch_tc(const PagedArgs& p, int D, cudaStream_t s);
 

@@ -25,11 +25,11 @@
 // bf16; the key's scale multiplies the score, the value's scale P. The reference m of a row
 // moves only when a score exceeds it by 2^8 (P stays in range and bf16's relative precision
 // does not depend on it), so the usual tile needs no exchange of maxima and no rescaling: the
-// CTA votes on it at the barrier that publishes P anyway. P is rounded once to bf16, half a
-// step of 2^-8 relative per term, and the normaliser sums the rounded values, so that the
-// weights add up to one; with a Q8 cache, where the value's scale is part of P, P goes in as a
-// high and a low part instead. Its bound is the issue of instructions: 4 sequences x 8 heads
-// of 8k tokens, 64 rows, 52 us for 132 MB of bf16 and 58 us for 68 MB of Q8.
+// CTA votes on it at the barrier that publishes P anyway. P (with a Q8 cache the value's scale is
+// in it) goes in as a high and a low bf16 part, off by 2^-16 relative; rounded once it would be
+// off by 2^-8, and a result by 1.4 times its own rounding, for 52 instead of 60 us below. Its
+// bound is the issue of instructions: 4 sequences x 8 heads of 8k tokens, 64 rows, 60 us for 132
+// MB of bf16 as for 68 MB of Q8.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -49,11 +49,10 @@ struct Shape {
   static constexpr int RB = D * (kQ8 ? 1 : 2);          // bytes of a cached row
   static constexpr int kMat = kTile * RB;
   static constexpr int kStage = 2 * kMat + (kQ8 ? 2 * kTile * 4 : 0);
-  static constexpr bool kSplit = kQ8;                   // P as a high and a low part
   static constexpr int kQ = kRows * D * 2;
-  static constexpr int kP = kRows * kTile * 2;
+  static constexpr int kP = kRows * kTile * 2;          // one of the two parts of P
   static constexpr int kRed = 4 * kRows * 4;
-  static constexpr int kFixed = kQ + kP * (kSplit ? 2 : 1) + kRed + 64;
+  static constexpr int kFixed = kQ + 2 * kP + kRed + 64;
   static constexpr int kFit = (227 * 1024 - kFixed) / kStage;
   static constexpr int kStages = kFit > 5 ? 5 : kFit;
   static constexpr int kSmem = kFixed + kStages * kStage;
@@ -67,7 +66,7 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* sQ = sm + S * C::kStage;
   uint8_t* sP = sQ + C::kQ;
-  float* red = reinterpret_cast<float*>(sP + C::kP * (C::kSplit ? 2 : 1));   // [4][kRows]
+  float* red = reinterpret_cast<float*>(sP + 2 * C::kP);   // [4][kRows]
   bool* there = reinterpret_cast<bool*>(red + 4 * C::kRows);   // [stage][4] 16-token groups
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w4 = warp & 3, row0 = (warp >> 2) * MT * 16;
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
             float p0 = exp2_fast(__fsub_rn(s0, ref[mt][e]));
             float p1 = exp2_fast(__fsub_rn(s1, ref[mt][e]));
             uint8_t* dst = sP + swz<2 * kTile>(row, 2 * w4 + nt) + 4 * q;
-            if constexpr (C::kSplit) sum = __fadd_rn(sum, __fadd_rn(p0, p1));
+            sum = __fadd_rn(sum, __fadd_rn(p0, p1));
             if constexpr (kQ8) {
               p0 = __fmul_rn(p0, vs[nt][0]);
               p1 = __fmul_rn(p1, vs[nt][1]);
@@ -310,11 +309,8 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
             }
             const uint32_t w = pack2(p0, p1);
             *reinterpret_cast<uint32_t*>(dst) = w;
-            if constexpr (C::kSplit)
-              *reinterpret_cast<uint32_t*>(dst + C::kP) =
-                  pack2(__fsub_rn(p0, bf16_lo(w)), __fsub_rn(p1, bf16_hi(w)));
-            else
-              sum = __fadd_rn(sum, __fadd_rn(bf16_lo(w), bf16_hi(w)));
+            *reinterpret_cast<uint32_t*>(dst + C::kP) =
+                pack2(__fsub_rn(p0, bf16_lo(w)), __fsub_rn(p1, bf16_hi(w)));
           }
           lt[mt][e] = sum;
         }
@@ -415,12 +411,10 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
           ldsm_x4(pb + swz<2 * kTile>(row0 + 16 * mt + (lane & 15), 2 * ks + (lane >> 4)), pf);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816(o[mt][nt], pf, b[nt][0], b[nt][1]);
-          if constexpr (C::kSplit) {
-            ldsm_x4(pb + C::kP + swz<2 * kTile>(row0 + 16 * mt + (lane & 15), 2 * ks + (lane >> 4)),
-                    pf);
+          ldsm_x4(pb + C::kP + swz<2 * kTile>(row0 + 16 * mt + (lane & 15), 2 * ks + (lane >> 4)),
+                  pf);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(o[mt][nt], pf, b[nt][0], b[nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[mt][nt], pf, b[nt][0], b[nt][1]);
         }
       }
     }
@@ -440,9 +434,9 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
               if (t0 + t >= seen0 + rr[mt][e]) continue;
               const int row = row0 + 16 * mt + g + 8 * e;
               const uint8_t* ps = sP + swz<2 * kTile>(row, t >> 3) + 2 * (t & 7);
-              float p = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(ps));
-              if constexpr (C::kSplit)
-                p = __fadd_rn(p, bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(ps + C::kP)));
+              const float p =
+                  __fadd_rn(bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(ps)),
+                            bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(ps + C::kP)));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 o[mt][nt][2 * e] = __fmaf_rn(p, bf16_lo(v[nt]), o[mt][nt][2 * e]);
@@ -643,19 +637,23 @@ auto with_rows(int M, F&& f) {
 // More rows: the tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and
 // end, and is ahead from several tiles per SM on. k_paged | paged_tc, us, 4 sequences x 8 heads:
 //   tokens per sequence        500      1k       2k       4k        8k       64k
-//   bf16, D = 128, 40 rows   12 | 16           21 | 19  31 | 25   51 | 34  335 | 158
-//                  96 rows   15 | 20           26 | 23  38 | 29   63 | 39  403 | 166
-//                 128 rows   19 | 25  22 | 25  32 | 29  46 | 36   (16k: 134 | 77)
-//   Q8,   D = 128, 64 rows   13 | 19           22 | 24  34 | 29   58 | 42  389 | 207
-//                  96 rows            19 | 24  28 | 29  45 | 35   76 | 52
-//   bf16, D = 64,  64 rows                     16 | 17            40 | 31  257 | 137
-//   Q8,   D = 64,  64 rows                     17 | 19            43 | 39  282 | 189
-// One head of 32k, D = 128, 96 rows: bf16 17 | 17, Q8 19 | 19. From 25 rows on it is ahead of
+//   bf16, D = 128, 40 rows   13 | 16  15 | 16  23 | 20  35 | 24   60 | 34  397 | 160
+//                  96 rows   17 | 20  19 | 21  30 | 25  45 | 29   76 | 43  505 | 203
+//                 128 rows   21 | 25  24 | 26  38 | 32  55 | 40   92 | 57  610 | 290
+//   Q8,   D = 128, 64 rows   13 | 20  15 | 19  23 | 26  35 | 29   60 | 42  405 | 207
+//                  96 rows   16 | 24  19 | 25  29 | 32  45 | 40   77 | 60  525 | 312
+//                 128 rows   20 | 33  24 | 38  36 | 38  56 | 48   96 | 69  650 | 364
+//   bf16, D = 64,  64 rows   11 | 16  13 | 16  18 | 18  27 | 22   44 | 30  290 | 136
+//                 128 rows   17 | 24  19 | 24  26 | 28  39 | 36   66 | 51  434 | 258
+//   Q8,   D = 64,  64 rows   11 | 18  12 | 19  18 | 22  26 | 26   45 | 38  301 | 187
+//                  96 rows   13 | 25  16 | 28  22 | 31  34 | 32   57 | 46  382 | 216
+// One head of 32k, D = 128, 96 rows: bf16 19 | 18, Q8 20 | 20. From 25 rows on it is ahead of
 // paged_few.cu as well at D = 128: 32 rows, 32 sequences x 8 heads at 8k, bf16 177 against 164,
 // Q8 196 against 169; 8 x 8 heads at 2k, 24.3 against 21.5 and 24.5 against 23.4; at 1k, 16.9
 // against 16.9 and 16.3 against 18.8; but 24 rows at 8k 170 against 163 and 158 against 166, and 32
 // rows at D = 64 111 against 110 and 126 against 153. `places`: tokens x key heads there can be
-// (lengths are not known here).
+// (lengths are not known here: short ones in a table with room for long ones pay paged_tc.cu's
+// beginning).
 Kernel which(int M, int D, bool q8, int64_t places) {
   const bool lengthy = places >= (int64_t)(q8 ? 4 : 2) * (128 / D) * 128 * device_sm_count();
   static_assert(kPagedMaxRows <= kTcMaxRows, "it takes any rows");

@@ -8,22 +8,23 @@
 //                    K-major; TMEM lane = token, column = query row (N = M up to a multiple
 //                    of 32);
 //   O^T += V^T P^T   A = the value tile, read MN-major (its rows are tokens, the MMA's K),
-//                    B = P [128 tokens][N rows], also MN-major, a high bf16 part and,
-//                    up to 64 rows, a low one in columns of its own; TMEM lane = value
-//                    dimension, column = query row (of either part). With one part a weight
-//                    is off by half a step of bf16, as the results are; over a bf16 cache
-//                    the normaliser sums what is multiplied.
+//                    B = P [128 tokens][N rows], also MN-major, as a high and a low bf16
+//                    part; TMEM lane = value dimension, column = query row (of either part:
+//                    see Parts).
 // Roles: warps 0-7 turn scores into P (a row's reference maximum moves only when a score
 // exceeds it by 2^8, agreed by one barrier vote per tile), keep the normaliser of their
 // token in TMEM, and write the results; two warps copy tiles page by page, by TMA straight
 // into the swizzled operand layout (bf16) or as raw codes that eight more warps widen to bf16
 // (Q8); one thread each of the last two warps issues the MMAs of S and of O. Up to 96 rows S is
 // double-buffered: the next tile's scores are computed while this tile's are exponentiated.
-// Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 38.5 us with the join,
-// which takes 6 to 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 rows 158 us, 96
-// rows 166 (6.3 TB/s, bound by memory); Q8 (0.54 GB) 207, and D = 64, bf16, 137 (0.52 GB), bound
-// by the chain of a tile through widening, scores and P. (Bringing the tiles behind the ring
-// into L2 ahead of time costs: 96 rows 176 us without, 190 two tiles ahead, 241 with four.)
+// Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 43.5 us with the join,
+// which takes 6 to 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 and 64 rows 160 us
+// (6.6 TB/s, bound by memory), 96 rows 203, 128 rows 290; Q8 (0.54 GB), 64 rows 206, 96 rows 311,
+// 128 rows 363, and D = 64, bf16, 64 rows 135 (0.52 GB), bound by the chain of a tile through
+// widening, scores and P: beyond 64 rows shared memory has no room for two tiles of all of them.
+// (With one part of P beyond 64 rows: 96 rows 165 us, Q8 234; 128 rows 247, Q8 284; results off
+// by 1.4 times their own rounding. Bringing the tiles behind the ring into L2 ahead of time
+// costs 8% two tiles ahead, 37% with four.)
 // A token of a bf16 cache that only some rows see may hold infinities, and 0 x infinity is
 // not 0: where one of its values is not finite they are cleared before the product, and the
 // (at most 7) such tokens are added row by row when the run ends. Every wait is bounded; a
@@ -49,12 +50,30 @@ constexpr uint32_t kWaitPolls = 1u << 20;
 struct TcArgs {
   PagedArgs p;
   int N;            // query rows, padded to a multiple of 32
-  int parts;        // parts of P side by side: a high and a low one, or 1
   int k_ring, v_ring;   // stages of the key and of the value operand tiles
   int raw;          // stages of raw codes (Q8)
   int p_bufs;       // 2: P of one tile is multiplied while the next is formed
   int s_bufs;       // 2: the next tile's scores are computed while this tile's are read
   uint32_t tmem_cols;
+};
+
+// Where the two parts of P are among its columns, in chunks of 64 (128 bytes of a token), and what
+// they are added to in O. Up to 64 rows: side by side, and O has columns of either, so that
+// one MMA does both. 128 rows: two chunks each, two MMAs into the same columns (tensor memory
+// has 512). 96 rows: high 0..95, low 64..95, low 0..63, so that one MMA takes two whole chunks
+// (its last 32 columns are the low part of rows 64..95) and a second one adds the third.
+template <bool kBeside>   // up to 64 rows
+struct Parts {
+  int N;
+  __host__ __device__ int p_chunks() const { return (2 * N + 63) / 64; }
+  __host__ __device__ int o_columns() const { return kBeside ? 2 * N : 128; }
+  // of the low part of rows c .. c + 15, in P
+  __device__ int low_in_p(int c) const {
+    return kBeside ? N + c : (N == 96 && c >= 64 ? c + 32 : 128 + c);
+  }
+  // and in O, where it has columns there
+  __device__ bool low_apart(int c) const { return kBeside || (N == 96 && c >= 64); }
+  __device__ int low_in_o(int c) const { return kBeside ? N + c : c + 32; }
 };
 
 template <int D, bool kQ8>
@@ -208,8 +227,7 @@ __device__ __forceinline__ float over_lanes(float (&v)[16], int lane, Op op) {
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// kSplit: P in two parts.
-template <int D, bool kQ8, bool kSplit>
+template <int D, bool kQ8, bool kBeside>
 __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     k_paged_tc(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap k_map,
                const __grid_constant__ CUtensorMap v_map) {
@@ -220,10 +238,11 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   const uint32_t pad = (1024u - (smem_at(smem_raw) & 1023u)) & 1023u;
   uint8_t* const base = smem_raw + pad;
   TcSmem& sh = *reinterpret_cast<TcSmem*>(base);
-  const int N = ta.N, NP = ta.N * ta.parts;   // columns of S, of P and O
+  const int N = ta.N;                                           // columns of S
+  const Parts<kBeside> cols{N};
   uint8_t* const sQ = base + kSmallBytes;                       // [halves][N][128 B]
-  const uint32_t p_size = (uint32_t)((NP + 63) / 64) * kTok * 128;
-  uint8_t* const sP = sQ + T::kHalves * N * 128;                // [buffers][NP / 64][tokens][128 B]
+  const uint32_t p_size = (uint32_t)cols.p_chunks() * kTok * 128;
+  uint8_t* const sP = sQ + T::kHalves * N * 128;                // [buffers][chunks][tokens][128 B]
   uint8_t* const sK = sP + ta.p_bufs * p_size;                  // [ring][halves][tokens][128 B]
   uint8_t* const sV = sK + ta.k_ring * T::kMat;
   uint8_t* const sRaw = sV + ta.v_ring * T::kMat;               // Q8: [2][raw][tokens][D]
@@ -340,8 +359,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       const int t0 = cur.tile * kTok, tok = t0 + tk;
       const int seen0 = cur.len - (a.R - 1);            // row r sees t < seen0 + r
       const uint32_t tS = tmem + lane_at + (i & (ta.s_bufs - 1)) * N;
-      const uint32_t tL = tO + NP + (i & 1) * N;
-      const uint32_t tLnew = tO + NP + (~i & 1) * N;
+      const uint32_t tL = tO + cols.o_columns() + (i & 1) * N;
+      const uint32_t tLnew = tO + cols.o_columns() + (~i & 1) * N;
       uint8_t* const p_at = sP + (i & (ta.p_bufs - 1)) * p_size + tk * 128;
       const int slot = i % kInfo;
       // what is known of the tile, its scores, and P's buffer (free after the tile p_bufs before)
@@ -399,8 +418,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         for (int c = col0; c < col0 + half; c += 16) {
 #pragma unroll 1
           for (int x = 0; x < 3; ++x) {    // O, its low part, the sums
-            if (x == 1 && !kSplit) continue;
-            const uint32_t at = (x == 2 ? tL : tO + x * N) + c;
+            if (x == 1 && !cols.low_apart(c)) continue;
+            const uint32_t at = x == 2 ? tL + c : tO + (x ? cols.low_in_o(c) : c);
             __syncwarp();
             sm100::tmem_ld16(at, t);
 #pragma unroll
@@ -462,13 +481,9 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             for (int e = 0; e < 4; ++e) {
               const int j = 8 * c8 + 2 * e;
               float p0 = exp2_fast(t[j]), p1 = exp2_fast(t[j + 1]);
-              if (!kSplit && !kQ8) {   // (the sums of what is multiplied: weights add up to 1)
-                hi4[e] = pack2(p0, p1);
-                p0 = bf16_lo(hi4[e]);
-                p1 = bf16_hi(hi4[e]);
-              }
-              l[j] = __fadd_rn(l[j], p0);
-              l[j + 1] = __fadd_rn(l[j + 1], p1);
+              const float2 sum = parts(add2(pair(l[j], l[j + 1]), pair(p0, p1)));
+              l[j] = sum.x;
+              l[j + 1] = sum.y;
               if constexpr (kQ8) {
                 p0 = __fmul_rn(p0, vs0);
                 p1 = __fmul_rn(p1, vs0);
@@ -480,10 +495,10 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
                 sh.pe[tok - seen0][c + j] = p0;
                 sh.pe[tok - seen0][c + j + 1] = p1;
               }
-              if (kSplit || kQ8) hi4[e] = pack2(p0, p1);
-              if (kSplit) {
-                lo4[e] = pack2(__fsub_rn(p0, bf16_lo(hi4[e])), __fsub_rn(p1, bf16_hi(hi4[e])));
-              }
+              hi4[e] = pack2(p0, p1);
+              const float2 rest =
+                  parts(fma2(pair(bf16_lo(hi4[e]), bf16_hi(hi4[e])), less, pair(p0, p1)));
+              lo4[e] = pack2(rest.x, rest.y);
             }
             auto put = [&](int ch, const uint32_t(&x)[4]) {
               *reinterpret_cast<uint4*>(p_at + (ch >> 3) * kTok * 128 +
@@ -491,7 +506,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
                   make_uint4(x[0], x[1], x[2], x[3]);
             };
             put(c / 8 + c8, hi4);
-            if (kSplit) put((N + c) / 8 + c8, lo4);
+            put(cols.low_in_p(c) / 8 + c8, lo4);
           }
           __syncwarp();
           tmem_st(tLnew + c, l);
@@ -567,8 +582,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           float o[16];
           __syncwarp();
           sm100::tmem_ld16(tO + c, o);
-          if (kSplit) {
-            sm100::tmem_ld16(tO + N + c, l);
+          if (cols.low_apart(c)) {
+            sm100::tmem_ld16(tO + cols.low_in_o(c), l);
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = __fadd_rn(o[j], l[j]);
           }
@@ -780,7 +795,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   } else {
     // ---------------------------------------------------------------- MMAs of the values ---
     const bool leader = elect_one();
-    const uint32_t idesc = sm100::idesc_bf16_f32(kTok, NP) | kMajorMN;
+    const uint32_t idesc = sm100::idesc_bf16_f32(kTok, cols.o_columns()) | kMajorMN;
+    const uint32_t idesc2 = sm100::idesc_bf16_f32(kTok, 2 * N - 128) | kMajorMN;   // (!kBeside)
     // (D = 64: the upper half of the M rows repeats the lower one)
     const uint64_t v_desc = desc_mn_sw128(smem_at(sV), D == 128 ? kTok * 128 : 0);
     const uint64_t p_desc = desc_mn_sw128(smem_at(sP), kTok * 128);
@@ -797,8 +813,11 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       const bool fresh = i == 0 || cur.tile == 0;
       if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < kTok / 16; ++ks)   // 16 tokens: 2 KB
+        for (int ks = 0; ks < kTok / 16; ++ks) {   // 16 tokens: 2 KB
           sm100::mma_bf16(tmem + ta.s_bufs * N, vd + ks * 128, pd + ks * 128, idesc, !(fresh && ks == 0));
+          if (!kBeside)   // the chunks from the third on
+            sm100::mma_bf16(tmem + ta.s_bufs * N, vd + ks * 128, pd + kTok * 16 + ks * 128, idesc2, 1);
+        }
         sm100::mma_commit(&sh.odone[i & 1]);
         sm100::mma_commit(&sh.vfree[st]);
       }
@@ -816,17 +835,17 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
 }
 
 // Shared memory of a call.
-template <int D, bool kQ8>
+template <int D, bool kQ8, bool kBeside>
 int smem_bytes(const TcArgs& a) {
   using T = Tc<D, kQ8>;
   return 1024 + kSmallBytes + T::kHalves * a.N * 128 +
-         a.p_bufs * ((a.N * a.parts + 63) / 64) * kTok * 128 + (a.k_ring + a.v_ring) * T::kMat +
+         a.p_bufs * Parts<kBeside>{a.N}.p_chunks() * kTok * 128 + (a.k_ring + a.v_ring) * T::kMat +
          2 * a.raw * T::kRawMat + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
 }
 
-template <int D, bool kQ8, bool kSplit>
+template <int D, bool kQ8, bool kBeside>
 cudaError_t start_as(const TcArgs& a, int room, int smem, cudaStream_t s) {
-  const auto kernel = k_paged_tc<D, kQ8, kSplit>;
+  const auto kernel = k_paged_tc<D, kQ8, kBeside>;
   static OncePerDevice ready;
   const cudaError_t e = ready.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
@@ -843,29 +862,31 @@ cudaError_t start_as(const TcArgs& a, int room, int smem, cudaStream_t s) {
   return launch_pdl(kernel, dim3(a.p.grid), Tc<D, kQ8>::kThreads, smem, s, a, k_map, v_map);
 }
 
-template <int D, bool kQ8>
-cudaError_t start(const PagedArgs& p, cudaStream_t s) {
+template <int D, bool kQ8, bool kBeside>
+cudaError_t start_with(const PagedArgs& p, cudaStream_t s) {
   TcArgs a{};
   a.p = p;
   a.N = p.M <= 32 ? 32 : (p.M <= 64 ? 64 : (p.M <= 96 ? 96 : 128));
-  a.parts = a.N <= 64 ? 2 : 1;
   a.s_bufs = a.N <= 96 ? 2 : 1;   // (tensor memory has 512 columns)
   const int room = 227 * 1024;
-  // The least first, then what fits: a second buffer of P (Q8, 64 rows, D = 128: 207 us with two,
-  // 234 with one and a second value tile), a second value tile, deeper rings.
+  // The least first, then what fits: two stages of codes, a second buffer of P (Q8, 64 rows, D =
+  // 128: 207 us with two, 234 with one and a second value tile; bf16, 96 rows: 203 with two and a
+  // second value tile, 241 with two and a second key tile, 245 with one and both), a second
+  // value tile, deeper rings. (Q8, 96 rows: 311 us with any that fits.)
   a.p_bufs = 1;
-  a.k_ring = a.v_ring = kQ8 ? 1 : 2;
-  a.raw = kQ8 ? 2 : 0;
+  a.k_ring = a.v_ring = 1;
+  a.raw = kQ8 ? 1 : 0;
   auto grow = [&](int TcArgs::*what, int most) {
     while (a.*what < most) {
       ++(a.*what);
-      if (smem_bytes<D, kQ8>(a) <= room) continue;
+      if (smem_bytes<D, kQ8, kBeside>(a) <= room) continue;
       --(a.*what);
       break;
     }
   };
+  if (kQ8) grow(&TcArgs::raw, 2);
   grow(&TcArgs::p_bufs, 2);
-  if (kQ8) grow(&TcArgs::v_ring, 2);
+  grow(&TcArgs::v_ring, 2);
   if (kQ8) {
     grow(&TcArgs::k_ring, 2);
     grow(&TcArgs::raw, kMaxRing);
@@ -878,15 +899,19 @@ cudaError_t start(const PagedArgs& p, cudaStream_t s) {
   // back the scores are done, and two further back P (the two buffers of S).
   static_assert(kMaxRing + 2 + 2 <= kInfo, "slots of the tile information");
   a.tmem_cols = 128;
-  while ((int)a.tmem_cols < (a.s_bufs + 2 + a.parts) * a.N) a.tmem_cols *= 2;
+  while ((int)a.tmem_cols < (a.s_bufs + 2) * a.N + Parts<kBeside>{a.N}.o_columns()) a.tmem_cols *= 2;
   // (the results of a run pass through P's buffers)
-  if (a.p_bufs * ((a.N * a.parts + 63) / 64) * 128 < (32 + (kQ8 ? 0 : 14)) * 4)
+  if (a.p_bufs * Parts<kBeside>{a.N}.p_chunks() * 128 < (32 + (kQ8 ? 0 : 14)) * 4)
     return cudaErrorInvalidValue;
   // (at least half of the SM's shared memory, so that one CTA has the SM's tensor memory)
-  int smem = smem_bytes<D, kQ8>(a);
+  int smem = smem_bytes<D, kQ8, kBeside>(a);
   smem = smem < 120 * 1024 ? 120 * 1024 : smem;
-  if (a.N <= 64) return start_as<D, kQ8, true>(a, room, smem, s);
-  return start_as<D, kQ8, false>(a, room, smem, s);
+  return start_as<D, kQ8, kBeside>(a, room, smem, s);
+}
+
+template <int D, bool kQ8>
+cudaError_t start(const PagedArgs& p, cudaStream_t s) {
+  return p.M <= 64 ? start_with<D, kQ8, true>(p, s) : start_with<D, kQ8, false>(p, s);
 }
 
 }  // namespace paged_tc

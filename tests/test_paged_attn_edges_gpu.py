@@ -82,3 +82,63 @@ def test_scores_of_any_size(q8, D, scale, M, wide):
         err = (got - want).abs()
         tol = ref.HALF_BF16 * want.abs() + size * (2.0 ** -16 + max(lens) * 2 * ref.U32)
         assert bool((err <= tol).all()), (exp, float((err - tol).max()))
+
+
+# -------------------------------------------------------------------------- weights in two parts
+@pytest.mark.parametrize("M,wide", KERNELS + [(33, False), (64, False), (96, False), (64, True),
+                                              (65, True), (96, True), (97, True)])
+@pytest.mark.parametrize("D,q8", [(128, False), (64, True), (128, True), (64, False)])
+def test_weights_have_two_parts(D, q8, M, wide):
+    # Values chosen so that everything cancels at a weight of 0.75 + 2^-9, which lies half way
+    # between two bf16 values: what is left of a result is 2^-9 of sum p |v| or less, and its
+    # own rounding to bf16 is 2^-17 of it, so an error of the weight shows. A weight in two
+    # bf16 parts is off by (2^-8)^2 relative; the score by fp32 (magnitudes below 1).
+    n, page = 300, 16
+    q, cache, table, lengths = problem([n, n], 1, M, 1, D, page, q8, seed=M, wide=wide)
+    g = torch.Generator()
+    g.manual_seed(M + D)
+    weights = torch.tensor([0.75 + 2.0 ** -9, 0.75, 0.75 - 3 * 2.0 ** -10], dtype=torch.float64)
+    pick = torch.randint(0, 3, (2, M), generator=g)
+    # a query of two values whose sum reaches the wanted score closely: log(w) = q . (1, 1)
+    s = torch.log(weights)[pick]
+    hi = s.float().to(torch.bfloat16)
+    q.zero_()
+    q[:, 0, :, 0] = hi.to(DEV)
+    q[:, 0, :, 1] = (s - hi.double()).float().to(torch.bfloat16).to(DEV)
+    kind = torch.randint(0, 4, (n,), generator=g)          # 0, 1: weight w; 2: 1; 3: 1, the rest
+    count = [int((kind <= 1).sum()), int((kind == 2).sum()), int((kind == 3).sum())]
+    w0 = float(weights[0])
+    keys = torch.zeros(n, 1, D)
+    keys[kind <= 1, 0, :2] = 1.0
+    vb = torch.rand(D, generator=g, dtype=torch.float64) + 0.5
+    if q8:
+        unit = [2.0 ** -6, 2.0 ** -5, 2.0 ** -12]
+        code = torch.round(vb / unit[0])
+        vb = code * unit[0]
+        ca = torch.round(-count[0] * w0 * vb / count[1] / unit[1])
+        va = ca * unit[1]
+        cc = torch.round(-(count[0] * w0 * vb + count[1] * va) / count[2] / unit[2]).clamp(-127, 127)
+        codes = torch.stack((code, ca, cc))
+        assert float(codes.abs().max()) <= 127
+        idx = (kind - 1).clamp(min=0)
+        vals, scales = codes[idx][:, None], torch.tensor(unit, dtype=torch.float64)[idx][:, None]
+    else:
+        vb = vb.to(torch.bfloat16).double()
+        va = (-count[0] * w0 * vb / count[1]).to(torch.bfloat16).double()
+        vc = (-(count[0] * w0 * vb + count[1] * va) / count[2]).to(torch.bfloat16).double()
+        vals, scales = torch.stack((vb, va, vc))[(kind - 1).clamp(min=0)][:, None], None
+    for b in range(2):
+        slots = slots_of(table, page, b, n)
+        if q8:
+            put(cache, "k", slots, keys.to(torch.int8), torch.ones(n, 1))
+            put(cache, "v", slots, vals.to(torch.int8), scales.float())
+        else:
+            put(cache, "k", slots, keys.to(torch.bfloat16))
+            put(cache, "v", slots, vals.to(torch.bfloat16))
+    got = dsm.paged_attention(q, cache, table, lengths, scale=1.0).cpu().double()
+    want, mag, _, top = ref.attention(q, cache, table, lengths, 1.0)
+    assert float((want.abs() / mag).max()) < 2.0 ** -7
+    tol = ref.HALF_BF16 * want.abs() + mag * (2.0 ** -16 + 2 * (top * 8 * ref.U32 + 2.0 ** -21) +
+                                              n * 2 * ref.U32)
+    err = (got - want).abs()
+    assert bool((err <= tol).all()), float((err / mag).max())
