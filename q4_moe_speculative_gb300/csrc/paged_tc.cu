@@ -714,8 +714,12 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         }
       }
       if (edge) {   // clear what is no value, and the partly seen values that are not finite
-        alive = wait(&sh.vedge, edges++ & 1);
-        if (!__all_sync(0xffffffffu, alive)) break;
+        const uint32_t edge_par = edges++ & 1;
+        alive = wait(&sh.vedge, edge_par);
+        if (!__all_sync(0xffffffffu, alive)) {   // (no full[] counts these copies)
+          sm100::mbar_wait(&sh.vedge, edge_par, kWaitPolls);
+          break;
+        }
         unsigned apart = 0;
         for (int r = lane; r < kTok; r += 32) {
           bool none = t0 + r >= cur.len || !(there >> (r >> a.c.page_shift) & 1u);
