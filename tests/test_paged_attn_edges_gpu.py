@@ -142,3 +142,95 @@ def test_weights_have_two_parts(D, q8, M, wide):
                                               n * 2 * ref.U32)
     err = (got - want).abs()
     assert bool((err <= tol).all()), float((err / mag).max())
+
+
+# ------------------------------------------------------------ new tokens that only some rows see
+def attention64(q, cache, table, lengths, scale):
+    """What paged_ref.attention gives without its third part, in fp64 on the device."""
+    B, R, H, D = q.shape
+    kv, page = cache.k.shape[1:3]
+    out = torch.zeros(q.shape, dtype=torch.float64, device=DEV)
+    mag, top = torch.zeros_like(out), 0.0
+    for b in range(B):
+        n = int(lengths[b])
+        slots = slots_of(table, page, b, n).to(DEV)
+        k, v = (ref.flat(getattr(cache, s))[slots].double() for s in ("k", "v"))
+        if cache.q8:
+            k = k * ref.flat(cache.k_scale)[slots].double()[..., None]
+            v = v * ref.flat(cache.v_scale)[slots].double()[..., None]
+        for r in range(R):
+            see = n - (R - 1 - r)
+            if see <= 0:
+                continue
+            x = q[b, r].double().view(kv, H // kv, D)
+            p = torch.softmax(torch.einsum("hgd,thd->hgt", x, k[:see]) * scale, -1)
+            out[b, r] = torch.einsum("hgt,thd->hgd", p, v[:see]).reshape(H, D)
+            mag[b, r] = torch.einsum("hgt,thd->hgd", p, v[:see].abs()).reshape(H, D)
+            top = max(top, float(torch.einsum("hgd,thd->hgt", x.abs(), k[:see].abs()).max() * scale))
+    return out, mag, top
+
+
+def tolerance(out, mag, top, n, D):
+    """Per element, as in paged_ref.check_attention, with weights of two bf16 parts: 2^-16. (A
+    weight below 2^-126 of the largest may be taken as 0: n of them times values below 2^12 are
+    far below 1e-30.)"""
+    score = top * (D + 4) * 2 * ref.U32 + 2.0 ** -21
+    return ref.HALF_BF16 * out.abs() + mag * (2.0 ** -16 + 2 * score + n * 2 * ref.U32) + 1e-30
+
+
+@pytest.mark.parametrize("R,G,wide", [(8, 1, False), (4, 5, False), (8, 3, False), (5, 8, False),
+                                      (8, 16, False), (7, 4, True), (5, 8, True), (5, 16, True),
+                                      (8, 16, True)])
+@pytest.mark.parametrize("D,q8", [(128, False), (64, False), (128, True), (64, True)])
+@pytest.mark.parametrize("rising", [False, True])
+def test_new_tokens_that_some_rows_see(R, G, wide, D, q8, rising):
+    # One new token holds NaN in its keys, or infinities in a few of its values: rows before it
+    # are those of the clean cache, rows from it on are NaN, or infinite in those values and
+    # right in the others. Lengths put the new tokens on both sides of a tile's border (16, 64
+    # and 128 tokens); 8 heads of these sequences give every CTA several tiles. rising: the last
+    # tokens have scores that move every row's reference.
+    kv, page = 8, 64
+    lens = [5 * 128 + 1, 6 * 128 + 3, 8 * 128 + 5, R - 1]
+    if wide or R * G <= 24:
+        lens = [5 * 128 + 1, 6 * 128 + 3, 16 * 128 + 5, 17 * 128 + 2, 5000, R - 1]
+    q, cache, table, lengths = problem(lens, R, G * kv, kv, D, page, q8, seed=R * G + D, wide=wide)
+    if rising:
+        q[..., 0] = q[..., 0].abs() + 1
+        for b, n in enumerate(lens[:-1]):
+            slots = slots_of(table, page, b, n)[-7:]
+            p, off = (slots // page).to(DEV), (slots % page).to(DEV)
+            step = torch.arange(1, 8, device=DEV)[:, None]
+            if q8:   # (the scale of the row's other codes as well)
+                cache.k[p, :, off, 0] = 127
+                cache.k_scale[p, :, off] = 0.02 * step * (8 if D == 128 else 6)
+            else:
+                cache.k[p, :, off, 0] = (20 * step).to(torch.bfloat16).expand(7, kv)
+    clean, mag, top = attention64(q, cache, table, lengths, D ** -0.5)
+    tol = tolerance(clean, mag, top, max(lens), D)
+    got = dsm.paged_attention(q, cache, table, lengths).double()
+    assert bool(((got - clean).abs() <= tol).all()), float(((got - clean).abs() - tol).max())
+    bad_dims = [3, D // 2 + 1, D - 1]
+    fine_dims = [d for d in range(D) if d not in bad_dims]
+    for u in sorted({0, (R - 1) // 2, R - 2}):            # seen by the rows after row u
+        for side, what in (("k", float("nan")), ("v", float("inf")), ("v", -float("inf"))):
+            if q8 and what == -float("inf"):
+                continue
+            dirty = dsm.PagedCache(*(None if t is None else t.clone() for t in (
+                cache.k, cache.v, cache.k_scale, cache.v_scale)))
+            for b, n in enumerate(lens):
+                t = n - (R - 1) + u
+                slot = int(slots_of(table, page, b, n)[t])
+                at = getattr(dirty, side + "_scale" if q8 else side)
+                if q8 or side == "k":
+                    at[slot // page, :, slot % page] = what
+                else:
+                    at[slot // page, :, slot % page, bad_dims] = what
+            out = dsm.paged_attention(q, dirty, table, lengths).double()
+            blind, sees = list(range(u + 1)), list(range(u + 1, R))
+            fine = (out - clean).abs() <= tol
+            assert bool(fine[:, blind].all()), (u, side, what)
+            if q8 or side == "k":
+                assert not bool(torch.isfinite(out[:, sees]).any()), (u, side)
+                continue
+            assert bool((out[:, sees][..., bad_dims] == what).all()), (u, side, what)
+            assert bool(fine[:, sees][..., fine_dims].all()), (u, side, what)
