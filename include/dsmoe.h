@@ -452,7 +452,9 @@ ds_status ds_cache_read(const ds_paged_cache* cache, const int32_t* slots, int32
 /* ------------------------------------------------------------------------------------
  * Norms of queries and keys per head with the position rotation, in one pass. For every
  * row x of head_dim values (one head of one token), in fp32, rounded once at the end:
- *   with a weight w:  x[d] <- x[d] * w[d] / sqrt(mean(x^2) + eps)   (no weight: no norm);
+ *   with a weight w:  x[d] <- x[d] * w[d] / sqrt(mean(x^2) + eps)   (no weight: no norm;
+ *   magnitudes up to 2^60, beyond which the squares' sum overflows; eps = 0 makes a row of
+ *   zeros NaN);
  *   then the first rotary_dim = n values are rotated in pairs i < n/2 by the angle
  *   position * freqs[i] (in turns of 2^64, modulo one turn: an exact integer product, so
  *   far positions lose nothing):  (u, v) <- (u cos - v sin, v cos + u sin), where the pair
@@ -500,9 +502,11 @@ ds_status ds_qk_norm_rope_write(const ds_norm_rope_args* args, const uint16_t* v
  *   s_t = scale * q_{b,r,h} . k_{b,g,t} over the tokens t < len - (n_rows - 1 - r),
  *   p = softmax(s),   out_{b,r,h} = bf16_RNE(sum_t p_t v_{b,g,t}),
  * token t in page page_table[b][t / page_tokens], offset t % page_tokens. A row with no
- * visible token gets 0, and a score of -infinity counts as not visible; tokens that a row
- * does not see do not reach it, whatever they hold (an infinity among the values that it
- * does see gives infinities or NaN). len is taken as 0 when negative and as
+ * visible token gets 0; tokens that a row does not see do not reach it, whatever they hold
+ * (an infinity or a NaN among the values that it does see gives infinities or NaN). A score
+ * of -infinity gives its token the weight 0, and a row all of whose scores are -infinity gets
+ * 0; such a token is still one that the row sees, so its values must be finite. Values must
+ * be below 2^95 in magnitude: fp32 holds sums of 2^24 of them times weights of up to 2^8. len is taken as 0 when negative and as
  * max_pages * page_tokens when larger; page table entries outside 0 .. n_pages - 1 are
  * skipped as if their tokens were not there, and entries behind the last needed page are
  * not read. Scores, softmax and sums in fp32 on the tensor cores; for the product with the

@@ -234,3 +234,61 @@ def test_new_tokens_that_some_rows_see(R, G, wide, D, q8, rising):
                 continue
             assert bool((out[:, sees][..., bad_dims] == what).all()), (u, side, what)
             assert bool(fine[:, sees][..., fine_dims].all()), (u, side, what)
+
+
+# ------------------------------------------------------------------------- scores of -infinity
+@pytest.mark.parametrize("M,wide", KERNELS)
+@pytest.mark.parametrize("q8", [False, True])
+def test_scores_of_minus_infinity_weigh_nothing(q8, M, wide):
+    # tokens whose score overflows to -infinity, among them all of the first tiles of one
+    # sequence and all tokens of another
+    lens, page, D = [400, 150, 90], 16, 128
+    q, cache, table, lengths = problem(lens, 1, M, 1, D, page, q8, seed=M, wide=wide)
+    q[..., 0] = 2.0 ** 20
+    gone = [torch.arange(lens[0]) < 260, torch.arange(lens[1]) % 3 > 0, torch.ones(lens[2], dtype=torch.bool)]
+    for b, n in enumerate(lens):
+        slots = slots_of(table, page, b, n)
+        low = slots[gone[b]]
+        p, off = (slots // page).to(DEV), (slots % page).to(DEV)
+        cache.k[p, :, off, 0] = 0
+        p, off = (low // page).to(DEV), (low % page).to(DEV)
+        if q8:
+            cache.k[p, :, off] = 0
+            cache.k[p, :, off, 0] = -127
+            cache.k_scale[p, :, off] = 2.0 ** 120
+        else:
+            cache.k[p, :, off, 0] = -2.0 ** 126
+    got = dsm.paged_attention(q, cache, table, lengths)
+    assert bool((got[2] == 0).all())
+    kept = [torch.nonzero(~g).flatten() for g in gone[:2]]
+    # the same tokens without them
+    for b in range(2):
+        slots = slots_of(table, page, b, lens[b])[kept[b]]
+        k, v = (ref.values(cache, s)[slots, 0] for s in ("k", "v"))
+        s = q[b, 0].cpu().double() @ k.t() * D ** -0.5
+        p = torch.softmax(s, -1)
+        mag = p @ v.abs()
+        # (the dimension of 2^20 adds nothing to a score: its keys are 0)
+        x = q[b, 0].cpu().double().clone()
+        x[:, 0] = 0
+        top = float((x.abs() @ k.abs().t()).max() * D ** -0.5)
+        tol = tolerance(p @ v, mag, top, lens[b], D)
+        assert bool(((got[b, 0].cpu().double() - p @ v).abs() <= tol).all()), b
+
+
+# ---------------------------------------------------------------------- large and small values
+@pytest.mark.parametrize("M,wide", KERNELS)
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("exp", [92, -96])
+def test_large_and_small_values(exp, q8, M, wide):
+    # a power of two in front of the values (below 8 times it) is one in front of the results
+    lens, page, D = [1500, 130], 64, 64
+    q, cache, table, lengths = problem(lens, 1, M, 1, D, page, q8, seed=M, wide=wide)
+    want = dsm.paged_attention(q, cache, table, lengths)
+    if q8:
+        cache.v_scale *= 2.0 ** exp
+    else:
+        cache.v *= 2.0 ** exp
+    got = dsm.paged_attention(q, cache, table, lengths)
+    assert bool(torch.isfinite(got).all())
+    assert torch.equal(got.float(), want.float() * 2.0 ** exp)
