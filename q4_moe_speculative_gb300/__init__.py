@@ -722,9 +722,11 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     if out is not None:
         _need_on(out, "out", torch.bfloat16, (B, R, Hq, D), dev)
     if workspace is not None:
-        _need_on(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    args = N.DsPagedAttnArgs(B, R, Hq, max_pages, D ** -0.5 if scale is None else scale,
-                             q.data_ptr(), c, page_table.data_ptr(), lengths.data_ptr())
+        _need_on(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
+    if scale is None:
+        scale = max(D, 1) ** -0.5
+    args = N.DsPagedAttnArgs(B, R, Hq, max_pages, scale, q.data_ptr(), c,
+                             page_table.data_ptr(), lengths.data_ptr())
 
     s, undo = _enter(dev, stream)
     try:

@@ -292,3 +292,15 @@ def test_large_and_small_values(exp, q8, M, wide):
     got = dsm.paged_attention(q, cache, table, lengths)
     assert bool(torch.isfinite(got).all())
     assert torch.equal(got.float(), want.float() * 2.0 ** exp)
+
+
+# ------------------------------------------------------------------------------------ refusals
+def test_arguments_that_are_refused():
+    q, cache, table, lengths = problem([40], 1, 2, 1, 64, 16, False, seed=1)
+    for bad in (5, [1], "ws"):
+        with pytest.raises(TypeError):
+            dsm.paged_attention(q, cache, table, lengths, workspace=bad)
+    none = dsm.PagedCache.zeros(2, 1, 16, 0)               # no head_dim
+    with pytest.raises(dsm.DsmoeError) as e:
+        dsm.paged_attention(q[..., :0].contiguous(), none, table, lengths)
+    assert e.value.status == 1
