@@ -416,6 +416,12 @@ def _cuda_tensor(t: torch.Tensor, name: str, dims: int) -> torch.device:
     return t.device
 
 
+def _c_int(n: int) -> int:
+    """n as a 32-bit argument: what does not fit is as much out of range as the largest that
+    does (ctypes alone would drop the upper bits)."""
+    return min(n, 2 ** 31 - 1)
+
+
 def _enter(dev: torch.device, stream):
     """(stream handle, what to close afterwards or None): makes `dev` current, and `stream`
     current on it, so that what the call allocates belongs to the stream it is launched on.
@@ -461,8 +467,8 @@ def q4_project(tiles: torch.Tensor, x: torch.Tensor, *, y=None, stream=None) -> 
     try:
         if y is None:
             y = torch.empty((R, 16 * units), dtype=torch.bfloat16, device=dev)
-        _check(lib.ds_q4_project(N.DsQ4Tiled(tiles.data_ptr()), 16 * units, 64 * Tk, x.data_ptr(),
-                                 R, y.data_ptr(), s), "ds_q4_project")
+        _check(lib.ds_q4_project(N.DsQ4Tiled(tiles.data_ptr()), 16 * units, _c_int(64 * Tk),
+                                 x.data_ptr(), R, y.data_ptr(), s), "ds_q4_project")
     finally:
         if undo:
             undo.close()
@@ -725,7 +731,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
         _need_on(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
     if scale is None:
         scale = max(D, 1) ** -0.5
-    args = N.DsPagedAttnArgs(B, R, Hq, max_pages, scale, q.data_ptr(), c,
+    args = N.DsPagedAttnArgs(B, R, Hq, _c_int(max_pages), scale, q.data_ptr(), c,
                              page_table.data_ptr(), lengths.data_ptr())
 
     s, undo = _enter(dev, stream)

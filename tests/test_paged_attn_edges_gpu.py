@@ -304,3 +304,21 @@ def test_arguments_that_are_refused():
     with pytest.raises(dsm.DsmoeError) as e:
         dsm.paged_attention(q[..., :0].contiguous(), none, table, lengths)
     assert e.value.status == 1
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    # (what 32 bits keep of these sizes would be a call that is allowed)
+    q, cache, table, lengths = problem([40], 1, 2, 1, 64, 16, False, seed=2)
+    wide = torch.empty((1, 2 ** 32 + 4), dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    with pytest.raises(dsm.DsmoeError) as e:
+        dsm.paged_attention(q, cache, wide, lengths)
+    assert e.value.status == 1
+    del wide
+    tiles = torch.empty((1, 2 ** 26 + 1, 576), dtype=torch.uint8, device=DEV)
+    x = torch.empty((1, 2 ** 32 + 64), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(dsm.DsmoeError) as e:
+        dsm.q4_project(tiles, x)
+    assert e.value.status == 1
+    del tiles, x
+    torch.cuda.empty_cache()
