@@ -559,7 +559,6 @@ __global__ void __launch_bounds__(kWarps == 1 ? 256 : 32 * kWarps)
   // (in one CTA: already written; not noted: the kernel gave up, and the status says so)
   if (!empty && (c0 < 0 || c1 <= c0 || c1 >= a.grid)) return;
   if (row >= a.M) return;   // (all warps of the block, when they share the row)
-  auto piece = [&](int c) { return (2 * (int64_t)c + (c == c0 ? 1 : 0)) * a.M + row; };
   // a warp's pieces, as many at a time as keep memory's latency down, the reference moving up
   constexpr int kAt = kWarps == 32 ? 5 : 8;
   float top = kNegInf, acc[V], norm = 0.f;
