@@ -88,6 +88,12 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
+// Two values rounded to a bf16 pair.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // Pairs of fp32 values.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pair(float lo, float hi) {

@@ -18,7 +18,7 @@
 // 57.8 us, 5.2 TB/s; 4096 x 4096, R = 1: 3.8 us.
 #include "common.cuh"
 #include "kernels.h"
-#include "sm100.cuh"
+#include "mma.cuh"
 
 namespace dsmoe {
 namespace {
@@ -57,15 +57,6 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t w) {
   asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(p) : "r"(w));
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(p), "r"(0x43084308u));
   return d;
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1,
-                                         const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
-        "f"(c[3]));
 }
 
 // acc += scales x (block of 16 rows x 32 values) x X: the K order of the two MMAs is

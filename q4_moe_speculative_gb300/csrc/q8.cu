@@ -29,6 +29,7 @@
 // call writes the same bytes as R one-row calls.
 #include "common.cuh"
 #include "kernels.h"
+#include "mma.cuh"
 #include "sm100.cuh"
 
 namespace dsmoe {
@@ -67,16 +68,6 @@ __device__ __forceinline__ uint32_t q8_pair(uint32_t w) {
   asm("lop3.b32 %0, %1, 0x00800080, 0x43004300, 0xEA;" : "=r"(c) : "r"(w));
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(c));
   return d;
-}
-
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1,
-                                         const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
-        "f"(c[2]), "f"(c[3]));
 }
 
 // One Q8 block for the 16 rows of a tile: W holds this lane's words (row g step 0, row g+8
