@@ -416,7 +416,9 @@ ds_status ds_q4_project(const ds_q4_tiled* w, int64_t rows, int32_t K, const uin
  * 2^31; page_stride >= n_kv_heads * page_tokens * head_dim and a multiple of 16;
  * scale_page_stride >= n_kv_heads * page_tokens and a multiple of 4 (all strides at most
  * 2^31); k, v, k_scale and v_scale 16-byte aligned. k and v may share one allocation
- * (strided pages).
+ * (strided pages). With one key-value head, DS_CACHE_BF16, head_dim 128 and contiguous
+ * pages, token t in slot t, k and v are what ds_sparse_attention takes for one layer, and k
+ * what ds_select_blocks does.
  * ---------------------------------------------------------------------------------- */
 #define DS_CACHE_BF16 0
 #define DS_CACHE_Q8 1
@@ -520,7 +522,9 @@ ds_status ds_qk_norm_rope_write(const ds_norm_rope_args* args, const uint16_t* v
  * ---------------------------------------------------------------------------------- */
 typedef struct {
   int32_t n_seqs, n_rows, n_heads;
-  int32_t max_pages;           /* entries of page_table per sequence                */
+  int32_t max_pages;           /* entries of page_table per sequence; the kernel is
+                                  chosen for this room, so short contexts in tables
+                                  for long ones cost some microseconds              */
   float scale;
   const uint16_t* q;           /* bf16 [n_seqs][n_rows][n_heads][head_dim]          */
   ds_paged_cache cache;

@@ -480,7 +480,9 @@ class PagedCache:
     """Paged key-value cache of one layer (include/dsmoe.h): k and v [pages, kv_heads,
     page_tokens, head_dim], bf16, or int8 with k_scale and v_scale fp32 [pages, kv_heads,
     page_tokens] (Q8). Pages may be strided (k and v parts of one allocation); the rest is
-    contiguous. The slot of a token is page * page_tokens + its offset in the page."""
+    contiguous. The slot of a token is page * page_tokens + its offset in the page. With one
+    head of 128, bf16 and token t in slot t, k.view(1, -1, 128) and v.view(1, -1, 128) are what
+    sparse_attention takes, and the first what select_blocks does."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor | None = None
