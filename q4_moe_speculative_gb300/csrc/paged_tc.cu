@@ -60,8 +60,9 @@ struct TcArgs {
 // Where the two parts of P are among its columns, in chunks of 64 (128 bytes of a token), and what
 // they are added to in O. Up to 64 rows: side by side, and O has columns of either, so that
 // one MMA does both. 128 rows: two chunks each, two MMAs into the same columns (tensor memory
-// has 512). 96 rows: high 0..95, low 64..95, low 0..63, so that one MMA takes two whole chunks
-// (its last 32 columns are the low part of rows 64..95) and a second one adds the third.
+// has 512). 96 rows: high 0..63; high and low 64..95; low 0..63; an MMA for each, the third into
+// the columns of the first. MMAs into the same columns follow one another in order because
+// their shapes are the same as well.
 template <bool kBeside>   // up to 64 rows
 struct Parts {
   int N;
@@ -74,6 +75,11 @@ struct Parts {
   // and in O, where it has columns there
   __device__ bool low_apart(int c) const { return kBeside || (N == 96 && c >= 64); }
   __device__ int low_in_o(int c) const { return kBeside ? N + c : c + 32; }
+  // the MMAs of one step, their columns of P, and where the x-th one's sums are in O
+  __device__ int mmas() const { return kBeside ? 1 : (N == 96 ? 3 : 2); }
+  __device__ int mma_columns() const { return kBeside ? 2 * N : (N == 96 ? 64 : 128); }
+  __device__ int mma_at(int x) const { return N == 96 && x == 1 ? 64 : 0; }
+  __device__ bool mma_adds(int x) const { return x == mmas() - 1 && x > 0; }   // never the first
 };
 
 template <int D, bool kQ8>
@@ -799,8 +805,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   } else {
     // ---------------------------------------------------------------- MMAs of the values ---
     const bool leader = elect_one();
-    const uint32_t idesc = sm100::idesc_bf16_f32(kTok, cols.o_columns()) | kMajorMN;
-    const uint32_t idesc2 = sm100::idesc_bf16_f32(kTok, 2 * N - 128) | kMajorMN;   // (!kBeside)
+    const uint32_t idesc = sm100::idesc_bf16_f32(kTok, cols.mma_columns()) | kMajorMN;
     // (D = 64: the upper half of the M rows repeats the lower one)
     const uint64_t v_desc = desc_mn_sw128(smem_at(sV), D == 128 ? kTok * 128 : 0);
     const uint64_t p_desc = desc_mn_sw128(smem_at(sP), kTok * 128);
@@ -818,9 +823,15 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       if (leader) {
 #pragma unroll
         for (int ks = 0; ks < kTok / 16; ++ks) {   // 16 tokens: 2 KB
-          sm100::mma_bf16(tmem + ta.s_bufs * N, vd + ks * 128, pd + ks * 128, idesc, !(fresh && ks == 0));
-          if (!kBeside)   // the chunks from the third on
-            sm100::mma_bf16(tmem + ta.s_bufs * N, vd + ks * 128, pd + kTok * 16 + ks * 128, idesc2, 1);
+          const uint32_t tO = tmem + ta.s_bufs * N, more = !(fresh && ks == 0);
+          if constexpr (kBeside) {
+            sm100::mma_bf16(tO, vd + ks * 128, pd + ks * 128, idesc, more);
+          } else {
+            for (int x = 0; x < cols.mmas(); ++x)   // (mma_columns: a chunk or two)
+              sm100::mma_bf16(tO + cols.mma_at(x), vd + ks * 128,
+                              pd + (uint32_t)(x * cols.mma_columns() * (kTok / 8)) + ks * 128, idesc,
+                              cols.mma_adds(x) || more);
+          }
         }
         sm100::mma_commit(&sh.odone[i & 1]);
         sm100::mma_commit(&sh.vfree[st]);
