@@ -12,7 +12,7 @@
 // a 64-bit integer product that wraps, exact at any position, of which the upper 32 bits go
 // to sincospif. Each lane computes the angles of its own 8 values once per token, times the
 // weights, and keeps them in registers over the heads of its chunk. Memory-bound by bytes,
-// by instruction issue in practice (59 to 68% of the slots): fp32 arithmetic is done two values
+// by instruction issue in practice (55 to 70% of the slots): fp32 arithmetic is done two values
 // at a time (f32x2). 16,384 tokens x 20 heads of 128, rotated: 31.8 us, 5.3 TB/s; 32,768 tokens x
 // 8 heads into a Q8 cache: 40 us, 5.1 TB/s.
 #include "common.cuh"
@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     k_rows(const __grid_constant__ RowsArgs a) {
   constexpr int LPH = D / 8, kTokens = 32 / LPH;   // lanes per row, tokens per warp
   // rows whose loads are in flight together (the write above: 2 50 us, 4 43, 8 40, but of one
-  // head, 16,384 tokens with the reading back, 4 8.2 and 8 8.6; the rotation: 4 31.9 us, 5, which
-  // spills, 36.4)
+  // head, 16,384 tokens with the reading back, 4 8.2 and 8 8.6; the rotation: 4 31.9 us, 5 36.4.
+  // With four CTAs per SM the rotating forms spill with 4 as well, 40 to 80 bytes a thread)
   constexpr int kBatch = kTurn ? 4 : 8;
   pdl_trigger();
   pdl_wait();
@@ -378,8 +378,9 @@ cudaError_t pick_turn(const RowsProblem& p, const CacheView* c, cudaStream_t s) 
 template <int D>
 cudaError_t pick_rows(const RowsProblem& p, const CacheView* c, cudaStream_t s) {
   if (p.Hq == 0) return c->q8 ? start_rows<D, 2, 0, 4>(p, c, s) : start_rows<D, 1, 0, 4>(p, c, s);
-  // CTAs per SM: four have 64 registers a thread. Into a Q8 cache that is too few (8192 tokens x
-  // 48 heads 58.6 us, with four 60.1, with two 62.0); without a cache three are faster while all
+  // CTAs per SM: four have 64 registers a thread. Into a Q8 cache that is too few (16,384
+  // tokens x 32 + 8 heads, halves 85.2 us, with four 86.3, with two 98.1; neighbours 78.3, 82.7, 93.0),
+  // into a bf16 one it is as good (halves 76.0, with three 77.1; neighbours 73.5, 72.3); without a cache three are faster while all
   // tokens fit the SMs at once (384 tokens x 40 heads 5.0 against 6.4 us, 2048 10.8 against 13.0),
   // four beyond (16,384 tokens x 20 heads 31.8 against 34.8).
   if (c) return c->q8 ? pick_turn<D, 2, 3>(p, c, s) : pick_turn<D, 1, 4>(p, c, s);

@@ -632,25 +632,25 @@ auto with_rows(int M, F&& f) {
 }
 
 // Up to 32 rows: paged_few.cu, which costs no more for 1 row than it has to (24 rows, 32
-// sequences x 8 heads at 8k, bf16 169 us, Q8 158; k_paged's design with 16-row tiles: 207, 186).
+// sequences x 8 heads at 8k, bf16 167 us, Q8 160; k_paged's design with 16-row tiles: 207, 186).
 // More rows: the tcgen05 kernel (paged_tc.cu) has the higher rate and the longer beginning and
 // end, and is ahead from several tiles per SM on. k_paged | paged_tc, us, 4 sequences x 8 heads:
 //   tokens per sequence        500      1k       2k       4k        8k       64k
 //   bf16, D = 128, 40 rows   13 | 16  15 | 16  23 | 20  35 | 24   60 | 34  397 | 160
-//                  96 rows   17 | 20  19 | 21  30 | 25  45 | 29   76 | 43  505 | 203
-//                 128 rows   21 | 25  24 | 26  38 | 32  55 | 40   92 | 57  610 | 290
+//                  96 rows   17 | 20  19 | 21  30 | 25  45 | 30   76 | 43  504 | 195
+//                 128 rows   21 | 25  24 | 26  37 | 32  55 | 40   92 | 57  610 | 291
 //   Q8,   D = 128, 64 rows   13 | 20  15 | 19  23 | 26  35 | 29   60 | 42  405 | 207
-//                  96 rows   16 | 24  19 | 25  29 | 32  45 | 40   77 | 60  525 | 312
-//                 128 rows   20 | 33  24 | 38  36 | 38  56 | 48   96 | 69  650 | 364
+//                  96 rows   16 | 24  19 | 25  29 | 32  45 | 41   77 | 61  524 | 314
+//                 128 rows   20 | 33  24 | 38  36 | 38  56 | 48   95 | 68  649 | 356
 //   bf16, D = 64,  64 rows   11 | 16  13 | 16  18 | 18  27 | 22   44 | 30  290 | 136
-//                 128 rows   17 | 24  19 | 24  26 | 28  39 | 36   66 | 51  434 | 258
+//                 128 rows   17 | 24  18 | 24  26 | 28  39 | 35   66 | 50  433 | 251
 //   Q8,   D = 64,  64 rows   11 | 18  12 | 19  18 | 22  26 | 26   45 | 38  301 | 187
-//                  96 rows   13 | 25  16 | 28  22 | 31  34 | 32   57 | 46  382 | 216
+//                  96 rows   13 | 25  16 | 29  22 | 32  33 | 33   57 | 47  382 | 224
 // One head of 32k, D = 128, 96 rows: bf16 19 | 18, Q8 20 | 20. From 25 rows on it is ahead of
-// paged_few.cu as well at D = 128: 32 rows, 32 sequences x 8 heads at 8k, bf16 177 against 164,
-// Q8 196 against 169; 8 x 8 heads at 2k, 24.3 against 21.5 and 24.5 against 23.4; at 1k, 16.9
-// against 16.9 and 16.3 against 18.8; but 24 rows at 8k 170 against 163 and 158 against 166, and 32
-// rows at D = 64 111 against 110 and 126 against 153. `places`: tokens x key heads there can be
+// paged_few.cu as well at D = 128: 32 rows, 32 sequences x 8 heads at 8k, bf16 176 against 162,
+// Q8 198 against 164; 8 x 8 heads at 2k, 24.6 against 21.5 and 24.8 against 24.5; at 1k, 17.5
+// against 17.1 and 16.3 against 20.2; but 24 rows at 8k 167 against 161 and 160 against 162, and 32
+// rows at D = 64 112 against 109 and 127 against 148. `places`: tokens x key heads there can be
 // (lengths are not known here: short ones in a table with room for long ones pay paged_tc.cu's
 // beginning).
 Kernel which(int M, int D, bool q8, int64_t places) {

@@ -16,10 +16,11 @@
 // reference of a row moves only when a score exceeds it by 2^8.
 //
 // Measured on 32 sequences x 8 heads of 8k tokens, D = 128: bf16 (1.05 GB) 160 us for 1 to 8
-// rows, 6.6 TB/s, bound by memory, and 177 us for 32 rows; Q8 (0.54 GB) 102, 127, 158 and 196 us
-// for 8, 16, 24 and 32 rows, bound by the issue of instructions (700 per 16 tokens and warp at 16
-// rows, of which 224 widen codes and 48 are products). A single head of 500 tokens: 6.3 us, of
-// which launching the two kernels is most.
+// rows, 6.6 TB/s, bound by memory, and 176 us for 32 rows; Q8 (0.54 GB) 102, 127, 160 and 198 us
+// for 8, 16, 24 and 32 rows, bound by the latency of dependent instructions (700 per 16 tokens and
+// warp at 16 rows, of which 224 widen codes and 48 are products; at 24 rows, with two warps per
+// scheduler, 47% of the issue slots are used). A single head of 500 tokens: 6.4 us, of which
+// launching the two kernels is most.
 #include <type_traits>
 
 #include "paged.cuh"

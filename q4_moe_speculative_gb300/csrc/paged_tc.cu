@@ -19,8 +19,8 @@
 // double-buffered: the next tile's scores are computed while this tile's are exponentiated.
 // Measured: 96 rows of one head of 300k tokens, D = 128, bf16 (154 MB) 43.5 us with the join,
 // which takes 6 to 8 of them; 4 sequences x 8 heads of 64k, bf16 (1.05 GB), 40 and 64 rows 160 us
-// (6.6 TB/s, bound by memory), 96 rows 203, 128 rows 290; Q8 (0.54 GB), 64 rows 206, 96 rows 311,
-// 128 rows 363, and D = 64, bf16, 64 rows 135 (0.52 GB), bound by the chain of a tile through
+// (6.6 TB/s, bound by memory), 96 rows 195, 128 rows 291; Q8 (0.54 GB), 64 rows 206, 96 rows 314,
+// 128 rows 356, and D = 64, bf16, 64 rows 135 (0.52 GB), bound by the chain of a tile through
 // widening, scores and P: beyond 64 rows shared memory has no room for two tiles of all of them.
 // (With one part of P beyond 64 rows: 96 rows 165 us, Q8 234; 128 rows 247, Q8 284; results off
 // by 1.4 times their own rounding. Bringing the tiles behind the ring into L2 ahead of time
@@ -885,9 +885,9 @@ cudaError_t start_with(const PagedArgs& p, cudaStream_t s) {
   a.s_bufs = a.N <= 96 ? 2 : 1;   // (tensor memory has 512 columns)
   const int room = 227 * 1024;
   // The least first, then what fits: two stages of codes, a second buffer of P (Q8, 64 rows, D =
-  // 128: 207 us with two, 234 with one and a second value tile; bf16, 96 rows: 203 with two and a
-  // second value tile, 241 with two and a second key tile, 245 with one and both), a second
-  // value tile, deeper rings. (Q8, 96 rows: 311 us with any that fits.)
+  // 128: 207 us with two, 234 with one and a second value tile; bf16, 96 rows: 195 with two and a
+  // second value tile, 263 with two and a second key tile, 262 with one and both), a second
+  // value tile, deeper rings. (Q8, 96 rows: 314 us with any that fits.)
   a.p_bufs = 1;
   a.k_ring = a.v_ring = 1;
   a.raw = kQ8 ? 1 : 0;

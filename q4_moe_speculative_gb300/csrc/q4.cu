@@ -15,7 +15,10 @@
 // partials meet in shared memory, kGroup units at a time (the barrier is paid once per group),
 // in warp order, rounded once. Nothing depends on R. Bound: rows x K x 9/16 bytes; in practice
 // the issue of about 80 instructions per tile, of which 44 widen nibbles. 129,280 x 4096, R = 6:
-// 57.8 us, 5.2 TB/s; 4096 x 4096, R = 1: 3.8 us.
+// 57.8 us, 5.2 TB/s; 4096 x 4096, R = 1: 3.8 us. 300 MB of weights (45 us at the copy rate), R = 6:
+// K = 4096 58 us, 2048 62, 8192 73, 12,288 73 (beyond 4096 the activations are read again); a K
+// that is no multiple of 1024 also pays for the tiles that fill its warps' batches up: 1088 107,
+// 2560 84, 4160 131, 5120 109, 7168 82.
 #include "common.cuh"
 #include "kernels.h"
 #include "mma.cuh"
