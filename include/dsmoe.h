@@ -543,6 +543,111 @@ ds_status ds_paged_attention(const ds_paged_attn_args* args, uint16_t* out, void
                              size_t ws_bytes, ds_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * Attention of sequences that share prefixes (one prompt with many samples, many requests behind
+ * one system prompt): ds_paged_attention for sequences whose context is a prefix's tokens and
+ * then their own, each prefix read once for all its sequences. Prefix p belongs to the
+ * sequences p * n .. p * n + n - 1, n = own.n_seqs / n_prefixes. Its tokens are
+ * t < prefix_lengths[p] of the pages prefix_table[p]; own.lengths and own.page_table are those
+ * of the sequences' own tokens, which begin in a page of their own, the new rows among them.
+ * Row r of sequence b sees all tokens of its prefix, and of its own the t < lengths[b] -
+ * (n_rows - 1 - r); scores, softmax and sums as for ds_paged_attention, over both together. A
+ * sequence with a negative length is not there (a padded batch): its rows get 0, whatever its
+ * prefix. prefix_lengths are taken as 0 when negative and as the room when larger; prefix table
+ * entries outside the cache are skipped, and entries behind the last needed one not read.
+ * Limits: those of ds_paged_attention for own; 1 <= n_prefixes, own.n_seqs a multiple of it,
+ * 1 <= max_prefix_pages, max_prefix_pages * page_tokens <= 2^24.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  ds_paged_attn_args own;
+  int32_t n_prefixes;
+  int32_t max_prefix_pages;       /* entries of prefix_table per prefix             */
+  const int32_t* prefix_table;    /* int32 [n_prefixes][max_prefix_pages]           */
+  const int32_t* prefix_lengths;  /* int32 [n_prefixes]                             */
+} ds_prefix_attn_args;
+
+/* Workspace bytes on the current device (0 when the arguments are invalid, unsupported or
+ * own.n_seqs == 0), from the sizes alone. */
+size_t ds_prefix_attn_workspace_size(const ds_prefix_attn_args* args);
+/* out, workspace, errors and status as for ds_paged_attention. */
+ds_status ds_prefix_attention(const ds_prefix_attn_args* args, uint16_t* out, void* workspace,
+                              size_t ws_bytes, ds_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The norms around a block, its gate and its way onto the residual stream, in one pass over the
+ * rows. For every row, in fp32 (H = hidden; squares' sums overflow beyond magnitudes of 2^55):
+ *   y <- y * (post_weight + weight_offset) / sqrt(mean(y^2) + eps)    (with a post_weight)
+ *   x <- x_scale * x + y_scale * gate * y                             (with a y; no gate: 1)
+ *   x_out = x, rounded to its type;
+ *   h_out = bf16_RNE(x * (weight + weight_offset) / sqrt(mean(x^2) + eps)), of the x before its
+ *           rounding                                                  (with a weight).
+ * eps = 0 makes a row of zeros NaN.
+ * Limits: 0 <= n_rows <= 2^24 (0 enqueues nothing), hidden a multiple of 8 from 8 to 16384; eps
+ * finite and >= 0, weight_offset and the scales finite; strides at least hidden, multiples of 8,
+ * at most 2^31; all pointers 16-byte aligned. x_out may be NULL when only h_out is wanted, and y
+ * for the norm alone (x_out is then not written); a call that would write nothing is an invalid
+ * argument.
+ * ---------------------------------------------------------------------------------- */
+#define DS_ROWS_BF16 0
+#define DS_ROWS_FP32 1
+typedef struct {
+  int32_t n_rows, hidden;
+  int32_t x_format;             /* DS_ROWS_BF16 or DS_ROWS_FP32: of x and x_out        */
+  float eps, weight_offset, x_scale, y_scale;
+  const void* x;                /* [n_rows][hidden]: the residual stream               */
+  int64_t x_stride;             /* values between rows                                 */
+  const uint16_t* y;            /* bf16 [n_rows][hidden], a block's output, or NULL    */
+  int64_t y_stride;
+  const uint16_t* post_weight;  /* bf16 [hidden], or NULL: y is not normed             */
+  const uint16_t* gate;         /* bf16 [n_rows][hidden], or NULL                      */
+  int64_t gate_stride;          /* or 0: one row for all                               */
+  const uint16_t* weight;       /* bf16 [hidden], or NULL: no h_out                    */
+} ds_block_norm_args;
+
+/* x_out [n_rows][hidden] of x's type, h_out bf16 [n_rows][hidden]. Either may be x or y itself,
+ * where the types agree and that one's rows are contiguous; other overlaps are a caller error.
+ * Errors: DS_ERR_INVALID_ARG, DS_ERR_CUDA. */
+ds_status ds_block_norm(const ds_block_norm_args* args, void* x_out, uint16_t* h_out,
+                        ds_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Drawing a token per row of logits. For row b, with l_i its logits, m the largest, T its
+ * temperature and w_i = exp((l_i - m) / T):
+ *   top_k = k > 0 keeps the k largest logits; of equal ones the lowest ids.
+ *   top_p < 1 keeps, of those in falling order (equal ones by id), each token before which their
+ *           mass is less than top_p times all of it; the first always.
+ *   min_p > 0 keeps those with l_i - m >= T log(min_p), i.e. w_i >= min_p; the largest always.
+ *   token = the smallest id whose cumulative w over the kept ones (token order) exceeds u times
+ *           their sum; prob = its w over that sum, rounded to fp32.
+ * T <= 2^-64 (or NaN): the largest logit, the lowest id of equal ones, prob 1. T = infinity: all
+ * finite logits alike. A NaN logit counts as -infinity, which is never drawn; a row with nothing
+ * else gets the token -1 and prob 0. u is taken as 0 when negative or NaN and as the last value
+ * below 1 when not below it. top_p NaN is 1, min_p NaN is 0, and m - l_i beyond the range of fp32
+ * is w_i = 0.
+ * Decisions are taken in integers: w in units of 2^-s, s = 45 up to a vocabulary of 2^17 and one
+ * less for each doubling, off by half a unit and a few 2^-40 relative; their sums are exact. A border or a draw
+ * closer than that to a 64-bit evaluation's may go the other way.
+ * Limits: 0 <= n_rows <= 2^20 (0 enqueues nothing), 1 <= n_vocab <= 2^24, row stride >= n_vocab
+ * and at most 2^31.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t n_rows, n_vocab;
+  int32_t logits_format;        /* DS_ROWS_BF16 or DS_ROWS_FP32                        */
+  const void* logits;           /* [n_rows][n_vocab]                                   */
+  int64_t logits_stride;        /* values between rows                                 */
+  const double* u;              /* fp64 [n_rows] in [0, 1)                             */
+  float temperature, top_p, min_p;   /* for all rows, where the pointer below is NULL  */
+  int32_t top_k;
+  const float* temperatures;    /* fp32 [n_rows], or NULL                              */
+  const float* top_ps;
+  const float* min_ps;
+  const int32_t* top_ks;        /* int32 [n_rows], or NULL                             */
+} ds_sample_args;
+
+/* token int32 [n_rows]; prob fp32 [n_rows], or NULL. No workspace. Errors: DS_ERR_INVALID_ARG,
+ * DS_ERR_CUDA. */
+ds_status ds_sample(const ds_sample_args* args, int32_t* token, float* prob, ds_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Verify acceptance (page "DeepSeek V4.1F Q4 on M3 Ultra with native DSpark MTP
  * (40tps / 800tps)", paragraph "DSpark": a decode step verifies the last committed token
  * and R - 1 drafts in one pass; greedy decode gives the same output as without the

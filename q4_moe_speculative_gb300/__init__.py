@@ -19,7 +19,7 @@ __all__ = [
     "select_blocks", "workspace_status", "version", "DsmoeError", "verify_greedy",
     "verify_sample", "q8_tile", "q8_project", "sparse_attention", "q4_project", "PagedCache",
     "rope_frequencies", "qk_norm_rope", "qk_norm_rope_write", "cache_write", "cache_read",
-    "paged_attention",
+    "paged_attention", "prefix_attention", "block_norm", "sample",
 ]
 
 DsmoeError = N.DsmoeError
@@ -717,6 +717,12 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     lengths int32 [B] (tokens in the cache, the R new ones among them) -> bf16 [B, R, Hq, D].
     scale defaults to 1 / sqrt(D)."""
     lib = N.load()
+    args = _paged_args(q, cache, page_table, lengths, scale, out, workspace)
+    return _attend(lib.ds_paged_attn_workspace_size, lib.ds_paged_attention, "ds_paged_attention",
+                   args, q, out, workspace, stream)
+
+
+def _paged_args(q, cache, page_table, lengths, scale, out, workspace) -> N.DsPagedAttnArgs:
     c, dev = cache.struct(), cache.k.device
     _cuda_tensor(q, "q", 4)
     _cuda_tensor(page_table, "page_table", 2)
@@ -733,22 +739,160 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
         _need_on(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
     if scale is None:
         scale = max(D, 1) ** -0.5
-    args = N.DsPagedAttnArgs(B, R, Hq, _c_int(max_pages), scale, q.data_ptr(), c,
+    return N.DsPagedAttnArgs(B, R, Hq, _c_int(max_pages), scale, q.data_ptr(), c,
                              page_table.data_ptr(), lengths.data_ptr())
 
-    s, undo = _enter(dev, stream)
+
+def _attend(size, call, what, args, q, out, workspace, stream) -> torch.Tensor:
+    s, undo = _enter(q.device, stream)
     try:
         if out is None:
-            out = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         if workspace is None:
-            workspace = torch.empty(lib.ds_paged_attn_workspace_size(args), dtype=torch.uint8,
-                                    device=dev)
-        _check(lib.ds_paged_attention(args, out.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel(), s), "ds_paged_attention")
+            workspace = torch.empty(size(args), dtype=torch.uint8, device=q.device)
+        _check(call(args, out.data_ptr(), workspace.data_ptr(), workspace.numel(), s), what)
     finally:
         if undo:
             undo.close()
     return out
+
+
+def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_table: torch.Tensor,
+                     prefix_lengths: torch.Tensor, page_table: torch.Tensor,
+                     lengths: torch.Tensor, *, scale: float | None = None, out=None,
+                     workspace=None, stream=None) -> torch.Tensor:
+    """paged_attention for sequences that share prefixes, each read once for all its sequences
+    (ds_prefix_attention): prefix_table int32 [P, max_prefix_pages] and prefix_lengths int32 [P],
+    prefix p for the B / P sequences from p * B / P on; page_table int32 [B, max_pages] and
+    lengths int32 [B] of the sequences' own tokens (the R new ones among them; negative: not
+    there). q and the result bf16 [B, R, Hq, D]."""
+    lib = N.load()
+    own = _paged_args(q, cache, page_table, lengths, scale, out, workspace)
+    _cuda_tensor(prefix_table, "prefix_table", 2)
+    P, max_pages = prefix_table.shape
+    _need_on(prefix_table, "prefix_table", torch.int32, (P, max_pages), q.device)
+    _need_on(prefix_lengths, "prefix_lengths", torch.int32, (P,), q.device)
+    if P == 0 or q.shape[0] % P:
+        raise ValueError(f"{q.shape[0]} sequences cannot share {P} prefixes evenly")
+    args = N.DsPrefixAttnArgs(own, P, _c_int(max_pages), prefix_table.data_ptr(),
+                              prefix_lengths.data_ptr())
+    return _attend(lib.ds_prefix_attn_workspace_size, lib.ds_prefix_attention,
+                   "ds_prefix_attention", args, q, out, workspace, stream)
+
+
+def _hidden_rows(t: torch.Tensor, name: str, dtype, shape: tuple, dev: torch.device) -> int:
+    """Values between the rows of t [rows, hidden]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev} "
+                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the values of a row of {name} must be contiguous")
+    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8
+
+
+def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, weight=None, post_weight=None,
+               gate=None, eps: float = 1e-6, weight_offset: float = 0.0, x_scale: float = 1.0,
+               y_scale: float = 1.0, x_out=None, h_out=None, stream=None):
+    """The norms around a block in one pass (ds_block_norm): x [T, H] (bf16 or fp32, the residual
+    stream) becomes x_scale * x + y_scale * gate * norm(y), with y bf16 [T, H], normed where a
+    post_weight is given, and gate bf16 [H] or [T, H]; h is its norm with `weight`. Weights bf16
+    [H], weight_offset added to each. Rows of x, y and gate may be strided. Returns (x_out, h),
+    contiguous: x itself without a y, None for h without a weight. An output may be x or y
+    itself, if that is contiguous and of its type."""
+    lib = N.load()
+    dev = _cuda_tensor(x, "x", 2)
+    T, H = x.shape
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x must be bfloat16 or float32 (got {x.dtype})")
+    a = N.DsBlockNormArgs(T, _c_int(H), N.DS_ROWS_FP32 if x.dtype is torch.float32 else N.DS_ROWS_BF16,
+                          eps, weight_offset, x_scale, y_scale, x.data_ptr(),
+                          _hidden_rows(x, "x", x.dtype, (T, H), dev))
+    if y is None:
+        if post_weight is not None or gate is not None or x_out is not None:
+            raise ValueError("post_weight, gate and x_out need a y")
+        if weight is None:
+            raise ValueError("without a y a weight is needed")
+    else:
+        a.y_stride = _hidden_rows(y, "y", torch.bfloat16, (T, H), dev)
+        a.y = y.data_ptr()
+    if post_weight is not None:
+        _need_on(post_weight, "post_weight", torch.bfloat16, (H,), dev)
+        a.post_weight = post_weight.data_ptr()
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+            _need_on(gate, "gate", torch.bfloat16, (H,), dev)
+        else:
+            a.gate_stride = _hidden_rows(gate, "gate", torch.bfloat16, (T, H), dev)
+        a.gate = gate.data_ptr()
+    if weight is not None:
+        _need_on(weight, "weight", torch.bfloat16, (H,), dev)
+        a.weight = weight.data_ptr()
+    elif h_out is not None:
+        raise ValueError("h_out needs a weight")
+    if x_out is not None:
+        _need_on(x_out, "x_out", x.dtype, (T, H), dev)
+    if h_out is not None:
+        _need_on(h_out, "h_out", torch.bfloat16, (T, H), dev)
+
+    s, undo = _enter(dev, stream)
+    try:
+        if y is not None and x_out is None:
+            x_out = torch.empty((T, H), dtype=x.dtype, device=dev)
+        if weight is not None and h_out is None:
+            h_out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        _check(lib.ds_block_norm(a, _ptr(x_out), _ptr(h_out), s), "ds_block_norm")
+    finally:
+        if undo:
+            undo.close()
+    return (x if y is None else x_out), h_out
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k=0, top_p=1.0,
+           min_p=0.0, out=None, prob=None, stream=None):
+    """A token per row of logits [B, V] (bf16 or fp32, rows may be strided), drawn with the
+    uniforms u fp64 [B] (ds_sample). temperature, top_p and min_p are numbers or fp32 [B], top_k
+    a number or int32 [B]; 0, 1.0 and 0.0 leave top_k, top_p and min_p out, and temperature 0 takes
+    the largest logit. Returns (tokens int32 [B], their probabilities fp32 [B])."""
+    lib = N.load()
+    dev = _cuda_tensor(logits, "logits", 2)
+    B, V = logits.shape
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits must be bfloat16 or float32 (got {logits.dtype})")
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row must be contiguous")
+    _need_on(u, "u", torch.float64, (B,), dev)
+    a = N.DsSampleArgs(B, _c_int(V), N.DS_ROWS_FP32 if logits.dtype is torch.float32
+                       else N.DS_ROWS_BF16, logits.data_ptr(),
+                       logits.stride(0) if B > 1 else V, u.data_ptr())
+    for name, value in (("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
+        if isinstance(value, torch.Tensor):
+            _need_on(value, name, torch.float32, (B,), dev)
+            setattr(a, name + "s", value.data_ptr())
+        else:
+            setattr(a, name, float(value))
+    if isinstance(top_k, torch.Tensor):
+        _need_on(top_k, "top_k", torch.int32, (B,), dev)
+        a.top_ks = top_k.data_ptr()
+    else:
+        a.top_k = _c_int(max(0, int(top_k)))
+    if out is not None:
+        _need_on(out, "out", torch.int32, (B,), dev)
+    if prob is not None:
+        _need_on(prob, "prob", torch.float32, (B,), dev)
+
+    s, undo = _enter(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty((B,), dtype=torch.int32, device=dev)
+        if prob is None:
+            prob = torch.empty((B,), dtype=torch.float32, device=dev)
+        _check(lib.ds_sample(a, out.data_ptr(), prob.data_ptr(), s), "ds_sample")
+    finally:
+        if undo:
+            undo.close()
+    return out, prob
 
 
 def noalloc_status(stream=None) -> int:

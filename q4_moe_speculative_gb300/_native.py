@@ -26,7 +26,8 @@ EXPORTS = (
     "ds_verify_sample", "ds_q8_tiled_bytes", "ds_q8_tile", "ds_q8_workspace_size",
     "ds_q8_project", "ds_attn_workspace_size", "ds_sparse_attention", "ds_q4_project",
     "ds_cache_write", "ds_cache_read", "ds_qk_norm_rope", "ds_qk_norm_rope_write",
-    "ds_paged_attn_workspace_size", "ds_paged_attention",
+    "ds_paged_attn_workspace_size", "ds_paged_attention", "ds_prefix_attn_workspace_size",
+    "ds_prefix_attention", "ds_block_norm", "ds_sample",
 )
 SELECT_WS_PARTS = {"union": 0, "union_count": 1, "scores": 2, "key_norms": 3, "row_scales": 4}
 
@@ -117,6 +118,37 @@ class DsPagedAttnArgs(C.Structure):
     ]
 
 
+class DsPrefixAttnArgs(C.Structure):
+    _fields_ = [
+        ("own", DsPagedAttnArgs), ("n_prefixes", C.c_int32), ("max_prefix_pages", C.c_int32),
+        ("prefix_table", C.c_void_p), ("prefix_lengths", C.c_void_p),
+    ]
+
+
+DS_ROWS_BF16 = 0
+DS_ROWS_FP32 = 1
+
+
+class DsBlockNormArgs(C.Structure):
+    _fields_ = [
+        ("n_rows", C.c_int32), ("hidden", C.c_int32), ("x_format", C.c_int32),
+        ("eps", C.c_float), ("weight_offset", C.c_float), ("x_scale", C.c_float),
+        ("y_scale", C.c_float), ("x", C.c_void_p), ("x_stride", C.c_int64), ("y", C.c_void_p),
+        ("y_stride", C.c_int64), ("post_weight", C.c_void_p), ("gate", C.c_void_p),
+        ("gate_stride", C.c_int64), ("weight", C.c_void_p),
+    ]
+
+
+class DsSampleArgs(C.Structure):
+    _fields_ = [
+        ("n_rows", C.c_int32), ("n_vocab", C.c_int32), ("logits_format", C.c_int32),
+        ("logits", C.c_void_p), ("logits_stride", C.c_int64), ("u", C.c_void_p),
+        ("temperature", C.c_float), ("top_p", C.c_float), ("min_p", C.c_float),
+        ("top_k", C.c_int32), ("temperatures", C.c_void_p), ("top_ps", C.c_void_p),
+        ("min_ps", C.c_void_p), ("top_ks", C.c_void_p),
+    ]
+
+
 class DsmoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -202,6 +234,15 @@ def load() -> C.CDLL:
     lib.ds_paged_attention.argtypes = [C.POINTER(DsPagedAttnArgs), C.c_void_p, C.c_void_p,
                                        C.c_size_t, C.c_void_p]
     lib.ds_paged_attention.restype = C.c_int
+    lib.ds_prefix_attn_workspace_size.argtypes = [C.POINTER(DsPrefixAttnArgs)]
+    lib.ds_prefix_attn_workspace_size.restype = C.c_size_t
+    lib.ds_prefix_attention.argtypes = [C.POINTER(DsPrefixAttnArgs), C.c_void_p, C.c_void_p,
+                                        C.c_size_t, C.c_void_p]
+    lib.ds_prefix_attention.restype = C.c_int
+    lib.ds_block_norm.argtypes = [C.POINTER(DsBlockNormArgs), C.c_void_p, C.c_void_p, C.c_void_p]
+    lib.ds_block_norm.restype = C.c_int
+    lib.ds_sample.argtypes = [C.POINTER(DsSampleArgs), C.c_void_p, C.c_void_p, C.c_void_p]
+    lib.ds_sample.restype = C.c_int
     lib.ds_verify_workspace_size.argtypes = [C.c_int32, C.c_int32, C.c_int32]
     lib.ds_verify_workspace_size.restype = C.c_size_t
     lib.ds_verify_greedy.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,

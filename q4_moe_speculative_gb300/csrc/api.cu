@@ -592,6 +592,128 @@ ds_status ds_paged_attention(const ds_paged_attn_args* a, uint16_t* out, void* w
 
 namespace {
 
+// Sizes only (no pointers).
+ds_status check_prefix_sizes(const ds_prefix_attn_args* a) {
+  if (!a) return DS_ERR_INVALID_ARG;
+  const ds_status st = check_paged_sizes(&a->own);
+  if (st != DS_OK) return st;
+  if (a->n_prefixes < 1 || a->own.n_seqs % a->n_prefixes) return DS_ERR_INVALID_ARG;
+  if (a->max_prefix_pages < 1 ||
+      (int64_t)a->max_prefix_pages * a->own.cache.page_tokens > (1 << 24))
+    return DS_ERR_INVALID_ARG;
+  return DS_OK;
+}
+
+PrefixAttnProblem prefix_of(const ds_prefix_attn_args* a, uint16_t* out) {
+  return PrefixAttnProblem{paged_of(&a->own, out), a->n_prefixes, a->max_prefix_pages,
+                           a->prefix_table, a->prefix_lengths};
+}
+
+}  // namespace
+
+size_t ds_prefix_attn_workspace_size(const ds_prefix_attn_args* a) {
+  if (check_prefix_sizes(a) != DS_OK || a->own.n_seqs == 0) return 0;
+  return prefix_attn_workspace(prefix_of(a, nullptr));
+}
+
+ds_status ds_prefix_attention(const ds_prefix_attn_args* a, uint16_t* out, void* workspace,
+                              size_t ws_bytes, ds_stream_t stream) {
+  ds_status st = check_prefix_sizes(a);
+  if (st != DS_OK) return st;
+  st = check_cache(&a->own.cache);
+  if (st != DS_OK) return st;
+  if (a->own.n_seqs == 0) return DS_OK;
+  if (!a->own.q || !out || !a->own.page_table || !a->own.lengths || !a->prefix_table ||
+      !a->prefix_lengths || !aligned(a->own.q, 16) || !aligned(out, 16) ||
+      !aligned(a->own.page_table, 4) || !aligned(a->own.lengths, 4) ||
+      !aligned(a->prefix_table, 4) || !aligned(a->prefix_lengths, 4))
+    return DS_ERR_INVALID_ARG;
+  const PrefixAttnProblem p = prefix_of(a, out);
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < prefix_attn_workspace(p))
+    return DS_ERR_WORKSPACE;
+  return launch_prefix_attn(p, static_cast<uint8_t*>(workspace),
+                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? DS_OK
+             : DS_ERR_CUDA;
+}
+
+ds_status ds_block_norm(const ds_block_norm_args* a, void* x_out, uint16_t* h_out,
+                        ds_stream_t stream) {
+  if (!a) return DS_ERR_INVALID_ARG;
+  if (a->n_rows < 0 || a->n_rows > kMaxTokens || a->hidden < 8 || a->hidden > kNormMaxHidden ||
+      a->hidden % 8)
+    return DS_ERR_INVALID_ARG;
+  if (a->x_format != DS_ROWS_BF16 && a->x_format != DS_ROWS_FP32) return DS_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.f) || !std::isfinite(a->eps) || !std::isfinite(a->weight_offset) ||
+      !std::isfinite(a->x_scale) || !std::isfinite(a->y_scale))
+    return DS_ERR_INVALID_ARG;
+  if (a->n_rows == 0) return DS_OK;
+  const int32_t H = a->hidden;
+  auto stride_ok = [&](int64_t n) { return n >= H && n % 8 == 0 && n <= ((int64_t)1 << 31); };
+  if (!a->x || !aligned(a->x, 16) || !stride_ok(a->x_stride)) return DS_ERR_INVALID_ARG;
+  if (a->y && (!aligned(a->y, 16) || !stride_ok(a->y_stride))) return DS_ERR_INVALID_ARG;
+  if (a->y && a->gate && (!aligned(a->gate, 16) || (a->gate_stride && !stride_ok(a->gate_stride))))
+    return DS_ERR_INVALID_ARG;
+  if ((a->y && a->post_weight && !aligned(a->post_weight, 16)) ||
+      (a->weight && !aligned(a->weight, 16)))
+    return DS_ERR_INVALID_ARG;
+  if (!a->y) x_out = nullptr;   // (x stays as it is)
+  if (!a->weight) h_out = nullptr;
+  if ((a->weight && !h_out) || (!x_out && !h_out) || !aligned(x_out, 16) || !aligned(h_out, 16) ||
+      x_out == h_out)
+    return DS_ERR_INVALID_ARG;
+  // an output in place of an input: row by row, value by value
+  const bool fp32 = a->x_format == DS_ROWS_FP32;
+  if (x_out == a->x && a->x_stride != H) return DS_ERR_INVALID_ARG;
+  if (a->y && x_out == a->y && (fp32 || a->y_stride != H)) return DS_ERR_INVALID_ARG;
+  if (a->y && h_out == a->y && a->y_stride != H) return DS_ERR_INVALID_ARG;
+  if (h_out == a->x && (fp32 || a->x_stride != H)) return DS_ERR_INVALID_ARG;
+  BlockNormProblem p{};
+  p.T = a->n_rows;
+  p.H = H;
+  p.fp32 = fp32;
+  p.eps = a->eps;
+  p.weight_offset = a->weight_offset;
+  p.x_scale = a->x_scale;
+  p.y_scale = a->y_scale;
+  p.x = a->x;
+  p.x_stride = a->x_stride;
+  p.y = a->y;
+  p.y_stride = a->y_stride;
+  p.post_weight = a->y ? a->post_weight : nullptr;
+  p.gate = a->y ? a->gate : nullptr;
+  p.gate_stride = a->gate_stride;
+  p.weight = a->weight;
+  p.x_out = x_out;
+  p.h_out = h_out;
+  return launch_block_norm(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DS_OK
+                                                                                    : DS_ERR_CUDA;
+}
+
+ds_status ds_sample(const ds_sample_args* a, int32_t* token, float* prob, ds_stream_t stream) {
+  if (!a) return DS_ERR_INVALID_ARG;
+  if (a->n_rows < 0 || a->n_rows > (1 << 20) || a->n_vocab < 1 || a->n_vocab > (1 << 24))
+    return DS_ERR_INVALID_ARG;
+  if (a->logits_format != DS_ROWS_BF16 && a->logits_format != DS_ROWS_FP32)
+    return DS_ERR_INVALID_ARG;
+  if (a->n_rows == 0) return DS_OK;
+  const bool bf16 = a->logits_format == DS_ROWS_BF16;
+  if (!a->logits || !aligned(a->logits, bf16 ? 2 : 4) || a->logits_stride < a->n_vocab ||
+      a->logits_stride > ((int64_t)1 << 31))
+    return DS_ERR_INVALID_ARG;
+  if (!a->u || !aligned(a->u, 8) || !token || !aligned(token, 4) || !aligned(prob, 4) ||
+      !aligned(a->temperatures, 4) || !aligned(a->top_ps, 4) || !aligned(a->min_ps, 4) ||
+      !aligned(a->top_ks, 4))
+    return DS_ERR_INVALID_ARG;
+  const SampleProblem p{a->n_rows, a->n_vocab, bf16, a->logits, a->logits_stride, a->u,
+                        a->temperature, a->top_p, a->min_p, a->top_k, a->temperatures, a->top_ps,
+                        a->min_ps, a->top_ks, token, prob};
+  return launch_sample(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DS_OK
+                                                                                : DS_ERR_CUDA;
+}
+
+namespace {
+
 bool verify_sizes_ok(int32_t B, int32_t R, int32_t V) {
   return B >= 1 && B <= 4096 && R >= 1 && R <= kAcceptMaxRows && V >= 1 && V <= (1 << 24);
 }

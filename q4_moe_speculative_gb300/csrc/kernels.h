@@ -202,6 +202,54 @@ struct PagedAttnProblem {
 size_t paged_attn_workspace(const PagedAttnProblem& p);
 cudaError_t launch_paged_attn(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s);
 
+// ---- attention of sequences that share prefixes (prefix.cu)
+struct PrefixAttnProblem {
+  PagedAttnProblem own;        // the sequences' own tokens
+  int P, max_pages;            // prefixes (own.B a multiple), pages of one
+  const int32_t* table;
+  const int32_t* lengths;
+};
+// Workspace bytes, from the sizes in p alone.
+size_t prefix_attn_workspace(const PrefixAttnProblem& p);
+cudaError_t launch_prefix_attn(const PrefixAttnProblem& p, uint8_t* ws, cudaStream_t s);
+
+// ---- norms around a block (norm.cu)
+constexpr int kNormMaxHidden = 16384;
+struct BlockNormProblem {
+  int T, H;
+  bool fp32;                   // x and x_out: fp32 or bf16
+  float eps, weight_offset, x_scale, y_scale;
+  const void* x;
+  int64_t x_stride;
+  const uint16_t* y;           // NULL: x as it is
+  int64_t y_stride;
+  const uint16_t* post_weight; // NULL: y is not normed
+  const uint16_t* gate;        // NULL: none
+  int64_t gate_stride;         // 0: one row for all
+  const uint16_t* weight;      // NULL: no h
+  void* x_out;                 // NULL: not wanted
+  uint16_t* h_out;
+};
+cudaError_t launch_block_norm(const BlockNormProblem& p, cudaStream_t s);
+
+// ---- drawing tokens (sample.cu)
+struct SampleProblem {
+  int B, V;
+  bool bf16;
+  const void* logits;
+  int64_t stride;
+  const double* u;
+  float temperature, top_p, min_p;
+  int top_k;
+  const float* temperatures;   // per row, each or NULL for the one above
+  const float* top_ps;
+  const float* min_ps;
+  const int32_t* top_ks;
+  int32_t* out;
+  float* prob;                 // NULL: not wanted
+};
+cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s);
+
 // ---- verify acceptance (accept.cu)
 constexpr int kAcceptChunk = 4096;    // tokens of a row per CTA
 constexpr int kAcceptChunkSmall = 1024;   // the same for batches of few steps

@@ -26,7 +26,16 @@ struct PagedArgs {
   float* part_ml;   // [2 grid][M][2]
   int* span;        // [B][key heads][2]: the CTAs that begin and end a (sequence, head)
   int grid;         // CTAs that share the tiles
+  bool pieces;      // all results are left as sums in the workspace, for another kernel's join
 };
+
+// Where a CTA leaves its sums of a (sequence, key head): slot 0 when the run began before this CTA,
+// slot 1 when it begins here and goes on in the next; `all` of it: behind those of the CTAs
+// (PagedArgs::pieces only).
+__device__ __forceinline__ int64_t piece_at(const PagedArgs& a, int b, int h, bool begins, bool all) {
+  return all ? 2 * (int64_t)a.grid + (int64_t)b * a.c.heads + h
+             : 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
+}
 
 // paged_few.cu: tiles of 64 tokens, up to 32 query rows per key head.
 constexpr int kFewMaxRows = 32;
@@ -38,6 +47,12 @@ cudaError_t launch_few(const PagedArgs& p, int D, cudaStream_t s);
 // buffer of S, up to 64 columns of O for either part of P).
 constexpr int kTcMaxRows = 128;
 cudaError_t launch_tc(const PagedArgs& p, int D, cudaStream_t s);
+
+// paged_attn.cu: the kernel of a call alone, every (sequence, key head) left as pieces in the
+// workspace (of pieces_workspace() bytes, the status word first) for the caller's join. *args: what
+// the kernel was given.
+size_t pieces_workspace(const PagedAttnProblem& p);
+cudaError_t launch_pieces(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s, PagedArgs* args);
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

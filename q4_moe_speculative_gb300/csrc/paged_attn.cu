@@ -461,9 +461,8 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
         }
       __syncthreads();
       const int run = i < cur.tile ? i : cur.tile;   // tiles before this one in it
-      const bool whole = whole_end && cur.tile == run;
-      // slot 0: the run began before this CTA; slot 1: it begins here and goes on in the next
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.tile == run ? 1 : 0);
+      const bool all = whole_end && cur.tile == run, whole = all && !a.pieces;
+      const int64_t slot = piece_at(a, cur.b, cur.h, cur.tile == run, all);
       if (tid == 0) note_span(a, cur, cur.tile == run, whole_end);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -667,7 +666,8 @@ int begin_of(Kernel k, bool q8) {
   return k == Kernel::kFew ? 3 : (k == Kernel::kTensor ? (q8 ? 4 : 5) : 2);
 }
 
-Plan make_plan(const PagedAttnProblem& p) {
+// pieces: every (sequence, key head) is left in the workspace, none is finished.
+Plan make_plan(const PagedAttnProblem& p, bool pieces) {
   const int M = p.R * (p.Hq / p.cache.heads);
   Plan pl{};
   const int64_t cap = (int64_t)p.max_pages << p.cache.page_shift;
@@ -682,15 +682,19 @@ Plan make_plan(const PagedAttnProblem& p) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   pl.span = 256;   // behind the status word
   pl.ml = pl.span + up((size_t)runs * 2 * sizeof(int));
-  pl.po = pl.ml + up((size_t)2 * pl.grid * M * 2 * sizeof(float));
-  pl.total = pl.po + up((size_t)2 * pl.grid * M * p.D * sizeof(float));
+  const size_t places = 2 * (size_t)pl.grid + (pieces ? runs : 0);
+  pl.po = pl.ml + up(places * M * 2 * sizeof(float));
+  pl.total = pl.po + up(places * M * p.D * sizeof(float));
   return pl;
 }
 
+// The kernel of the runs; *args: what it was given.
 template <int D, bool kQ8>
-cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
-  const Plan pl = make_plan(p);
-  PagedArgs a{};
+cudaError_t run_pieces(const PagedAttnProblem& p, bool pieces, uint8_t* ws, cudaStream_t s,
+                       PagedArgs* args) {
+  const Plan pl = make_plan(p, pieces);
+  PagedArgs& a = *args;
+  a = PagedArgs{};
   a.B = p.B;
   a.R = p.R;
   a.Hq = p.Hq;
@@ -710,38 +714,53 @@ cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   a.part_ml = reinterpret_cast<float*>(ws + pl.ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.po);
   a.grid = pl.grid;
-  cudaError_t err;
-  if (pl.kernel == Kernel::kFew) {
-    err = launch_few(a, D, s);
-  } else if (pl.kernel == Kernel::kTensor) {
-    err = launch_tc(a, D, s);
-  } else {
-    err = with_rows(a.M, [&](auto mt) {
-      using C = Shape<D, kQ8, decltype(mt)::value>;
-      const auto kernel = k_paged<D, kQ8, decltype(mt)::value>;
-      static OncePerDevice ready;
-      const cudaError_t e = ready.run([&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-      });
-      if (e != cudaSuccess) return e;
-      return launch_pdl(kernel, dim3(pl.grid), C::kThreads, C::kSmem, s, a);
+  a.pieces = pieces;
+  if (pl.kernel == Kernel::kFew) return launch_few(a, D, s);
+  if (pl.kernel == Kernel::kTensor) return launch_tc(a, D, s);
+  return with_rows(a.M, [&](auto mt) {
+    using C = Shape<D, kQ8, decltype(mt)::value>;
+    const auto kernel = k_paged<D, kQ8, decltype(mt)::value>;
+    static OncePerDevice ready;
+    const cudaError_t e = ready.run([&] {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
-  }
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(pl.grid), C::kThreads, C::kSmem, s, a);
+  });
+}
+
+template <int D, bool kQ8>
+cudaError_t run(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
+  PagedArgs a;
+  const cudaError_t err = run_pieces<D, kQ8>(p, false, ws, s, &a);
   if (err != cudaSuccess) return err;
   const int heads = p.B * p.cache.heads;
-  if (pl.grid > 64 * heads)   // pieces per head
+  if (a.grid > 64 * heads)   // pieces per head
     return launch_pdl(k_paged_join<D, 32>, dim3(heads, a.M), 1024, 0, s, a);
-  if (pl.grid > 8 * heads) return launch_pdl(k_paged_join<D, 8>, dim3(heads, a.M), 256, 0, s, a);
+  if (a.grid > 8 * heads) return launch_pdl(k_paged_join<D, 8>, dim3(heads, a.M), 256, 0, s, a);
   return launch_pdl(k_paged_join<D, 1>, dim3(heads, (a.M + 7) / 8), 256, 0, s, a);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(const PagedAttnProblem& p) { return make_plan(p).total; }
+size_t paged_attn_workspace(const PagedAttnProblem& p) { return make_plan(p, false).total; }
 
 cudaError_t launch_paged_attn(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s) {
   if (p.D == 128) return p.cache.q8 ? run<128, true>(p, ws, s) : run<128, false>(p, ws, s);
   return p.cache.q8 ? run<64, true>(p, ws, s) : run<64, false>(p, ws, s);
 }
 
+namespace paged {
+
+size_t pieces_workspace(const PagedAttnProblem& p) { return make_plan(p, true).total; }
+
+cudaError_t launch_pieces(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s, PagedArgs* args) {
+  if (p.D == 128)
+    return p.cache.q8 ? run_pieces<128, true>(p, true, ws, s, args)
+                      : run_pieces<128, false>(p, true, ws, s, args);
+  return p.cache.q8 ? run_pieces<64, true>(p, true, ws, s, args)
+                    : run_pieces<64, false>(p, true, ws, s, args);
+}
+
+}  // namespace paged
 }  // namespace dsmoe

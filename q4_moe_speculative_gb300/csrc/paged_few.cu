@@ -445,9 +445,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Few<D, kQ8, NT>::kPerSm))
                      fmaxf(top_s[2 * C::kRows + row], top_s[3 * C::kRows + row]));
       };
       const int run = i < here.tile ? i : here.tile;   // tiles before this one in it
-      const bool whole = whole_end && here.tile == run;
-      // slot 0: the run began before this CTA; slot 1: it begins here and goes on in the next
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (here.tile == run ? 1 : 0);
+      const bool all = whole_end && here.tile == run, whole = all && !a.pieces;
+      const int64_t slot = piece_at(a, here.b, here.h, here.tile == run, all);
       if (tid == 0) note_span(a, here, here.tile == run, whole_end);
       if (tid < a.M) {
         const float top = top_of(tid);

@@ -29,8 +29,7 @@
 // not 0: where one of its values is not finite they are cleared before the product, and the
 // (at most 7) such tokens are added row by row when the run ends. Every wait is bounded; a
 // give-up sets the status word.
-#include "paged.cuh"
-#include "sm100.cuh"
+#include "paged_tc.cuh"
 
 namespace dsmoe {
 namespace paged_tc {
@@ -111,37 +110,6 @@ struct alignas(16) TcSmem {   // small arrays in front of the tiles
 constexpr int kSmallBytes = (sizeof(TcSmem) + 1023) / 1024 * 1024;
 static_assert(kSmallBytes <= 10240, "the largest call fills the SM's shared memory");
 
-__device__ __forceinline__ void fence_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-// Copies bytes (a multiple of 16, both addresses 16-byte aligned), counted by `bar`.
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(smem_at(dst)), "l"(src), "r"(bytes), "r"(smem_at(bar))
-      : "memory");
-}
-// Whether one of two bf16 values is infinite or NaN.
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-// One lane of a converged warp, always the same.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(bar)) : "memory");
-}
-// One arrival for the whole warp, after what its lanes did before.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-  __syncwarp();
-  if (lane == 0) arrive(bar);
-}
 // Whether three phases are complete: one round trip when they are.
 __device__ __forceinline__ bool ready3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
                                        uint64_t* c, uint32_t pc) {
@@ -168,19 +136,6 @@ __device__ __forceinline__ bool score_any(bool x) {
       : "memory");
   return r != 0;
 }
-// An operand stored with its K (tokens) as rows of 128 bytes of 64 M or N values, 128-byte
-// swizzle: groups of 8 tokens are 1024 bytes apart, the next 64 values `next` bytes further.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t next) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(next >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-constexpr uint32_t kMajorMN = (1u << 15) | (1u << 16);   // instruction descriptor: A and B
-
 // To 16 columns; tmem_wait_st() waits for it.
 __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[16]) {
   uint32_t r[16];
@@ -193,9 +148,6 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[16]) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 // Twice 16 columns, one wait.
 __device__ __forceinline__ void tmem_ld16x2(uint32_t at0, float (&v)[16], uint32_t at1,
@@ -527,7 +479,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       if (last) {
         // ------------------------------------------------------------ results -------------
         const int run = i < cur.tile ? i : cur.tile;    // tiles before this one in the run
-        const bool whole = ends && cur.tile == run;
+        const bool all = ends && cur.tile == run, whole = all && !a.pieces;
         // this thread's dimension of the values (codes are widened as (0, 2, 1, 3))
         const int dim = kQ8 ? (tk & ~3) | ((tk & 1) << 1) | ((tk >> 1) & 1) : tk;
         float v[7];
@@ -540,7 +492,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           if (lane < 16) sh.red[kMaxN * quad + c + lane] = sum;
         }
         score_sync();
-        const int64_t piece = 2 * (int64_t)blockIdx.x + (cur.tile == run ? 1 : 0);
+        const int64_t piece = piece_at(a, cur.b, cur.h, cur.tile == run, all);
         if (tid == 0) note_span(a, cur, cur.tile == run, ends);
         if (tid < N) {
           const float norm = __fadd_rn(__fadd_rn(sh.red[tid], sh.red[kMaxN + tid]),

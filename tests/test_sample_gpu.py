@@ -1,0 +1,221 @@
+"""Drawing tokens (ds_sample) against its definition in 64 bits, row by row on the CPU. Decisions
+are compared exactly; a border or draw within 2^-30 of the mass of a 64-bit evaluation's (the
+header's rounding of weights is below 2^-34 of it at these sizes) is left out, and hardly any is."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import q4_moe_speculative_gb300 as dsm
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+CLOSE = 2.0 ** -30
+
+
+def reference(l, u, T, k, p, mp):
+    """(token, its probability, whether any decision is clear) of one row, l as float64."""
+    l = np.where(np.isnan(l), -np.inf, l)
+    top = l.max()
+    if top == -np.inf:
+        return -1, 0.0, True
+    if not T > 2.0 ** -64:
+        return int(np.argmax(l)), 1.0, True
+    with np.errstate(invalid="ignore", over="ignore"):
+        near = np.where(l == top, 0.0, l - top)
+        w = np.exp(near / T)
+    order = np.argsort(-l, kind="stable")
+    if k > 0:
+        order = order[:k]
+    clear = True
+    # weights of 0 and 1 are exact in both, and so are their sums and (24 bits by 24) the top-p border
+    exact = bool(((w == 0) | (w == 1)).all())
+    p = 1.0 if math.isnan(p) else p
+    if p < 1:
+        mass = w[order]
+        upto = np.cumsum(mass)
+        before = upto - mass
+        gap = np.abs(before[1:] - p * upto[-1])
+        clear &= exact or len(gap) == 0 or gap.min() > CLOSE * upto[-1]
+        order = order[:max(1, int((before < p * upto[-1]).sum()))]
+    if mp > 0:
+        cut = min(0.0, T * math.log(mp))
+        off = near[order]
+        clear &= bool((np.abs(off - cut)[off < 0] > 2.0 ** -40 * abs(cut)).all())
+        order = order[off >= cut]
+    ids = np.sort(order)
+    mass = w[ids]
+    upto = np.cumsum(mass)
+    u = min(max(0.0 if math.isnan(u) else u, 0.0), 1 - 2.0 ** -53)
+    clear &= bool(np.abs(upto - u * upto[-1]).min() > CLOSE * upto[-1]) or u == 0.0
+    at = min(int((upto <= u * upto[-1]).sum()), len(ids) - 1)
+    while mass[at] < 2.0 ** -46:    # no weight in the header's units
+        at += 1
+    return int(ids[at]), float(mass[at] / upto[-1]), clear
+
+
+def check(logits, u, T=1.0, k=0, p=1.0, mp=0.0, most_unclear=0.02, **kw):
+    got, prob = dsm.sample(logits, u, temperature=T, top_k=k, top_p=p, min_p=mp, **kw)
+    got, prob = got.cpu().tolist(), prob.cpu().tolist()
+    l, u = logits.cpu().double().numpy(), u.cpu().tolist()
+    per = lambda x, b: x[b].item() if isinstance(x, torch.Tensor) else x  # noqa: E731
+    f32 = lambda x: float(np.float32(x))  # noqa: E731
+    unclear = 0
+    for b in range(l.shape[0]):
+        tok, pr, clear = reference(l[b], u[b], f32(per(T, b)), per(k, b), f32(per(p, b)),
+                                   f32(per(mp, b)))
+        if not clear:
+            unclear += 1
+            continue
+        assert got[b] == tok, (b, got[b], tok)
+        # the mass off by 2^-33 relative, one rounding to fp32
+        assert abs(prob[b] - pr) <= pr * (2.0 ** -24 + 2.0 ** -32) + 1e-45, (b, prob[b], pr)
+    assert unclear <= most_unclear * len(got) + 1
+    return got
+
+
+def inputs(B, V, dtype, seed, sigma=2.0):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    z = torch.randn(B, V, generator=g) * sigma
+    return z.to(dtype).to(DEV), torch.rand(B, generator=g, dtype=torch.float64).to(DEV)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,V", [(1, 1), (5, 2), (7, 33), (40, 1000), (16, 2048), (16, 2049), (9, 4097),
+                                 (8, 8200), (6, 32003), (3, 129280), (1, 700_001)])
+def test_every_setting_matches_64_bits(B, V, dtype):
+    z, u = inputs(B, V, dtype, seed=V)
+    check(z, u)
+    check(z, u, T=0.7, k=1)
+    check(z, u, T=0.7, k=max(1, V // 3))
+    check(z, u, T=1.3, p=0.9)
+    check(z, u, T=1.0, p=0.3)
+    check(z, u, mp=0.05)
+    check(z, u, T=0.9, k=50, p=0.95, mp=0.02)
+    check(z, u, T=0.0)
+
+
+def test_settings_per_row():
+    B, V = 64, 5000
+    z, u = inputs(B, V, torch.float32, seed=1)
+    row = torch.arange(B, device=DEV)
+    check(z, u, T=(0.3 * (row % 5)).float(), k=(row % 7 * 10).int(), p=(0.4 + 0.1 * (row % 8)).float(),
+          mp=(0.03 * (row % 3)).float())
+    check(z, u, T=(0.3 * (row % 5)).float(), k=11, p=0.8, mp=(0.03 * (row % 3)).float())
+
+
+@pytest.mark.parametrize("k,p", [(0, 0.5), (37, 1.0), (37, 0.5), (1, 1.0), (900, 0.999)])
+def test_ties_go_to_the_lowest_ids(k, p):
+    # few values, many equal: half of them at the border
+    g = torch.Generator()
+    g.manual_seed(k)
+    z = torch.randint(0, 3, (32, 9000), generator=g).float()
+    u = torch.rand(32, generator=g, dtype=torch.float64).to(DEV)
+    check(z.to(DEV), u, k=k, p=p)
+    check((z * -0.0).to(DEV), u, k=k, p=p)                       # all equal, some -0
+    check((z.to(torch.bfloat16) * 4 - 20).to(DEV), u, k=k, p=p, T=2.0)
+
+
+def test_tokens_that_are_masked():
+    z, u = inputs(24, 3001, torch.float32, seed=2)
+    z[:, ::2] = -float("inf")
+    z[:, 1::6] = float("nan")
+    z[3, :] = -float("inf")
+    z[4, :] = float("nan")
+    z[5, 77] = float("inf")
+    z[6, 50:60] = float("inf")
+    z[7, 3::6] = torch.finfo(torch.float32).min
+    for kw in (dict(), dict(k=20), dict(p=0.8), dict(mp=0.1), dict(k=5, p=0.5, mp=0.3), dict(T=0.0)):
+        got = check(z, u, **kw)
+        assert got[3] == got[4] == -1 and got[5] == 77 and 50 <= got[6] < 60
+    low = torch.full((2, 100), torch.finfo(torch.float32).min, device=DEV)
+    check(low, u[:2])
+    check(low.to(torch.bfloat16), u[:2], k=3)
+
+
+def test_uniforms_at_the_ends():
+    z, _ = inputs(6, 500, torch.float32, seed=3)
+    u = torch.tensor([0.0, 1 - 2.0 ** -53, 1.0, 5.0, -1.0, float("nan")], dtype=torch.float64, device=DEV)
+    got = check(z, u, T=1.0, most_unclear=1.0)
+    w = torch.softmax(z.cpu().double(), -1)
+    last = [int((r > 2.0 ** -46 * r.max()).nonzero().max()) for r in w]
+    assert got[0] == got[4] == got[5] == 0 and got[1:4] == last[1:4]
+
+
+def test_settings_at_the_ends():
+    z, u = inputs(16, 700, torch.float32, seed=4)
+    check(z, u, T=float("inf"))
+    check(z, u, T=1e30, k=10)
+    check(z, u, T=1e-3)
+    check(z, u, T=-1.0)
+    check(z, u, T=float("nan"))
+    check(z, u, k=700)
+    check(z, u, k=2 ** 40)
+    check(z, u, k=-3)
+    check(z, u, p=0.0)
+    check(z, u, p=-2.0)
+    check(z, u, p=float("nan"))
+    check(z, u, p=5.0)
+    check(z, u, mp=1.0)
+    check(z, u, mp=3.0)
+    check(z, u, mp=1e-30)
+    check(z * 1e4, u, p=0.9)
+    check(z * 1e-6, u, p=0.9, k=300)
+
+
+def test_strided_rows_and_other_outputs():
+    z, u = inputs(10, 4001, torch.bfloat16, seed=5)
+    want = dsm.sample(z[:, :3001].contiguous(), u, top_p=0.8)
+    out, prob = (torch.full((10,), -7, dtype=t, device=DEV) for t in (torch.int32, torch.float32))
+    got = dsm.sample(z[:, :3001], u, top_p=0.8, out=out, prob=prob)
+    assert got[0] is out and got[1] is prob
+    assert torch.equal(out, want[0]) and torch.equal(prob, want[1])
+    shifted = dsm.sample(z[:, 1:3002], u, top_p=0.8)
+    want = dsm.sample(z[:, 1:3002].contiguous(), u, top_p=0.8)
+    assert torch.equal(shifted[0], want[0]) and torch.equal(shifted[1], want[1])
+
+
+def test_frequencies_follow_the_distribution():
+    # 200,000 draws of one row: each token's count within 6 standard deviations
+    z = torch.randn(200, generator=torch.Generator().manual_seed(6)) * 1.5
+    n = 200_000
+    u = torch.rand(n, generator=torch.Generator().manual_seed(7), dtype=torch.float64)
+    got, _ = dsm.sample(z.expand(n, -1).contiguous().to(DEV), u.to(DEV), temperature=0.8, top_k=40)
+    w = torch.softmax(z.double() / 0.8, 0)
+    w[torch.argsort(-z)[40:]] = 0
+    w /= w.sum()
+    count = torch.bincount(got.cpu().long(), minlength=200).double()
+    assert bool(((count - n * w).abs() <= 6 * torch.sqrt(n * w * (1 - w)) + 1e-9).all())
+
+
+def test_no_rows_streams_and_replays():
+    e = torch.empty(0, 100, device=DEV)
+    assert dsm.sample(e, torch.empty(0, dtype=torch.float64, device=DEV))[0].shape == (0,)
+    z, u = inputs(20, 9001, torch.float32, seed=8)
+    want = dsm.sample(z, u, top_k=50, top_p=0.9)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = dsm.sample(z, u, top_k=50, top_p=0.9, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsm.sample(z, u, top_k=50, top_p=0.9, out=want[0], prob=want[1])
+    z2, u2 = inputs(20, 9001, torch.float32, seed=9)
+    z.copy_(z2)
+    u.copy_(u2)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = dsm.sample(z, u, top_k=50, top_p=0.9)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_verify_sample_and_sample_agree_on_a_row():
+    # the bonus token of a step of one row is a draw from the whole distribution
+    z, u = inputs(30, 3000, torch.float32, seed=10)
+    a, _ = dsm.sample(z, u, temperature=0.8)
+    b, n = dsm.verify_sample(z[:, None].contiguous(), float(np.float32(0.8)), None, None, None, u[:, None].contiguous())
+    assert torch.equal(a, b[:, 0]) and bool((n == 1).all())
