@@ -7,7 +7,9 @@
 //
 // Masses are integers: weight exp((l - max) / T) in units of 2^-scale, the scale such that a
 // vocabulary's sum fits 63 bits. Sums of integers do not depend on their order, so the borders and
-// the draw are the same whatever the grid, and no token is drawn beyond its share by rounding.
+// the draw are the same whatever the grid, and no token is drawn beyond its share by rounding. The
+// weights come from fp32 pairs and integers (Row::units), good to 2^-37: fp64 exponentials, which
+// this GPU has few units for, took 1050 us for 64 rows of 129,280 with top-p.
 //
 // Where the order is cut (the k-th largest logit; the logit at which the mass before it reaches
 // top_p), the border is found by counts or masses per bin: first 2048 bins of equal width in
@@ -15,6 +17,9 @@
 // ordered integers) in 2048 bins, until a bin is one key. Of the tokens with the border's logit the
 // lowest ids are kept.
 #include <cooperative_groups.h>
+
+#include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -31,22 +36,25 @@ constexpr int kBins = 2048;
 constexpr float kReach = 46.f;       // log2: a lighter token has the weight 0
 constexpr float kBinsPerLog2 = kBins / kReach;
 constexpr float kNegInf = -INFINITY;
+constexpr int kRoots = 64;
 
 struct SampleArgs {
   SampleProblem p;
   int chunk;        // tokens per CTA, a multiple of 8
   int scale;        // log2 of the weight 1
   bool staged;      // the chunk is kept in shared memory
+  unsigned long long root[kRoots];   // 2^(-j / kRoots) in units of 2^-40
 };
 
 struct Shared {
   unsigned lo[kBins], hi[kBins];
   unsigned long long upto[kBins];          // of this CTA's slice of the bins, merged
-  unsigned long long slice[kMaxCluster];   // totals of the slices
+  unsigned long long slice[2][kMaxCluster];   // totals of the slices, of this level and the last
   unsigned long long mass[kMaxCluster];    // of the CTAs: mass above the border
   unsigned long long ties[kMaxCluster];    // and tokens at it
   unsigned long long warp_mass[kWarps];
   unsigned long long warp_ties[kWarps];
+  unsigned long long root[kRoots];
   unsigned long long above;                // a border found: what is above its bin
   float top[kMaxCluster];
   float warp_top[kWarps];
@@ -65,23 +73,67 @@ __device__ __forceinline__ float from_key(unsigned k) {
 
 // What a row's weights need.
 struct Row {
-  float top, per_log2;     // the largest logit; log2(e) / T
-  double inv_t;
+  float top, per_log2, per_log2_low;     // the largest logit; log2(e) / T, in two parts
   int scale;
+  const unsigned long long* root;
   // (max - l) / T in log2: never falls as l does; NaN or beyond kReach: no weight
   __device__ __forceinline__ float reach(float l) const {
-    return l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), per_log2);
+    return __fmul_rn(__fsub_rn(top, l), per_log2);
   }
   __device__ __forceinline__ bool alive(float l) const { return reach(l) < kReach; }
-  __device__ __forceinline__ double weight(float l) const {
-    return l == top ? 1.0 : exp(((double)l - (double)top) * inv_t);
-  }
-  __device__ __forceinline__ unsigned long long units(float l) const {
-    return __double2ull_rn(weight(l) * (double)(1ull << scale));
-  }
   __device__ __forceinline__ int bin(float l) const {
     return min(kBins - 1, (int)__fmul_rn(reach(l), kBinsPerLog2));
   }
+  // The weights of two logits: 2^-t, t = (top - l) log2(e) / T as a pair of fp32 values (the
+  // difference and the product with their rounding errors), off by 2^-45 relative to t. With k =
+  // 64 t rounded, t = k / 64 + x, |x| <= 1 / 128: a root from the table, shifted, times e^-y, y =
+  // x log(2) <= 0.0055. e^-y - 1 = -y + y^2 / 2 - y^3 / 6 + y^4 / 24, the next term being 2^-44: all
+  // but the first are below 2^-16 and take one fp32 value (off by 2^-39); the first goes to an
+  // integer in two parts. Integers from fp32 by adding 1.5 x 2^23.
+  __device__ __forceinline__ void units2(float l0, float l1, unsigned long long* u0,
+                                         unsigned long long* u1) const {
+    constexpr float kMagic = 12582912.f;
+    const f2 minus = pair(-1.f, -1.f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
+    const f2 a = pair(top, top), b = mul2(pair(l0, l1), minus);
+    const f2 d = add2(a, b), bb = fma2(a, minus, d);     // d + e = top - l
+    const f2 e = add2(fma2(fma2(bb, minus, d), minus, a), fma2(bb, minus, b));
+    const f2 c = pair(per_log2, per_log2), cl = pair(per_log2_low, per_log2_low);
+    const f2 t = mul2(d, c);
+    const f2 te = fma2(e, c, fma2(d, cl, fma2(d, c, mul2(t, minus))));
+    const f2 km = fma2(t, pair(64.f, 64.f), magic);
+    const f2 r = fma2(add2(km, unmagic), pair(-1.f / 64, -1.f / 64), t);
+    const f2 ln = pair(kLn2, kLn2);
+    const f2 y = mul2(r, ln);
+    const f2 ye = fma2(te, ln, fma2(r, pair(kLn2Low, kLn2Low), fma2(r, ln, mul2(y, minus))));
+    f2 q = fma2(y, pair(1.f / 24, 1.f / 24), pair(-1.f / 6, -1.f / 6));
+    q = fma2(y, q, pair(0.5f, 0.5f));
+    q = fma2(mul2(y, y), q, mul2(ye, minus));
+    // -y = -m 2^-16 + rest
+    const f2 ym = fma2(y, pair(65536.f, 65536.f), magic);
+    const f2 rest = add2(fma2(add2(ym, unmagic), pair(1.f / 65536, 1.f / 65536), mul2(y, minus)), q);
+    const f2 low = fma2(rest, pair(0x1p37f, 0x1p37f), magic);
+    const float2 k2 = parts(km), m2 = parts(ym), low2 = parts(low), t2 = parts(t);
+    *u0 = t2.x < kReach ? compose(k2.x, m2.x, low2.x) : 0ull;
+    *u1 = t2.y < kReach ? compose(k2.y, m2.y, low2.y) : 0ull;
+  }
+  __device__ __forceinline__ unsigned long long units(float l) const {
+    unsigned long long u, v;
+    units2(l, l, &u, &v);
+    return u;
+  }
+  // Root k mod 64 times (1 + (low - m 2^21) 2^-37), shifted by k / 64.
+  __device__ __forceinline__ unsigned long long compose(float k_magic, float m_magic,
+                                                        float low_magic) const {
+    constexpr int kBits = 0x4B400000;   // of the magic number
+    const int k = __float_as_int(k_magic) - kBits;
+    const int f = __float_as_int(low_magic) - kBits - ((__float_as_int(m_magic) - kBits) << 21);
+    const unsigned long long z = root[k & (kRoots - 1)];
+    const long long w = (long long)z + (((long long)f * (int)(z >> 10)) >> 27);   // units of 2^-40
+    const int shift = (k >> 6) + 40 - scale;
+    return shift <= 0 ? (unsigned long long)w << -shift
+                      : (unsigned long long)(w + (1ll << (shift - 1))) >> shift;
+  }
+  static constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;   // log(2) in two parts
 };
 
 // Where the order is cut: tokens with a larger key are kept, and `ties` of those with this one.
@@ -116,33 +168,77 @@ __device__ __forceinline__ unsigned long long block_upto(unsigned long long v,
   return v + before;
 }
 
+// Adds u to a bin's sum in two words.
+__device__ __forceinline__ void bin_add(Shared& sh, int at, unsigned long long u) {
+  const unsigned add = (unsigned)u, old = atomicAdd(&sh.lo[at], add);
+  const unsigned up = (unsigned)(u >> 32) + (old + add < old ? 1u : 0u);
+  if (up) atomicAdd(&sh.hi[at], up);
+}
+
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a) {
-  extern __shared__ float stage[];
+__global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ SampleArgs a) {
+  extern __shared__ __align__(16) float stage_mem[];
   __shared__ Shared sh;
+  using Raw = typename std::conditional<kBf16, uint16_t, float>::type;
   const SampleProblem& p = a.p;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int b = blockIdx.x / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int v0 = min(p.V, rank * a.chunk), n = min(p.V, v0 + a.chunk) - v0;
+  if (tid < kRoots) sh.root[tid] = a.root[tid];
   pdl_wait();
-  const int64_t row_at = (int64_t)b * p.stride + v0;
-  auto raw = [&](int i) {   // NaN is never drawn
+  const Raw* const from = static_cast<const Raw*>(p.logits) + (int64_t)b * p.stride + v0;
+  auto widen = [](Raw x) {   // (NaN is never drawn, and -0 is 0)
     float l;
-    if constexpr (kBf16)
-      l = bf16_bits_to_f32(static_cast<const uint16_t*>(p.logits)[row_at + i]);
-    else
-      l = static_cast<const float*>(p.logits)[row_at + i];
-    return l == l ? __fadd_rn(l, 0.f) : kNegInf;   // (and -0 is 0)
+    if constexpr (kBf16) l = bf16_bits_to_f32(x);
+    else l = x;
+    return l == l ? __fadd_rn(l, 0.f) : kNegInf;
   };
   // ------------------------------------------------------------------ the largest logit
+  // (vectors of 16 bytes between a head and a tail of single values; places in shared memory are
+  // shifted so that they are vectors there as well)
+  constexpr int kVec = 16 / sizeof(Raw);
+  const int skew = (int)(reinterpret_cast<uintptr_t>(from) / sizeof(Raw)) & (kVec - 1);
+  float* const stage = stage_mem + skew;
   float top = kNegInf;
-  for (int i = tid; i < n; i += kThreads) {
-    const float l = raw(i);
-    if (a.staged) stage[i] = l;
-    top = fmaxf(top, l);
+  if (a.staged) {
+    const int head = min(n, (kVec - skew) & (kVec - 1)), vectors = (n - head) / kVec;
+    auto single = [&](int i) {
+      const float l = widen(from[i]);
+      stage[i] = l;
+      top = fmaxf(top, l);
+    };
+    if (tid < head) single(tid);
+    const int tail = head + vectors * kVec;
+    if (tid < n - tail) single(tail + tid);
+    const uint4* const vec = reinterpret_cast<const uint4*>(from + head);
+    float4* const to = reinterpret_cast<float4*>(stage + head);
+    constexpr int kAt = 4;
+    for (int i0 = tid; i0 < vectors; i0 += kAt * kThreads) {
+      uint4 x[kAt];
+#pragma unroll
+      for (int j = 0; j < kAt; ++j)
+        if (i0 + j * kThreads < vectors) x[j] = __ldcs(vec + i0 + j * kThreads);
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const int i = i0 + j * kThreads;
+        if (i >= vectors) break;
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        float l[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          if constexpr (kBf16) l[e] = widen((uint16_t)(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu));
+          else l[e] = widen(__uint_as_float(w[e]));
+          top = fmaxf(top, l[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; e += 4)
+          to[i * (kVec / 4) + e / 4] = make_float4(l[e], l[e + 1], l[e + 2], l[e + 3]);
+      }
+    }
+  } else {
+    for (int i = tid; i < n; i += kThreads) top = fmaxf(top, widen(from[i]));
   }
-  auto logit = [&](int i) { return a.staged ? stage[i] : raw(i); };
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) sh.warp_top[warp] = top;
@@ -160,21 +256,29 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a) {
     cluster.sync();
     return;
   }
+  const bool endless = top == INFINITY;   // only the infinite ones count, all alike
+  if (endless) top = 0.f;
+  auto logit = [&](int i) {   // a token past the CTA's last one has no weight
+    if (i >= n) return kNegInf;
+    const float l = a.staged ? stage[i] : widen(from[i]);
+    return endless ? (l == INFINITY ? 0.f : kNegInf) : l;
+  };
   // ------------------------------------------------------------------ the row's settings
   float T = p.temperatures ? p.temperatures[b] : p.temperature;
   int k = p.top_ks ? p.top_ks[b] : p.top_k;
   const float top_p = p.top_ps ? p.top_ps[b] : p.top_p;
-  float min_p = p.min_ps ? p.min_ps[b] : p.min_p;
-  const bool greedy = !(T > 0x1p-64f);
-  if (greedy) T = 1.f, k = 1;
+  const float min_p = p.min_ps ? p.min_ps[b] : p.min_p;
+  if (!(T > 0x1p-64f)) T = 1.f, k = 1;
+  const double inv_t = 1.0 / (double)T, per_log2 = inv_t * 1.4426950408889634;
   Row row;
   row.top = top;
-  row.inv_t = 1.0 / (double)T;
-  row.per_log2 = (float)(row.inv_t * 1.4426950408889634);
+  row.per_log2 = (float)per_log2;
+  row.per_log2_low = (float)(per_log2 - (double)row.per_log2);
   row.scale = a.scale;
+  row.root = sh.root;
 
-  // The border at which counts (masses) from above reach `target` (>= 1) units; tokens all kept: key
-  // 0 with no limit of ties. All threads of the cluster together.
+  // The border at which, from above, the count reaches `target`, or the mass top_p of what `limit`
+  // keeps; key 0 if there is not as much. All threads of the cluster together.
   auto cut = [&](bool masses, unsigned long long target, const Border& limit) {
     unsigned high = 0xFFFFFFFFu, low = 0u;   // the range of keys of the bin (level 0: none yet)
     int shift = 0;
@@ -182,35 +286,31 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a) {
     for (int level = 0;; ++level) {
       for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0u;
       __syncthreads();
-      for (int i = tid; i < n; i += kThreads) {
-        const float l = logit(i);
-        if (!row.alive(l)) continue;
-        const unsigned key = key_of(l);
-        // (tokens at the limit's key: their number is known, and counted once below)
-        if (key <= limit.key) continue;
-        int at;
-        if (level == 0) {
-          at = row.bin(l);
-        } else {
-          if (key > high || key < low) continue;
-          at = (int)((high - key) >> shift);
+      auto place = [&](float l, unsigned key) {   // its bin
+        if (!row.alive(l)) return -1;
+        if (level == 0) return row.bin(l);
+        return key > high || key < low ? -1 : (int)((high - key) >> shift);
+      };
+      for (int i = tid; i < n; i += 2 * kThreads) {
+        const float l0 = logit(i), l1 = logit(i + kThreads);
+        const unsigned key0 = key_of(l0), key1 = key_of(l1);
+        // (those at the limit's key: their number is known, and they are counted once below)
+        const int at0 = key0 <= limit.key ? -1 : place(l0, key0);
+        const int at1 = key1 <= limit.key ? -1 : place(l1, key1);
+        if (!masses) {
+          if (at0 >= 0) atomicAdd(&sh.lo[at0], 1u);
+          if (at1 >= 0) atomicAdd(&sh.lo[at1], 1u);
+        } else if (at0 >= 0 || at1 >= 0) {
+          unsigned long long u0, u1;
+          row.units2(l0, l1, &u0, &u1);
+          if (at0 >= 0) bin_add(sh, at0, u0);
+          if (at1 >= 0) bin_add(sh, at1, u1);
         }
-        const unsigned long long u = masses ? row.units(l) : 1ull;
-        const unsigned add = (unsigned)u, old = atomicAdd(&sh.lo[at], add);
-        const unsigned up = (unsigned)(u >> 32) + (old + add < old ? 1u : 0u);
-        if (up) atomicAdd(&sh.hi[at], up);
       }
       if (rank == 0 && tid == 0 && limit.key) {
         const float l = from_key(limit.key);
-        const int at = level == 0 ? row.bin(l)
-                                  : (limit.key <= high && limit.key >= low
-                                         ? (int)((high - limit.key) >> shift) : -1);
-        if (at >= 0) {
-          const unsigned long long u = (masses ? row.units(l) : 1ull) * limit.ties;
-          const unsigned add = (unsigned)u, old = atomicAdd(&sh.lo[at], add);
-          const unsigned up = (unsigned)(u >> 32) + (old + add < old ? 1u : 0u);
-          if (up) atomicAdd(&sh.hi[at], up);
-        }
+        const int at = place(l, limit.key);
+        if (at >= 0) bin_add(sh, at, (masses ? row.units(l) : 1ull) * limit.ties);
       }
       cluster.sync();
       // this CTA's slice of the bins, over all CTAs
@@ -228,50 +328,51 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a) {
         __syncthreads();
         before = sh.upto[min(per, i0 + kThreads) - 1];
       }
-      if (tid < C) *cluster.map_shared_rank(&sh.slice[rank], tid) = before;
+      if (tid < C) *cluster.map_shared_rank(&sh.slice[level & 1][rank], tid) = before;
       cluster.sync();
+      const unsigned long long* const slice = sh.slice[level & 1];
+      if (masses && level == 0) {
+        unsigned long long total = 0;
+        for (int c = 0; c < C; ++c) total += slice[c];
+        const double share = ceil((double)total * (double)top_p);
+        target = share >= 1.0 ? min(total, __double2ull_rz(share)) : 1ull;
+      }
       unsigned long long start = above;
       int owner = 0;
-      while (owner < C && start + sh.slice[owner] < target) start += sh.slice[owner++];
-      if (owner == C) return Border{0u, ~0ull};   // (level 0 only: there is not as much)
-      if (owner == rank) {
-        for (int i = tid; i < per; i += kThreads) {
-          const unsigned long long lower = start + (i ? sh.upto[i - 1] : 0);
-          if (lower < target && start + sh.upto[i] >= target)
-            for (int c = 0; c < C; ++c) {
-              *cluster.map_shared_rank(&sh.bin, c) = first + i;
-              *cluster.map_shared_rank(&sh.above, c) = lower;
-            }
+      while (owner < C && start + slice[owner] < target) start += slice[owner++];
+      if (owner == C) return Border{0u, ~0ull};   // (level 0 only)
+      const unsigned long long* const upto = cluster.map_shared_rank(sh.upto, owner);
+      for (int i = tid; i < per; i += kThreads) {
+        const unsigned long long lower = start + (i ? upto[i - 1] : 0);
+        if (lower < target && start + upto[i] >= target) {   // (one of them)
+          sh.bin = owner * per + i;
+          sh.above = lower;
         }
       }
-      cluster.sync();
+      __syncthreads();
       const int bin = sh.bin;
       above = sh.above;
       if (level == 0) {
-        // the keys of the bin: those of the largest and the smallest logit that fall into it
+        // the keys of the bin, between those of logits beyond it and those before it
         if (tid < 2) {
-          unsigned in = 0u, ex = 0xFFFFFFFFu;   // tid 0: the largest key whose bin is >= bin
-          const unsigned top_key = key_of(row.top);
-          // (bins fall as keys rise; no key above the top's counts)
-          ex = top_key + 1;
-          in = key_of(-INFINITY);
+          unsigned in = key_of(kNegInf), ex = key_of(row.top) + 1;
           while (ex - in > 1) {
             const unsigned mid = in + (ex - in) / 2;
             const float l = from_key(mid);
             const bool beyond = !row.alive(l) || row.bin(l) > bin;
-            const bool inside = !beyond && row.bin(l) == bin;
-            if (tid == 0 ? (beyond || inside) : beyond) in = mid;
+            if (beyond || (tid == 0 && row.bin(l) == bin)) in = mid;
             else ex = mid;
           }
-          sh.range[tid] = tid == 0 ? in : ex;   // (tid 1: the smallest key that is not beyond)
+          sh.range[tid] = tid == 0 ? in : ex;
         }
         __syncthreads();
         high = sh.range[0];
         low = sh.range[1];
       } else {
-        const unsigned span = shift ? (1u << shift) - 1 : 0u;
+        const unsigned span = (1u << shift) - 1;
         high = high - ((unsigned)bin << shift);
         low = high - low > span ? high - span : low;
+        __syncthreads();   // (sh.bin may be overwritten)
       }
       if (high == low) {
         const unsigned long long each = masses ? row.units(from_key(high)) : 1ull;
@@ -283,21 +384,40 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a) {
       while ((high - low) >> shift >= kBins) ++shift;
     }
   };
-  // Mass above the border and tokens at it: of each warp's stretch and each CTA. The total.
+
+  Border border{0u, ~0ull};
+  if (k > 0 && k < p.V) border = cut(false, (unsigned long long)k, border);
+  if (top_p < 1.f) border = cut(true, 0ull, border);
+  float least = kNegInf;   // the smallest logit that min-p leaves
+  if (min_p > 0.f) {
+    const double less = min_p < 1.f ? (double)T * log((double)min_p) : 0.0;
+    least = fminf(top, __double2float_ru((double)top + less));
+    auto enough = [&](float l) { return (double)l - (double)top >= less; };
+    while (least < top && !enough(least)) least = from_key(key_of(least) + 1);
+    while (least > kNegInf && enough(from_key(key_of(least) - 1)))
+      least = from_key(key_of(least) - 1);
+  }
+  // ------------------------------------------------------------------ the draw
+  // the mass above the border, and the tokens at it, of each warp's stretch and of each CTA
   const int stretch = (n + kWarps - 1) / kWarps;
-  auto weigh = [&](const Border& cutoff, float least) {
+  const unsigned least_key = key_of(least);
+  {
     unsigned long long mass = 0, ties = 0;
     const int end = min(n, (warp + 1) * stretch);
-    for (int i = warp * stretch + lane; i < end; i += 32) {
-      const float l = logit(i);
-      if (!row.alive(l) || l < least) continue;
-      const unsigned key = key_of(l);
-      if (key > cutoff.key) mass += row.units(l);
-      else if (key == cutoff.key) ++ties;
+    for (int i0 = warp * stretch; i0 < end; i0 += 64) {
+      const int i = i0 + lane;
+      const float l0 = i < end ? logit(i) : kNegInf, l1 = i + 32 < end ? logit(i + 32) : kNegInf;
+      const unsigned key0 = key_of(l0), key1 = key_of(l1);
+      const bool in0 = key0 >= least_key, in1 = key1 >= least_key;
+      const bool over0 = in0 && key0 > border.key, over1 = in1 && key1 > border.key;
+      ties += (in0 && key0 == border.key ? 1 : 0) + (in1 && key1 == border.key ? 1 : 0);
+      if (!__any_sync(0xffffffffu, over0 || over1)) continue;
+      unsigned long long u0, u1;
+      row.units2(l0, l1, &u0, &u1);
+      mass += (over0 ? u0 : 0ull) + (over1 ? u1 : 0ull);
     }
     mass = warp_sum(mass);
     ties = warp_sum(ties);
-    __syncthreads();
     if (lane == 0) {
       sh.warp_mass[warp] = mass;
       sh.warp_ties[warp] = ties;
@@ -313,36 +433,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a) {
       *cluster.map_shared_rank(&sh.ties[rank], tid) = ties;
     }
     cluster.sync();
-  };
-
-  Border border{0u, ~0ull};
-  if (k > 0 && k < p.V) border = cut(false, (unsigned long long)k, border);
-  const bool nucleus = top_p < 1.f;
-  if (nucleus) {
-    // the mass of what top-k kept
-    weigh(border, kNegInf);
-    unsigned long long total = 0, ties = 0;
-    for (int c = 0; c < C; ++c) {
-      total += sh.mass[c];
-      ties += sh.ties[c];
-    }
-    if (border.key) total += min(ties, border.ties) * row.units(from_key(border.key));
-    double share = ceil((double)total * (double)top_p);
-    unsigned long long target = share >= 1.0 ? __double2ull_rz(share) : 1ull;
-    if (target > total) target = total;
-    border = cut(true, target, border);
   }
-  float least = kNegInf;   // the smallest logit that min-p leaves
-  if (min_p > 0.f) {
-    const double less = min_p < 1.f ? (double)T * log((double)min_p) : 0.0;
-    least = fminf(top, __double2float_ru((double)top + less));
-    auto enough = [&](float l) { return (double)l - (double)top >= less; };
-    while (least < top && !enough(least)) least = from_key(key_of(least) + 1);
-    while (least > kNegInf && enough(from_key(key_of(least) - 1)))
-      least = from_key(key_of(least) - 1);
-  }
-  // ------------------------------------------------------------------ the draw
-  weigh(border, least);
   const unsigned long long each = border.key ? row.units(from_key(border.key)) : 0ull;
   unsigned long long total = 0, mine = 0, start = 0, ties_start = 0, ties_upto = 0;
   for (int c = 0; c < C; ++c) {
@@ -373,31 +464,32 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs a) {
       tied = next;
     }
     const int begin = w * stretch, end = min(n, begin + stretch);
-    __syncthreads();
     const int per = (stretch + kThreads - 1) / kThreads;
     const int i0 = begin + tid * per, i1 = min(end, i0 + per);
     unsigned long long mass = 0, ties = 0;
     for (int i = i0; i < i1; ++i) {
       const float l = logit(i);
-      if (!row.alive(l) || l < least) continue;
-      if (key_of(l) > border.key) mass += row.units(l);
-      else if (key_of(l) == border.key) ++ties;
+      const unsigned key = key_of(l);
+      if (key < least_key) continue;
+      if (key > border.key) mass += row.units(l);
+      else if (key == border.key) ++ties;
     }
     const unsigned long long ties_to = tied + block_upto(ties, sh.warp_ties);
     const unsigned long long ties_from = ties_to - ties;
     mass += (min(ties_to, border.ties) - min(ties_from, border.ties)) * each;
-    const unsigned long long to = at + block_upto(mass, sh.warp_mass), from = to - mass;
-    if (target >= from && target < to) {
-      unsigned long long sum = from, place = ties_from;
+    const unsigned long long to = at + block_upto(mass, sh.warp_mass), begins = to - mass;
+    if (target >= begins && target < to) {
+      unsigned long long sum = begins, place = ties_from;
       for (int i = i0; i < i1; ++i) {
         const float l = logit(i);
-        if (!row.alive(l) || l < least) continue;
         const unsigned key = key_of(l);
+        if (key < least_key) continue;
         if (key > border.key || (key == border.key && place++ < border.ties)) sum += row.units(l);
         if (sum > target) {
           p.out[b] = v0 + i;
           if (p.prob)
-            p.prob[b] = (float)(row.weight(l) / ((double)total / (double)(1ull << row.scale)));
+            p.prob[b] = (float)(exp(((double)l - (double)top) * inv_t) /
+                                ((double)total / (double)(1ull << row.scale)));
           break;
         }
       }
@@ -417,8 +509,10 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   int C = 1;
   while (C < kMaxCluster && p.V > 2048 * C) C *= 2;
   a.chunk = ((p.V + C - 1) / C + 7) / 8 * 8;
-  const int room = 160 * 1024;
-  a.staged = a.chunk * 4 <= room;
+  for (int j = 0; j < kRoots; ++j)
+    a.root[j] = (unsigned long long)std::llrint(std::exp2(40.0 - j / (double)kRoots));
+  const int room = 160 * 1024, stage = (a.chunk + 8) * 4;
+  a.staged = stage <= room;
   const auto kernel = p.bf16 ? k_sample<true> : k_sample<false>;
   static OncePerDevice ready;
   cudaError_t e = ready.run([&] {
@@ -432,7 +526,7 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.B * C);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.staged ? a.chunk * 4 : 0;
+  cfg.dynamicSmemBytes = a.staged ? stage : 0;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
