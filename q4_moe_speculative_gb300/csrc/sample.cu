@@ -37,6 +37,7 @@ constexpr float kReach = 46.f;       // log2: a lighter token has the weight 0
 constexpr float kBinsPerLog2 = kBins / kReach;
 constexpr float kNegInf = -INFINITY;
 constexpr int kRoots = 64;
+constexpr int kList = 512;
 
 struct SampleArgs {
   SampleProblem p;
@@ -58,8 +59,11 @@ struct Shared {
   unsigned long long above;                // a border found: what is above its bin
   float top[kMaxCluster];
   float warp_top[kWarps];
-  int bin;
+  double inv_t, less;                      // 1 / T, T log(min_p)
+  float per_log2, per_log2_low, least;
+  int bin, listed;
   unsigned range[2];
+  int list[kList];                         // tokens of the border's bin
 };
 
 // Logits as integers in the same order (NaN never gets here).
@@ -80,18 +84,19 @@ struct Row {
   __device__ __forceinline__ float reach(float l) const {
     return __fmul_rn(__fsub_rn(top, l), per_log2);
   }
-  __device__ __forceinline__ bool alive(float l) const { return reach(l) < kReach; }
-  __device__ __forceinline__ int bin(float l) const {
-    return min(kBins - 1, (int)__fmul_rn(reach(l), kBinsPerLog2));
+  static __device__ __forceinline__ int bin_of(float reach) {
+    return min(kBins - 1, (int)__fmul_rn(reach, kBinsPerLog2));
   }
+  __device__ __forceinline__ int bin(float l) const { return bin_of(reach(l)); }
   // The weights of two logits: 2^-t, t = (top - l) log2(e) / T as a pair of fp32 values (the
   // difference and the product with their rounding errors), off by 2^-45 relative to t. With k =
   // 64 t rounded, t = k / 64 + x, |x| <= 1 / 128: a root from the table, shifted, times e^-y, y =
   // x log(2) <= 0.0055. e^-y - 1 = -y + y^2 / 2 - y^3 / 6 + y^4 / 24, the next term being 2^-44: all
   // but the first are below 2^-16 and take one fp32 value (off by 2^-39); the first goes to an
   // integer in two parts. Integers from fp32 by adding 1.5 x 2^23.
+  // (where[]: the reach of each)
   __device__ __forceinline__ void units2(float l0, float l1, unsigned long long* u0,
-                                         unsigned long long* u1) const {
+                                         unsigned long long* u1, float2* where) const {
     constexpr float kMagic = 12582912.f;
     const f2 minus = pair(-1.f, -1.f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
     const f2 a = pair(top, top), b = mul2(pair(l0, l1), minus);
@@ -113,12 +118,14 @@ struct Row {
     const f2 rest = add2(fma2(add2(ym, unmagic), pair(1.f / 65536, 1.f / 65536), mul2(y, minus)), q);
     const f2 low = fma2(rest, pair(0x1p37f, 0x1p37f), magic);
     const float2 k2 = parts(km), m2 = parts(ym), low2 = parts(low), t2 = parts(t);
+    *where = t2;
     *u0 = t2.x < kReach ? compose(k2.x, m2.x, low2.x) : 0ull;
     *u1 = t2.y < kReach ? compose(k2.y, m2.y, low2.y) : 0ull;
   }
   __device__ __forceinline__ unsigned long long units(float l) const {
     unsigned long long u, v;
-    units2(l, l, &u, &v);
+    float2 where;
+    units2(l, l, &u, &v, &where);
     return u;
   }
   // Root k mod 64 times (1 + (low - m 2^21) 2^-37), shifted by k / 64.
@@ -176,7 +183,7 @@ __device__ __forceinline__ void bin_add(Shared& sh, int at, unsigned long long u
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) float stage_mem[];
   __shared__ Shared sh;
   using Raw = typename std::conditional<kBf16, uint16_t, float>::type;
@@ -187,6 +194,19 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
   const int v0 = min(p.V, rank * a.chunk), n = min(p.V, v0 + a.chunk) - v0;
   if (tid < kRoots) sh.root[tid] = a.root[tid];
   pdl_wait();
+  // ------------------------------------------------------------------ the row's settings
+  float T = p.temperatures ? p.temperatures[b] : p.temperature;
+  int k = p.top_ks ? p.top_ks[b] : p.top_k;
+  const float top_p = p.top_ps ? p.top_ps[b] : p.top_p;
+  const float min_p = p.min_ps ? p.min_ps[b] : p.min_p;
+  if (!(T > 0x1p-64f)) T = 1.f, k = 1;
+  if (tid == kThreads - 1) {   // (fp64, so one thread, beside the loads)
+    const double inv_t = 1.0 / (double)T, per_log2 = inv_t * 1.4426950408889634;
+    sh.inv_t = inv_t;
+    sh.per_log2 = (float)per_log2;
+    sh.per_log2_low = (float)(per_log2 - (double)(float)per_log2);
+    sh.less = min_p > 0.f && min_p < 1.f ? (double)T * log((double)min_p) : 0.0;
+  }
   const Raw* const from = static_cast<const Raw*>(p.logits) + (int64_t)b * p.stride + v0;
   auto widen = [](Raw x) {   // (NaN is never drawn, and -0 is 0)
     float l;
@@ -263,53 +283,83 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
     const float l = a.staged ? stage[i] : widen(from[i]);
     return endless ? (l == INFINITY ? 0.f : kNegInf) : l;
   };
-  // ------------------------------------------------------------------ the row's settings
-  float T = p.temperatures ? p.temperatures[b] : p.temperature;
-  int k = p.top_ks ? p.top_ks[b] : p.top_k;
-  const float top_p = p.top_ps ? p.top_ps[b] : p.top_p;
-  const float min_p = p.min_ps ? p.min_ps[b] : p.min_p;
-  if (!(T > 0x1p-64f)) T = 1.f, k = 1;
-  const double inv_t = 1.0 / (double)T, per_log2 = inv_t * 1.4426950408889634;
   Row row;
   row.top = top;
-  row.per_log2 = (float)per_log2;
-  row.per_log2_low = (float)(per_log2 - (double)row.per_log2);
+  row.per_log2 = sh.per_log2;
+  row.per_log2_low = sh.per_log2_low;
   row.scale = a.scale;
   row.root = sh.root;
+  if (tid == 0) {   // the smallest logit that min-p leaves (read after the next barrier)
+    float least = kNegInf;
+    if (min_p > 0.f) {
+      const double less = sh.less;
+      auto enough = [&](float l) { return (double)l - (double)top >= less; };
+      least = fminf(top, __double2float_ru((double)top + less));
+      while (least < top && !enough(least)) least = from_key(key_of(least) + 1);
+      while (least > kNegInf && enough(from_key(key_of(least) - 1)))
+        least = from_key(key_of(least) - 1);
+    }
+    sh.least = least;
+  }
 
   // The border at which, from above, the count reaches `target`, or the mass top_p of what `limit`
-  // keeps; key 0 if there is not as much. All threads of the cluster together.
-  auto cut = [&](bool masses, unsigned long long target, const Border& limit) {
+  // keeps; key 0 if there is not as much. *own: where nothing is limited, this CTA's part of what is
+  // above it, and its tokens at it. All threads of the cluster together.
+  auto cut = [&](bool masses, unsigned long long target, const Border& limit,
+                 unsigned long long* own, unsigned long long* own_ties) {
     unsigned high = 0xFFFFFFFFu, low = 0u;   // the range of keys of the bin (level 0: none yet)
     int shift = 0;
     unsigned long long above = 0;
+    *own = 0;
     for (int level = 0;; ++level) {
+      const bool listed = level >= 2 && sh.listed <= kList;
       for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0u;
       __syncthreads();
-      auto place = [&](float l, unsigned key) {   // its bin
-        if (!row.alive(l)) return -1;
-        if (level == 0) return row.bin(l);
-        return key > high || key < low ? -1 : (int)((high - key) >> shift);
-      };
-      for (int i = tid; i < n; i += 2 * kThreads) {
-        const float l0 = logit(i), l1 = logit(i + kThreads);
-        const unsigned key0 = key_of(l0), key1 = key_of(l1);
-        // (those at the limit's key: their number is known, and they are counted once below)
-        const int at0 = key0 <= limit.key ? -1 : place(l0, key0);
-        const int at1 = key1 <= limit.key ? -1 : place(l1, key1);
-        if (!masses) {
-          if (at0 >= 0) atomicAdd(&sh.lo[at0], 1u);
-          if (at1 >= 0) atomicAdd(&sh.lo[at1], 1u);
-        } else if (at0 >= 0 || at1 >= 0) {
-          unsigned long long u0, u1;
-          row.units2(l0, l1, &u0, &u1);
-          if (at0 >= 0) bin_add(sh, at0, u0);
-          if (at1 >= 0) bin_add(sh, at1, u1);
+      if (level == 1 && tid == 0) sh.listed = 0;
+      if (level == 1) __syncthreads();
+      if (level == 0) {
+        for (int i = tid; i < n; i += 2 * kThreads) {
+          const float l0 = logit(i), l1 = logit(i + kThreads);
+          // (those at the limit's key: their number is known, and they are counted once below)
+          const bool in0 = key_of(l0) > limit.key, in1 = key_of(l1) > limit.key;
+          if (!masses) {
+            const float t0 = row.reach(l0), t1 = row.reach(l1);
+            if (t0 < kReach) atomicAdd(&sh.lo[Row::bin_of(t0)], 1u);
+            if (t1 < kReach) atomicAdd(&sh.lo[Row::bin_of(t1)], 1u);
+          } else if (in0 || in1) {
+            unsigned long long u0, u1;
+            float2 t;
+            row.units2(l0, l1, &u0, &u1, &t);
+            if (in0 && t.x < kReach) bin_add(sh, Row::bin_of(t.x), u0);
+            if (in1 && t.y < kReach) bin_add(sh, Row::bin_of(t.y), u1);
+          }
+        }
+      } else {
+        // few tokens are in the range: after the first look at all of them from a list, if it holds
+        auto token = [&](int i) {
+          const float l = logit(i);
+          const unsigned key = key_of(l);
+          if (key > high || key < low || key <= limit.key) return;
+          const int at = (int)((high - key) >> shift);
+          if (masses) bin_add(sh, at, row.units(l));
+          else atomicAdd(&sh.lo[at], 1u);
+          if (level == 1) {
+            const int place = atomicAdd(&sh.listed, 1);
+            if (place < kList) sh.list[place] = i;
+          }
+        };
+        if (listed) {
+          if (tid < sh.listed) token(sh.list[tid]);
+        } else {
+#pragma unroll 4
+          for (int i = tid; i < n; i += kThreads) token(i);
         }
       }
       if (rank == 0 && tid == 0 && limit.key) {
         const float l = from_key(limit.key);
-        const int at = place(l, limit.key);
+        const int at = level == 0 ? row.bin(l)
+                                  : (limit.key > high || limit.key < low
+                                         ? -1 : (int)((high - limit.key) >> shift));
         if (at >= 0) bin_add(sh, at, (masses ? row.units(l) : 1ull) * limit.ties);
       }
       cluster.sync();
@@ -352,15 +402,19 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
       __syncthreads();
       const int bin = sh.bin;
       above = sh.above;
+      if (masses)
+        for (int i = tid; i < bin; i += kThreads)   // (this thread's part; summed at the end)
+          *own += ((unsigned long long)sh.hi[i] << 32) + sh.lo[i];
+      const unsigned long long in_bin = ((unsigned long long)sh.hi[bin] << 32) + sh.lo[bin];
       if (level == 0) {
         // the keys of the bin, between those of logits beyond it and those before it
         if (tid < 2) {
           unsigned in = key_of(kNegInf), ex = key_of(row.top) + 1;
           while (ex - in > 1) {
             const unsigned mid = in + (ex - in) / 2;
-            const float l = from_key(mid);
-            const bool beyond = !row.alive(l) || row.bin(l) > bin;
-            if (beyond || (tid == 0 && row.bin(l) == bin)) in = mid;
+            const float t = row.reach(from_key(mid));
+            const bool beyond = !(t < kReach) || Row::bin_of(t) > bin;
+            if (beyond || (tid == 0 && Row::bin_of(t) == bin)) in = mid;
             else ex = mid;
           }
           sh.range[tid] = tid == 0 ? in : ex;
@@ -372,12 +426,16 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
         const unsigned span = (1u << shift) - 1;
         high = high - ((unsigned)bin << shift);
         low = high - low > span ? high - span : low;
-        __syncthreads();   // (sh.bin may be overwritten)
+        __syncthreads();   // (sh.bin and the bins may be overwritten)
       }
       if (high == low) {
         const unsigned long long each = masses ? row.units(from_key(high)) : 1ull;
         unsigned long long ties = (target - above + each - 1) / each;
         if (high == limit.key && ties > limit.ties) ties = limit.ties;
+        if (masses) {
+          if (tid == kThreads - 1) *own_ties = in_bin / each;
+          *own = block_upto(*own, sh.warp_mass);   // (the last thread has all of it)
+        }
         return Border{high, ties};
       }
       shift = 0;
@@ -386,22 +444,20 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
   };
 
   Border border{0u, ~0ull};
-  if (k > 0 && k < p.V) border = cut(false, (unsigned long long)k, border);
-  if (top_p < 1.f) border = cut(true, 0ull, border);
-  float least = kNegInf;   // the smallest logit that min-p leaves
-  if (min_p > 0.f) {
-    const double less = min_p < 1.f ? (double)T * log((double)min_p) : 0.0;
-    least = fminf(top, __double2float_ru((double)top + less));
-    auto enough = [&](float l) { return (double)l - (double)top >= less; };
-    while (least < top && !enough(least)) least = from_key(key_of(least) + 1);
-    while (least > kNegInf && enough(from_key(key_of(least) - 1)))
-      least = from_key(key_of(least) - 1);
+  unsigned long long own = 0, own_ties = 0;
+  bool weighed = false;   // the cut has this CTA's mass above the border and its tokens at it
+  if (k > 0 && k < p.V) border = cut(false, (unsigned long long)k, border, &own, &own_ties);
+  if (top_p < 1.f) {
+    weighed = border.key == 0u;
+    border = cut(true, 0ull, border, &own, &own_ties);
   }
+  __syncthreads();
+  const unsigned least_key = key_of(sh.least);
+  weighed = weighed && least_key <= border.key;
   // ------------------------------------------------------------------ the draw
-  // the mass above the border, and the tokens at it, of each warp's stretch and of each CTA
+  // the mass above the border, and the tokens at it, of each warp's stretch
   const int stretch = (n + kWarps - 1) / kWarps;
-  const unsigned least_key = key_of(least);
-  {
+  auto weigh = [&] {
     unsigned long long mass = 0, ties = 0;
     const int end = min(n, (warp + 1) * stretch);
     for (int i0 = warp * stretch; i0 < end; i0 += 64) {
@@ -413,7 +469,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
       ties += (in0 && key0 == border.key ? 1 : 0) + (in1 && key1 == border.key ? 1 : 0);
       if (!__any_sync(0xffffffffu, over0 || over1)) continue;
       unsigned long long u0, u1;
-      row.units2(l0, l1, &u0, &u1);
+      float2 t;
+      row.units2(l0, l1, &u0, &u1, &t);
       mass += (over0 ? u0 : 0ull) + (over1 ? u1 : 0ull);
     }
     mass = warp_sum(mass);
@@ -423,17 +480,23 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
       sh.warp_ties[warp] = ties;
     }
     __syncthreads();
-    if (tid < C) {
-      mass = ties = 0;
+  };
+  if (!weighed) {
+    weigh();
+    if (tid == kThreads - 1) {
+      own = own_ties = 0;
       for (int w = 0; w < kWarps; ++w) {
-        mass += sh.warp_mass[w];
-        ties += sh.warp_ties[w];
+        own += sh.warp_mass[w];
+        own_ties += sh.warp_ties[w];
       }
-      *cluster.map_shared_rank(&sh.mass[rank], tid) = mass;
-      *cluster.map_shared_rank(&sh.ties[rank], tid) = ties;
     }
-    cluster.sync();
   }
+  if (tid == kThreads - 1)
+    for (int c = 0; c < C; ++c) {
+      *cluster.map_shared_rank(&sh.mass[rank], c) = own;
+      *cluster.map_shared_rank(&sh.ties[rank], c) = own_ties;
+    }
+  cluster.sync();
   const unsigned long long each = border.key ? row.units(from_key(border.key)) : 0ull;
   unsigned long long total = 0, mine = 0, start = 0, ties_start = 0, ties_upto = 0;
   for (int c = 0; c < C; ++c) {
@@ -453,6 +516,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
   const unsigned long long target = __umul64hi(u64, total);   // drawn: the first beyond it
   if (target >= start && target < start + mine) {   // (one CTA of the cluster)
     // the warp's stretch that crosses it, and the same again inside that stretch
+    if (weighed) weigh();
     unsigned long long at = start, tied = ties_start;
     int w = 0;
     for (; w < kWarps - 1; ++w) {
@@ -488,7 +552,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ Sam
         if (sum > target) {
           p.out[b] = v0 + i;
           if (p.prob)
-            p.prob[b] = (float)(exp(((double)l - (double)top) * inv_t) /
+            p.prob[b] = (float)(exp(((double)l - (double)top) * sh.inv_t) /
                                 ((double)total / (double)(1ull << row.scale)));
           break;
         }
@@ -507,7 +571,8 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   while ((1 << bits) < p.V) ++bits;
   a.scale = 62 - bits < 45 ? 62 - bits : 45;
   int C = 1;
-  while (C < kMaxCluster && p.V > 2048 * C) C *= 2;
+  while (C < kMaxCluster && p.V > 16384 * C) C *= 2;
+  while (C < kMaxCluster && p.V > 1024 * C && (int64_t)p.B * C < 2 * device_sm_count()) C *= 2;
   a.chunk = ((p.V + C - 1) / C + 7) / 8 * 8;
   for (int j = 0; j < kRoots; ++j)
     a.root[j] = (unsigned long long)std::llrint(std::exp2(40.0 - j / (double)kRoots));
