@@ -37,7 +37,7 @@ constexpr float kReach = 46.f;       // log2: a lighter token has the weight 0
 constexpr float kBinsPerLog2 = kBins / kReach;
 constexpr float kNegInf = -INFINITY;
 constexpr int kRoots = 64;
-constexpr int kList = 512;
+constexpr int kGathered = 2048;      // tokens of a border's bin that one CTA sorts out
 
 struct SampleArgs {
   SampleProblem p;
@@ -48,22 +48,25 @@ struct SampleArgs {
 };
 
 struct Shared {
-  unsigned lo[kBins], hi[kBins];
-  unsigned long long upto[kBins];          // of this CTA's slice of the bins, merged
-  unsigned long long slice[2][kMaxCluster];   // totals of the slices, of this level and the last
+  unsigned lo[kBins], hi[kBins];           // sums of the bins, in two words
+  unsigned long long upto[kBins];          // of this CTA's slice of the bins, over the cluster
+  unsigned keys[kGathered];                // rank 0: of the tokens in the border's bin
+  int list[kThreads];                      // this CTA's tokens there
+  unsigned long long slice[kMaxCluster];   // totals of the slices
   unsigned long long mass[kMaxCluster];    // of the CTAs: mass above the border
   unsigned long long ties[kMaxCluster];    // and tokens at it
   unsigned long long warp_mass[kWarps];
   unsigned long long warp_ties[kWarps];
   unsigned long long root[kRoots];
   unsigned long long above;                // a border found: what is above its bin
+  unsigned long long border_ties;
+  unsigned border_key;
   float top[kMaxCluster];
   float warp_top[kWarps];
   double inv_t, less;                      // 1 / T, T log(min_p)
   float per_log2, per_log2_low, least;
-  int bin, listed;
-  unsigned range[2];
-  int list[kList];                         // tokens of the border's bin
+  int bin, listed, gathered;
+  unsigned low[kWarps], high[kWarps];
 };
 
 // Logits as integers in the same order (NaN never gets here).
@@ -87,7 +90,6 @@ struct Row {
   static __device__ __forceinline__ int bin_of(float reach) {
     return min(kBins - 1, (int)__fmul_rn(reach, kBinsPerLog2));
   }
-  __device__ __forceinline__ int bin(float l) const { return bin_of(reach(l)); }
   // The weights of two logits: 2^-t, t = (top - l) log2(e) / T as a pair of fp32 values (the
   // difference and the product with their rounding errors), off by 2^-45 relative to t. With k =
   // 64 t rounded, t = k / 64 + x, |x| <= 1 / 128: a root from the table, shifted, times e^-y, y =
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   row.per_log2_low = sh.per_log2_low;
   row.scale = a.scale;
   row.root = sh.root;
-  if (tid == 0) {   // the smallest logit that min-p leaves (read after the next barrier)
+  if (tid == 0) {   // the smallest logit that min-p leaves
     float least = kNegInf;
     if (min_p > 0.f) {
       const double less = sh.less;
@@ -301,159 +303,225 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     }
     sh.least = least;
   }
-
-  // The border at which, from above, the count reaches `target`, or the mass top_p of what `limit`
-  // keeps; key 0 if there is not as much. *own: where nothing is limited, this CTA's part of what is
-  // above it, and its tokens at it. All threads of the cluster together.
-  auto cut = [&](bool masses, unsigned long long target, const Border& limit,
-                 unsigned long long* own, unsigned long long* own_ties) {
-    unsigned high = 0xFFFFFFFFu, low = 0u;   // the range of keys of the bin (level 0: none yet)
-    int shift = 0;
-    unsigned long long above = 0;
-    *own = 0;
-    for (int level = 0;; ++level) {
-      const bool listed = level >= 2 && sh.listed <= kList;
+  __syncthreads();
+  const float least = sh.least;
+  const unsigned least_key = key_of(least);
+  // Among the tokens that each(f) gives to f, keys low .. high: the key at which what is above, with
+  // `above` beside them, reaches target. all: every CTA of the cluster has some of the tokens, and
+  // finds the same; else the CTA that calls has them.
+  auto find = [&](bool masses, unsigned long long target, unsigned long long above, unsigned low,
+                  unsigned high, const Border& limit, bool all, auto&& each) {
+    constexpr int kPer = kBins / kThreads;
+    for (;;) {
+      int shift = 0;
+      while ((high - low) >> shift >= kBins) ++shift;
       for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0u;
       __syncthreads();
-      if (level == 1 && tid == 0) sh.listed = 0;
-      if (level == 1) __syncthreads();
-      if (level == 0) {
-        for (int i = tid; i < n; i += 2 * kThreads) {
-          const float l0 = logit(i), l1 = logit(i + kThreads);
-          // (those at the limit's key: their number is known, and they are counted once below)
-          const bool in0 = key_of(l0) > limit.key, in1 = key_of(l1) > limit.key;
-          if (!masses) {
-            const float t0 = row.reach(l0), t1 = row.reach(l1);
-            if (t0 < kReach) atomicAdd(&sh.lo[Row::bin_of(t0)], 1u);
-            if (t1 < kReach) atomicAdd(&sh.lo[Row::bin_of(t1)], 1u);
-          } else if (in0 || in1) {
-            unsigned long long u0, u1;
-            float2 t;
-            row.units2(l0, l1, &u0, &u1, &t);
-            if (in0 && t.x < kReach) bin_add(sh, Row::bin_of(t.x), u0);
-            if (in1 && t.y < kReach) bin_add(sh, Row::bin_of(t.y), u1);
-          }
-        }
-      } else {
-        // few tokens are in the range: after the first look at all of them from a list, if it holds
-        auto token = [&](int i) {
-          const float l = logit(i);
-          const unsigned key = key_of(l);
-          if (key > high || key < low || key <= limit.key) return;
-          const int at = (int)((high - key) >> shift);
-          if (masses) bin_add(sh, at, row.units(l));
-          else atomicAdd(&sh.lo[at], 1u);
-          if (level == 1) {
-            const int place = atomicAdd(&sh.listed, 1);
-            if (place < kList) sh.list[place] = i;
-          }
-        };
-        if (listed) {
-          if (tid < sh.listed) token(sh.list[tid]);
-        } else {
-#pragma unroll 4
-          for (int i = tid; i < n; i += kThreads) token(i);
-        }
-      }
-      if (rank == 0 && tid == 0 && limit.key) {
-        const float l = from_key(limit.key);
-        const int at = level == 0 ? row.bin(l)
-                                  : (limit.key > high || limit.key < low
-                                         ? -1 : (int)((high - limit.key) >> shift));
-        if (at >= 0) bin_add(sh, at, (masses ? row.units(l) : 1ull) * limit.ties);
-      }
-      cluster.sync();
-      // this CTA's slice of the bins, over all CTAs
-      const int per = kBins / C, first = rank * per;
-      unsigned long long before = 0;
-      for (int i0 = 0; i0 < per; i0 += kThreads) {
-        const int i = i0 + tid;
-        unsigned long long v = 0;
-        if (i < per)
+      auto place = [&](unsigned key) { return (int)((high - key) >> shift); };
+      each([&](unsigned key) {
+        if (key > high || key < low) return;
+        if (masses) bin_add(sh, place(key), row.units(from_key(key)));
+        else atomicAdd(&sh.lo[place(key)], 1u);
+      });
+      if (rank == 0 && tid == 0 && limit.key && limit.key <= high && limit.key >= low)
+        bin_add(sh, place(limit.key), (masses ? row.units(from_key(limit.key)) : 1ull) * limit.ties);
+      if (all) {
+        cluster.sync();
+        for (int i = tid; i < kBins; i += kThreads) {
+          unsigned long long v = 0;
           for (int c = 0; c < C; ++c)
-            v += ((unsigned long long)cluster.map_shared_rank(sh.hi, c)[first + i] << 32) +
-                 cluster.map_shared_rank(sh.lo, c)[first + i];
-        const unsigned long long upto = before + block_upto(v, sh.warp_mass);
-        if (i < per) sh.upto[i] = upto;
+            v += ((unsigned long long)cluster.map_shared_rank(sh.hi, c)[i] << 32) +
+                 cluster.map_shared_rank(sh.lo, c)[i];
+          sh.upto[i] = v;
+        }
+        cluster.sync();
+      } else {
         __syncthreads();
-        before = sh.upto[min(per, i0 + kThreads) - 1];
       }
-      if (tid < C) *cluster.map_shared_rank(&sh.slice[level & 1][rank], tid) = before;
-      cluster.sync();
-      const unsigned long long* const slice = sh.slice[level & 1];
-      if (masses && level == 0) {
-        unsigned long long total = 0;
-        for (int c = 0; c < C; ++c) total += slice[c];
-        const double share = ceil((double)total * (double)top_p);
-        target = share >= 1.0 ? min(total, __double2ull_rz(share)) : 1ull;
+      unsigned long long v[kPer], sum = 0;   // of neighbouring bins
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int i = tid * kPer + e;
+        v[e] = all ? sh.upto[i] : ((unsigned long long)sh.hi[i] << 32) + sh.lo[i];
+        sum += v[e];
       }
-      unsigned long long start = above;
-      int owner = 0;
-      while (owner < C && start + slice[owner] < target) start += slice[owner++];
-      if (owner == C) return Border{0u, ~0ull};   // (level 0 only)
-      const unsigned long long* const upto = cluster.map_shared_rank(sh.upto, owner);
-      for (int i = tid; i < per; i += kThreads) {
-        const unsigned long long lower = start + (i ? upto[i - 1] : 0);
-        if (lower < target && start + upto[i] >= target) {   // (one of them)
-          sh.bin = owner * per + i;
+      unsigned long long lower = above + block_upto(sum, sh.warp_mass) - sum;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (lower < target && lower + v[e] >= target) {   // (one of them)
+          sh.bin = tid * kPer + e;
           sh.above = lower;
         }
+        lower += v[e];
       }
       __syncthreads();
-      const int bin = sh.bin;
       above = sh.above;
-      if (masses)
-        for (int i = tid; i < bin; i += kThreads)   // (this thread's part; summed at the end)
-          *own += ((unsigned long long)sh.hi[i] << 32) + sh.lo[i];
-      const unsigned long long in_bin = ((unsigned long long)sh.hi[bin] << 32) + sh.lo[bin];
-      if (level == 0) {
-        // the keys of the bin, between those of logits beyond it and those before it
-        if (tid < 2) {
-          unsigned in = key_of(kNegInf), ex = key_of(row.top) + 1;
-          while (ex - in > 1) {
-            const unsigned mid = in + (ex - in) / 2;
-            const float t = row.reach(from_key(mid));
-            const bool beyond = !(t < kReach) || Row::bin_of(t) > bin;
-            if (beyond || (tid == 0 && Row::bin_of(t) == bin)) in = mid;
-            else ex = mid;
-          }
-          sh.range[tid] = tid == 0 ? in : ex;
-        }
-        __syncthreads();
-        high = sh.range[0];
-        low = sh.range[1];
-      } else {
-        const unsigned span = (1u << shift) - 1;
-        high = high - ((unsigned)bin << shift);
-        low = high - low > span ? high - span : low;
-        __syncthreads();   // (sh.bin and the bins may be overwritten)
-      }
+      high -= (unsigned)sh.bin << shift;
+      const unsigned span = (1u << shift) - 1;
+      low = high - low > span ? high - span : low;
       if (high == low) {
-        const unsigned long long each = masses ? row.units(from_key(high)) : 1ull;
-        unsigned long long ties = (target - above + each - 1) / each;
+        const unsigned long long u = masses ? row.units(from_key(high)) : 1ull;
+        unsigned long long ties = (target - above + u - 1) / u;
         if (high == limit.key && ties > limit.ties) ties = limit.ties;
-        if (masses) {
-          if (tid == kThreads - 1) *own_ties = in_bin / each;
-          *own = block_upto(*own, sh.warp_mass);   // (the last thread has all of it)
-        }
         return Border{high, ties};
       }
-      shift = 0;
-      while ((high - low) >> shift >= kBins) ++shift;
+      __syncthreads();   // (sh.bin and the bins may be overwritten)
     }
+  };
+  // The border at which, from above, the count reaches `target`, or the mass top_p of what `limit`
+  // keeps; key 0 where there is not as much, or where min-p cuts before. *own: this CTA's mass above
+  // the border and its tokens at it, if *weighed. All threads of the cluster together.
+  auto cut = [&](bool masses, unsigned long long target, const Border& limit, bool* weighed,
+                 unsigned long long* own, unsigned long long* own_ties) {
+    *weighed = false;
+    for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0u;
+    if (tid == 0) sh.listed = sh.gathered = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += 2 * kThreads) {
+      const float l0 = logit(i), l1 = logit(i + kThreads);
+      // (those at the limit's key: their number is known, and they are counted once below)
+      const bool in0 = key_of(l0) > limit.key, in1 = key_of(l1) > limit.key;
+      if (!masses) {
+        const float t0 = row.reach(l0), t1 = row.reach(l1);
+        if (t0 < kReach) atomicAdd(&sh.lo[Row::bin_of(t0)], 1u);
+        if (t1 < kReach) atomicAdd(&sh.lo[Row::bin_of(t1)], 1u);
+      } else if (in0 || in1) {
+        unsigned long long u0, u1;
+        float2 t;
+        row.units2(l0, l1, &u0, &u1, &t);
+        if (in0 && t.x < kReach) bin_add(sh, Row::bin_of(t.x), u0);
+        if (in1 && t.y < kReach) bin_add(sh, Row::bin_of(t.y), u1);
+      }
+    }
+    if (rank == 0 && tid == 0 && limit.key) {
+      const float l = from_key(limit.key);
+      bin_add(sh, Row::bin_of(row.reach(l)), (masses ? row.units(l) : 1ull) * limit.ties);
+    }
+    cluster.sync();
+    // this CTA's slice of the bins, over all CTAs
+    const int per = kBins / C, first = rank * per;
+    unsigned long long before = 0;
+    for (int i0 = 0; i0 < per; i0 += kThreads) {
+      const int i = i0 + tid;
+      unsigned long long v = 0;
+      if (i < per)
+        for (int c = 0; c < C; ++c)
+          v += ((unsigned long long)cluster.map_shared_rank(sh.hi, c)[first + i] << 32) +
+               cluster.map_shared_rank(sh.lo, c)[first + i];
+      const unsigned long long upto = before + block_upto(v, sh.warp_mass);
+      if (i < per) sh.upto[i] = upto;
+      __syncthreads();
+      before = sh.upto[min(per, i0 + kThreads) - 1];
+    }
+    if (tid < C) *cluster.map_shared_rank(&sh.slice[rank], tid) = before;
+    cluster.sync();
+    if (masses) {
+      unsigned long long total = 0;
+      for (int c = 0; c < C; ++c) total += sh.slice[c];
+      const double share = ceil((double)total * (double)top_p);
+      target = share >= 1.0 ? min(total, __double2ull_rz(share)) : 1ull;
+    }
+    unsigned long long start = 0;
+    int owner = 0;
+    while (owner < C && start + sh.slice[owner] < target) start += sh.slice[owner++];
+    if (owner == C) return Border{0u, ~0ull};
+    const unsigned long long* const upto = cluster.map_shared_rank(sh.upto, owner);
+    for (int i = tid; i < per; i += kThreads) {
+      const unsigned long long lower = start + (i ? upto[i - 1] : 0);
+      if (lower < target && start + upto[i] >= target) {   // (one of them)
+        sh.bin = owner * per + i;
+        sh.above = lower;
+      }
+    }
+    __syncthreads();
+    int bin = sh.bin;
+    const unsigned long long above = sh.above;
+    // where min-p cuts in an earlier bin, its own tokens decide
+    const int least_bin = least > kNegInf ? (row.reach(least) < kReach ? Row::bin_of(row.reach(least)) : kBins)
+                                          : kBins;
+    const bool min_p_cuts = masses && least_bin < bin;
+    if (min_p_cuts) bin = least_bin;
+    *weighed = masses && !limit.key;
+    unsigned long long part = 0, ties = 0;
+    if (*weighed)
+      for (int i = tid; i < bin; i += kThreads)
+        part += ((unsigned long long)sh.hi[i] << 32) + sh.lo[i];
+    // the tokens of the bin
+    unsigned* const keys = cluster.map_shared_rank(sh.keys, 0);
+    int* const gathered = cluster.map_shared_rank(&sh.gathered, 0);
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThreads) {
+      const float l = logit(i), t = row.reach(l);
+      if (!(t < kReach) || Row::bin_of(t) != bin || key_of(l) <= limit.key) continue;
+      if (min_p_cuts) {
+        if (key_of(l) >= least_key) part += row.units(l);
+        continue;
+      }
+      const int place = atomicAdd(&sh.listed, 1), at = atomicAdd(gathered, 1);
+      if (place < kThreads) sh.list[place] = i;
+      if (at < kGathered) keys[at] = key_of(l);
+    }
+    if (min_p_cuts) {
+      *own = block_upto(part, sh.warp_mass);   // (the last thread has all of it)
+      *own_ties = 0;
+      return Border{0u, ~0ull};
+    }
+    cluster.sync();
+    Border found;
+    const int all = *gathered;
+    auto each_own = [&](auto&& f) {   // this CTA's tokens in the bin
+      if (sh.listed <= kThreads) {
+        if (tid < sh.listed) f(key_of(logit(sh.list[tid])));
+        return;
+      }
+      for (int i = tid; i < n; i += kThreads) {
+        const float l = logit(i), t = row.reach(l);
+        if (t < kReach && Row::bin_of(t) == bin && key_of(l) > limit.key) f(key_of(l));
+      }
+    };
+    if (all > kGathered) {   // (many equal logits, mostly)
+      found = find(masses, target, above, 0u, 0xFFFFFFFFu, limit, true, each_own);
+    } else {
+      if (rank == 0) {
+        unsigned low = 0xFFFFFFFFu, high = 0u;
+        if (limit.key && Row::bin_of(row.reach(from_key(limit.key))) == bin) low = high = limit.key;
+        for (int i = tid; i < all; i += kThreads) {
+          low = min(low, sh.keys[i]);
+          high = max(high, sh.keys[i]);
+        }
+        low = __reduce_min_sync(0xffffffffu, low);
+        high = __reduce_max_sync(0xffffffffu, high);
+        if (lane == 0) sh.low[warp] = low, sh.high[warp] = high;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) low = min(low, sh.low[w]), high = max(high, sh.high[w]);
+        found = find(masses, target, above, low, high, limit, false, [&](auto&& f) {
+          for (int i = tid; i < all; i += kThreads) f(sh.keys[i]);
+        });
+        if (tid < C) {
+          *cluster.map_shared_rank(&sh.border_key, tid) = found.key;
+          *cluster.map_shared_rank(&sh.border_ties, tid) = found.ties;
+        }
+      }
+      cluster.sync();
+      found = Border{sh.border_key, sh.border_ties};
+    }
+    if (*weighed) {
+      each_own([&](unsigned key) {
+        if (key < least_key) return;
+        if (key > found.key) part += row.units(from_key(key));
+        else if (key == found.key) ++ties;
+      });
+      *own = block_upto(part, sh.warp_mass);   // (the last thread has all of it)
+      *own_ties = block_upto(ties, sh.warp_ties);
+    }
+    return found;
   };
 
   Border border{0u, ~0ull};
   unsigned long long own = 0, own_ties = 0;
-  bool weighed = false;   // the cut has this CTA's mass above the border and its tokens at it
-  if (k > 0 && k < p.V) border = cut(false, (unsigned long long)k, border, &own, &own_ties);
-  if (top_p < 1.f) {
-    weighed = border.key == 0u;
-    border = cut(true, 0ull, border, &own, &own_ties);
-  }
-  __syncthreads();
-  const unsigned least_key = key_of(sh.least);
-  weighed = weighed && least_key <= border.key;
+  bool weighed = false;
+  if (k > 0 && k < p.V) border = cut(false, (unsigned long long)k, border, &weighed, &own, &own_ties);
+  if (top_p < 1.f) border = cut(true, 0ull, border, &weighed, &own, &own_ties);
   // ------------------------------------------------------------------ the draw
   // the mass above the border, and the tokens at it, of each warp's stretch
   const int stretch = (n + kWarps - 1) / kWarps;
