@@ -37,14 +37,16 @@ constexpr float kReach = 46.f;       // log2: a lighter token has the weight 0
 constexpr float kBinsPerLog2 = kBins / kReach;
 constexpr float kNegInf = -INFINITY;
 constexpr int kRoots = 64;
+constexpr float kMagic = 12582912.f;   // 1.5 x 2^23: added, it leaves an integer in the lowest bits
+constexpr int kMagicBits = 0x4B400000;
+constexpr int kPad = 2 * kThreads;   // tokens without weight behind a CTA's last one
 constexpr int kGathered = 2048;      // tokens of a border's bin that one CTA sorts out
 
 struct SampleArgs {
   SampleProblem p;
   int chunk;        // tokens per CTA, a multiple of 8
   int scale;        // log2 of the weight 1
-  bool staged;      // the chunk is kept in shared memory
-  unsigned long long root[kRoots];   // 2^(-j / kRoots) in units of 2^-40
+  unsigned long long root[kRoots];   // 2^(-j / kRoots) in units of 2^-47
 };
 
 struct Shared {
@@ -63,8 +65,8 @@ struct Shared {
   unsigned border_key;
   float top[kMaxCluster];
   float warp_top[kWarps];
-  double inv_t, less;                      // 1 / T, T log(min_p)
-  float per_log2, per_log2_low, least;
+  double less;                             // T log(min_p)
+  float least;
   int bin, listed, gathered;
   unsigned low[kWarps], high[kWarps];
 };
@@ -88,7 +90,7 @@ struct Row {
     return __fmul_rn(__fsub_rn(top, l), per_log2);
   }
   static __device__ __forceinline__ int bin_of(float reach) {
-    return min(kBins - 1, (int)__fmul_rn(reach, kBinsPerLog2));
+    return min(kBins - 1, __float_as_int(__fmaf_rn(reach, kBinsPerLog2, kMagic)) - kMagicBits);
   }
   // The weights of two logits: 2^-t, t = (top - l) log2(e) / T as a pair of fp32 values (the
   // difference and the product with their rounding errors), off by 2^-45 relative to t. With k =
@@ -99,7 +101,6 @@ struct Row {
   // (where[]: the reach of each)
   __device__ __forceinline__ void units2(float l0, float l1, unsigned long long* u0,
                                          unsigned long long* u1, float2* where) const {
-    constexpr float kMagic = 12582912.f;
     const f2 minus = pair(-1.f, -1.f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
     const f2 a = pair(top, top), b = mul2(pair(l0, l1), minus);
     const f2 d = add2(a, b), bb = fma2(a, minus, d);     // d + e = top - l
@@ -130,17 +131,31 @@ struct Row {
     units2(l, l, &u, &v, &where);
     return u;
   }
+  // A logit's weight over a total of units, rounded to fp32 (within 2^-10 of half a step): the weight
+  // before it is shifted, and the total, as fp32 pairs; the quotient and its remainder's.
+  __device__ __forceinline__ float share(float l, unsigned long long total) const {
+    const float d = __fsub_rn(top, l), t = __fmul_rn(d, per_log2);
+    const int k = __float_as_int(__fmaf_rn(t, 64.f, kMagic)) - kMagicBits;
+    Row wide = *this;
+    wide.scale = 45 + (k >> 6);   // (the shift of compose() is 1)
+    const unsigned long long w = wide.units(l);
+    auto high = [](unsigned long long x) { return __ull2float_rn(x); };
+    auto low = [](unsigned long long x, float h) {
+      return __ll2float_rn((long long)(x - __float2ull_rn(h)));
+    };
+    const float wh = high(w), wl = low(w, wh), th = high(total), tl = low(total, th);
+    const float q = __fdiv_rn(wh, th);
+    const float r = __fadd_rn(__fmaf_rn(-q, th, wh), __fmaf_rn(-q, tl, wl));
+    return scalbnf(__fadd_rn(q, __fdiv_rn(r, th)), scale - wide.scale);
+  }
   // Root k mod 64 times (1 + (low - m 2^21) 2^-37), shifted by k / 64.
   __device__ __forceinline__ unsigned long long compose(float k_magic, float m_magic,
                                                         float low_magic) const {
-    constexpr int kBits = 0x4B400000;   // of the magic number
-    const int k = __float_as_int(k_magic) - kBits;
-    const int f = __float_as_int(low_magic) - kBits - ((__float_as_int(m_magic) - kBits) << 21);
+    const int k = __float_as_int(k_magic) - kMagicBits;
+    const int f = __float_as_int(low_magic) - kMagicBits - ((__float_as_int(m_magic) - kMagicBits) << 21);
     const unsigned long long z = root[k & (kRoots - 1)];
-    const long long w = (long long)z + (((long long)f * (int)(z >> 10)) >> 27);   // units of 2^-40
-    const int shift = (k >> 6) + 40 - scale;
-    return shift <= 0 ? (unsigned long long)w << -shift
-                      : (unsigned long long)(w + (1ll << (shift - 1))) >> shift;
+    const long long w = (long long)z + (((long long)f * (int)(z >> 17)) >> 20);   // units of 2^-47
+    return (((unsigned long long)w >> ((k >> 6) + 46 - scale)) + 1) >> 1;
   }
   static constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;   // log(2) in two parts
 };
@@ -172,11 +187,31 @@ __device__ __forceinline__ unsigned long long block_upto(unsigned long long v,
   __syncthreads();
   if (lane == 31) sums[warp] = v;
   __syncthreads();
-  unsigned long long before = 0;
-  for (int w = 0; w < warp; ++w) before += sums[w];
-  return v + before;
+#pragma unroll
+  for (int w = 0; w < kWarps - 1; ++w) v += w < warp ? sums[w] : 0ull;
+  return v;
 }
 
+// The smallest integer not below total * p, 0 < p < 1, total < 2^63.
+__device__ __forceinline__ unsigned long long share_of(unsigned long long total, float p) {
+  const int bits = __float_as_int(p), exponent = bits >> 23;
+  const unsigned long long m = (bits & 0x7FFFFF) | (exponent ? 0x800000 : 0);
+  const unsigned long long lo = total * m, hi = __umul64hi(total, m);
+  const int s = 150 - max(exponent, 1);   // of m, 24 .. 149
+  if (s >= 128) return 1ull;              // (total is not 0, hi below 2^23)
+  if (s >= 64) {
+    const unsigned long long whole = s == 64 ? hi : hi >> (s - 64);
+    return whole + ((s > 64 && (hi & ((1ull << (s - 64)) - 1))) || lo ? 1 : 0);
+  }
+  return (hi << (64 - s) | lo >> s) + (lo & ((1ull << s) - 1) ? 1 : 0);
+}
+// The smallest q with q u >= x, for q below 2^25.
+__device__ __forceinline__ unsigned long long ceil_div(unsigned long long x, unsigned long long u) {
+  unsigned long long q = (unsigned long long)__fdividef((float)x, (float)u);   // off by a few
+  while (q * u < x) ++q;
+  while (q && (q - 1) * u >= x) --q;
+  return q;
+}
 // Adds u to a bin's sum in two words.
 __device__ __forceinline__ void bin_add(Shared& sh, int at, unsigned long long u) {
   const unsigned add = (unsigned)u, old = atomicAdd(&sh.lo[at], add);
@@ -184,7 +219,7 @@ __device__ __forceinline__ void bin_add(Shared& sh, int at, unsigned long long u
   if (up) atomicAdd(&sh.hi[at], up);
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kStaged>
 __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) float stage_mem[];
   __shared__ Shared sh;
@@ -201,14 +236,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   int k = p.top_ks ? p.top_ks[b] : p.top_k;
   const float top_p = p.top_ps ? p.top_ps[b] : p.top_p;
   const float min_p = p.min_ps ? p.min_ps[b] : p.min_p;
+  const double u = p.u[b];
   if (!(T > 0x1p-64f)) T = 1.f, k = 1;
-  if (tid == kThreads - 1) {   // (fp64, so one thread, beside the loads)
-    const double inv_t = 1.0 / (double)T, per_log2 = inv_t * 1.4426950408889634;
-    sh.inv_t = inv_t;
-    sh.per_log2 = (float)per_log2;
-    sh.per_log2_low = (float)(per_log2 - (double)(float)per_log2);
+  // log2(e) / T as a pair: quotient and remainder
+  constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f;
+  const float per_log2 = __fdiv_rn(kLog2e, T);
+  const float per_log2_low =
+      T < 0x1p64f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-per_log2, T, kLog2e), kLog2eLow), T) : 0.f;
+  if (tid == kThreads - 1)   // (fp64: one thread, beside the loads)
     sh.less = min_p > 0.f && min_p < 1.f ? (double)T * log((double)min_p) : 0.0;
-  }
   const Raw* const from = static_cast<const Raw*>(p.logits) + (int64_t)b * p.stride + v0;
   auto widen = [](Raw x) {   // (NaN is never drawn, and -0 is 0)
     float l;
@@ -223,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const int skew = (int)(reinterpret_cast<uintptr_t>(from) / sizeof(Raw)) & (kVec - 1);
   float* const stage = stage_mem + skew;
   float top = kNegInf;
-  if (a.staged) {
+  if constexpr (kStaged) {
     const int head = min(n, (kVec - skew) & (kVec - 1)), vectors = (n - head) / kVec;
     auto single = [&](int i) {
       const float l = widen(from[i]);
@@ -279,16 +315,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     return;
   }
   const bool endless = top == INFINITY;   // only the infinite ones count, all alike
-  if (endless) top = 0.f;
-  auto logit = [&](int i) {   // a token past the CTA's last one has no weight
+  if (endless) {
+    top = 0.f;
+    if (kStaged)
+      for (int i = tid; i < n; i += kThreads) stage[i] = stage[i] == INFINITY ? 0.f : kNegInf;
+  }
+  if (kStaged)   // tokens past the CTA's last one have no weight
+    for (int i = n + tid; i < n + kPad; i += kThreads) stage[i] = kNegInf;
+  auto logit = [&](int i) {   // (i < n + kPad)
+    if constexpr (kStaged) return stage[i];
     if (i >= n) return kNegInf;
-    const float l = a.staged ? stage[i] : widen(from[i]);
+    const float l = widen(from[i]);
     return endless ? (l == INFINITY ? 0.f : kNegInf) : l;
   };
   Row row;
   row.top = top;
-  row.per_log2 = sh.per_log2;
-  row.per_log2_low = sh.per_log2_low;
+  row.per_log2 = per_log2;
+  row.per_log2_low = per_log2_low;
   row.scale = a.scale;
   row.root = sh.root;
   if (tid == 0) {   // the smallest logit that min-p leaves
@@ -361,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       low = high - low > span ? high - span : low;
       if (high == low) {
         const unsigned long long u = masses ? row.units(from_key(high)) : 1ull;
-        unsigned long long ties = (target - above + u - 1) / u;
+        unsigned long long ties = ceil_div(target - above, u);
         if (high == limit.key && ties > limit.ties) ties = limit.ties;
         return Border{high, ties};
       }
@@ -398,28 +441,33 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       bin_add(sh, Row::bin_of(row.reach(l)), (masses ? row.units(l) : 1ull) * limit.ties);
     }
     cluster.sync();
-    // this CTA's slice of the bins, over all CTAs
+    // this CTA's slice of the bins, over all CTAs (neighbouring bins to a thread)
     const int per = kBins / C, first = rank * per;
-    unsigned long long before = 0;
-    for (int i0 = 0; i0 < per; i0 += kThreads) {
-      const int i = i0 + tid;
-      unsigned long long v = 0;
-      if (i < per)
+    constexpr int kMost = kBins / kThreads;
+    const int mine = max(1, per / kThreads), i0 = tid * mine;
+    unsigned long long v[kMost], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kMost; ++e) {
+      v[e] = 0;
+      if (e < mine && i0 < per)
         for (int c = 0; c < C; ++c)
-          v += ((unsigned long long)cluster.map_shared_rank(sh.hi, c)[first + i] << 32) +
-               cluster.map_shared_rank(sh.lo, c)[first + i];
-      const unsigned long long upto = before + block_upto(v, sh.warp_mass);
-      if (i < per) sh.upto[i] = upto;
-      __syncthreads();
-      before = sh.upto[min(per, i0 + kThreads) - 1];
+          v[e] += ((unsigned long long)cluster.map_shared_rank(sh.hi, c)[first + i0 + e] << 32) +
+                  cluster.map_shared_rank(sh.lo, c)[first + i0 + e];
+      sum += v[e];
     }
-    if (tid < C) *cluster.map_shared_rank(&sh.slice[rank], tid) = before;
+    unsigned long long upto_mine = block_upto(sum, sh.warp_mass) - sum;
+#pragma unroll
+    for (int e = 0; e < kMost; ++e) {
+      upto_mine += v[e];
+      if (e < mine && i0 < per) sh.upto[i0 + e] = upto_mine;
+    }
+    if (tid == kThreads - 1)   // (all of it)
+      for (int c = 0; c < C; ++c) *cluster.map_shared_rank(&sh.slice[rank], c) = upto_mine;
     cluster.sync();
     if (masses) {
       unsigned long long total = 0;
       for (int c = 0; c < C; ++c) total += sh.slice[c];
-      const double share = ceil((double)total * (double)top_p);
-      target = share >= 1.0 ? min(total, __double2ull_rz(share)) : 1ull;
+      target = top_p > 0.f ? share_of(total, top_p) : 1ull;
     }
     unsigned long long start = 0;
     int owner = 0;
@@ -578,9 +626,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     }
     total += sh.mass[c] + kept * each;
   }
-  const double u = p.u[b];
   // floor(u * total), u in units of 2^-64
-  const unsigned long long u64 = u > 0.0 ? (u < 1.0 ? __double2ull_rz(u * 0x1p64) : ~0ull) : 0ull;
+  unsigned long long u64 = 0;
+  if (u >= 1.0) u64 = ~0ull;
+  else if (u > 0x1p-1000) {
+    const unsigned long long bits = (unsigned long long)__double_as_longlong(u);
+    const int shift = (int)(bits >> 52) - 1011;   // of the mantissa
+    const unsigned long long m = (bits & ((1ull << 52) - 1)) | 1ull << 52;
+    u64 = shift >= 0 ? m << shift : (shift > -53 ? m >> -shift : 0ull);
+  }
   const unsigned long long target = __umul64hi(u64, total);   // drawn: the first beyond it
   if (target >= start && target < start + mine) {   // (one CTA of the cluster)
     // the warp's stretch that crosses it, and the same again inside that stretch
@@ -619,9 +673,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
         if (key > border.key || (key == border.key && place++ < border.ties)) sum += row.units(l);
         if (sum > target) {
           p.out[b] = v0 + i;
-          if (p.prob)
-            p.prob[b] = (float)(exp(((double)l - (double)top) * sh.inv_t) /
-                                ((double)total / (double)(1ull << row.scale)));
+          if (p.prob) p.prob[b] = row.share(l, total);
           break;
         }
       }
@@ -643,23 +695,25 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   while (C < kMaxCluster && p.V > 1024 * C && (int64_t)p.B * C < 2 * device_sm_count()) C *= 2;
   a.chunk = ((p.V + C - 1) / C + 7) / 8 * 8;
   for (int j = 0; j < kRoots; ++j)
-    a.root[j] = (unsigned long long)std::llrint(std::exp2(40.0 - j / (double)kRoots));
-  const int room = 160 * 1024, stage = (a.chunk + 8) * 4;
-  a.staged = stage <= room;
-  const auto kernel = p.bf16 ? k_sample<true> : k_sample<false>;
+    a.root[j] = (unsigned long long)std::llrint(std::exp2(47.0 - j / (double)kRoots));
+  const int room = 160 * 1024, stage = (a.chunk + 8 + kPad) * 4;
+  const bool staged = stage <= room;
+  const auto kernel = p.bf16 ? (staged ? k_sample<true, true> : k_sample<true, false>)
+                             : (staged ? k_sample<false, true> : k_sample<false, false>);
   static OncePerDevice ready;
-  cudaError_t e = ready.run([&] {
+  const cudaError_t e = ready.run([&] {
     const cudaError_t x = cudaFuncSetAttribute(
-        k_sample<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
-    return x != cudaSuccess ? x
-                            : cudaFuncSetAttribute(
-                                  k_sample<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
+        k_sample<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
+    return x != cudaSuccess
+               ? x
+               : cudaFuncSetAttribute(k_sample<false, true>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, room);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.B * C);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.staged ? stage : 0;
+  cfg.dynamicSmemBytes = staged ? stage : 0;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
