@@ -23,32 +23,30 @@ __global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ Pre
   const PagedArgs& o = a.own;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const int64_t row = kWarps > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
-  if (row >= (int64_t)o.B * o.R * o.Hq) return;
-  const int hq = (int)(row % o.Hq), h = hq / o.G;
-  const int b = (int)(row / o.Hq / o.R), m = (int)(row / o.Hq % o.R) * o.G + hq % o.G;
-  uint16_t* const dst = o.out + row * D + V * lane;
-  const bool absent = o.lengths[b] < 0;
+  const int64_t row64 = kWarps > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
+  if (row64 >= (int64_t)o.B * o.R * o.Hq) return;
+  const unsigned row = (unsigned)row64;   // (4096 sequences x 128 rows x 256 heads: below 2^32)
+  const unsigned hq = row % o.Hq, br = row / o.Hq, h = hq / o.G;
+  const unsigned b = br / o.R, m = br % o.R * o.G + hq % o.G;
+  uint16_t* const dst = o.out + row64 * D + V * lane;
+  const int own_len = o.lengths[b];
 
   // the pieces of the prefix: of the CTAs that share the row's unit, one or two (its streams) of each
-  const int p = b / a.per, mp = (b % a.per) * o.M + m, u = mp / (2 * kRows);
+  const unsigned p = b / a.per, mp = (b % a.per) * o.M + m, u = mp / (2 * kRows);
   const int w = unit_tiles(a, u), subs = w == 2 ? 1 : 2;
   const int sub0 = w == 2 ? mp / kRows % 2 : 0;
-  const int T = absent ? 0 : token_tiles(prefix_len(a, p));
-  const int64_t total = a.starts[a.P], ctas = list_ctas(a, total);
-  const int64_t first = a.starts[p] + h * head_places(a, T) + u * (2 * (int64_t)T + kBegin);
-  const int64_t behind = first + (int64_t)w * T + kBegin;
-  int c0 = 0, n_prefix = 0;
-  if (T) {   // CTA c has the positions from c total / ctas on
-    c0 = (int)(((first + 1) * ctas - 1) / total);
-    n_prefix = ((int)((behind * ctas - 1) / total) - c0 + 1) * subs;
-  }
-  // the pieces of its own tokens
-  const int bh = b * o.c.heads + h;
+  const int unit = (p * o.c.heads + h) * a.units + u;
+  const int2 first = __ldcg(reinterpret_cast<const int2*>(a.span) + unit);
+  // and those of its own tokens
+  const unsigned bh = b * o.c.heads + h;
   const int2 span = __ldcg(reinterpret_cast<const int2*>(o.span) + bh);
-  const bool empty = seq_len(o, b) == 0;
-  const bool noted = !empty && span.x >= 0 && span.y >= span.x && span.y < o.grid;
-  const int n_all = n_prefix + (noted ? span.y - span.x + 1 : 0);
+  const bool absent = own_len < 0;
+  // (spans that were not noted: the kernel gave up, and the status says so)
+  const bool has_prefix = !absent && prefix_len(a, p) > 0 && first.x >= 0 && first.y >= first.x &&
+                          first.y < a.grid;
+  const bool has_own = own_len > 0 && span.x >= 0 && span.y >= span.x && span.y < o.grid;
+  const int n_prefix = has_prefix ? (first.y - first.x + 1) * subs : 0;
+  const int n_all = n_prefix + (has_own ? span.y - span.x + 1 : 0);
 
   float top = kNegInf, norm = 0.f, acc[V];
 #pragma unroll
@@ -58,15 +56,10 @@ __global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ Pre
     float2 ml = make_float2(kNegInf, 0.f);
     const float* from = a.part_o;
     if (i < n_prefix) {
-      const int c = c0 + i / subs;
-      const int64_t begin = c * total / ctas, end = (c + 1) * total / ctas;
-      const int t0 = begin > first ? tile_at(begin - first, w) : 0;
-      const int t1 = end >= behind ? T : tile_at(end - first, w);
-      if (t1 > t0) {
-        const int64_t at = (unit_piece(a, p, h, u, c) * 2 + sub0 + i % subs) * kRows + mp % kRows;
-        ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
-        from = a.part_o + at * D;
-      }
+      const int c = first.x + (subs == 2 ? i >> 1 : i), sub = subs == 2 ? i & 1 : sub0;
+      const int64_t at = ((int64_t)(unit + c) * 2 + sub) * kRows + mp % kRows;
+      ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
+      from = a.part_o + at * D;
     } else if (i < n_all) {
       const int c = span.x + i - n_prefix;
       const int64_t piece = span.x == span.y ? 2 * (int64_t)o.grid + bh
@@ -148,7 +141,7 @@ __global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ Pre
 struct Plan {
   int grid;
   int64_t pieces;
-  size_t starts, ml, po, total;
+  size_t span, ml, po, total;
 };
 
 Plan make_plan(const PrefixAttnProblem& p, PrefixArgs* a) {
@@ -167,8 +160,8 @@ Plan make_plan(const PrefixAttnProblem& p, PrefixArgs* a) {
   pl.grid = (int)(most < sms ? most : sms);
   pl.pieces = heads * a->units + pl.grid;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-  pl.starts = up(pieces_workspace(p.own));
-  pl.ml = pl.starts + up((size_t)(p.P + 1) * sizeof(int64_t));
+  pl.span = up(pieces_workspace(p.own));
+  pl.ml = pl.span + up((size_t)heads * a->units * 2 * sizeof(int));
   pl.po = pl.ml + up((size_t)pl.pieces * 2 * kRows * 2 * sizeof(float));
   pl.total = pl.po + up((size_t)pl.pieces * 2 * kRows * p.own.D * sizeof(float));
   return pl;
@@ -195,7 +188,7 @@ cudaError_t launch_prefix_attn(const PrefixAttnProblem& p, uint8_t* ws, cudaStre
   a.table = p.table;
   a.lengths = p.lengths;
   a.grid = pl.grid;
-  a.starts = reinterpret_cast<int64_t*>(ws + pl.starts);
+  a.span = reinterpret_cast<int*>(ws + pl.span);
   a.part_ml = reinterpret_cast<float*>(ws + pl.ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.po);
   cudaError_t e = launch_pieces(p.own, ws, s, &a.own);   // (it clears the status word)

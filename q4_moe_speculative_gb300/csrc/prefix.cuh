@@ -29,7 +29,7 @@ struct PrefixArgs {
   const int32_t* table;
   const int32_t* lengths;
   int grid;
-  int64_t* starts;      // [P + 1]: places of the prefixes in the list
+  int* span;            // [units of all][2]: the CTAs that begin and end a unit
   float* part_o;        // [units of all + grid][2][128][D]
   float* part_ml;       // [units of all + grid][2][128][2]
 };
@@ -55,13 +55,15 @@ __device__ __forceinline__ int64_t list_places(const PrefixArgs& a, int lane) {
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum * a.own.c.heads;
 }
+// CTAs that share them, three positions or more each: so a CTA between those that begin and end a
+// unit has some of its tiles.
 __device__ __forceinline__ int64_t list_ctas(const PrefixArgs& a, int64_t total) {
-  return total < a.grid ? total : a.grid;
+  return total < 3 * (int64_t)a.grid ? (total + 2) / 3 : a.grid;
 }
 // The token tile that position x of a unit of w row tiles belongs to: where a CTA begins there, the
 // first it takes; where it ends, the first it leaves.
 __device__ __forceinline__ int tile_at(int64_t x, int w) {
-  return x < kBegin ? 0 : (int)((x - kBegin) / w);
+  return x < kBegin ? 0 : (int)(x - kBegin) >> (w - 1);
 }
 // Where CTA `cta` leaves its sums of a unit, counted over all: CTAs and units only ever go up along
 // the list, so no two pairs have the same sum.
@@ -83,8 +85,10 @@ struct Walk {
     const int64_t total = list_places(a, lane), ctas = list_ctas(a, total);
     pos = end = 0;
     if (cta >= ctas) return;
-    pos = cta * total / ctas;
-    end = (cta + 1) * total / ctas;
+    // (the first total % ctas have one more)
+    const int64_t each = total / ctas, more = total - each * ctas;
+    pos = cta * each + (cta < more ? cta : more);
+    end = pos + each + (cta < more ? 1 : 0);
     start = 0;
     p = -1;
     skip(a);
@@ -94,8 +98,11 @@ struct Walk {
       start += n;
       skip(a);
     }
-    h = (int)((pos - start) / head_places(a, T));
-    start += h * head_places(a, T);
+    const int64_t per_head = head_places(a, T);
+    h = (int)__fdividef((float)(pos - start), (float)per_head);   // (below 256, off by one at most)
+    if (h * per_head > pos - start) --h;
+    if ((h + 1) * per_head <= pos - start) ++h;
+    start += h * per_head;
   }
   __device__ __forceinline__ void skip(const PrefixArgs& a) {   // to the next prefix with tokens
     h = 0;
@@ -107,10 +114,11 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const PrefixArgs& a, Run* r) {
     while (pos < end) {
-      const int64_t x = pos - start, full = 2 * (int64_t)T + kBegin;
+      // (a head's positions fit 31 bits: up to 4096 row tiles of up to 2^17 token tiles)
+      const unsigned x = (unsigned)(pos - start), full = 2u * T + kBegin;
       const int u = (int)(x / full);
       const int w = unit_tiles(a, u);
-      const int64_t first = start + u * full, behind = first + (int64_t)w * T + kBegin;
+      const int64_t first = start + (int64_t)u * full, behind = first + (int64_t)w * T + kBegin;
       *r = Run{p, h, u, w, len, tile_at(pos - first, w), end >= behind ? T : tile_at(end - first, w)};
       if (end < behind) {
         pos = end;

@@ -15,6 +15,8 @@
 // int8 codes to bf16 (Q8; the key's scale multiplies the score, the value's scale P); one thread of
 // the last warp issues the MMAs. Bound by the tensor cores with two row tiles: three products of
 // 128 x 128 x 128 per 128 tokens and row tile. Every wait is bounded; a give-up sets the status word.
+#include <type_traits>
+
 #include "prefix.cuh"
 
 namespace dsmoe {
@@ -22,7 +24,8 @@ namespace prefix {
 
 constexpr int kInfo = 8;                  // tiles whose pages and scales are at hand
 constexpr uint32_t kWaitPolls = 1u << 20;
-constexpr int kScore = 256;               // softmax threads
+constexpr int kStream = 256;              // softmax threads of a stream: two per row
+constexpr int kScore = 2 * kStream;
 // Reference of a row that has seen no token yet: the least finite value, so that any score that
 // counts is above it by more than kSlack, or is equal to it and has the weight 1.
 constexpr float kNothing = -3.402823466e38f;
@@ -32,23 +35,27 @@ struct Tc {
   static constexpr int kHalves = D / 64;
   static constexpr int kMat = kTok * D * 2;             // bytes of an operand tile
   static constexpr int kRing = D == 128 ? 2 : 4;        // stages of keys, and of values
-  static constexpr int kWiden = kQ8 ? 128 : 32;         // threads per matrix that bring tiles
-  static constexpr int kThreads = kScore + 2 * kWiden + 32;
-  static constexpr int kMmaWarp = kThreads / 32 - 1;
-  static constexpr int kSmall = 1024 + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
-  static constexpr int kSmem = 1024 + kSmall + 2 * kMat + 2 * kRing * kMat;
+  static constexpr int kWiden = kQ8 ? 64 : 32;          // threads per matrix that bring tiles
+  // warp 0 issues the MMAs, the next bring tiles, then softmax from a multiple of four on
+  static constexpr int kBring = 32, kFirst = (kBring + 2 * kWiden + 127) / 128 * 128;
+  static constexpr int kThreads = kFirst + kScore;
+  static constexpr int kSmall = 5120 + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
+  static constexpr int kQ = kRows * 64 * 4;             // of a stream: its queries, then its sums
+  static constexpr int kSmem = 1024 + kSmall + 2 * kQ + 2 * kRing * kMat;
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA has an SM's tensor memory");
 };
 
 struct Small {
   uint64_t kfull[4], vfull[4], kfree[4], vfree[4];
-  uint64_t sfull[2], pfull[2], qfull[2], odone[2];
-  uint64_t info[kInfo], vedge, end;
+  uint64_t sfull[2], pfull[2][2], qfull[2], odone[2];   // P in two parts
+  uint64_t qfree[2], info[kInfo], vedge, end;
   uint32_t tmem;
   int abort;
   unsigned runs[kInfo];       // which pages of a tile are there
+  int row_at[kPagedMaxRows];  // where a row's values start in a sequence's queries
+  float top[2][2][2][kRows];  // [tile parity][stream][half of the columns]: largest scores
 };
-static_assert(sizeof(Small) <= 1024, "in front of the tiles");
+static_assert(sizeof(Small) <= 5120, "in front of the tiles");
 
 __device__ __forceinline__ void ld32(uint32_t at, float (&v)[32]) {
   uint32_t r[32];
@@ -80,6 +87,15 @@ __device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem desc], issued by one thread.
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -89,6 +105,11 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, u
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // Page of the prefix's token t, or -1: no such token, or a bad table entry.
 __device__ __forceinline__ int prefix_page(const PrefixArgs& a, int p, int t, int len) {
@@ -109,9 +130,9 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   const uint32_t pad = (1024u - (smem_at(smem_raw) & 1023u)) & 1023u;
   uint8_t* const base = smem_raw + pad;
   Small& sh = *reinterpret_cast<Small*>(base);
-  float* const sScale = reinterpret_cast<float*>(base + 1024);   // Q8: [kInfo][2][tokens]
+  float* const sScale = reinterpret_cast<float*>(base + 5120);   // Q8: [kInfo][2][tokens]
   uint8_t* const sQ = base + T::kSmall;                          // [2][halves][rows][128 B]
-  uint8_t* const sK = sQ + 2 * T::kMat;                          // [ring][halves][tokens][128 B]
+  uint8_t* const sK = sQ + 2 * T::kQ;                            // [ring][halves][tokens][128 B]
   uint8_t* const sV = sK + kRing * T::kMat;
 
   if (tid == 0) {
@@ -123,8 +144,10 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&sh.sfull[i], 1);
-      sm100::mbar_init(&sh.pfull[i], 4);
-      sm100::mbar_init(&sh.qfull[i], 4);
+      sm100::mbar_init(&sh.pfull[i][0], kStream / 32);
+      sm100::mbar_init(&sh.pfull[i][1], kStream / 32);
+      sm100::mbar_init(&sh.qfull[i], kStream / 32);
+      sm100::mbar_init(&sh.qfree[i], kStream / 32);
       sm100::mbar_init(&sh.odone[i], 1);
     }
     for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&sh.info[i], 1);
@@ -133,6 +156,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     sh.abort = 0;
     sm100::fence_mbar_init();
   }
+  if (tid < o.M) sh.row_at[tid] = (tid / o.G * o.Hq + tid % o.G) * D;
   if (warp == 0) {
     sm100::tmem_alloc(&sh.tmem, 512);
     sm100::tmem_relinquish();
@@ -140,10 +164,14 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
-  const uint32_t tmem = sh.tmem;   // S / P of either stream: 128 columns each; then O of either: D
+  // tensor memory, all of it, so from column 0 on: S / P of either stream, 128 columns each; then O of
+  // either, D columns
+  constexpr uint32_t tmem = 0;
   if (!kQ8 && tid < 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &v_map : &k_map) : "memory");
-  pdl_wait();
+  // (No wait for the kernel of the own tokens before this one: it began the dependents only after its
+  // own wait, and this one uses nothing that it writes. The join needs both: waited for at the end.)
+  pdl_trigger();
 
   volatile int* const abort_flag = &sh.abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -159,55 +187,63 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   Walk walk;
   walk.open(a, blockIdx.x, lane);
   Run run;
-  if (blockIdx.x == 0 && warp == 0) {   // for the join
-    int64_t total = 0;
-    for (int p0 = 0; p0 < a.P; p0 += 32) {
-      int64_t n = p0 + lane < a.P ? head_places(a, token_tiles(prefix_len(a, p0 + lane))) : 0;
-      n *= o.c.heads;
-      int64_t upto = n;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, x);
-        if (lane >= x) upto += v;
-      }
-      if (p0 + lane < a.P) a.starts[p0 + lane] = total + upto - n;
-      total += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) a.starts[a.P] = total;
-  }
   auto page_full = [&](const Run& r, int t0, unsigned there) {   // every token of the tile is there
     return t0 + kTok <= r.len && there == 0xFFFFFFFFu >> (32 - (kTok >> page_shift));
   };
 
-  if (warp < kScore / 32) {
+  if (tid >= T::kFirst) {
     // ------------------------------------------------------------ softmax, results ------
-    const int w = warp >> 2, quad = warp & 3, mine = 32 * quad + lane;   // stream; row of its tile
+    // two threads per row, each with half of the columns; the two warps of the same 32 rows agree on
+    // the row's reference
+    const int st = tid - T::kFirst;
+    const int w = st / kStream, quad = warp & 3, half = (st >> 7) & 1;   // w: the stream
+    const int mine = 32 * quad + lane;                                      // row of its tile
+    constexpr int kCols = kTok / 2;
     const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_at + w * kTok, tO = tmem + lane_at + 2 * kTok + w * D;
+    const uint32_t tS = tmem + lane_at + w * kTok + half * kCols;
+    const uint32_t tO = tmem + lane_at + 2 * kTok + w * D + half * (D / 2);
     // (a negative factor becomes its queries' sign, so that the largest product has the largest
     // score)
     const float fk = fabsf(o.scale_log2);
     const uint32_t flip = o.scale_log2 < 0.f ? 0x80008000u : 0u;
-    const f2 fk2 = pair(fk, fk);
+    // a barrier of the two warps: whether both are alive
+    auto together = [&](bool alive) {
+      int gone;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\t"
+          "barrier.cta.red.or.pred q, %1, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+          : "=r"(gone)
+          : "r"(1 + 4 * w + quad), "r"((int)!alive)
+          : "memory");
+      return !gone;
+    };
     uint32_t jobs = 0, runs = 0, tile0 = 0;   // before this run; tiles of the CTA
     bool alive = true;
     while (alive && walk.next(a, &run)) {
       const int n = run.t1 - run.t0, count = run.w == 2 ? n : (n + 1 - w) / 2;   // tiles of the stream
-      const int tile_row = run.u * 2 + (run.w == 2 ? w : 0);
-      const int row0 = tile_row * kRows;
+      const int row0 = (run.u * 2 + (run.w == 2 ? w : 0)) * kRows;
       if (count > 0) {
-        // ---- queries: eight threads of a warp take 64 values of a row
-        constexpr int kChunks = D / 8, kStep = 128 / kChunks;
-        const int lt = tid & 127, ch = lt % kChunks;
-#pragma unroll 4
-        for (int r = lt / kChunks; r < kRows; r += kStep) {
-          const int gr = row0 + r;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (gr < a.MP) {
-            const int s = run.p * a.per + gr / o.M, mm = gr % o.M;
-            x = reinterpret_cast<const uint4*>(
-                o.q + (((int64_t)s * o.R + mm / o.G) * o.Hq + run.h * o.G + mm % o.G) * D)[ch];
-          }
+        // ---- queries: 16 bytes of every kStep-th row (all loads before the first store)
+        constexpr int kChunks = D / 8, kStep = kStream / kChunks, kIters = kRows / kStep;
+        const int lt = st % kStream, ch = lt % kChunks, r0 = lt / kChunks;
+        const int each = kStep / o.M, rest = kStep % o.M;
+        int seq = run.p * a.per + (row0 + r0) / o.M, m = (row0 + r0) % o.M;
+        uint4 in[kIters];
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          in[it] = make_uint4(0u, 0u, 0u, 0u);
+          if (row0 + r0 + it * kStep < a.MP)
+            in[it] = reinterpret_cast<const uint4*>(
+                o.q + ((int64_t)seq * o.R * o.Hq + run.h * o.G) * D + sh.row_at[m])[ch];
+          seq += each;
+          m += rest;
+          if (m >= o.M) m -= o.M, ++seq;
+        }
+        // (the sums of the run before have left the room)
+        if (runs) alive = wait(&sh.qfree[w], (runs - 1) & 1);
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          uint4 x = in[it];
           if constexpr (kQ8) {   // each four values as (0, 2, 1, 3), the order of widened codes
             const uint4 y = x;
             x.x = __byte_perm(y.x, y.y, 0x5410);
@@ -216,160 +252,217 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             x.w = __byte_perm(y.z, y.w, 0x7632);
           }
           x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-          *reinterpret_cast<uint4*>(sQ + w * T::kMat + (ch >> 3) * (kRows * 128) + r * 128 +
+          const int r = r0 + it * kStep;
+          *reinterpret_cast<uint4*>(sQ + w * T::kQ + (ch >> 3) * (kRows * 128) + r * 128 +
                                     (((ch & 7) ^ (r & 7)) << 4)) = x;
         }
         fence_async();
         warp_arrive(&sh.qfull[w], lane);
       }
+      // ref: a score from which 2^(factor (score - ref)) is taken; norm: this thread's part of the sum
       float ref = kNothing, norm = 0.f;
       for (int i = 0; i < count && alive; ++i, ++jobs) {
         const int nt = run.w == 2 ? i : 2 * i + w;   // of the run
         const uint32_t tile = tile0 + nt;            // of the CTA
-        const int slot = tile % kInfo, t0 = (run.t0 + nt) * kTok;
+        const int slot = tile % kInfo, t0 = (run.t0 + nt) * kTok + half * kCols;
         alive = wait(&sh.info[slot], (tile / kInfo) & 1) && wait(&sh.sfull[w], jobs & 1);
         alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;
         sm100::tc_fence_after();
         volatile unsigned* const known = sh.runs;
         const unsigned there = known[slot];
-        const bool edge = !page_full(run, t0, there);
-        const float* const scales = sScale + 2 * slot * kTok;
+        const bool is_edge = !page_full(run, t0 - half * kCols, there);
+        const float* const scales = sScale + 2 * slot * kTok + half * kCols;
         // the tokens among 32 that count
         auto seen = [&](int c) {
           unsigned s = 0u;
           for (int x = 0; x < 32; x += 16)
-            if (there >> ((c + x) >> page_shift) & 1u) s |= 0xFFFFu << x;
+            if (there >> ((half * kCols + c + x) >> page_shift) & 1u) s |= 0xFFFFu << x;
           const int rest = run.len - t0 - c;
           return rest >= 32 ? s : (rest <= 0 ? 0u : s & ((1u << rest) - 1u));
         };
-        // 32 scores, in units of log2
-        auto scores = [&](int c, float (&t)[32]) {
+        // 32 scores before the factor (edge: masked)
+        auto scores = [&](auto edge, int c, float (&x)[32]) {
           __syncwarp();
-          ld32(tS + c, t);
+          ld32(tS + c, x);
+          if constexpr (kQ8) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            f2 f = fk2;
-            if constexpr (kQ8) {
-              const float2 k2 = *reinterpret_cast<const float2*>(scales + c + j);
-              f = mul2(f, pair(k2.x, k2.y));
+            for (int j = 0; j < 32; j += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(scales + c + j);
+              const float2 s0 = parts(mul2(pair(x[j], x[j + 1]), pair(k4.x, k4.y)));
+              const float2 s1 = parts(mul2(pair(x[j + 2], x[j + 3]), pair(k4.z, k4.w)));
+              x[j] = s0.x, x[j + 1] = s0.y, x[j + 2] = s1.x, x[j + 3] = s1.y;
             }
-            const float2 s = parts(mul2(pair(t[j], t[j + 1]), f));
-            t[j] = s.x;
-            t[j + 1] = s.y;
           }
-          if (edge) {
+          if constexpr (edge.value) {
             const unsigned s = seen(c);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!(s >> j & 1u)) t[j] = kNegInf;
+              if (!(s >> j & 1u)) x[j] = kNegInf;
           }
         };
-        float top = kNegInf;
+        using Inner = std::false_type;
+        using Edge = std::true_type;
+        auto largest = [&](auto edge) {
+          float top = kNegInf;
 #pragma unroll 1
-        for (int c = 0; c < kTok; c += 32) {
-          float t[32];
-          scores(c, t);
-          float m4[4] = {t[0], t[1], t[2], t[3]};
+          for (int c = 0; c < kCols; c += 32) {
+            float x[32];
+            scores(edge, c, x);
+            float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], t[j]);
-          top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-        }
+            for (int j = 4; j < 28; j += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], x[j + e], x[j + 4 + e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[28 + e]);
+            top = max3(top, max3(m4[0], m4[1], m4[2]), m4[3]);
+          }
+          return top;
+        };
+        float top = is_edge ? largest(Edge{}) : largest(Inner{});
+        sh.top[jobs & 1][w][half][mine] = top;
+        if (!(alive = together(alive))) break;
+        top = fmaxf(top, sh.top[jobs & 1][w][half ^ 1][mine]);
         // the reference moves only when a score exceeds it by 2^kSlack, and O with it (at rest: the
         // scores were issued after the product of this stream's tile before)
-        const bool up = i == 0 || __fsub_rn(top, ref) > kSlack;
+        const bool up = i == 0 || __fmul_rn(__fsub_rn(top, ref), fk) > kSlack;
         if (__any_sync(0xffffffffu, up)) {
-          const float now = fmaxf(ref, top), f = exp2_fast(__fsub_rn(ref, now));
+          const float now = fmaxf(ref, top);
+          const float f = i == 0 ? 0.f : exp2_fast(__fmul_rn(__fsub_rn(ref, now), fk));
           ref = now;
           norm = __fmul_rn(norm, f);
           if (i > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float t[32];
+            for (int c = 0; c < D / 2; c += 32) {
+              float x[32];
               uint32_t r[32];
               __syncwarp();
-              ld32(tO + c, t);
+              ld32(tO + c, x);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__fmul_rn(t[j], f));
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__fmul_rn(x[j], f));
               st32(tO + c, r);
             }
-            tmem_wait_st();
           }
         }
-        const f2 less = pair(-1.f, -1.f), back = pair(-ref, -ref);
+        const f2 less = pair(-1.f, -1.f), back = pair(-ref, -ref), fk2 = pair(fk, fk);
         f2 sum0 = pair(0.f, 0.f), sum1 = pair(0.f, 0.f);
+        auto weigh = [&](auto edge) {
 #pragma unroll 1
-        for (int c = 0; c < kTok; c += 32) {
-          float t[32];
-          uint32_t r[32];
-          scores(c, t);
+          for (int c = 0; c < kCols; c += 32) {
+            float x[32];
+            scores(edge, c, x);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 d = parts(add2(pair(t[j], t[j + 1]), back));
-            f2 p = pair(exp2_fast(d.x), exp2_fast(d.y));
-            if (j & 2) sum1 = add2(sum1, p);
-            else sum0 = add2(sum0, p);
-            if constexpr (kQ8) {
-              const float2 v2 = *reinterpret_cast<const float2*>(scales + kTok + c + j);
-              p = mul2(p, pair(v2.x, v2.y));
+            for (int c16 = 0; c16 < 32; c16 += 16) {   // 8 columns of high parts, 8 of low ones
+              uint32_t r[16];
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                [[maybe_unused]] float4 v4;
+                if constexpr (kQ8)
+                  v4 = *reinterpret_cast<const float4*>(scales + kTok + c + c16 + j);
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  const float x0 = x[c16 + j + e], x1 = x[c16 + j + e + 1];
+                  float2 d = parts(mul2(add2(pair(x0, x1), back), fk2));
+                  if constexpr (edge.value) {   // (a factor of 0 makes NaN of -infinity)
+                    d.x = x0 == kNegInf ? kNegInf : d.x;
+                    d.y = x1 == kNegInf ? kNegInf : d.y;
+                  }
+                  f2 p = pair(exp2_fast(d.x), exp2_fast(d.y));
+                  if (e) sum1 = add2(sum1, p);
+                  else sum0 = add2(sum0, p);
+                  if constexpr (kQ8) {
+                    p = mul2(p, e ? pair(v4.z, v4.w) : pair(v4.x, v4.y));
+                    if constexpr (edge.value) {   // a masked token's scale may be anything
+                      float2 y = parts(p);
+                      y.x = d.x == kNegInf ? 0.f : y.x;
+                      y.y = d.y == kNegInf ? 0.f : y.y;
+                      p = pair(y.x, y.y);
+                    }
+                  }
+                  const float2 y = parts(p);
+                  const uint32_t hi = pack2(y.x, y.y);
+                  const float2 rest = parts(fma2(pair(bf16_lo(hi), bf16_hi(hi)), less, p));
+                  r[(j + e) / 2] = hi;
+                  r[8 + (j + e) / 2] = pack2(rest.x, rest.y);
+                }
+              }
+              __syncwarp();
+              st16(tS + c + c16, r);
             }
-            float2 x = parts(p);
-            if (kQ8 && edge) {   // a masked token's scale may be anything
-              x.x = t[j] == kNegInf ? 0.f : x.x;
-              x.y = t[j + 1] == kNegInf ? 0.f : x.y;
-              p = pair(x.x, x.y);
+            if (c + 32 < kCols) {   // half of this thread's columns: products with these may begin
+              tmem_wait_st();
+              sm100::tc_fence_before();
+              warp_arrive(&sh.pfull[w][0], lane);
             }
-            const uint32_t hi = pack2(x.x, x.y);
-            const float2 rest = parts(fma2(pair(bf16_lo(hi), bf16_hi(hi)), less, p));
-            r[j / 2] = hi;
-            r[16 + j / 2] = pack2(rest.x, rest.y);
           }
-          __syncwarp();
-          st32(tS + c, r);
-        }
+        };
+        if (is_edge) weigh(Edge{});
+        else weigh(Inner{});
         const float2 s2 = parts(add2(sum0, sum1));
         norm = __fadd_rn(norm, __fadd_rn(s2.x, s2.y));
         tmem_wait_st();
         sm100::tc_fence_before();
-        warp_arrive(&sh.pfull[w], lane);
+        warp_arrive(&sh.pfull[w][1], lane);
       }
       // ---------------------------------------------------------------- results -----------
       if (alive) {
+        sh.top[jobs & 1][w][half][mine] = norm;
+        together(true);
+        const float other = sh.top[jobs & 1][w][half ^ 1][mine];
+        norm = half ? __fadd_rn(other, norm) : __fadd_rn(norm, other);
         const int64_t at = (unit_piece(a, run.p, run.h, run.u, blockIdx.x) * 2 + w) * kRows + mine;
-        *reinterpret_cast<float2*>(a.part_ml + 2 * at) =
-            make_float2(norm == 0.f ? kNegInf : ref, norm);
+        if (half == 0)
+          *reinterpret_cast<float2*>(a.part_ml + 2 * at) =
+              make_float2(norm == 0.f ? kNegInf : __fmul_rn(ref, fk), norm);
         if (count > 0) {
           alive = __all_sync(0xffffffffu, wait(&sh.odone[w], runs & 1));
           ++runs;
           if (alive) {
             sm100::tc_fence_after();
-            float4* const to = reinterpret_cast<float4*>(a.part_o + at * D);
+            // (32 rows x 32 columns at a time pass through the warp's part of the queries' room, so
+            // that whole lines are written)
+            float4* const room =
+                reinterpret_cast<float4*>(sQ + w * T::kQ + (4 * half + quad) * (T::kQ / 8));
+            float* const to = a.part_o + (at - lane) * D + half * (D / 2);
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float t[32];
+            for (int c = 0; c < D / 2; c += 32) {
+              float x[32];
               __syncwarp();
-              ld32(tO + c, t);
-              if (row0 + mine < a.MP) {
+              ld32(tO + c, x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)   // (columns of widened codes: (0, 2, 1, 3))
-                  to[c / 4 + j] = kQ8 ? make_float4(t[4 * j], t[4 * j + 2], t[4 * j + 1], t[4 * j + 3])
-                                      : make_float4(t[4 * j], t[4 * j + 1], t[4 * j + 2], t[4 * j + 3]);
+              for (int j = 0; j < 8; ++j)   // (columns of widened codes: (0, 2, 1, 3))
+                room[8 * lane + (j ^ (lane & 7))] =
+                    kQ8 ? make_float4(x[4 * j], x[4 * j + 2], x[4 * j + 1], x[4 * j + 3])
+                        : make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int r = 4 * j + lane / 8, col = lane % 8;
+                if (row0 + 32 * quad + r < a.MP)
+                  reinterpret_cast<float4*>(to + r * D + c)[col] = room[8 * r + (col ^ (r & 7))];
               }
             }
+            warp_arrive(&sh.qfree[w], lane);
             sm100::tc_fence_before();
           }
+        }
+        alive = together(alive);   // (and sh.top is free)
+        if (alive && half == 0 && w == 0 && quad == 0 && lane == 0) {
+          int* const span = a.span + 2 * (((int64_t)run.p * o.c.heads + run.h) * a.units + run.u);
+          if (run.t0 == 0) span[0] = blockIdx.x;
+          if (run.t1 == (run.len + kTok - 1) / kTok) span[1] = blockIdx.x;
         }
       }
       tile0 += n;
     }
-  } else if (warp < T::kMmaWarp) {
+  } else if (warp > 0 && tid < T::kBring + 2 * T::kWiden) {
     // ------------------------------------------------------------- tiles from the pages ---
-    const bool values = warp >= (kScore + T::kWiden) / 32;
+    const bool values = tid >= T::kBring + T::kWiden;
     uint64_t* const full = values ? sh.vfull : sh.kfull;
     uint64_t* const free_bar = values ? sh.vfree : sh.kfree;
     uint8_t* const tiles = values ? sV : sK;
     const int pages = kTok >> page_shift;
-    const bool teller = !values && (warp == kScore / 32);   // fills in the tile information
+    const bool teller = warp == 1;   // fills in the tile information
     int done = 0, edges = 0, st = 0;
     uint32_t par = 1;
     bool alive = true;
@@ -379,15 +472,15 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         const int t0 = t * kTok;
         const bool ok = page >= 0;
         const unsigned there = __ballot_sync(0xffffffffu, ok);
-        uint4 codes[kQ8 ? 8 : 1];
-        int rows_of = 0;
-        if constexpr (kQ8) {   // this tile's codes, on their way while the stage gets free
-          constexpr int kChunks = D / 16, kStep = 128 / kChunks, kIters = kTok / kStep;
-          static_assert(kIters <= 8, "codes");
-          const int lt = (tid - kScore) & 127;
-          const int my_row = D == 128 ? (lt >> 4) * 2 + ((lt >> 2) & 1) : lt / kChunks;
-          const int my_chunk = D == 128 ? (lt & 3) + ((lt >> 1) & 4) : lt % kChunks;
-          const uint8_t* const from = values ? o.c.v : o.c.k;
+        // Q8: this thread's codes, 16 of a token at a time, on their way while the stage gets free
+        constexpr int kChunks = D / 16, kStep = T::kWiden / kChunks, kIters = kQ8 ? kTok / kStep : 1;
+        const int lt = (tid - T::kBring) % T::kWiden;
+        // (eight lanes take 4 chunks of 2 rows, so that a quarter warp's stores meet all banks)
+        const int my_row = D == 128 ? (lt >> 4) * 2 + ((lt >> 2) & 1) : lt / kChunks;
+        const int my_chunk = D == 128 ? (lt & 3) + ((lt >> 1) & 4) : lt % kChunks;
+        uint4 codes[kIters];
+        if constexpr (kQ8) {
+          const uint8_t* const from = (values ? o.c.v : o.c.k) + my_chunk * 16;
 #pragma unroll
           for (int it = 0; it < kIters; ++it) {
             const int r = my_row + it * kStep;
@@ -395,10 +488,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             codes[it] = make_uint4(0u, 0u, 0u, 0u);
             if (pg >= 0 && t0 + r < run.len)
               codes[it] = __ldg(reinterpret_cast<const uint4*>(
-                  from + pg * o.c.stride +
-                  (((int64_t)run.h << page_shift) + (r & (pt - 1))) * D + my_chunk * 16));
+                  from + pg * o.c.stride + (((int64_t)run.h << page_shift) + (r & (pt - 1))) * D));
           }
-          rows_of = my_row * 128 + (my_chunk >> 2) * (kTok * 128);
         }
         if (done >= kRing) alive = wait(&free_bar[st], par);
         if (!(alive = __all_sync(0xffffffffu, alive))) break;
@@ -417,12 +508,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           }
         }
         if constexpr (kQ8) {
-          constexpr int kChunks = D / 16, kStep = 128 / kChunks, kIters = kTok / kStep;
-          const int lt = (tid - kScore) & 127;
-          const int my_row = D == 128 ? (lt >> 4) * 2 + ((lt >> 2) & 1) : lt / kChunks;
-          const int my_chunk = D == 128 ? (lt & 3) + ((lt >> 1) & 4) : lt % kChunks;
           const int c0 = ((2 * my_chunk & 7) ^ (my_row & 7)) << 4;   // (kStep: a multiple of 8 rows)
-          uint8_t* const dst = tiles + st * T::kMat + rows_of;
+          uint8_t* const dst = tiles + st * T::kMat + my_row * 128 + (my_chunk >> 2) * (kTok * 128);
 #pragma unroll
           for (int it = 0; it < kIters; ++it) {
             const uint4 v = codes[it];
@@ -477,80 +564,107 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         for (int j = done - kInfo < 0 ? 0 : done - kInfo; j < done; ++j)
           sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
     }
-  } else {
+  } else if (warp == 0) {
     // --------------------------------------------------------------------------- MMAs ----
-    // (the whole warp walks the loop; one lane issues)
+    // One lane issues, but the whole warp walks the loop, and what the MMAs are given is kept the same
+    // for all lanes in a way that the compiler sees (constants, tensor memory from column 0 on,
+    // reductions of loop bounds): operands then stay in uniform registers. With operands moved
+    // there for every MMA their issue took longer than their work: 167 against 130 us for 1536 rows of 8
+    // heads over 16k tokens.
     const bool leader = elect_one();
-    const uint32_t s_idesc = sm100::idesc_bf16_f32(kRows, kTok);
-    const uint32_t o_idesc = sm100::idesc_bf16_f32(kRows, D) | (kMajorMN & (1u << 16));
+    constexpr uint32_t s_idesc = sm100::idesc_bf16_f32(kRows, kTok);
+    constexpr uint32_t o_idesc = sm100::idesc_bf16_f32(kRows, D) | (kMajorMN & (1u << 16));
     const uint64_t q_desc = sm100::desc_k_sw128(smem_at(sQ));
     const uint64_t k_desc = sm100::desc_k_sw128(smem_at(sK));
     const uint64_t v_desc = desc_mn_sw128(smem_at(sV), kTok * 128);
     uint32_t ktiles = 0, vtiles = 0;    // tiles taken up
-    uint32_t summed[2] = {0, 0}, queries[2] = {0, 0};
+    uint32_t q_par = 0, p_par = 0;      // bit w: parity of stream w
     bool alive = true;
     while (alive && walk.next(a, &run)) {
-      const int n = run.t1 - run.t0, jobs = n * run.w;
-      auto score = [&](int j) {
-        const int w = j & 1;
-        const bool opens = run.w == 1 || w == 0, closes = run.w == 1 || w == 1;
-        const uint32_t tile = opens ? ktiles : ktiles - 1;
-        const int st = tile % kRing;
+      const bool two = __reduce_max_sync(0xffffffffu, run.w) == 2;   // row tiles
+      const int jobs = __reduce_max_sync(0xffffffffu, (run.t1 - run.t0) * run.w);
+      // what the scores of tile j, and the sums of tile j, have to wait for beside P
+      auto keys = [&](auto stream, int j) {
+        constexpr int w = decltype(stream)::value;
+        if (j >= jobs) return true;
         bool ok = true;
-        if (j < 2) ok = wait(&sh.qfull[w], queries[w]++ & 1);
-        if (opens) {
-          ok = ok && wait(&sh.kfull[st], (tile / kRing) & 1);
-          ++ktiles;
+        if (j < 2) {
+          ok = wait(&sh.qfull[w], q_par >> w & 1u);
+          q_par ^= 1u << w;
         }
+        if (two && w == 1) return ok;
+        ++ktiles;
+        return ok && wait(&sh.kfull[(ktiles - 1) % kRing], ((ktiles - 1) / kRing) & 1);
+      };
+      auto values = [&](auto stream) {
+        if (two && decltype(stream)::value == 1) return true;
+        ++vtiles;
+        return wait(&sh.vfull[(vtiles - 1) % kRing], ((vtiles - 1) / kRing) & 1);
+      };
+      auto score = [&](auto stream) {
+        constexpr int w = decltype(stream)::value;
+        const uint32_t st = (ktiles - 1) % kRing;
+        const uint64_t kd = k_desc + st * (uint32_t)(T::kMat >> 4);
+        const uint64_t qd = q_desc + (uint32_t)w * (T::kQ >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {   // 16 values: 32 bytes, or the next 64 values
+          const uint32_t off = (ks >> 2) * (kTok * 8) + (ks & 3) * 2;
+          sm100::mma_bf16(w * kTok, qd + off, kd + off, s_idesc, ks > 0);
+        }
+        sm100::mma_commit(&sh.sfull[w]);
+        if (!two || w == 1) sm100::mma_commit(&sh.kfree[st]);
+      };
+      // half of the sums: the steps whose P comes first (32 of 64 columns), or the others
+      auto sum = [&](auto stream, auto part, bool fresh) {
+        constexpr int w = decltype(stream)::value, x = decltype(part)::value;
+        const uint64_t vd = v_desc + (vtiles - 1) % kRing * (uint32_t)(T::kMat >> 4);
+        constexpr uint32_t p = w * kTok, to = 2 * kTok + w * D;
+#pragma unroll
+        for (int n = 0; n < kTok / 32; ++n) {   // 16 tokens: 2 KB of values, 16 columns of P
+          const int ks = (n >> 1) * 4 + 2 * x + (n & 1);
+          mma_tmem_a(to, p + 16 * ks, vd + ks * 128, o_idesc, !(fresh && n == 0));
+          mma_tmem_a(to, p + 16 * ks + 8, vd + ks * 128, o_idesc, 1u);
+        }
+      };
+      using C0 = std::integral_constant<int, 0>;
+      using C1 = std::integral_constant<int, 1>;
+      // tile j's sums, and behind them, without a pause, the scores of its stream's next tile. What
+      // the next unit needs beside P is waited for while this one's products run.
+      auto unit = [&](auto stream, int j) {
+        constexpr int w = decltype(stream)::value;
+        using Other = std::integral_constant<int, 1 - w>;
+        const bool more = j + 2 < jobs;
+        bool ok = wait(&sh.pfull[w][0], p_par >> w & 1u);
         if (!__all_sync(0xffffffffu, ok)) return false;
         sm100::tc_fence_after();
-        fence_async();
+        if (leader) sum(stream, C0{}, j < 2);
+        __syncwarp();
+        ok = wait(&sh.pfull[w][1], p_par >> w & 1u);
+        p_par ^= 1u << w;
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        sm100::tc_fence_after();
         if (leader) {
-          const uint64_t kd = k_desc + (uint32_t)st * (T::kMat >> 4);
-          const uint64_t qd = q_desc + (uint32_t)w * (T::kMat >> 4);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {   // 16 values: 32 bytes, or the next 64 values
-            const uint32_t off = (ks >> 2) * (kTok * 8) + (ks & 3) * 2;
-            sm100::mma_bf16(tmem + w * kTok, qd + off, kd + off, s_idesc, ks > 0);
-          }
-          sm100::mma_commit(&sh.sfull[w]);
-          if (closes) sm100::mma_commit(&sh.kfree[st]);
+          sum(stream, C1{}, false);
+          if (!two || w == 1) sm100::mma_commit(&sh.vfree[(vtiles - 1) % kRing]);
+          if (!more) sm100::mma_commit(&sh.odone[w]);
+          if (more) score(stream);
         }
+        __syncwarp();
+        ok = j + 1 >= jobs || (values(Other{}) && keys(Other{}, j + 3));
+        return (bool)__all_sync(0xffffffffu, ok);
+      };
+      auto first = [&](auto stream, int j) {
+        const bool ok = keys(stream, j);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        sm100::tc_fence_after();
+        if (leader && j < jobs) score(stream);
         __syncwarp();
         return true;
       };
-      auto sum = [&](int j) {
-        const int w = j & 1;
-        const bool opens = run.w == 1 || w == 0, closes = run.w == 1 || w == 1;
-        const uint32_t tile = opens ? vtiles : vtiles - 1;
-        const int st = tile % kRing;
-        bool ok = wait(&sh.pfull[w], summed[w]++ & 1);
-        if (opens) {
-          ok = ok && wait(&sh.vfull[st], (tile / kRing) & 1);
-          ++vtiles;
-        }
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        sm100::tc_fence_after();
-        fence_async();
-        if (leader) {
-          const uint64_t vd = v_desc + (uint32_t)st * (T::kMat >> 4);
-          const uint32_t p = tmem + w * kTok, to = tmem + 2 * kTok + w * D;
-#pragma unroll
-          for (int ks = 0; ks < kTok / 16; ++ks) {   // 16 tokens: 2 KB of values, 8 columns of P
-            const uint32_t at = p + 32 * (ks >> 1) + 8 * (ks & 1);
-            mma_tmem_a(to, at, vd + ks * 128, o_idesc, j >= 2 || ks > 0);
-            mma_tmem_a(to, at + 16, vd + ks * 128, o_idesc, 1u);
-          }
-          if (closes) sm100::mma_commit(&sh.vfree[st]);
-          if (j + 2 >= jobs) sm100::mma_commit(&sh.odone[w]);
-        }
-        __syncwarp();
-        return true;
-      };
-      for (int j = 0; j <= jobs && alive; ++j) {
-        if (j < jobs) alive = score(j);
-        if (alive && j > 0) alive = sum(j - 1);
-      }
+      alive = first(C0{}, 0) && first(C1{}, 1);
+      if (alive) alive = __all_sync(0xffffffffu, values(C0{}) && keys(C0{}, 2));
+      for (int j = 0; j < jobs && alive; j += 2)
+        alive = unit(C0{}, j) && (j + 1 >= jobs || unit(C1{}, j + 1));
     }
     // MMAs issued but maybe not observed complete: wait (bounded) before TMEM is freed
     if (leader) sm100::mma_commit(&sh.end);
@@ -558,9 +672,10 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     sm100::mbar_wait(&sh.end, 0, kWaitPolls);
   }
   __syncwarp();
+  pdl_wait();
   sm100::tc_fence_before();
   __syncthreads();
-  if (warp == 0) sm100::tmem_dealloc(tmem, 512);
+  if (warp == 0) sm100::tmem_dealloc(sh.tmem, 512);
 }
 
 template <int D, bool kQ8>
