@@ -14,7 +14,8 @@ using namespace prefix;
 
 // k_prefix_join: kWarps warps per row of the result (one head of one new token); with 1, a row for
 // each of 8 warps. 32 pieces at a time: a lane looks one up, and the warp adds up those there are,
-// four at a time, each lane D / 32 of the values.
+// four at a time, each lane D / 32 of the values. Its time is latency: with several pieces per row, 8
+// warps.
 template <int D, int kWarps>
 __global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ PrefixArgs a) {
   constexpr int V = D / 32;
@@ -51,8 +52,8 @@ __global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ Pre
   float top = kNegInf, norm = 0.f, acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  for (int i0 = kWarps > 1 ? 32 * warp : 0; i0 < n_all; i0 += 32 * (kWarps > 1 ? kWarps : 1)) {
-    const int i = i0 + lane;
+  for (int i0 = kWarps > 1 ? warp : 0; i0 < n_all; i0 += 32 * kWarps) {
+    const int i = i0 + kWarps * lane;
     float2 ml = make_float2(kNegInf, 0.f);
     const float* from = a.part_o;
     if (i < n_prefix) {
@@ -151,6 +152,7 @@ Plan make_plan(const PrefixAttnProblem& p, PrefixArgs* a) {
   a->MP = a->per * M;
   a->tiles = (a->MP + kRows - 1) / kRows;
   a->units = (a->tiles + 1) / 2;
+  a->m_inverse = (uint32_t)((((uint64_t)1 << 32) + M - 1) / M);
   a->max_pages = p.max_pages;
   const int64_t cap = ((int64_t)p.max_pages << p.own.cache.page_shift), T = (cap + kTok - 1) / kTok;
   const int64_t heads = (int64_t)p.P * p.own.cache.heads;
@@ -170,7 +172,7 @@ Plan make_plan(const PrefixAttnProblem& p, PrefixArgs* a) {
 template <int D>
 cudaError_t join(const PrefixArgs& a, int64_t units, cudaStream_t s) {
   const int64_t rows = (int64_t)a.own.B * a.own.R * a.own.Hq;
-  if (a.grid > 16 * units)   // pieces of a unit
+  if (a.grid > 4 * units)   // pieces of a unit
     return launch_pdl(k_prefix_join<D, 8>, dim3((unsigned)rows), 256, 0, s, a);
   return launch_pdl(k_prefix_join<D, 1>, dim3((unsigned)((rows + 7) / 8)), 256, 0, s, a);
 }

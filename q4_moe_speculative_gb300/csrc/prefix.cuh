@@ -24,6 +24,7 @@ struct PrefixArgs {
   PagedArgs own;        // the sequences' own tokens; queries, cache, results
   int P, per;           // prefixes; sequences of each
   int MP;               // query rows of a prefix per key head
+  uint32_t m_inverse;   // 2^32 / own.M, rounded up (M = 1: 0, for 2^32)
   int tiles, units;     // row tiles and units of a prefix per key head
   int max_pages;        // of a prefix
   const int32_t* table;
@@ -47,10 +48,14 @@ __device__ __forceinline__ int64_t head_places(const PrefixArgs& a, int T) {
 __device__ __forceinline__ int unit_tiles(const PrefixArgs& a, int u) {
   return 2 * u + 1 < a.tiles ? 2 : 1;
 }
-// Positions of the whole list. All lanes of a warp together.
-__device__ __forceinline__ int64_t list_places(const PrefixArgs& a, int lane) {
-  int64_t sum = 0;
-  for (int p = lane; p < a.P; p += 32) sum += head_places(a, token_tiles(prefix_len(a, p)));
+// n / own.M of a row number n < 2^19 (the rounding of the inverse adds less than 2^19 x 2^7 / 2^32).
+__device__ __forceinline__ unsigned over_m(const PrefixArgs& a, unsigned n) {
+  return a.m_inverse ? __umulhi(n, a.m_inverse) : n;
+}
+// Positions of the whole list, given the length of prefix `lane`. All lanes of a warp together.
+__device__ __forceinline__ int64_t list_places(const PrefixArgs& a, int lane, int len) {
+  int64_t sum = lane < a.P ? head_places(a, token_tiles(len)) : 0;
+  for (int p = lane + 32; p < a.P; p += 32) sum += head_places(a, token_tiles(prefix_len(a, p)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum * a.own.c.heads;
@@ -81,12 +86,14 @@ struct Walk {
   int64_t pos, end, start;   // start: of the head that pos is in
   int p, h, len, T;
   // All lanes of a warp together.
-  __device__ __forceinline__ void open(const PrefixArgs& a, int cta, int lane) {
-    const int64_t total = list_places(a, lane), ctas = list_ctas(a, total);
+  // (len: prefix_len() of prefix `lane`)
+  __device__ __forceinline__ void open(const PrefixArgs& a, int cta, int lane, int lane_len) {
+    const int64_t total = list_places(a, lane, lane_len), ctas = list_ctas(a, total);
     pos = end = 0;
     if (cta >= ctas) return;
     // (the first total % ctas have one more)
-    const int64_t each = total / ctas, more = total - each * ctas;
+    const int64_t each = total >> 32 ? total / ctas : (unsigned)total / (unsigned)ctas;
+    const int64_t more = total - each * ctas;
     pos = cta * each + (cta < more ? cta : more);
     end = pos + each + (cta < more ? 1 : 0);
     start = 0;

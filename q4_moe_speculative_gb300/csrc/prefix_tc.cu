@@ -11,9 +11,9 @@
 // for the other. Their order is S(j), then O of j - 1; an MMA reads P before a later one
 // overwrites it, since a CTA's MMAs run in the order of their issue.
 // Roles: two groups of four warps turn scores into P and write the sums; one warp each copies key and
-// value tiles page by page, by TMA into the swizzled operand layout (bf16), or four warps each widen
-// int8 codes to bf16 (Q8; the key's scale multiplies the score, the value's scale P); one thread of
-// the last warp issues the MMAs. Bound by the tensor cores with two row tiles: three products of
+// value tiles page by page, by TMA into the swizzled operand layout (bf16), or seven warps
+// widen int8 codes to bf16 (Q8; the key's scale multiplies the score, the value's scale P); one
+// thread of the first warp issues the MMAs. Bound by the tensor cores with two row tiles: three products of
 // 128 x 128 x 128 per 128 tokens and row tile. Every wait is bounded; a give-up sets the status word.
 #include <type_traits>
 
@@ -33,11 +33,12 @@ constexpr float kNothing = -3.402823466e38f;
 template <int D, bool kQ8>
 struct Tc {
   static constexpr int kHalves = D / 64;
+  static constexpr int kC = kQ8 ? 16 : 32;              // columns of scores at a time (Q8: 80 registers)
   static constexpr int kMat = kTok * D * 2;             // bytes of an operand tile
   static constexpr int kRing = D == 128 ? 2 : 4;        // stages of keys, and of values
-  static constexpr int kWiden = kQ8 ? 64 : 32;          // threads per matrix that bring tiles
+  static constexpr int kBringers = kQ8 ? 7 : 2;         // warps that bring tiles
   // warp 0 issues the MMAs, the next bring tiles, then softmax from a multiple of four on
-  static constexpr int kBring = 32, kFirst = (kBring + 2 * kWiden + 127) / 128 * 128;
+  static constexpr int kFirst = (1 + kBringers + 3) / 4 * 128;
   static constexpr int kThreads = kFirst + kScore;
   static constexpr int kSmall = 5120 + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
   static constexpr int kQ = kRows * 64 * 4;             // of a stream: its queries, then its sums
@@ -74,19 +75,9 @@ __device__ __forceinline__ void ld32(uint32_t at, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-// To 32 columns; tmem_wait_st() waits for it.
-__device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-      "%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
+__device__ __forceinline__ void load_columns(uint32_t at, float (&v)[32]) { ld32(at, v); }
+__device__ __forceinline__ void load_columns(uint32_t at, float (&v)[16]) { sm100::tmem_ld16(at, v); }
+// To 16 columns; tmem_wait_st() waits for it.
 __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -137,8 +128,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      sm100::mbar_init(&sh.kfull[i], kQ8 ? T::kWiden / 32 : 1);
-      sm100::mbar_init(&sh.vfull[i], kQ8 ? T::kWiden / 32 : 1);
+      sm100::mbar_init(&sh.kfull[i], kQ8 ? T::kBringers : 1);
+      sm100::mbar_init(&sh.vfull[i], kQ8 ? T::kBringers : 1);
       sm100::mbar_init(&sh.kfree[i], 1);
       sm100::mbar_init(&sh.vfree[i], 1);
     }
@@ -156,6 +147,9 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     sh.abort = 0;
     sm100::fence_mbar_init();
   }
+  // (No wait for the kernel of the own tokens before this one: it began the dependents only after its
+  // own wait, and this one uses nothing that it writes. The join needs both: waited for at the end.)
+  const int lane_len = lane < a.P ? prefix_len(a, lane) : 0;
   if (tid < o.M) sh.row_at[tid] = (tid / o.G * o.Hq + tid % o.G) * D;
   if (warp == 0) {
     sm100::tmem_alloc(&sh.tmem, 512);
@@ -169,8 +163,6 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   constexpr uint32_t tmem = 0;
   if (!kQ8 && tid < 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &v_map : &k_map) : "memory");
-  // (No wait for the kernel of the own tokens before this one: it began the dependents only after its
-  // own wait, and this one uses nothing that it writes. The join needs both: waited for at the end.)
   pdl_trigger();
 
   volatile int* const abort_flag = &sh.abort;
@@ -185,7 +177,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   };
   const int page_shift = o.c.page_shift, pt = 1 << page_shift;
   Walk walk;
-  walk.open(a, blockIdx.x, lane);
+  walk.open(a, blockIdx.x, lane, lane_len);
   Run run;
   auto page_full = [&](const Run& r, int t0, unsigned there) {   // every token of the tile is there
     return t0 + kTok <= r.len && there == 0xFFFFFFFFu >> (32 - (kTok >> page_shift));
@@ -226,8 +218,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         // ---- queries: 16 bytes of every kStep-th row (all loads before the first store)
         constexpr int kChunks = D / 8, kStep = kStream / kChunks, kIters = kRows / kStep;
         const int lt = st % kStream, ch = lt % kChunks, r0 = lt / kChunks;
-        const int each = kStep / o.M, rest = kStep % o.M;
-        int seq = run.p * a.per + (row0 + r0) / o.M, m = (row0 + r0) % o.M;
+        const int each = over_m(a, kStep), rest = kStep - each * o.M, before = over_m(a, row0 + r0);
+        int seq = run.p * a.per + before, m = row0 + r0 - before * o.M;
         uint4 in[kIters];
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
@@ -280,13 +272,13 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           const int rest = run.len - t0 - c;
           return rest >= 32 ? s : (rest <= 0 ? 0u : s & ((1u << rest) - 1u));
         };
-        // 32 scores before the factor (edge: masked)
-        auto scores = [&](auto edge, int c, float (&x)[32]) {
+        // T::kC scores before the factor (edge: masked)
+        auto scores = [&](auto edge, int c, float (&x)[T::kC]) {
           __syncwarp();
-          ld32(tS + c, x);
+          load_columns(tS + c, x);
           if constexpr (kQ8) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
+            for (int j = 0; j < T::kC; j += 4) {
               const float4 k4 = *reinterpret_cast<const float4*>(scales + c + j);
               const float2 s0 = parts(mul2(pair(x[j], x[j + 1]), pair(k4.x, k4.y)));
               const float2 s1 = parts(mul2(pair(x[j + 2], x[j + 3]), pair(k4.z, k4.w)));
@@ -296,7 +288,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           if constexpr (edge.value) {
             const unsigned s = seen(c);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < T::kC; ++j)
               if (!(s >> j & 1u)) x[j] = kNegInf;
           }
         };
@@ -305,16 +297,16 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         auto largest = [&](auto edge) {
           float top = kNegInf;
 #pragma unroll 1
-          for (int c = 0; c < kCols; c += 32) {
-            float x[32];
+          for (int c = 0; c < kCols; c += T::kC) {
+            float x[T::kC];
             scores(edge, c, x);
             float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int j = 4; j < 28; j += 8)
+            for (int j = 4; j < T::kC - 4; j += 8)
 #pragma unroll
               for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], x[j + e], x[j + 4 + e]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[28 + e]);
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[T::kC - 4 + e]);
             top = max3(top, max3(m4[0], m4[1], m4[2]), m4[3]);
           }
           return top;
@@ -333,14 +325,14 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           norm = __fmul_rn(norm, f);
           if (i > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 32) {
-              float x[32];
-              uint32_t r[32];
+            for (int c = 0; c < D / 2; c += 16) {
+              float x[16];
+              uint32_t r[16];
               __syncwarp();
-              ld32(tO + c, x);
+              load_columns(tO + c, x);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__fmul_rn(x[j], f));
-              st32(tO + c, r);
+              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__fmul_rn(x[j], f));
+              st16(tO + c, r);
             }
           }
         }
@@ -348,11 +340,11 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         f2 sum0 = pair(0.f, 0.f), sum1 = pair(0.f, 0.f);
         auto weigh = [&](auto edge) {
 #pragma unroll 1
-          for (int c = 0; c < kCols; c += 32) {
-            float x[32];
+          for (int c = 0; c < kCols; c += T::kC) {
+            float x[T::kC];
             scores(edge, c, x);
 #pragma unroll
-            for (int c16 = 0; c16 < 32; c16 += 16) {   // 8 columns of high parts, 8 of low ones
+            for (int c16 = 0; c16 < T::kC; c16 += 16) {   // 8 columns of high parts, 8 of low ones
               uint32_t r[16];
 #pragma unroll
               for (int j = 0; j < 16; j += 4) {
@@ -389,7 +381,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
               __syncwarp();
               st16(tS + c + c16, r);
             }
-            if (c + 32 < kCols) {   // half of this thread's columns: products with these may begin
+            if (c + T::kC == kCols / 2) {   // half of this thread's columns: products with these may begin
               tmem_wait_st();
               sm100::tc_fence_before();
               warp_arrive(&sh.pfull[w][0], lane);
@@ -455,72 +447,110 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       }
       tile0 += n;
     }
-  } else if (warp > 0 && tid < T::kBring + 2 * T::kWiden) {
+  } else if (warp > 0 && warp <= T::kBringers) {
     // ------------------------------------------------------------- tiles from the pages ---
-    const bool values = tid >= T::kBring + T::kWiden;
-    uint64_t* const full = values ? sh.vfull : sh.kfull;
-    uint64_t* const free_bar = values ? sh.vfree : sh.kfree;
-    uint8_t* const tiles = values ? sV : sK;
+    // bf16: a warp copies key tiles and one value tiles, page by page. Q8: all widen both, in turn.
     const int pages = kTok >> page_shift;
+    const bool values = warp == 2;   // (bf16)
     const bool teller = warp == 1;   // fills in the tile information
-    int done = 0, edges = 0, st = 0;
+    int done = 0, st = 0, told = 0;
     uint32_t par = 1;
     bool alive = true;
-    while (alive && walk.next(a, &run)) {
-      int page = lane < pages ? prefix_page(a, run.p, run.t0 * kTok + lane * pt, run.len) : -1;
-      for (int t = run.t0; t < run.t1; ++t) {
-        const int t0 = t * kTok;
-        const bool ok = page >= 0;
-        const unsigned there = __ballot_sync(0xffffffffu, ok);
-        // Q8: this thread's codes, 16 of a token at a time, on their way while the stage gets free
-        constexpr int kChunks = D / 16, kStep = T::kWiden / kChunks, kIters = kQ8 ? kTok / kStep : 1;
-        const int lt = (tid - T::kBring) % T::kWiden;
-        // (eight lanes take 4 chunks of 2 rows, so that a quarter warp's stores meet all banks)
-        const int my_row = D == 128 ? (lt >> 4) * 2 + ((lt >> 2) & 1) : lt / kChunks;
-        const int my_chunk = D == 128 ? (lt & 3) + ((lt >> 1) & 4) : lt % kChunks;
-        uint4 codes[kIters];
-        if constexpr (kQ8) {
-          const uint8_t* const from = (values ? o.c.v : o.c.k) + my_chunk * 16;
+    auto tell = [&](int page, unsigned there) {
+      // (its slot is free: the scores of the tile kRing before are done)
+      const int slot = told++ % kInfo;
+      if (lane == 0) {
+        sh.runs[slot] = there;
+        sm100::mbar_arrive_expect_tx(&sh.info[slot], kQ8 ? __popc(there) * pt * 8 : 0);
+      }
+      __syncwarp();
+      if (kQ8 && page >= 0) {
+        const int64_t at = page * o.c.scale_stride + ((int64_t)run.h << page_shift);
+        float* const dst = sScale + 2 * slot * kTok + lane * pt;
+        bulk_copy(dst, o.c.k_scale + at, pt * 4, &sh.info[slot]);
+        bulk_copy(dst + kTok, o.c.v_scale + at, pt * 4, &sh.info[slot]);
+      }
+    };
+    if constexpr (kQ8) {
+      // a lane takes 16 codes of a token; a warp 512, of kTokens tokens, every kBringers-th time. One
+      // matrix's codes are on their way while the other's are widened.
+      constexpr int kTokens = 512 / D, kTurns = kTok / kTokens;
+      constexpr int kMost = (kTurns + T::kBringers - 1) / T::kBringers;
+      // (eight lanes take 4 chunks of 2 rows, so that a quarter warp's stores meet all banks)
+      const int my_row = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
+      const int my_chunk = D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3;
+      const int turn0 = warp - 1;
+      auto fetch = [&](uint4 (&codes)[kMost], const uint8_t* from, int page, int t0) {
 #pragma unroll
-          for (int it = 0; it < kIters; ++it) {
-            const int r = my_row + it * kStep;
-            const int pg = __shfl_sync(0xffffffffu, page, r >> page_shift);
-            codes[it] = make_uint4(0u, 0u, 0u, 0u);
-            if (pg >= 0 && t0 + r < run.len)
-              codes[it] = __ldg(reinterpret_cast<const uint4*>(
-                  from + pg * o.c.stride + (((int64_t)run.h << page_shift) + (r & (pt - 1))) * D));
-          }
+        for (int it = 0; it < kMost; ++it) {
+          const int turn = turn0 + it * T::kBringers, r = (turn * kTokens + my_row) & (kTok - 1);
+          const int pg = __shfl_sync(0xffffffffu, page, r >> page_shift);
+          codes[it] = make_uint4(0u, 0u, 0u, 0u);
+          if (turn < kTurns && pg >= 0 && t0 + r < run.len)
+            codes[it] = __ldg(reinterpret_cast<const uint4*>(
+                from + pg * o.c.stride + (((int64_t)run.h << page_shift) + (r & (pt - 1))) * D +
+                my_chunk * 16));
         }
-        if (done >= kRing) alive = wait(&free_bar[st], par);
-        if (!(alive = __all_sync(0xffffffffu, alive))) break;
-        if (teller) {   // (its slot is free: the scores of the tile kRing before are done)
-          const int slot = done % kInfo;
-          if (lane == 0) {
-            sh.runs[slot] = there;
-            sm100::mbar_arrive_expect_tx(&sh.info[slot], kQ8 ? __popc(there) * pt * 8 : 0);
-          }
-          __syncwarp();
-          if (kQ8 && ok) {
-            const int64_t at = page * o.c.scale_stride + ((int64_t)run.h << page_shift);
-            float* const dst = sScale + 2 * slot * kTok + lane * pt;
-            bulk_copy(dst, o.c.k_scale + at, pt * 4, &sh.info[slot]);
-            bulk_copy(dst + kTok, o.c.v_scale + at, pt * 4, &sh.info[slot]);
-          }
-        }
-        if constexpr (kQ8) {
-          const int c0 = ((2 * my_chunk & 7) ^ (my_row & 7)) << 4;   // (kStep: a multiple of 8 rows)
-          uint8_t* const dst = tiles + st * T::kMat + my_row * 128 + (my_chunk >> 2) * (kTok * 128);
+      };
+      auto widen = [&](const uint4 (&codes)[kMost], uint8_t* tile) {
+        tile += (my_chunk >> 2) * (kTok * 128);
 #pragma unroll
-          for (int it = 0; it < kIters; ++it) {
-            const uint4 v = codes[it];
-            *reinterpret_cast<uint4*>(dst + it * (kStep * 128) + c0) = make_uint4(
-                code_pair(v.x), code_pair(v.x >> 8), code_pair(v.y), code_pair(v.y >> 8));
-            *reinterpret_cast<uint4*>(dst + it * (kStep * 128) + (c0 ^ 16)) = make_uint4(
-                code_pair(v.z), code_pair(v.z >> 8), code_pair(v.w), code_pair(v.w >> 8));
-          }
+        for (int it = 0; it < kMost; ++it) {
+          const int turn = turn0 + it * T::kBringers, r = turn * kTokens + my_row;
+          if (turn >= kTurns) break;
+          const uint4 v = codes[it];
+          const int c0 = ((2 * my_chunk & 7) ^ (r & 7)) << 4;
+          *reinterpret_cast<uint4*>(tile + r * 128 + c0) = make_uint4(
+              code_pair(v.x), code_pair(v.x >> 8), code_pair(v.y), code_pair(v.y >> 8));
+          *reinterpret_cast<uint4*>(tile + r * 128 + (c0 ^ 16)) = make_uint4(
+              code_pair(v.z), code_pair(v.z >> 8), code_pair(v.w), code_pair(v.w >> 8));
+        }
+      };
+      while (alive && walk.next(a, &run)) {
+        auto page_of_tile = [&](int t) {
+          return lane < pages && t < run.t1 ? prefix_page(a, run.p, t * kTok + lane * pt, run.len) : -1;
+        };
+        int page = page_of_tile(run.t0);
+        uint4 kc[kMost], vc[kMost];
+        fetch(kc, o.c.k, page, run.t0 * kTok);
+        for (int t = run.t0; t < run.t1; ++t) {
+          const int next = page_of_tile(t + 1);
+          const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
+          fetch(vc, o.c.v, page, t * kTok);
+          if (done >= kRing) alive = wait(&sh.kfree[st], par);
+          if (!(alive = __all_sync(0xffffffffu, alive))) break;
+          if (teller) tell(page, there);
+          widen(kc, sK + st * T::kMat);
           fence_async();
-          warp_arrive(&full[st], lane);
-        } else {
+          warp_arrive(&sh.kfull[st], lane);
+          if (t + 1 < run.t1) fetch(kc, o.c.k, next, (t + 1) * kTok);
+          if (done >= kRing) alive = wait(&sh.vfree[st], par);
+          if (!(alive = __all_sync(0xffffffffu, alive))) break;
+          widen(vc, sV + st * T::kMat);
+          fence_async();
+          warp_arrive(&sh.vfull[st], lane);
+          ++done;
+          if (++st == kRing) st = 0, par ^= 1;
+          page = next;
+        }
+      }
+      if (*abort_flag && teller)   // copies in flight end (bounded) before the CTA does
+        for (int j = told - kInfo < 0 ? 0 : told - kInfo; j < told; ++j)
+          sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
+    } else {
+      uint64_t* const full = values ? sh.vfull : sh.kfull;
+      uint64_t* const free_bar = values ? sh.vfree : sh.kfree;
+      uint8_t* const tiles = values ? sV : sK;
+      int edges = 0;
+      while (alive && walk.next(a, &run)) {
+        int page = lane < pages ? prefix_page(a, run.p, run.t0 * kTok + lane * pt, run.len) : -1;
+        for (int t = run.t0; t < run.t1; ++t) {
+          const int t0 = t * kTok;
+          const bool ok = page >= 0;
+          const unsigned there = __ballot_sync(0xffffffffu, ok);
+          if (done >= kRing) alive = wait(&free_bar[st], par);
+          if (!(alive = __all_sync(0xffffffffu, alive))) break;
+          if (teller) tell(page, there);
           const bool edge = values && !page_full(run, t0, there);
           uint64_t* const bar = edge ? &sh.vedge : &full[st];
           if (lane == 0) sm100::mbar_arrive_expect_tx(bar, __popc(there) * pt * 2 * D);
@@ -548,21 +578,16 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive(&full[st]);
           }
+          ++done;
+          if (++st == kRing) st = 0, par ^= 1;
+          page = -1;
+          if (t + 1 < run.t1 && lane < pages)
+            page = prefix_page(a, run.p, (t + 1) * kTok + lane * pt, run.len);
         }
-        ++done;
-        if (++st == kRing) st = 0, par ^= 1;
-        page = -1;
-        if (t + 1 < run.t1 && lane < pages)
-          page = prefix_page(a, run.p, (t + 1) * kTok + lane * pt, run.len);
       }
-    }
-    if (*abort_flag) {   // copies in flight end (bounded) before the CTA does
-      if (!kQ8)
+      if (*abort_flag)   // copies in flight end (bounded) before the CTA does
         for (int j = done - kRing < 0 ? 0 : done - kRing; j < done; ++j)
           sm100::mbar_wait(&full[j % kRing], (j / kRing) & 1, kWaitPolls);
-      if (teller)
-        for (int j = done - kInfo < 0 ? 0 : done - kInfo; j < done; ++j)
-          sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
     }
   } else if (warp == 0) {
     // --------------------------------------------------------------------------- MMAs ----
