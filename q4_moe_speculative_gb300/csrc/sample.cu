@@ -12,9 +12,9 @@
 // this GPU has few units for, took 1050 us for 64 rows of 129,280 with top-p.
 //
 // Where the order is cut (the k-th largest logit; the logit at which the mass before it reaches
-// top_p), the border is found by counts or masses per bin: first 2048 bins of equal width in
+// top_p), the border is found by counts or masses per bin: first 1024 bins of equal width in
 // (max - l) / T, which spread a vocabulary's logits, then the border bin's range of keys (logits as
-// ordered integers) in 2048 bins, until a bin is one key. Of the tokens with the border's logit the
+// ordered integers) in 1024 bins, until a bin is one key. Of the tokens with the border's logit the
 // lowest ids are kept.
 #include <cooperative_groups.h>
 
@@ -32,25 +32,34 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;
 constexpr float kReach = 46.f;       // log2: a lighter token has the weight 0
 constexpr float kBinsPerLog2 = kBins / kReach;
 constexpr float kNegInf = -INFINITY;
 constexpr int kRoots = 64;
 constexpr float kMagic = 12582912.f;   // 1.5 x 2^23: added, it leaves an integer in the lowest bits
 constexpr int kMagicBits = 0x4B400000;
-constexpr int kPad = 2 * kThreads;   // tokens without weight behind a CTA's last one
+constexpr int kPad = 4 * kThreads;   // tokens without weight behind a CTA's last one
+constexpr int kFew = 512;           // kept tokens that one CTA finishes alone
 constexpr int kGathered = 2048;      // tokens of a border's bin that one CTA sorts out
 
 struct SampleArgs {
   SampleProblem p;
   int chunk;        // tokens per CTA, a multiple of 8
   int scale;        // log2 of the weight 1
-  unsigned long long root[kRoots];   // 2^(-j / kRoots) in units of 2^-47
+  unsigned long long root[kRoots];   // 2^(j / kRoots) in units of 2^-46
 };
 
 struct Shared {
-  unsigned lo[kBins], hi[kBins];           // sums of the bins, in two words
+  union {
+    struct {
+      unsigned lo[kBins], hi[kBins];       // sums of the bins, in two words
+    };
+    struct {                               // rank 0, when few tokens are kept:
+      unsigned long long units[kFew];      // weights in falling order
+      int ids[kFew];                       // of the tokens in keys
+    };
+  };
   unsigned long long upto[kBins];          // of this CTA's slice of the bins, over the cluster
   unsigned keys[kGathered];                // rank 0: of the tokens in the border's bin
   int list[kThreads];                      // this CTA's tokens there
@@ -68,6 +77,9 @@ struct Shared {
   double less;                             // T log(min_p)
   float least;
   int bin, listed, gathered;
+  unsigned long long inside;               // with a border found: what is in its bin and above
+  unsigned sorted[kFew];                   // and with units: the keys and ids of the order
+  int sorted_ids[kFew];
   unsigned low[kWarps], high[kWarps];
 };
 
@@ -85,45 +97,45 @@ struct Row {
   float top, per_log2, per_log2_low;     // the largest logit; log2(e) / T, in two parts
   int scale;
   const unsigned long long* root;
-  // (max - l) / T in log2: never falls as l does; NaN or beyond kReach: no weight
+  // (max - l) / T in log2: never rises with l; NaN or beyond kReach: no weight
   __device__ __forceinline__ float reach(float l) const {
     return __fmul_rn(__fsub_rn(top, l), per_log2);
   }
   static __device__ __forceinline__ int bin_of(float reach) {
     return min(kBins - 1, __float_as_int(__fmaf_rn(reach, kBinsPerLog2, kMagic)) - kMagicBits);
   }
-  // The weights of two logits: 2^-t, t = (top - l) log2(e) / T as a pair of fp32 values (the
-  // difference and the product with their rounding errors), off by 2^-45 relative to t. With k =
-  // 64 t rounded, t = k / 64 + x, |x| <= 1 / 128: a root from the table, shifted, times e^-y, y =
-  // x log(2) <= 0.0055. e^-y - 1 = -y + y^2 / 2 - y^3 / 6 + y^4 / 24, the next term being 2^-44: all
+  // The weights of two logits: 2^s, s = (l - top) log2(e) / T <= 0 as a pair of fp32 values (the
+  // difference and the product with their rounding errors), off by 2^-45 relative to s. With k =
+  // 64 s rounded, s = k / 64 + r, |r| <= 1 / 128: a root from the table, shifted, times e^y, y =
+  // r log(2), |y| <= 0.0055. e^y - 1 = y + y^2 / 2 + y^3 / 6 + y^4 / 24, the next term being 2^-44: all
   // but the first are below 2^-16 and take one fp32 value (off by 2^-39); the first goes to an
   // integer in two parts. Integers from fp32 by adding 1.5 x 2^23.
-  // (where[]: the reach of each)
+  // (where[]: the reach of each, negative)
   __device__ __forceinline__ void units2(float l0, float l1, unsigned long long* u0,
                                          unsigned long long* u1, float2* where) const {
     const f2 minus = pair(-1.f, -1.f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
-    const f2 a = pair(top, top), b = mul2(pair(l0, l1), minus);
-    const f2 d = add2(a, b), bb = fma2(a, minus, d);     // d + e = top - l
-    const f2 e = add2(fma2(fma2(bb, minus, d), minus, a), fma2(bb, minus, b));
+    const f2 l = pair(l0, l1), m_top = pair(-top, -top);
+    const f2 n = add2(l, m_top), bb = fma2(l, minus, n);     // n + e = l - top
+    const f2 e = add2(fma2(fma2(bb, minus, n), minus, l), fma2(bb, minus, m_top));
     const f2 c = pair(per_log2, per_log2), cl = pair(per_log2_low, per_log2_low);
-    const f2 t = mul2(d, c);
-    const f2 te = fma2(e, c, fma2(d, cl, fma2(d, c, mul2(t, minus))));
+    const f2 t = mul2(n, c);
+    const f2 te = fma2(e, c, fma2(n, cl, fma2(n, c, mul2(n, pair(-per_log2, -per_log2)))));
     const f2 km = fma2(t, pair(64.f, 64.f), magic);
     const f2 r = fma2(add2(km, unmagic), pair(-1.f / 64, -1.f / 64), t);
     const f2 ln = pair(kLn2, kLn2);
     const f2 y = mul2(r, ln);
-    const f2 ye = fma2(te, ln, fma2(r, pair(kLn2Low, kLn2Low), fma2(r, ln, mul2(y, minus))));
-    f2 q = fma2(y, pair(1.f / 24, 1.f / 24), pair(-1.f / 6, -1.f / 6));
+    const f2 ye = fma2(te, ln, fma2(r, pair(kLn2Low, kLn2Low), fma2(r, ln, mul2(r, pair(-kLn2, -kLn2)))));
+    f2 q = fma2(y, pair(1.f / 24, 1.f / 24), pair(1.f / 6, 1.f / 6));
     q = fma2(y, q, pair(0.5f, 0.5f));
-    q = fma2(mul2(y, y), q, mul2(ye, minus));
-    // -y = -m 2^-16 + rest
+    q = fma2(mul2(y, y), q, ye);
+    // y = m 2^-16 + rest
     const f2 ym = fma2(y, pair(65536.f, 65536.f), magic);
-    const f2 rest = add2(fma2(add2(ym, unmagic), pair(1.f / 65536, 1.f / 65536), mul2(y, minus)), q);
+    const f2 rest = add2(fma2(add2(ym, unmagic), pair(-1.f / 65536, -1.f / 65536), y), q);
     const f2 low = fma2(rest, pair(0x1p37f, 0x1p37f), magic);
     const float2 k2 = parts(km), m2 = parts(ym), low2 = parts(low), t2 = parts(t);
     *where = t2;
-    *u0 = t2.x < kReach ? compose(k2.x, m2.x, low2.x) : 0ull;
-    *u1 = t2.y < kReach ? compose(k2.y, m2.y, low2.y) : 0ull;
+    *u0 = t2.x > -kReach ? compose(k2.x, m2.x, low2.x) : 0ull;
+    *u1 = t2.y > -kReach ? compose(k2.y, m2.y, low2.y) : 0ull;
   }
   __device__ __forceinline__ unsigned long long units(float l) const {
     unsigned long long u, v;
@@ -134,10 +146,10 @@ struct Row {
   // A logit's weight over a total of units, rounded to fp32 (within 2^-10 of half a step): the weight
   // before it is shifted, and the total, as fp32 pairs; the quotient and its remainder's.
   __device__ __forceinline__ float share(float l, unsigned long long total) const {
-    const float d = __fsub_rn(top, l), t = __fmul_rn(d, per_log2);
+    const float t = __fmul_rn(__fsub_rn(l, top), per_log2);
     const int k = __float_as_int(__fmaf_rn(t, 64.f, kMagic)) - kMagicBits;
     Row wide = *this;
-    wide.scale = 45 + (k >> 6);   // (the shift of compose() is 1)
+    wide.scale = 45 - (k >> 6);   // (the shift of compose() is 1)
     const unsigned long long w = wide.units(l);
     auto high = [](unsigned long long x) { return __ull2float_rn(x); };
     auto low = [](unsigned long long x, float h) {
@@ -148,14 +160,14 @@ struct Row {
     const float r = __fadd_rn(__fmaf_rn(-q, th, wh), __fmaf_rn(-q, tl, wl));
     return scalbnf(__fadd_rn(q, __fdiv_rn(r, th)), scale - wide.scale);
   }
-  // Root k mod 64 times (1 + (low - m 2^21) 2^-37), shifted by k / 64.
+  // Root k mod 64 times (1 + (low + m 2^21) 2^-37), shifted by k / 64.
   __device__ __forceinline__ unsigned long long compose(float k_magic, float m_magic,
                                                         float low_magic) const {
     const int k = __float_as_int(k_magic) - kMagicBits;
-    const int f = __float_as_int(low_magic) - kMagicBits - ((__float_as_int(m_magic) - kMagicBits) << 21);
+    const int f = __float_as_int(low_magic) - kMagicBits + ((__float_as_int(m_magic) - kMagicBits) << 21);
     const unsigned long long z = root[k & (kRoots - 1)];
-    const long long w = (long long)z + (((long long)f * (int)(z >> 17)) >> 20);   // units of 2^-47
-    return (((unsigned long long)w >> ((k >> 6) + 46 - scale)) + 1) >> 1;
+    const long long w = (long long)z + (((long long)f * (int)(z >> 17)) >> 20);   // units of 2^-46
+    return (((unsigned long long)w >> (45 - scale - (k >> 6))) + 1) >> 1;
   }
   static constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;   // log(2) in two parts
 };
@@ -311,7 +323,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       p.out[b] = -1;
       if (p.prob) p.prob[b] = 0.f;
     }
-    cluster.sync();
     return;
   }
   const bool endless = top == INFINITY;   // only the infinite ones count, all alike
@@ -349,6 +360,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   __syncthreads();
   const float least = sh.least;
   const unsigned least_key = key_of(least);
+  // Calls f(place, logit) for this thread's tokens whose reach passes the test, few of all.
+  auto scan = [&](auto&& test, auto&& f) {
+    for (int i = tid; i < n; i += 4 * kThreads) {
+      float l[4];
+      unsigned pass = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        l[e] = logit(i + e * kThreads);
+        pass |= test(row.reach(l[e])) ? 1u << e : 0u;
+      }
+      if (!pass) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (pass >> e & 1u) f(i + e * kThreads, l[e]);
+    }
+  };
   // Among the tokens that each(f) gives to f, keys low .. high: the key at which what is above, with
   // `above` beside them, reaches target. all: every CTA of the cluster has some of the tokens, and
   // finds the same; else the CTA that calls has them.
@@ -420,20 +447,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0u;
     if (tid == 0) sh.listed = sh.gathered = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += 2 * kThreads) {
-      const float l0 = logit(i), l1 = logit(i + kThreads);
-      // (those at the limit's key: their number is known, and they are counted once below)
-      const bool in0 = key_of(l0) > limit.key, in1 = key_of(l1) > limit.key;
-      if (!masses) {
-        const float t0 = row.reach(l0), t1 = row.reach(l1);
-        if (t0 < kReach) atomicAdd(&sh.lo[Row::bin_of(t0)], 1u);
-        if (t1 < kReach) atomicAdd(&sh.lo[Row::bin_of(t1)], 1u);
-      } else if (in0 || in1) {
+    if (!masses) {
+      for (int i = tid; i < n; i += 4 * kThreads) {
+        float t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = row.reach(logit(i + e * kThreads));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t[e] < kReach) atomicAdd(&sh.lo[Row::bin_of(t[e])], 1u);
+      }
+    } else {
+      for (int i = tid; i < n; i += 2 * kThreads) {
+        const float l0 = logit(i), l1 = logit(i + kThreads);
+        // (those at the limit's key: their number is known, and they are counted once below)
+        const bool in0 = key_of(l0) > limit.key, in1 = key_of(l1) > limit.key;
+        if (!in0 && !in1) continue;
         unsigned long long u0, u1;
         float2 t;
         row.units2(l0, l1, &u0, &u1, &t);
-        if (in0 && t.x < kReach) bin_add(sh, Row::bin_of(t.x), u0);
-        if (in1 && t.y < kReach) bin_add(sh, Row::bin_of(t.y), u1);
+        if (in0 && t.x > -kReach) bin_add(sh, Row::bin_of(-t.x), u0);
+        if (in1 && t.y > -kReach) bin_add(sh, Row::bin_of(-t.y), u1);
       }
     }
     if (rank == 0 && tid == 0 && limit.key) {
@@ -479,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       if (lower < target && start + upto[i] >= target) {   // (one of them)
         sh.bin = owner * per + i;
         sh.above = lower;
+        sh.inside = start + upto[i];
       }
     }
     __syncthreads();
@@ -494,21 +528,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if (*weighed)
       for (int i = tid; i < bin; i += kThreads)
         part += ((unsigned long long)sh.hi[i] << 32) + sh.lo[i];
+    // few tokens down to the bin's end: one CTA finishes the row with them
+    if (!masses && sh.inside <= kFew) {
+      unsigned* const to = cluster.map_shared_rank(sh.keys, 0);
+      int* const ids = cluster.map_shared_rank(sh.ids, 0);
+      int* const count = cluster.map_shared_rank(&sh.gathered, 0);
+      scan([&](float t) { return t < kReach && Row::bin_of(t) <= bin; }, [&](int i, float l) {
+        const int at = atomicAdd(count, 1);   // (below kFew: as many as were counted)
+        if (at < kFew) to[at] = key_of(l), ids[at] = v0 + i;
+      });
+      cluster.sync();
+      return Border{1u, 0ull};
+    }
     // the tokens of the bin
     unsigned* const keys = cluster.map_shared_rank(sh.keys, 0);
     int* const gathered = cluster.map_shared_rank(&sh.gathered, 0);
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) {
-      const float l = logit(i), t = row.reach(l);
-      if (!(t < kReach) || Row::bin_of(t) != bin || key_of(l) <= limit.key) continue;
+    scan([&](float t) { return t < kReach && Row::bin_of(t) == bin; }, [&](int i, float l) {
+      if (key_of(l) <= limit.key) return;
       if (min_p_cuts) {
         if (key_of(l) >= least_key) part += row.units(l);
-        continue;
+        return;
       }
       const int place = atomicAdd(&sh.listed, 1), at = atomicAdd(gathered, 1);
       if (place < kThreads) sh.list[place] = i;
       if (at < kGathered) keys[at] = key_of(l);
-    }
+    });
     if (min_p_cuts) {
       *own = block_upto(part, sh.warp_mass);   // (the last thread has all of it)
       *own_ties = 0;
@@ -565,10 +609,67 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     return found;
   };
 
+  // floor(u * total), u in units of 2^-64: drawn is the first token beyond it
+  auto place_of = [&](unsigned long long total) {
+    unsigned long long u64 = 0;
+    if (u >= 1.0) u64 = ~0ull;
+    else if (u > 0x1p-1000) {
+      const unsigned long long bits = (unsigned long long)__double_as_longlong(u);
+      const int shift = (int)(bits >> 52) - 1011;   // of the mantissa
+      const unsigned long long m = (bits & ((1ull << 52) - 1)) | 1ull << 52;
+      u64 = shift >= 0 ? m << shift : (shift > -53 ? m >> -shift : 0ull);
+    }
+    return __umul64hi(u64, total);
+  };
+  // Top-k, top-p, min-p and the draw among the few tokens in sh.keys and sh.ids, by this CTA: ranks and
+  // masses before a token by comparing it with all others.
+  auto finish = [&] {
+    const int m = min(sh.gathered, kFew);
+    const unsigned key = tid < m ? sh.keys[tid] : 0u;
+    const int id = tid < m ? sh.ids[tid] : 0;
+    if (tid < m) {   // in falling order, of equal logits the lowest ids first
+      int before = 0;
+      for (int j = 0; j < m; ++j) {
+        const unsigned other = sh.keys[j];
+        before += other > key || (other == key && sh.ids[j] < id) ? 1 : 0;
+      }
+      sh.sorted[before] = key;
+      sh.sorted_ids[before] = id;
+    }
+    __syncthreads();
+    const int first = min(k, m);   // top-k's
+    const unsigned my_key = tid < first ? sh.sorted[tid] : 0u;
+    const int my_id = tid < first ? sh.sorted_ids[tid] : 0;
+    const unsigned long long mine = tid < first ? row.units(from_key(my_key)) : 0ull;
+    const unsigned long long to = block_upto(mine, sh.warp_mass);
+    if (tid == kThreads - 1) sh.above = to;
+    __syncthreads();
+    const unsigned long long all = sh.above;
+    const unsigned long long limit =
+        top_p < 1.f ? (top_p > 0.f ? share_of(all, top_p) : 1ull) : ~0ull;
+    const bool kept = tid < first && (to - mine < limit) && my_key >= least_key;
+    sh.units[tid] = kept ? mine : 0ull;
+    const unsigned long long total_to = block_upto(kept ? mine : 0ull, sh.warp_ties);
+    if (tid == kThreads - 1) sh.inside = total_to;
+    __syncthreads();
+    const unsigned long long total = sh.inside, place = place_of(total);
+    if (!kept) return;
+    unsigned long long from = 0;   // of the kept tokens with lower ids
+    for (int j = 0; j < first; ++j) from += sh.sorted_ids[j] < my_id ? sh.units[j] : 0ull;
+    if (place < from || place >= from + mine) return;
+    p.out[b] = my_id;
+    if (p.prob) p.prob[b] = row.share(from_key(my_key), total);
+  };
   Border border{0u, ~0ull};
   unsigned long long own = 0, own_ties = 0;
   bool weighed = false;
-  if (k > 0 && k < p.V) border = cut(false, (unsigned long long)k, border, &weighed, &own, &own_ties);
+  if (k > 0 && k < p.V) {
+    border = cut(false, (unsigned long long)k, border, &weighed, &own, &own_ties);
+    if (border.key && border.ties == 0) {
+      if (rank == 0) finish();
+      return;
+    }
+  }
   if (top_p < 1.f) border = cut(true, 0ull, border, &weighed, &own, &own_ties);
   // ------------------------------------------------------------------ the draw
   // the mass above the border, and the tokens at it, of each warp's stretch
@@ -626,16 +727,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     }
     total += sh.mass[c] + kept * each;
   }
-  // floor(u * total), u in units of 2^-64
-  unsigned long long u64 = 0;
-  if (u >= 1.0) u64 = ~0ull;
-  else if (u > 0x1p-1000) {
-    const unsigned long long bits = (unsigned long long)__double_as_longlong(u);
-    const int shift = (int)(bits >> 52) - 1011;   // of the mantissa
-    const unsigned long long m = (bits & ((1ull << 52) - 1)) | 1ull << 52;
-    u64 = shift >= 0 ? m << shift : (shift > -53 ? m >> -shift : 0ull);
-  }
-  const unsigned long long target = __umul64hi(u64, total);   // drawn: the first beyond it
+  const unsigned long long target = place_of(total);   // drawn: the first beyond it
   if (target >= start && target < start + mine) {   // (one CTA of the cluster)
     // the warp's stretch that crosses it, and the same again inside that stretch
     if (weighed) weigh();
@@ -679,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       }
     }
   }
-  cluster.sync();   // (no CTA leaves while others may reach into its shared memory)
 }
 
 }  // namespace
@@ -695,7 +786,7 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   while (C < kMaxCluster && p.V > 1024 * C && (int64_t)p.B * C < 2 * device_sm_count()) C *= 2;
   a.chunk = ((p.V + C - 1) / C + 7) / 8 * 8;
   for (int j = 0; j < kRoots; ++j)
-    a.root[j] = (unsigned long long)std::llrint(std::exp2(47.0 - j / (double)kRoots));
+    a.root[j] = (unsigned long long)std::llrint(std::exp2(46.0 + j / (double)kRoots));
   const int room = 160 * 1024, stage = (a.chunk + 8 + kPad) * 4;
   const bool staged = stage <= room;
   const auto kernel = p.bf16 ? (staged ? k_sample<true, true> : k_sample<true, false>)
