@@ -608,24 +608,6 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     while (alive && walk.next(a, &run)) {
       const bool two = __reduce_max_sync(0xffffffffu, run.w) == 2;   // row tiles
       const int jobs = __reduce_max_sync(0xffffffffu, (run.t1 - run.t0) * run.w);
-      // what the scores of tile j, and the sums of tile j, have to wait for beside P
-      auto keys = [&](auto stream, int j) {
-        constexpr int w = decltype(stream)::value;
-        if (j >= jobs) return true;
-        bool ok = true;
-        if (j < 2) {
-          ok = wait(&sh.qfull[w], q_par >> w & 1u);
-          q_par ^= 1u << w;
-        }
-        if (two && w == 1) return ok;
-        ++ktiles;
-        return ok && wait(&sh.kfull[(ktiles - 1) % kRing], ((ktiles - 1) / kRing) & 1);
-      };
-      auto values = [&](auto stream) {
-        if (two && decltype(stream)::value == 1) return true;
-        ++vtiles;
-        return wait(&sh.vfull[(vtiles - 1) % kRing], ((vtiles - 1) / kRing) & 1);
-      };
       auto score = [&](auto stream) {
         constexpr int w = decltype(stream)::value;
         const uint32_t st = (ktiles - 1) % kRing;
@@ -653,41 +635,67 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       };
       using C0 = std::integral_constant<int, 0>;
       using C1 = std::integral_constant<int, 1>;
-      // tile j's sums, and behind them, without a pause, the scores of its stream's next tile. What
-      // the next unit needs beside P is waited for while this one's products run.
+      // Tile j's sums, and behind them, without a pause, the scores of its stream's next tile. What they
+      // need is looked up together, so that it costs one round trip when all of it is there.
       auto unit = [&](auto stream, int j) {
         constexpr int w = decltype(stream)::value;
-        using Other = std::integral_constant<int, 1 - w>;
-        const bool more = j + 2 < jobs;
-        bool ok = wait(&sh.pfull[w][0], p_par >> w & 1u);
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        const bool more = j + 2 < jobs, opens = !two || w == 0, keys = opens && more;
+        if (opens) ++vtiles;
+        if (keys) ++ktiles;
+        const uint32_t vt = vtiles - 1, kt = ktiles - 1, p = p_par >> w & 1u;
+        uint64_t* const p0 = &sh.pfull[w][0];
+        uint64_t* const v = opens ? &sh.vfull[vt % kRing] : p0;
+        uint64_t* const k = keys ? &sh.kfull[kt % kRing] : p0;
+        const uint32_t vp = opens ? (vt / kRing) & 1 : p, kp = keys ? (kt / kRing) & 1 : p;
+        // (Q8: the sums do not wait for keys that are still being widened)
+        bool ok = kQ8 ? ready3(v, vp, v, vp, p0, p) : ready3(v, vp, k, kp, p0, p);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = wait(v, vp) && (kQ8 || wait(k, kp)) && wait(p0, p);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+        }
+        // (all of P, maybe, if this warp is late)
+        uint64_t* const p1 = &sh.pfull[w][1];
+        const bool all = __all_sync(0xffffffffu, ready3(p1, p, p1, p, p1, p));
         sm100::tc_fence_after();
         if (leader) sum(stream, C0{}, j < 2);
         __syncwarp();
-        ok = wait(&sh.pfull[w][1], p_par >> w & 1u);
+        if (!all) {
+          ok = wait(p1, p);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          sm100::tc_fence_after();
+        }
         p_par ^= 1u << w;
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        sm100::tc_fence_after();
         if (leader) {
           sum(stream, C1{}, false);
-          if (!two || w == 1) sm100::mma_commit(&sh.vfree[(vtiles - 1) % kRing]);
+          if (!two || w == 1) sm100::mma_commit(&sh.vfree[vt % kRing]);
           if (!more) sm100::mma_commit(&sh.odone[w]);
-          if (more) score(stream);
+          if (!kQ8 && more) score(stream);
         }
         __syncwarp();
-        ok = j + 1 >= jobs || (values(Other{}) && keys(Other{}, j + 3));
-        return (bool)__all_sync(0xffffffffu, ok);
+        if (kQ8 && more) {
+          if (!__all_sync(0xffffffffu, wait(k, kp))) return false;
+          sm100::tc_fence_after();
+          if (leader) score(stream);
+          __syncwarp();
+        }
+        return true;
       };
-      auto first = [&](auto stream, int j) {
-        const bool ok = keys(stream, j);
+      // a stream's first scores of the run
+      auto first = [&](auto stream) {
+        constexpr int w = decltype(stream)::value;
+        bool ok = wait(&sh.qfull[w], q_par >> w & 1u);
+        q_par ^= 1u << w;
+        if (!two || w == 0) {
+          ++ktiles;
+          ok = ok && wait(&sh.kfull[(ktiles - 1) % kRing], ((ktiles - 1) / kRing) & 1);
+        }
         if (!__all_sync(0xffffffffu, ok)) return false;
         sm100::tc_fence_after();
-        if (leader && j < jobs) score(stream);
+        if (leader) score(stream);
         __syncwarp();
         return true;
       };
-      alive = first(C0{}, 0) && first(C1{}, 1);
-      if (alive) alive = __all_sync(0xffffffffu, values(C0{}) && keys(C0{}, 2));
+      alive = first(C0{}) && (jobs < 2 || first(C1{}));
       for (int j = 0; j < jobs && alive; j += 2)
         alive = unit(C0{}, j) && (j + 1 >= jobs || unit(C1{}, j + 1));
     }
