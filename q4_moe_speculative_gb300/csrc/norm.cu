@@ -191,14 +191,13 @@ cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
   const int64_t need = ((int64_t)a.p.T + rows - 1) / rows, sms = device_sm_count();
   int64_t grid = need;
   if (need > sms) {   // as many CTAs as fit, each with several rows
-    static int fit[33] = {};   // by warps
-    int& n = fit[threads / 32];
+    static std::atomic<int> fit[33] = {};   // by warps
+    int n = fit[threads / 32].load(std::memory_order_relaxed);
     if (n == 0) {
-      int found = 0;
-      const cudaError_t e =
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found, kernel, threads, 0);
+      const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
       if (e != cudaSuccess) return e;
-      n = found > 0 ? found : 1;
+      if (n < 1) n = 1;
+      fit[threads / 32].store(n, std::memory_order_relaxed);
     }
     if (need > sms * n) grid = sms * n;
   }

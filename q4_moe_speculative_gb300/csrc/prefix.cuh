@@ -63,7 +63,7 @@ __device__ __forceinline__ int64_t list_places(const PrefixArgs& a, int lane, in
 // CTAs that share them, three positions or more each: so a CTA between those that begin and end a
 // unit has some of its tiles.
 __device__ __forceinline__ int64_t list_ctas(const PrefixArgs& a, int64_t total) {
-  return total < 3 * (int64_t)a.grid ? (total + 2) / 3 : a.grid;
+  return total < 3 * (int64_t)a.grid ? total / 3 : a.grid;   // (a unit has three at least)
 }
 // The token tile that position x of a unit of w row tiles belongs to: where a CTA begins there, the
 // first it takes; where it ends, the first it leaves.
