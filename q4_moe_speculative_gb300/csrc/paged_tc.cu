@@ -110,6 +110,21 @@ struct alignas(16) TcSmem {   // small arrays in front of the tiles
 constexpr int kSmallBytes = (sizeof(TcSmem) + 1023) / 1024 * 1024;
 static_assert(kSmallBytes <= 10240, "the largest call fills the SM's shared memory");
 
+// Whether three phases are complete: one round trip when they are.
+__device__ __forceinline__ bool ready3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                       uint64_t* c, uint32_t pc) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q, s;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 s, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\tand.pred p, p, s;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(smem_at(a)), "r"(pa), "r"(smem_at(b)), "r"(pb), "r"(smem_at(c)), "r"(pc)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool score_any(bool x) {
   int r;

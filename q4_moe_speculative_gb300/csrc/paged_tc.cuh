@@ -38,21 +38,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) arrive(bar);
 }
-// Whether three phases are complete: one round trip when they are.
-__device__ __forceinline__ bool ready3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
-                                       uint64_t* c, uint32_t pc) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q, s;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 s, [%5], %6;\n\t"
-      "and.pred p, p, q;\n\tand.pred p, p, s;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(smem_at(a)), "r"(pa), "r"(smem_at(b)), "r"(pb), "r"(smem_at(c)), "r"(pc)
-      : "memory");
-  return r != 0;
-}
 // An operand stored with its K (tokens) as rows of 128 bytes of 64 M or N values, 128-byte
 // swizzle: groups of 8 tokens are 1024 bytes apart, the next 64 values `next` bytes further.
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t next) {

@@ -97,6 +97,24 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Whether three phases are complete (bit 0), and a fourth (bit 1): one round trip.
+__device__ __forceinline__ uint32_t ready3_1(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                             uint64_t* c, uint32_t pc, uint64_t* d, uint32_t pd) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q, s, t;\n\t.reg .u32 x;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 s, [%5], %6;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 t, [%7], %8;\n\t"
+      "and.pred p, p, q;\n\tand.pred p, p, s;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "selp.u32 x, 2, 0, t;\n\tor.b32 %0, %0, x;\n\t}"
+      : "=&r"(r)
+      : "r"(smem_at(a)), "r"(pa), "r"(smem_at(b)), "r"(pb), "r"(smem_at(c)), "r"(pc),
+        "r"(smem_at(d)), "r"(pd)
+      : "memory");
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -647,29 +665,35 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         uint64_t* const v = opens ? &sh.vfull[vt % kRing] : p0;
         uint64_t* const k = keys ? &sh.kfull[kt % kRing] : p0;
         const uint32_t vp = opens ? (vt / kRing) & 1 : p, kp = keys ? (kt / kRing) & 1 : p;
+        uint64_t* const p1 = &sh.pfull[w][1];
         // (Q8: the sums do not wait for keys that are still being widened)
-        bool ok = kQ8 ? ready3(v, vp, v, vp, p0, p) : ready3(v, vp, k, kp, p0, p);
-        if (!__all_sync(0xffffffffu, ok)) {
+        const uint32_t found = kQ8 ? ready3_1(v, vp, v, vp, p0, p, p1, p)
+                                   : ready3_1(v, vp, k, kp, p0, p, p1, p);
+        bool ok = __all_sync(0xffffffffu, found & 1u);
+        if (!ok) {
           ok = wait(v, vp) && (kQ8 || wait(k, kp)) && wait(p0, p);
           if (!__all_sync(0xffffffffu, ok)) return false;
         }
-        // (all of P, maybe, if this warp is late)
-        uint64_t* const p1 = &sh.pfull[w][1];
-        const bool all = __all_sync(0xffffffffu, ready3(p1, p, p1, p, p1, p));
-        sm100::tc_fence_after();
-        if (leader) sum(stream, C0{}, j < 2);
-        __syncwarp();
-        if (!all) {
-          ok = wait(p1, p);
-          if (!__all_sync(0xffffffffu, ok)) return false;
-          sm100::tc_fence_after();
-        }
         p_par ^= 1u << w;
-        if (leader) {
+        auto rest = [&] {
           sum(stream, C1{}, false);
           if (!two || w == 1) sm100::mma_commit(&sh.vfree[vt % kRing]);
           if (!more) sm100::mma_commit(&sh.odone[w]);
           if (!kQ8 && more) score(stream);
+        };
+        sm100::tc_fence_after();
+        if (__all_sync(0xffffffffu, found == 3u)) {   // all of P is there: this warp is late
+          if (leader) {
+            sum(stream, C0{}, j < 2);
+            rest();
+          }
+        } else {
+          if (leader) sum(stream, C0{}, j < 2);
+          __syncwarp();
+          ok = wait(p1, p);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          sm100::tc_fence_after();
+          if (leader) rest();
         }
         __syncwarp();
         if (kQ8 && more) {
