@@ -457,10 +457,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
           if (t[e] < kReach) atomicAdd(&sh.lo[Row::bin_of(t[e])], 1u);
       }
     } else {
+      const float limit_l = limit.key ? from_key(limit.key) : kNegInf;
       for (int i = tid; i < n; i += 2 * kThreads) {
         const float l0 = logit(i), l1 = logit(i + kThreads);
         // (those at the limit's key: their number is known, and they are counted once below)
-        const bool in0 = key_of(l0) > limit.key, in1 = key_of(l1) > limit.key;
+        const bool in0 = l0 > limit_l, in1 = l1 > limit_l;
         if (!in0 && !in1) continue;
         unsigned long long u0, u1;
         float2 t;
@@ -482,10 +483,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
 #pragma unroll
     for (int e = 0; e < kMost; ++e) {
       v[e] = 0;
-      if (e < mine && i0 < per)
-        for (int c = 0; c < C; ++c)
-          v[e] += ((unsigned long long)cluster.map_shared_rank(sh.hi, c)[first + i0 + e] << 32) +
-                  cluster.map_shared_rank(sh.lo, c)[first + i0 + e];
+      if (e < mine && i0 < per) {
+        auto from_cta = [&](int c) {
+          return ((unsigned long long)cluster.map_shared_rank(sh.hi, c)[first + i0 + e] << 32) +
+                 cluster.map_shared_rank(sh.lo, c)[first + i0 + e];
+        };
+        if (C == kMaxCluster) {   // (all loads on their way together)
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c) v[e] += from_cta(c);
+        } else {
+          for (int c = 0; c < C; ++c) v[e] += from_cta(c);
+        }
+      }
       sum += v[e];
     }
     unsigned long long upto_mine = block_upto(sum, sh.warp_mass) - sum;
@@ -497,15 +506,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if (tid == kThreads - 1)   // (all of it)
       for (int c = 0; c < C; ++c) *cluster.map_shared_rank(&sh.slice[rank], c) = upto_mine;
     cluster.sync();
-    if (masses) {
-      unsigned long long total = 0;
-      for (int c = 0; c < C; ++c) total += sh.slice[c];
-      target = top_p > 0.f ? share_of(total, top_p) : 1ull;
-    }
+    unsigned long long slice_to[kMaxCluster], total = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) slice_to[c] = total += c < C ? sh.slice[c] : 0ull;
+    if (masses) target = top_p > 0.f ? share_of(total, top_p) : 1ull;
+    if (total < target) return Border{0u, ~0ull};
     unsigned long long start = 0;
     int owner = 0;
-    while (owner < C && start + sh.slice[owner] < target) start += sh.slice[owner++];
-    if (owner == C) return Border{0u, ~0ull};
+#pragma unroll
+    for (int c = 0; c < kMaxCluster - 1; ++c)
+      if (slice_to[c] < target) start = slice_to[c], owner = c + 1;
     const unsigned long long* const upto = cluster.map_shared_rank(sh.upto, owner);
     for (int i = tid; i < per; i += kThreads) {
       const unsigned long long lower = start + (i ? upto[i - 1] : 0);
@@ -673,23 +683,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   if (top_p < 1.f) border = cut(true, 0ull, border, &weighed, &own, &own_ties);
   // ------------------------------------------------------------------ the draw
   // the mass above the border, and the tokens at it, of each warp's stretch
-  const int stretch = (n + kWarps - 1) / kWarps;
+  // (whole rounds of the loop below; the logits' order is their keys')
+  const int stretch = (n + 64 * kWarps - 1) / (64 * kWarps) * 64;
+  const float border_l = border.key ? from_key(border.key) : kNegInf;
   auto weigh = [&] {
     unsigned long long mass = 0, ties = 0;
-    const int end = min(n, (warp + 1) * stretch);
-    for (int i0 = warp * stretch; i0 < end; i0 += 64) {
-      const int i = i0 + lane;
-      const float l0 = i < end ? logit(i) : kNegInf, l1 = i + 32 < end ? logit(i + 32) : kNegInf;
-      const unsigned key0 = key_of(l0), key1 = key_of(l1);
-      const bool in0 = key0 >= least_key, in1 = key1 >= least_key;
-      const bool over0 = in0 && key0 > border.key, over1 = in1 && key1 > border.key;
-      ties += (in0 && key0 == border.key ? 1 : 0) + (in1 && key1 == border.key ? 1 : 0);
+    for (int i = warp * stretch + lane; i < min(n + lane, (warp + 1) * stretch); i += 64) {
+      const float l0 = logit(i), l1 = logit(i + 32);   // (behind the last token: -infinity)
+      const bool in0 = l0 >= least, in1 = l1 >= least;
+      const bool over0 = in0 && l0 > border_l, over1 = in1 && l1 > border_l;
+      ties += (in0 && l0 == border_l ? 1 : 0) + (in1 && l1 == border_l ? 1 : 0);
       if (!__any_sync(0xffffffffu, over0 || over1)) continue;
       unsigned long long u0, u1;
       float2 t;
       row.units2(l0, l1, &u0, &u1, &t);
       mass += (over0 ? u0 : 0ull) + (over1 ? u1 : 0ull);
     }
+    if (!border.key) ties = 0;
     mass = warp_sum(mass);
     ties = warp_sum(ties);
     if (lane == 0) {
@@ -741,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       at += m;
       tied = next;
     }
-    const int begin = w * stretch, end = min(n, begin + stretch);
+    const int begin = min(n, w * stretch), end = min(n, begin + stretch);
     const int per = (stretch + kThreads - 1) / kThreads;
     const int i0 = begin + tid * per, i1 = min(end, i0 + per);
     unsigned long long mass = 0, ties = 0;
