@@ -769,9 +769,10 @@ def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_table: torch.Ten
     lib = N.load()
     own = _paged_args(q, cache, page_table, lengths, scale, out, workspace)
     _cuda_tensor(prefix_table, "prefix_table", 2)
-    P, max_pages = prefix_table.shape
-    _need_on(prefix_table, "prefix_table", torch.int32, (P, max_pages), q.device)
-    _need_on(prefix_lengths, "prefix_lengths", torch.int32, (P,), q.device)
+    shape, dev = prefix_table.shape, q.device
+    P, max_pages = shape
+    _need_on(prefix_table, "prefix_table", torch.int32, shape, dev)
+    _need_on(prefix_lengths, "prefix_lengths", torch.int32, (P,), dev)
     if P == 0 or q.shape[0] % P:
         raise ValueError(f"{q.shape[0]} sequences cannot share {P} prefixes evenly")
     args = N.DsPrefixAttnArgs(own, P, _c_int(max_pages), prefix_table.data_ptr(),
@@ -787,9 +788,11 @@ def _hidden_rows(t: torch.Tensor, name: str, dtype, shape: tuple, dev: torch.dev
     if t.dtype is not dtype or t.shape != shape or t.device != dev:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev} "
                          f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
-    if shape[1] > 1 and t.stride(1) != 1:
+    per_row, per_value = t.stride()
+    T, H = shape
+    if per_value != 1 and H > 1:
         raise ValueError(f"the values of a row of {name} must be contiguous")
-    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8
+    return per_row if T > 1 else -(-H // 8) * 8
 
 
 def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, weight=None, post_weight=None,
@@ -803,45 +806,46 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, weight=None, p
     itself, if that is contiguous and of its type."""
     lib = N.load()
     dev = _cuda_tensor(x, "x", 2)
-    T, H = x.shape
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"x must be bfloat16 or float32 (got {x.dtype})")
-    a = N.DsBlockNormArgs(T, _c_int(H), N.DS_ROWS_FP32 if x.dtype is torch.float32 else N.DS_ROWS_BF16,
-                          eps, weight_offset, x_scale, y_scale, x.data_ptr(),
-                          _hidden_rows(x, "x", x.dtype, (T, H), dev))
-    if y is None:
-        if post_weight is not None or gate is not None or x_out is not None:
-            raise ValueError("post_weight, gate and x_out need a y")
-        if weight is None:
-            raise ValueError("without a y a weight is needed")
-    else:
-        a.y_stride = _hidden_rows(y, "y", torch.bfloat16, (T, H), dev)
-        a.y = y.data_ptr()
+    shape, dt = x.shape, x.dtype
+    T, H = shape
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"x must be bfloat16 or float32 (got {dt})")
+    xs = _hidden_rows(x, "x", dt, shape, dev)
+    y_p, ys, pw_p, gate_p, gs, w_p = None, 0, None, None, 0, None
+    if y is not None:
+        ys, y_p = _hidden_rows(y, "y", torch.bfloat16, shape, dev), y.data_ptr()
+    elif post_weight is not None or gate is not None or x_out is not None:
+        raise ValueError("post_weight, gate and x_out need a y")
+    elif weight is None:
+        raise ValueError("without a y a weight is needed")
     if post_weight is not None:
         _need_on(post_weight, "post_weight", torch.bfloat16, (H,), dev)
-        a.post_weight = post_weight.data_ptr()
+        pw_p = post_weight.data_ptr()
     if gate is not None:
         if isinstance(gate, torch.Tensor) and gate.dim() == 1:
             _need_on(gate, "gate", torch.bfloat16, (H,), dev)
         else:
-            a.gate_stride = _hidden_rows(gate, "gate", torch.bfloat16, (T, H), dev)
-        a.gate = gate.data_ptr()
+            gs = _hidden_rows(gate, "gate", torch.bfloat16, shape, dev)
+        gate_p = gate.data_ptr()
     if weight is not None:
         _need_on(weight, "weight", torch.bfloat16, (H,), dev)
-        a.weight = weight.data_ptr()
+        w_p = weight.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a weight")
     if x_out is not None:
-        _need_on(x_out, "x_out", x.dtype, (T, H), dev)
+        _need_on(x_out, "x_out", dt, shape, dev)
     if h_out is not None:
-        _need_on(h_out, "h_out", torch.bfloat16, (T, H), dev)
+        _need_on(h_out, "h_out", torch.bfloat16, shape, dev)
+    a = N.DsBlockNormArgs(T, _c_int(H), N.DS_ROWS_FP32 if dt is torch.float32 else N.DS_ROWS_BF16,
+                          eps, weight_offset, x_scale, y_scale, x.data_ptr(), xs, y_p, ys, pw_p,
+                          gate_p, gs, w_p)
 
     s, undo = _enter(dev, stream)
     try:
-        if y is not None and x_out is None:
-            x_out = torch.empty((T, H), dtype=x.dtype, device=dev)
-        if weight is not None and h_out is None:
-            h_out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        if y_p is not None and x_out is None:
+            x_out = torch.empty(shape, dtype=dt, device=dev)
+        if w_p is not None and h_out is None:
+            h_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         _check(lib.ds_block_norm(a, _ptr(x_out), _ptr(h_out), s), "ds_block_norm")
     finally:
         if undo:
@@ -863,20 +867,25 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k=0, t
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("the logits of a row must be contiguous")
     _need_on(u, "u", torch.float64, (B,), dev)
-    a = N.DsSampleArgs(B, _c_int(V), N.DS_ROWS_FP32 if logits.dtype is torch.float32
-                       else N.DS_ROWS_BF16, logits.data_ptr(),
-                       logits.stride(0) if B > 1 else V, u.data_ptr())
+    rows, given, each = (B,), [], []
     for name, value in (("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
         if isinstance(value, torch.Tensor):
-            _need_on(value, name, torch.float32, (B,), dev)
-            setattr(a, name + "s", value.data_ptr())
+            _need_on(value, name, torch.float32, rows, dev)
+            given.append(0.0)
+            each.append(value.data_ptr())
         else:
-            setattr(a, name, float(value))
+            given.append(float(value))
+            each.append(None)
     if isinstance(top_k, torch.Tensor):
-        _need_on(top_k, "top_k", torch.int32, (B,), dev)
-        a.top_ks = top_k.data_ptr()
+        _need_on(top_k, "top_k", torch.int32, rows, dev)
+        given.append(0)
+        each.append(top_k.data_ptr())
     else:
-        a.top_k = _c_int(max(0, int(top_k)))
+        given.append(_c_int(max(0, int(top_k))))
+        each.append(None)
+    a = N.DsSampleArgs(B, _c_int(V), N.DS_ROWS_FP32 if logits.dtype is torch.float32
+                       else N.DS_ROWS_BF16, logits.data_ptr(),
+                       logits.stride(0) if B > 1 else V, u.data_ptr(), *given, *each)
     if out is not None:
         _need_on(out, "out", torch.int32, (B,), dev)
     if prob is not None:
