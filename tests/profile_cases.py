@@ -10,6 +10,10 @@
     python tests/profile_cases.py rows     # norms and rotation of 16,384 tokens x 32 + 8 heads,
                                            # then a Q8 cache's write and read of 32,768 x 8 heads
     python tests/profile_cases.py q4       # Q4 projection, 129,280 x 4096, R 6
+    python tests/profile_cases.py prefix   # shared prefix, 64 x 6 rows x 32/8 heads, 8192 tokens, bf16
+    python tests/profile_cases.py prefix_q8   # the same in 8 bits
+    python tests/profile_cases.py norm     # block norm, 16,384 x 4096, bf16, both norms
+    python tests/profile_cases.py sample   # 64 rows of 129,280 logits, top-p 0.9
 
 Each case holds a few GB on the device at most, with weights / keys larger than L2, and
 runs its call `--reps` times (default 4) on synthetic inputs, then checks the workspace
@@ -110,6 +114,33 @@ def run(case: str, reps: int) -> None:
         ws = None
         for _ in range(reps):
             dsm.q4_project(tiles, x)
+    elif case in ("prefix", "prefix_q8"):
+        B, R, Hq, Hkv, n, own = 64, 6, 32, 8, 8192, 64
+        pages = n // 64 + B
+        cache = dsm.PagedCache.zeros(pages, Hkv, 64, 128, q8=case == "prefix_q8", device=dev)
+        slots = torch.arange(pages * 64, dtype=torch.int32, device=dev)
+        dsm.cache_write(cache, *(torch.randn(pages * 64, Hkv, 128, device=dev).bfloat16()
+                                 for _ in range(2)), slots)
+        order = torch.randperm(pages, device=dev).to(torch.int32)
+        table, own_table = order[None, B:].contiguous(), order[:B, None].contiguous()
+        lengths = torch.full((B,), own, dtype=torch.int32, device=dev)
+        lens = torch.full((1,), n, dtype=torch.int32, device=dev)
+        q = torch.randn(B, R, Hq, 128, device=dev).bfloat16()
+        ws = torch.zeros(1 << 27, dtype=torch.uint8, device=dev)
+        for _ in range(reps):
+            dsm.prefix_attention(q, cache, table, lens, own_table, lengths, workspace=ws)
+    elif case == "norm":
+        x, y = (torch.randn(16384, 4096, device=dev).bfloat16() for _ in range(2))
+        w = torch.ones(4096, dtype=torch.bfloat16, device=dev)
+        ws = None
+        for _ in range(reps):
+            dsm.block_norm(x, y, weight=w, post_weight=w)
+    elif case == "sample":
+        z = torch.randn(64, 129280, device=dev) * 2
+        u = torch.rand(64, dtype=torch.float64, device=dev)
+        ws = None
+        for _ in range(reps):
+            dsm.sample(z, u, top_p=0.9)
     else:
         raise SystemExit(f"unknown case {case}")
     torch.cuda.synchronize()
