@@ -75,6 +75,21 @@ def test_block_norm_matches_64_bits(T, H, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(20001, 8), (30003, 64), (19999, 72), (9001, 128), (9003, 136),
+                                 (5001, 256), (2501, 512), (700, 8200), (333, 9000), (309, 12288)])
+def test_more_rows_than_fit_at_once(T, H, dtype):
+    # rows of part of a warp, a warp or a CTA; each walks over several, the last ones beside none
+    x, y = rows(T, H, dtype, 1, 3.0), rows(T, H, seed=2)
+    w, p = vec(H, 3), vec(H, 4)
+    check(x, y, w, p, rows(T, H, seed=6), o=1.0, xs=0.9, ys=0.22)
+    check(x, y, w, None, vec(H, 5))
+    want = dsm.block_norm(x, y, weight=w, post_weight=p)
+    x1, y1 = x.clone(), y.clone()
+    got = dsm.block_norm(x1, y1, weight=w, post_weight=p, x_out=x1, h_out=y1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_strided_rows(dtype):
     T, H = 37, 520
     wide = rows(T, 3 * H, seed=1)
