@@ -305,3 +305,22 @@ def test_a_long_prefix_on_many_heads():
     pick = [0, 17, 47]
     check(q[pick].contiguous(), cache, ptable, plens, table[pick].contiguous(), lengths[pick],
           got=got[pick])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_pages_beyond_32_bits(q8):
+    # the same pages far apart in a cache of more than 2^32 values (8 bits: scales behind 2^26 too)
+    R, Hq, kv, D, page = 3, 16, 8, 128, 64
+    q, cache, ptable, plens, table, lens = problem([700], [90, 5, 64, 0], R, Hq, kv, D, page, q8, seed=7)
+    want = dsm.prefix_attention(q, cache, ptable, plens, table, lens)
+    pages = (1 << 32) // (kv * page * D) + cache.k.shape[0]
+    at = torch.tensor([i if i % 2 else pages - 1 - i for i in range(cache.k.shape[0])], device=DEV)
+    far = []
+    for name in ("k", "v") + (("k_scale", "v_scale") if q8 else ()):
+        t = getattr(cache, name)
+        big = torch.empty((pages, *t.shape[1:]), dtype=t.dtype, device=DEV)
+        big[at] = t
+        far.append(big)
+    move = lambda t: torch.where(t >= 0, at[t.clamp(min=0).long()], -1).to(torch.int32)  # noqa: E731
+    got = dsm.prefix_attention(q, dsm.PagedCache(*far), move(ptable), plens, move(table), lens)
+    assert torch.equal(got, want)
