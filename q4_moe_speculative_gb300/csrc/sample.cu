@@ -3,22 +3,32 @@
 //
 // A row belongs to a cluster of CTAs (up to 8), each of which keeps its part of the logits in shared
 // memory, so that they are read from memory once; what the CTAs have to agree on goes through
-// distributed shared memory.
+// distributed shared memory. Without top-k and top-p every weight is taken once, for its warp's sum;
+// the draw finds the CTA, the warp and the thread that it falls to.
 //
 // Masses are integers: weight exp((l - max) / T) in units of 2^-scale, the scale such that a
 // vocabulary's sum fits 63 bits. Sums of integers do not depend on their order, so the borders and
 // the draw are the same whatever the grid, and no token is drawn beyond its share by rounding. The
-// weights come from fp32 pairs and integers (Row::units), good to 2^-37: fp64 exponentials, which
-// this GPU has few units for, took 1050 us for 64 rows of 129,280 with top-p.
+// weights come from fp32 pairs, a table and integers (Row::units2), good to 2^-35: fp64 exponentials,
+// which this GPU has few units for, took 1050 us for 64 rows of 129,280 with top-p.
 //
 // Where the order is cut (the k-th largest logit; the logit at which the mass before it reaches
 // top_p), the border is found by counts or masses per bin: first 1024 bins of equal width in
-// (max - l) / T, which spread a vocabulary's logits, then the border bin's range of keys (logits as
-// ordered integers) in 1024 bins, until a bin is one key. Of the tokens with the border's logit the
-// lowest ids are kept.
+// (max - l) / T, which spread a vocabulary's logits (with 2048 only one CTA fits an SM), then the
+// border bin's tokens, which one CTA gathers, by their keys (logits as ordered integers) in 1024
+// bins, until a bin is one key. Of the tokens with the border's logit the lowest
+// ids are kept. Up to 512 tokens that top-k keeps are finished by one CTA without further
+// exchanges.
+//
+// Bound by the shared memory's pipe (a table look-up per weight, and an addition to a bin with
+// top-p) and by the exchanges' latency, not by memory. Measured, logits normal with twice unit
+// deviation, in us: 64 rows of 129,280 in fp32 (5 at the copy rate) with temperature alone 33.5, top-k
+// 50 34, top-p 0.9 70, and with min-p 0.02 55; 200 rows of 32,003 in bf16 27; one row of 129,280
+// 11.5, 14.5 with top-k, 28.5 with top-p.
 #include <cooperative_groups.h>
 
 #include <cmath>
+#include <cstring>
 #include <type_traits>
 
 #include "common.cuh"
@@ -36,7 +46,7 @@ constexpr int kBins = 1024;
 constexpr float kReach = 46.f;       // log2: a lighter token has the weight 0
 constexpr float kBinsPerLog2 = kBins / kReach;
 constexpr float kNegInf = -INFINITY;
-constexpr int kRoots = 64;
+constexpr int kRoots = 1024, kRootBits = 10;
 constexpr float kMagic = 12582912.f;   // 1.5 x 2^23: added, it leaves an integer in the lowest bits
 constexpr int kMagicBits = 0x4B400000;
 constexpr int kPad = 4 * kThreads;   // tokens without weight behind a CTA's last one
@@ -47,7 +57,7 @@ struct SampleArgs {
   SampleProblem p;
   int chunk;        // tokens per CTA, a multiple of 8
   int scale;        // log2 of the weight 1
-  unsigned long long root[kRoots];   // 2^(j / kRoots) in units of 2^-46
+  unsigned long long coarse[32], fine[32];   // 2^(j / 32) and 2^(j / 1024) in units of 2^-63
 };
 
 struct Shared {
@@ -68,7 +78,7 @@ struct Shared {
   unsigned long long ties[kMaxCluster];    // and tokens at it
   unsigned long long warp_mass[kWarps];
   unsigned long long warp_ties[kWarps];
-  unsigned long long root[kRoots];
+  unsigned long long root[kRoots];         // 2^(j / kRoots) in units of 2^-63
   unsigned long long above;                // a border found: what is above its bin
   unsigned long long border_ties;
   unsigned border_key;
@@ -96,7 +106,7 @@ __device__ __forceinline__ float from_key(unsigned k) {
 struct Row {
   float top, per_log2, per_log2_low;     // the largest logit; log2(e) / T, in two parts
   int scale;
-  const unsigned long long* root;
+  const unsigned long long* root;        // 2^(j / kRoots) in units of 2^-63
   // (max - l) / T in log2: never rises with l; NaN or beyond kReach: no weight
   __device__ __forceinline__ float reach(float l) const {
     return __fmul_rn(__fsub_rn(top, l), per_log2);
@@ -105,14 +115,15 @@ struct Row {
     return min(kBins - 1, __float_as_int(__fmaf_rn(reach, kBinsPerLog2, kMagic)) - kMagicBits);
   }
   // The weights of two logits: 2^s, s = (l - top) log2(e) / T <= 0 as a pair of fp32 values (the
-  // difference and the product with their rounding errors), off by 2^-45 relative to s. With k =
-  // 64 s rounded, s = k / 64 + r, |r| <= 1 / 128: a root from the table, shifted, times e^y, y =
-  // r log(2), |y| <= 0.0055. e^y - 1 = y + y^2 / 2 + y^3 / 6 + y^4 / 24, the next term being 2^-44: all
-  // but the first are below 2^-16 and take one fp32 value (off by 2^-39); the first goes to an
-  // integer in two parts. Integers from fp32 by adding 1.5 x 2^23.
-  // (where[]: the reach of each, negative)
+  // difference and the product with their rounding errors), off by 2^-41. With k = 1024 s rounded,
+  // s = k / 1024 + r, |r| <= 1 / 2048: a root from the table, shifted, times e^y, y = r log(2), |y| <=
+  // 2^-11.5. e^y - 1 = y + y^2 / 2 + y^3 / 6, the next term being 2^-50, is an integer f in units of
+  // 2^-37. It is formed in fp32, whose rounding at its size, 2^-36, is the largest error; with the
+  // root's upper part (below) and f's own rounding a weight is off by 2^-35 relative.
+  // (where[]: the reach of each, negative; beyond kReach the weight is 0)
   __device__ __forceinline__ void units2(float l0, float l1, unsigned long long* u0,
                                          unsigned long long* u1, float2* where) const {
+    constexpr float kLn2 = 0.693147182f, kBeyond = -kReach - 1.5f;
     const f2 minus = pair(-1.f, -1.f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
     const f2 l = pair(l0, l1), m_top = pair(-top, -top);
     const f2 n = add2(l, m_top), bb = fma2(l, minus, n);     // n + e = l - top
@@ -120,22 +131,18 @@ struct Row {
     const f2 c = pair(per_log2, per_log2), cl = pair(per_log2_low, per_log2_low);
     const f2 t = mul2(n, c);
     const f2 te = fma2(e, c, fma2(n, cl, fma2(n, c, mul2(n, pair(-per_log2, -per_log2)))));
-    const f2 km = fma2(t, pair(64.f, 64.f), magic);
-    const f2 r = fma2(add2(km, unmagic), pair(-1.f / 64, -1.f / 64), t);
-    const f2 ln = pair(kLn2, kLn2);
-    const f2 y = mul2(r, ln);
-    const f2 ye = fma2(te, ln, fma2(r, pair(kLn2Low, kLn2Low), fma2(r, ln, mul2(r, pair(-kLn2, -kLn2)))));
-    f2 q = fma2(y, pair(1.f / 24, 1.f / 24), pair(1.f / 6, 1.f / 6));
-    q = fma2(y, q, pair(0.5f, 0.5f));
-    q = fma2(mul2(y, y), q, ye);
-    // y = m 2^-16 + rest
-    const f2 ym = fma2(y, pair(65536.f, 65536.f), magic);
-    const f2 rest = add2(fma2(add2(ym, unmagic), pair(-1.f / 65536, -1.f / 65536), y), q);
-    const f2 low = fma2(rest, pair(0x1p37f, 0x1p37f), magic);
-    const float2 k2 = parts(km), m2 = parts(ym), low2 = parts(low), t2 = parts(t);
+    const float2 t2 = parts(t);
+    // (what is far below, and NaN, to where the shift leaves nothing of any f)
+    const f2 near = pair(t2.x > -kReach ? t2.x : kBeyond, t2.y > -kReach ? t2.y : kBeyond);
+    const f2 km = fma2(near, pair(1.f * kRoots, 1.f * kRoots), magic);
+    const f2 r = fma2(add2(km, unmagic), pair(-1.f / kRoots, -1.f / kRoots), near);
+    const f2 y = fma2(te, pair(kLn2, kLn2), mul2(r, pair(kLn2, kLn2)));
+    const f2 q = fma2(mul2(y, y), fma2(y, pair(0x1p37f / 6, 0x1p37f / 6), pair(0x1p36f, 0x1p36f)),
+                      mul2(te, pair(kLn2 * 0x1p37f, kLn2 * 0x1p37f)));
+    const float2 f = parts(fma2(r, pair(kLn2 * 0x1p37f, kLn2 * 0x1p37f), q)), k2 = parts(km);
+    *u0 = compose(__float_as_int(k2.x), __float2int_rn(f.x));
+    *u1 = compose(__float_as_int(k2.y), __float2int_rn(f.y));
     *where = t2;
-    *u0 = t2.x > -kReach ? compose(k2.x, m2.x, low2.x) : 0ull;
-    *u1 = t2.y > -kReach ? compose(k2.y, m2.y, low2.y) : 0ull;
   }
   __device__ __forceinline__ unsigned long long units(float l) const {
     unsigned long long u, v;
@@ -147,9 +154,9 @@ struct Row {
   // before it is shifted, and the total, as fp32 pairs; the quotient and its remainder's.
   __device__ __forceinline__ float share(float l, unsigned long long total) const {
     const float t = __fmul_rn(__fsub_rn(l, top), per_log2);
-    const int k = __float_as_int(__fmaf_rn(t, 64.f, kMagic)) - kMagicBits;
+    const int k = __float_as_int(__fmaf_rn(t, 1.f * kRoots, kMagic)) - kMagicBits;
     Row wide = *this;
-    wide.scale = 45 - (k >> 6);   // (the shift of compose() is 1)
+    wide.scale = 45 - (k >> kRootBits);   // (the root is shifted by 18)
     const unsigned long long w = wide.units(l);
     auto high = [](unsigned long long x) { return __ull2float_rn(x); };
     auto low = [](unsigned long long x, float h) {
@@ -160,16 +167,15 @@ struct Row {
     const float r = __fadd_rn(__fmaf_rn(-q, th, wh), __fmaf_rn(-q, tl, wl));
     return scalbnf(__fadd_rn(q, __fdiv_rn(r, th)), scale - wide.scale);
   }
-  // Root k mod 64 times (1 + (low + m 2^21) 2^-37), shifted by k / 64.
-  __device__ __forceinline__ unsigned long long compose(float k_magic, float m_magic,
-                                                        float low_magic) const {
-    const int k = __float_as_int(k_magic) - kMagicBits;
-    const int f = __float_as_int(low_magic) - kMagicBits + ((__float_as_int(m_magic) - kMagicBits) << 21);
-    const unsigned long long z = root[k & (kRoots - 1)];
-    const long long w = (long long)z + (((long long)f * (int)(z >> 17)) >> 20);   // units of 2^-46
-    return (((unsigned long long)w >> (45 - scale - (k >> 6))) + 1) >> 1;
+  // Root k mod 1024 times 1 + f 2^-37, shifted by k / 1024 (k behind the magic number's bits, whose
+  // lowest ten are 0). The product takes the root's upper 27 bits: off by 2^-26 of f.
+  __device__ __forceinline__ unsigned long long compose(int k_bits, int f) const {
+    const unsigned long long z = root[k_bits & (kRoots - 1)];
+    unsigned long long w = z + (unsigned long long)((long long)f * (int)(z >> 37));
+    const int shift = 62 + (kMagicBits >> kRootBits) - scale - (k_bits >> kRootBits);
+    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(w), "r"(shift));   // (64 and more: 0)
+    return (w + 1) >> 1;
   }
-  static constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;   // log(2) in two parts
 };
 
 // Where the order is cut: tokens with a larger key are kept, and `ties` of those with this one.
@@ -241,7 +247,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int b = blockIdx.x / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int v0 = min(p.V, rank * a.chunk), n = min(p.V, v0 + a.chunk) - v0;
-  if (tid < kRoots) sh.root[tid] = a.root[tid];
+  for (int i = tid; i < kRoots; i += kThreads) {
+    const unsigned long long c = a.coarse[i >> 5], f = a.fine[i & 31];
+    sh.root[i] = __umul64hi(c, f) << 1 | c * f >> 63;
+  }
   pdl_wait();
   // ------------------------------------------------------------------ the row's settings
   float T = p.temperatures ? p.temperatures[b] : p.temperature;
@@ -438,6 +447,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       __syncthreads();   // (sh.bin and the bins may be overwritten)
     }
   };
+  // Sums over the CTA's threads, for the last one.
+  auto sum_up = [&](unsigned long long mass, unsigned long long ties, unsigned long long* own,
+                    unsigned long long* own_ties) {
+    mass = warp_sum(mass);
+    ties = warp_sum(ties);
+    __syncthreads();
+    if (lane == 0) sh.warp_mass[warp] = mass, sh.warp_ties[warp] = ties;
+    __syncthreads();
+    if (warp < kWarps - 1) return;
+    *own = warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0ull);
+    *own_ties = warp_sum(lane < kWarps ? sh.warp_ties[lane] : 0ull);
+  };
   // The border at which, from above, the count reaches `target`, or the mass top_p of what `limit`
   // keeps; key 0 where there is not as much, or where min-p cuts before. *own: this CTA's mass above
   // the border and its tokens at it, if *weighed. All threads of the cluster together.
@@ -458,16 +479,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       }
     } else {
       const float limit_l = limit.key ? from_key(limit.key) : kNegInf;
-      for (int i = tid; i < n; i += 2 * kThreads) {
-        const float l0 = logit(i), l1 = logit(i + kThreads);
-        // (those at the limit's key: their number is known, and they are counted once below)
-        const bool in0 = l0 > limit_l, in1 = l1 > limit_l;
-        if (!in0 && !in1) continue;
-        unsigned long long u0, u1;
-        float2 t;
-        row.units2(l0, l1, &u0, &u1, &t);
-        if (in0 && t.x > -kReach) bin_add(sh, Row::bin_of(-t.x), u0);
-        if (in1 && t.y > -kReach) bin_add(sh, Row::bin_of(-t.y), u1);
+      for (int i = tid; i < n; i += 4 * kThreads) {
+        float l[4];
+        bool in[4], any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          l[e] = logit(i + e * kThreads);
+          // (those at the limit's key: their number is known, and they are counted once below)
+          in[e] = l[e] > limit_l;
+          any |= in[e];
+        }
+        if (!any) continue;
+        unsigned long long u[4];
+        float2 t[2];
+        row.units2(l[0], l[1], &u[0], &u[1], &t[0]);
+        row.units2(l[2], l[3], &u[2], &u[3], &t[1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float reach = e & 1 ? t[e / 2].y : t[e / 2].x;
+          if (in[e] && reach > -kReach) bin_add(sh, Row::bin_of(-reach), u[e]);
+        }
       }
     }
     if (rank == 0 && tid == 0 && limit.key) {
@@ -564,8 +595,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       if (at < kGathered) keys[at] = key_of(l);
     });
     if (min_p_cuts) {
-      *own = block_upto(part, sh.warp_mass);   // (the last thread has all of it)
-      *own_ties = 0;
+      sum_up(part, 0ull, own, own_ties);
       return Border{0u, ~0ull};
     }
     cluster.sync();
@@ -613,8 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
         if (key > found.key) part += row.units(from_key(key));
         else if (key == found.key) ++ties;
       });
-      *own = block_upto(part, sh.warp_mass);   // (the last thread has all of it)
-      *own_ties = block_upto(ties, sh.warp_ties);
+      sum_up(part, ties, own, own_ties);
     }
     return found;
   };
@@ -684,21 +713,63 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   // ------------------------------------------------------------------ the draw
   // the mass above the border, and the tokens at it, of each warp's stretch
   // (whole rounds of the loop below; the logits' order is their keys')
-  const int stretch = (n + 64 * kWarps - 1) / (64 * kWarps) * 64;
+  constexpr int kRound = 128;
+  static_assert(kRound * kWarps <= kGathered, "a round per warp in sh.keys");
+  const int stretch = (n + kRound * kWarps - 1) / (kRound * kWarps) * kRound;
   const float border_l = border.key ? from_key(border.key) : kNegInf;
   auto weigh = [&] {
     unsigned long long mass = 0, ties = 0;
-    for (int i = warp * stretch + lane; i < min(n + lane, (warp + 1) * stretch); i += 64) {
-      const float l0 = logit(i), l1 = logit(i + 32);   // (behind the last token: -infinity)
-      const bool in0 = l0 >= least, in1 = l1 >= least;
-      const bool over0 = in0 && l0 > border_l, over1 = in1 && l1 > border_l;
-      ties += (in0 && l0 == border_l ? 1 : 0) + (in1 && l1 == border_l ? 1 : 0);
-      if (!__any_sync(0xffffffffu, over0 || over1)) continue;
+    // where few of a round's tokens are above the border, they wait in shared memory until 64 are there
+    float* const room = reinterpret_cast<float*>(sh.keys) + warp * kRound;
+    int held = 0, taken = 0;
+    const bool all = !border.key && least == kNegInf;
+    auto add = [&](float l0, float l1) {
       unsigned long long u0, u1;
       float2 t;
       row.units2(l0, l1, &u0, &u1, &t);
-      mass += (over0 ? u0 : 0ull) + (over1 ? u1 : 0ull);
+      mass += u0 + u1;
+    };
+    for (int i = warp * stretch + lane; i < min(n + lane, (warp + 1) * stretch); i += kRound) {
+      float l[4];   // (behind the last token: -infinity, which has no weight)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) l[e] = logit(i + 32 * e);
+      if (all) {
+        add(l[0], l[1]);
+        add(l[2], l[3]);
+        continue;
+      }
+      unsigned over[4];
+      int count = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = l[e] >= least;
+        ties += in && l[e] == border_l ? 1 : 0;
+        over[e] = __ballot_sync(0xffffffffu, in && l[e] > border_l);
+        count += __popc(over[e]);
+      }
+      if (count > kRound / 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[e] = over[e] >> lane & 1u ? l[e] : kNegInf;
+        add(l[0], l[1]);
+        add(l[2], l[3]);
+      } else if (count) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (over[e] >> lane & 1u)
+            room[(held + __popc(over[e] & ((1u << lane) - 1u))) & (kRound - 1)] = l[e];
+          held += __popc(over[e]);
+        }
+        __syncwarp();
+        if (held - taken >= kRound / 2) {
+          add(room[(taken + lane) & (kRound - 1)], room[(taken + 32 + lane) & (kRound - 1)]);
+          taken += kRound / 2;
+          __syncwarp();
+        }
+      }
     }
+    if (held > taken)
+      add(taken + lane < held ? room[(taken + lane) & (kRound - 1)] : kNegInf,
+          taken + 32 + lane < held ? room[(taken + 32 + lane) & (kRound - 1)] : kNegInf);
     if (!border.key) ties = 0;
     mass = warp_sum(mass);
     ties = warp_sum(ties);
@@ -710,12 +781,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   };
   if (!weighed) {
     weigh();
-    if (tid == kThreads - 1) {
-      own = own_ties = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        own += sh.warp_mass[w];
-        own_ties += sh.warp_ties[w];
-      }
+    if (warp == kWarps - 1) {
+      own = warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0ull);
+      own_ties = warp_sum(lane < kWarps ? sh.warp_ties[lane] : 0ull);
     }
   }
   if (tid == kThreads - 1)
@@ -725,18 +793,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     }
   cluster.sync();
   const unsigned long long each = border.key ? row.units(from_key(border.key)) : 0ull;
-  unsigned long long total = 0, mine = 0, start = 0, ties_start = 0, ties_upto = 0;
-  for (int c = 0; c < C; ++c) {
-    const unsigned long long first = min(ties_upto, border.ties);
-    ties_upto += sh.ties[c];
-    const unsigned long long kept = min(ties_upto, border.ties) - first;
-    if (c == rank) {
-      start = total;
-      ties_start = ties_upto - sh.ties[c];
-      mine = sh.mass[c] + kept * each;
-    }
-    total += sh.mass[c] + kept * each;
-  }
+  // (a lane per CTA of the cluster)
+  const unsigned long long tied_here = lane < C ? sh.ties[lane] : 0ull;
+  const unsigned long long ties_upto = warp_upto(tied_here, lane);
+  const unsigned long long kept =
+      min(ties_upto, border.ties) - min(ties_upto - tied_here, border.ties);
+  const unsigned long long mass_here = (lane < C ? sh.mass[lane] : 0ull) + kept * each;
+  const unsigned long long mass_upto = warp_upto(mass_here, lane);
+  const unsigned long long total = __shfl_sync(0xffffffffu, mass_upto, 31);
+  const unsigned long long mine = __shfl_sync(0xffffffffu, mass_here, rank);
+  const unsigned long long start = __shfl_sync(0xffffffffu, mass_upto, rank) - mine;
+  const unsigned long long ties_start = __shfl_sync(0xffffffffu, ties_upto - tied_here, rank);
   const unsigned long long target = place_of(total);   // drawn: the first beyond it
   if (target >= start && target < start + mine) {   // (one CTA of the cluster)
     // the warp's stretch that crosses it, and the same again inside that stretch
@@ -791,12 +858,26 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   int bits = 0;
   while ((1 << bits) < p.V) ++bits;
   a.scale = 62 - bits < 45 ? 62 - bits : 45;
+  // CTAs per row: as many as give each 16k tokens, so that two fit an SM (64 rows of 129,280: eight
+  // 33.5 us, four 37 to 42, two 46), and for few rows more, down to 1024 tokens (one row of 32,003:
+  // eight 9 us, two 14; one of 129,280 eight 11.5, one 80). Where the rows fill the GPU, more only
+  // add exchanges: 512 rows of 4000 with one 22 us, with two 33; 200 of 32,003 with two 27, four 39.
   int C = 1;
   while (C < kMaxCluster && p.V > 16384 * C) C *= 2;
   while (C < kMaxCluster && p.V > 1024 * C && (int64_t)p.B * C < 2 * device_sm_count()) C *= 2;
   a.chunk = ((p.V + C - 1) / C + 7) / 8 * 8;
-  for (int j = 0; j < kRoots; ++j)
-    a.root[j] = (unsigned long long)std::llrint(std::exp2(46.0 + j / (double)kRoots));
+  struct Roots {
+    unsigned long long coarse[32], fine[32];
+    Roots() {
+      for (int j = 0; j < 32; ++j) {
+        coarse[j] = (unsigned long long)std::exp2(63.0 + j / 32.0);
+        fine[j] = (unsigned long long)std::exp2(63.0 + j / 1024.0);
+      }
+    }
+  };
+  static const Roots roots;
+  std::memcpy(a.coarse, roots.coarse, sizeof a.coarse);
+  std::memcpy(a.fine, roots.fine, sizeof a.fine);
   const int room = 160 * 1024, stage = (a.chunk + 8 + kPad) * 4;
   const bool staged = stage <= room;
   const auto kernel = p.bf16 ? (staged ? k_sample<true, true> : k_sample<true, false>)

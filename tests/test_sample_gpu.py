@@ -178,6 +178,26 @@ def test_strided_rows_and_other_outputs():
     assert torch.equal(shifted[0], want[0]) and torch.equal(shifted[1], want[1])
 
 
+@pytest.mark.parametrize("T", [1.0, 0.7, 1.9, 0.013])
+def test_weights_are_as_close_as_they_are_said_to_be(T):
+    # two tokens: the lighter one, of lower id, is drawn just below its share and not just above. The
+    # heavier's weight is exact, the lighter's off by 2^-35 and half a unit (2^-46, against 2^-9 or
+    # more), and the draw's place is rounded down to a unit: below 2^-34 of the share together
+    g = torch.Generator()
+    g.manual_seed(5)
+    t32 = float(np.float32(T))
+    diff = torch.rand(2000, generator=g).double() * 6.2 * t32
+    top = torch.randn(2000, generator=g) * 3
+    z = torch.stack([(top.double() - diff).float(), top], 1).to(DEV)
+    d = (z[:, 0].double() - z[:, 1].double()).cpu().numpy().astype(np.longdouble)
+    w = np.exp(d / np.longdouble(t32))
+    share = (w / (1 + w)).astype(np.float64)     # (rounded by 2^-54 of 1, below 2^-43 of it)
+    for side, token in ((1 - 2.0 ** -34, 0), (1 + 2.0 ** -34, 1)):
+        u = torch.from_numpy(share * side).to(DEV)
+        got, _ = dsm.sample(z, u, temperature=T)
+        assert bool((got == token).all())
+
+
 def test_frequencies_follow_the_distribution():
     # 200,000 draws of one row: each token's count within 6 standard deviations
     z = torch.randn(200, generator=torch.Generator().manual_seed(6)) * 1.5
