@@ -4,7 +4,9 @@
 // Three kernels. The sequences' own tokens go through the kernels of the paged attention, which leave
 // their maxima, normalisers and sums in the workspace (paged_attn.cu). k_prefix_tc (prefix_tc.cu) does
 // the same for the rows of all of a prefix's sequences together over its tokens. k_prefix_join
-// merges both per row, in a fixed order.
+// merges both per row, in a fixed order. The second starts as the first's CTAs leave, the third as the
+// second's do. Measured: 64 sequences x 6 rows, 32 heads on 8, after 16k tokens 133 us, of which the
+// second 105; after 128 tokens 30 (14, 8 and 8); 16 x 1 rows, 16 heads on one, after 100k 38 us.
 #include "prefix.cuh"
 
 namespace dsmoe {
@@ -14,8 +16,8 @@ using namespace prefix;
 
 // k_prefix_join: kWarps warps per row of the result (one head of one new token); with 1, a row for
 // each of 8 warps. 32 pieces at a time: a lane looks one up, and the warp adds up those there are,
-// four at a time, each lane D / 32 of the values. Its time is latency: with several pieces per row, 8
-// warps.
+// four at a time, each lane D / 32 of the values. Its time is latency (8 us for 12,288 rows of 4
+// pieces, which are in L2): with many pieces per row, 8 warps.
 template <int D, int kWarps>
 __global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ PrefixArgs a) {
   constexpr int V = D / 32;
