@@ -6,7 +6,7 @@
 // the same for the rows of all of a prefix's sequences together over its tokens. k_prefix_join
 // merges both per row, in a fixed order. The second starts as the first's CTAs leave, the third as the
 // second's do. Measured: 64 sequences x 6 rows, 32 heads on 8, after 16k tokens 133 us, of which the
-// second 105; after 128 tokens 30 (14, 8 and 8); 16 x 1 rows, 16 heads on one, after 100k 38 us.
+// second 105; after 128 tokens 30 (14, 8 and 8); 16 x 1 rows, 16 heads on one, after 100k 34 us.
 #include "prefix.cuh"
 
 namespace dsmoe {
@@ -17,21 +17,23 @@ using namespace prefix;
 // k_prefix_join: kWarps warps per row of the result (one head of one new token); with 1, a row for
 // each of 8 warps. 32 pieces at a time: a lane looks one up, and the warp adds up those there are,
 // four at a time, each lane D / 32 of the values. Its time is latency (8 us for 12,288 rows of 4
-// pieces, which are in L2): with many pieces per row, 8 warps.
+// pieces, which are in L2): where rows are few and pieces many, 8 warps, with registers for what they
+// have on their way (56; with 32 the 100k tokens below took 38 instead of 34 us).
 template <int D, int kWarps>
-__global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(256, kWarps == 1 ? 6 : 4) k_prefix_join(const __grid_constant__ PrefixArgs a) {
   constexpr int V = D / 32;
   __shared__ float acc_s[kWarps][D];
   __shared__ float2 l_s[kWarps];
   const PagedArgs& o = a.own;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
   const int64_t row64 = kWarps > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
   if (row64 >= (int64_t)o.B * o.R * o.Hq) return;
   const unsigned row = (unsigned)row64;   // (4096 sequences x 128 rows x 256 heads: below 2^32)
   const unsigned hq = row % o.Hq, br = row / o.Hq, h = hq / o.G;
   const unsigned b = br / o.R, m = br % o.R * o.G + hq % o.G;
   uint16_t* const dst = o.out + row64 * D + V * lane;
+  // (what the caller gives is there already: the kernels before began their dependents after
+  // their own wait, or wait for nothing that these two read)
   const int own_len = o.lengths[b];
 
   // the pieces of the prefix: of the CTAs that share the row's unit, one or two (its streams) of each
@@ -39,13 +41,15 @@ __global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ Pre
   const int w = unit_tiles(a, u), subs = w == 2 ? 1 : 2;
   const int sub0 = w == 2 ? mp / kRows % 2 : 0;
   const int unit = (p * o.c.heads + h) * a.units + u;
+  const int prefix_tokens = prefix_len(a, p);
+  pdl_wait();
   const int2 first = __ldcg(reinterpret_cast<const int2*>(a.span) + unit);
   // and those of its own tokens
   const unsigned bh = b * o.c.heads + h;
   const int2 span = __ldcg(reinterpret_cast<const int2*>(o.span) + bh);
   const bool absent = own_len < 0;
   // (spans that were not noted: the kernel gave up, and the status says so)
-  const bool has_prefix = !absent && prefix_len(a, p) > 0 && first.x >= 0 && first.y >= first.x &&
+  const bool has_prefix = !absent && prefix_tokens > 0 && first.x >= 0 && first.y >= first.x &&
                           first.y < a.grid;
   const bool has_own = own_len > 0 && span.x >= 0 && span.y >= span.x && span.y < o.grid;
   const int n_prefix = has_prefix ? (first.y - first.x + 1) * subs : 0;
@@ -174,10 +178,12 @@ Plan make_plan(const PrefixAttnProblem& p, PrefixArgs* a) {
 template <int D>
 cudaError_t join(const PrefixArgs& a, int64_t units, cudaStream_t s) {
   const int64_t rows = (int64_t)a.own.B * a.own.R * a.own.Hq;
-  // Eight warps when a unit has many pieces, at least 12 (CTAs that share it). With 152 (100k tokens for
-  // 16 rows of a head) 38 us against 76 with one warp, with 19 (192 rows of 8 heads) 28.9 against
-  // 30.8; with 9.5 (384 rows of 8 heads) 38.9 against 35.0, with 4 48.9 against 36.3.
-  if (a.grid >= 12 * units)
+  // Eight warps where rows are few and their pieces many: at least 12 CTAs that share a unit, and at
+  // most 12 rows per SM. With 152 CTAs (100k tokens for 16 rows of a head) 34 us against 76 with one
+  // warp, with 19 and 512 rows of the result 21.5 against 32, with 1536 rows 29.8 against 30.8; with
+  // 19 and 1920 rows 32.0 against 31.6, with 12.7 and 3072 39.6 against 33.4, with 9.5 38.9
+  // against 35.0.
+  if (a.grid >= 12 * units && rows <= 12 * a.grid)
     return launch_pdl(k_prefix_join<D, 8>, dim3((unsigned)rows), 256, 0, s, a);
   return launch_pdl(k_prefix_join<D, 1>, dim3((unsigned)((rows + 7) / 8)), 256, 0, s, a);
 }
