@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(256, kWarps == 1 ? 6 : 4) k_prefix_join(const 
     const float* from = a.part_o;
     if (i < n_prefix) {
       const int c = first.x + (subs == 2 ? i >> 1 : i), sub = subs == 2 ? i & 1 : sub0;
-      const int64_t at = ((int64_t)(unit + c) * 2 + sub) * kRows + mp % kRows;
+      const int64_t at = ((int64_t)(unit + c) * 2 + sub) * a.rows + mp % kRows;
       ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
       from = a.part_o + at * D;
     } else if (i < n_all) {
@@ -158,6 +158,7 @@ Plan make_plan(const PrefixAttnProblem& p, PrefixArgs* a) {
   a->MP = a->per * M;
   a->tiles = (a->MP + kRows - 1) / kRows;
   a->units = (a->tiles + 1) / 2;
+  a->rows = a->MP < kRows ? a->MP : kRows;
   a->m_inverse = (uint32_t)((((uint64_t)1 << 32) + M - 1) / M);
   a->max_pages = p.max_pages;
   const int64_t cap = ((int64_t)p.max_pages << p.own.cache.page_shift), T = (cap + kTok - 1) / kTok;
@@ -170,8 +171,8 @@ Plan make_plan(const PrefixAttnProblem& p, PrefixArgs* a) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   pl.span = up(pieces_workspace(p.own));
   pl.ml = pl.span + up((size_t)heads * a->units * 2 * sizeof(int));
-  pl.po = pl.ml + up((size_t)pl.pieces * 2 * kRows * 2 * sizeof(float));
-  pl.total = pl.po + up((size_t)pl.pieces * 2 * kRows * p.own.D * sizeof(float));
+  pl.po = pl.ml + up((size_t)pl.pieces * 2 * a->rows * 2 * sizeof(float));
+  pl.total = pl.po + up((size_t)pl.pieces * 2 * a->rows * p.own.D * sizeof(float));
   return pl;
 }
 

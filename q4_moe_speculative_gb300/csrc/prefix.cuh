@@ -26,13 +26,14 @@ struct PrefixArgs {
   int MP;               // query rows of a prefix per key head
   uint32_t m_inverse;   // 2^32 / own.M, rounded up (M = 1: 0, for 2^32)
   int tiles, units;     // row tiles and units of a prefix per key head
+  int rows;             // of a piece: 128, or MP
   int max_pages;        // of a prefix
   const int32_t* table;
   const int32_t* lengths;
   int grid;
   int* span;            // [units of all][2]: the CTAs that begin and end a unit
-  float* part_o;        // [units of all + grid][2][128][D]
-  float* part_ml;       // [units of all + grid][2][128][2]
+  float* part_o;        // [units of all + grid][2][rows][D]
+  float* part_ml;       // [units of all + grid][2][rows][2]
 };
 
 __device__ __forceinline__ int prefix_len(const PrefixArgs& a, int p) {

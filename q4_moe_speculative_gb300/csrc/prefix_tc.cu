@@ -428,8 +428,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         together(true);
         const float other = sh.top[jobs & 1][w][half ^ 1][mine];
         norm = half ? __fadd_rn(other, norm) : __fadd_rn(norm, other);
-        const int64_t at = (unit_piece(a, run.p, run.h, run.u, blockIdx.x) * 2 + w) * kRows + mine;
-        if (half == 0)
+        const int64_t at = (unit_piece(a, run.p, run.h, run.u, blockIdx.x) * 2 + w) * a.rows + mine;
+        if (half == 0 && row0 + mine < a.MP)
           *reinterpret_cast<float2*>(a.part_ml + 2 * at) =
               make_float2(norm == 0.f ? kNegInf : __fmul_rn(ref, fk), norm);
         if (count > 0) {

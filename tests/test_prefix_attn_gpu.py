@@ -278,6 +278,21 @@ def test_workspace_contents_streams_and_repeats():
         dsm.prefix_attention(*p, workspace=ws[:4096])
 
 
+@pytest.mark.parametrize("prefixes,per,R,Hq,D", [(300, 1, 1, 2, 64), (40, 3, 2, 4, 128),
+                                                 (3, 33, 1, 8, 128), (2, 40, 2, 16, 64)])
+def test_workspace_of_exactly_the_size(prefixes, per, R, Hq, D):
+    p = problem([1 + 37 * i % 150 for i in range(prefixes)], [3 + i % 5 for i in range(prefixes * per)],
+                R, Hq, 2, D, 16, False, seed=21)
+    q, cache, ptable, plens, table, lengths = p
+    lib, args = dsm.N.load(), dsm._paged_args(q, cache, table, lengths, None, None, None)
+    args = dsm.N.DsPrefixAttnArgs(args, prefixes, ptable.shape[1], ptable.data_ptr(), plens.data_ptr())
+    need = lib.ds_prefix_attn_workspace_size(args)
+    ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
+    got = check(*p, got=dsm.prefix_attention(*p, workspace=ws[:need]))
+    assert bool((ws[need:] == 0x5A).all())
+    assert torch.equal(got, dsm.prefix_attention(*p))
+
+
 def test_captured_replays_with_other_lengths():
     q, cache, ptable, plens, table, lengths = problem([600, 600], [50] * 6, 2, 8, 2, 128, 32, False,
                                                       seed=15)

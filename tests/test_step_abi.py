@@ -62,6 +62,12 @@ def test_prefix_workspace(lib):  # noqa: F811
     assert f(none, None, None, 0, None) == 0
 
 
+def test_prefix_workspace_of_many_prefixes(lib):  # noqa: F811
+    # sums of one row of each of 1024 x 8 heads, not of whole tiles of 128 rows (1 GB)
+    a = prefix(own=paged(n_seqs=1024, n_rows=1, n_heads=8, cache=cache(n_heads=8)), n_prefixes=1024)
+    assert 0 < lib.ds_prefix_attn_workspace_size(a) < 32 << 20
+
+
 # ------------------------------------------------------------------------------ block norm
 def norm(**kw):
     from q4_moe_speculative_gb300 import _native as N
