@@ -20,8 +20,8 @@
 // ids are kept. Up to 512 tokens that top-k keeps are finished by one CTA without further
 // exchanges.
 //
-// Bound by the shared memory's pipe (a table look-up per weight, and an addition to a bin with
-// top-p) and by the exchanges' latency, not by memory. Measured, logits normal with twice unit
+// Bound by instruction issue while weights are taken (about 50 per token with its bin, a quarter to a
+// half of the time) and by the latency of what the CTAs exchange before and after, not by memory. Measured, logits normal with twice unit
 // deviation, in us: 64 rows of 129,280 in fp32 (5 at the copy rate) with temperature alone 33.5, top-k
 // 50 34, top-p 0.9 70, and with min-p 0.02 55; 200 rows of 32,003 in bf16 27; one row of 129,280
 // 11.5, 14.5 with top-k, 28.5 with top-p.
