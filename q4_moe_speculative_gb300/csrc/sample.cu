@@ -805,49 +805,78 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const unsigned long long start = __shfl_sync(0xffffffffu, mass_upto, rank) - mine;
   const unsigned long long ties_start = __shfl_sync(0xffffffffu, ties_upto - tied_here, rank);
   const unsigned long long target = place_of(total);   // drawn: the first beyond it
-  if (target >= start && target < start + mine) {   // (one CTA of the cluster)
-    // the warp's stretch that crosses it, and the same again inside that stretch
-    if (weighed) weigh();
-    unsigned long long at = start, tied = ties_start;
-    int w = 0;
-    for (; w < kWarps - 1; ++w) {
-      const unsigned long long next = tied + sh.warp_ties[w];
-      const unsigned long long m =
-          sh.warp_mass[w] + (min(next, border.ties) - min(tied, border.ties)) * each;
-      if (target < at + m) break;
-      at += m;
-      tied = next;
+  if (target < start || target >= start + mine) return;
+  // (one CTA of the cluster) the warp's stretch that crosses it, a lane per warp
+  if (weighed) weigh();
+  const unsigned long long warp_tied = lane < kWarps ? sh.warp_ties[lane] : 0ull;
+  const unsigned long long tied_to = ties_start + warp_upto(warp_tied, lane);
+  const unsigned long long warp_mass =
+      (lane < kWarps ? sh.warp_mass[lane] : 0ull) +
+      (min(tied_to, border.ties) - min(tied_to - warp_tied, border.ties)) * each;
+  const unsigned long long mass_to = start + warp_upto(warp_mass, lane);
+  const int w = __ffs(__ballot_sync(0xffffffffu, target < mass_to)) - 1;   // (there is one)
+  unsigned long long at = __shfl_sync(0xffffffffu, mass_to - warp_mass, w);
+  unsigned long long tied = __shfl_sync(0xffffffffu, tied_to - warp_tied, w);
+  // four neighbouring tokens of a round: their weights above the border, and which are at it
+  auto round_of = [&](int r, unsigned long long (&u)[4], unsigned (&tie)[4]) {
+    float l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      l[e] = logit(w * stretch + r * kRound + 4 * lane + e);
+      const bool in = l[e] >= least;
+      tie[e] = __ballot_sync(0xffffffffu, in && border.key && l[e] == border_l);
+      l[e] = in && l[e] > border_l ? l[e] : kNegInf;
     }
-    const int begin = min(n, w * stretch), end = min(n, begin + stretch);
-    const int per = (stretch + kThreads - 1) / kThreads;
-    const int i0 = begin + tid * per, i1 = min(end, i0 + per);
-    unsigned long long mass = 0, ties = 0;
-    for (int i = i0; i < i1; ++i) {
-      const float l = logit(i);
-      const unsigned key = key_of(l);
-      if (key < least_key) continue;
-      if (key > border.key) mass += row.units(l);
-      else if (key == border.key) ++ties;
-    }
-    const unsigned long long ties_to = tied + block_upto(ties, sh.warp_ties);
-    const unsigned long long ties_from = ties_to - ties;
-    mass += (min(ties_to, border.ties) - min(ties_from, border.ties)) * each;
-    const unsigned long long to = at + block_upto(mass, sh.warp_mass), begins = to - mass;
-    if (target >= begins && target < to) {
-      unsigned long long sum = begins, place = ties_from;
-      for (int i = i0; i < i1; ++i) {
-        const float l = logit(i);
-        const unsigned key = key_of(l);
-        if (key < least_key) continue;
-        if (key > border.key || (key == border.key && place++ < border.ties)) sum += row.units(l);
-        if (sum > target) {
-          p.out[b] = v0 + i;
-          if (p.prob) p.prob[b] = row.share(l, total);
-          break;
-        }
-      }
+    float2 where;
+    row.units2(l[0], l[1], &u[0], &u[1], &where);
+    row.units2(l[2], l[3], &u[2], &u[3], &where);
+  };
+  // its rounds (1024 at most: 2^24 tokens in 8 CTAs of 16 warps)
+  const int rounds = stretch / kRound;
+  for (int r = warp; r < rounds; r += kWarps) {
+    unsigned long long u[4];
+    unsigned tie[4];
+    round_of(r, u, tie);
+    const unsigned long long mass = warp_sum(u[0] + u[1] + u[2] + u[3]);
+    if (lane == 0) {
+      sh.upto[r] = mass;
+      sh.lo[r] = __popc(tie[0]) + __popc(tie[1]) + __popc(tie[2]) + __popc(tie[3]);
     }
   }
+  __syncthreads();
+  if (warp) return;
+  int r = 0;
+  for (int r0 = 0; r0 < rounds; r0 += 32) {
+    const bool there = r0 + lane < rounds;
+    const unsigned long long t = there ? sh.lo[r0 + lane] : 0u, t_to = tied + warp_upto(t, lane);
+    const unsigned long long m = (there ? sh.upto[r0 + lane] : 0ull) +
+                                 (min(t_to, border.ties) - min(t_to - t, border.ties)) * each;
+    const unsigned long long m_to = at + warp_upto(m, lane);
+    const unsigned found = __ballot_sync(0xffffffffu, target < m_to);
+    const int last = found ? __ffs(found) - 1 : 31;
+    r = r0 + last;
+    at = __shfl_sync(0xffffffffu, found ? m_to - m : m_to, last);
+    tied = __shfl_sync(0xffffffffu, found ? t_to - t : t_to, last);
+    if (found) break;
+  }
+  // and its tokens
+  unsigned long long of[4], sum = 0;
+  unsigned tie[4];
+  round_of(r, of, tie);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) tied += __popc(tie[e] & ((1u << lane) - 1u));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((tie[e] >> lane & 1u) && tied++ < border.ties) of[e] = each;
+    sum += of[e];
+  }
+  unsigned long long from_lane = at + warp_upto(sum, lane) - sum;
+  if (target < from_lane || target >= from_lane + sum) return;   // (one lane)
+  int e = 0;
+  while (e < 3 && target >= from_lane + of[e]) from_lane += of[e++];
+  const int i = w * stretch + r * kRound + 4 * lane + e;
+  p.out[b] = v0 + i;
+  if (p.prob) p.prob[b] = row.share(logit(i), total);
 }
 
 }  // namespace
