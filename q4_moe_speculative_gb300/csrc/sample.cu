@@ -21,10 +21,10 @@
 // exchanges.
 //
 // Bound by instruction issue while weights are taken (about 50 per token with its bin, a quarter to a
-// half of the time) and by the latency of what the CTAs exchange before and after, not by memory. Measured, logits normal with twice unit
-// deviation, in us: 64 rows of 129,280 in fp32 (5 at the copy rate) with temperature alone 33.5, top-k
-// 50 34, top-p 0.9 70, and with min-p 0.02 55; 200 rows of 32,003 in bf16 27; one row of 129,280
-// 11.5, 14.5 with top-k, 28.5 with top-p.
+// half of the time) and by the latency of what the CTAs exchange before and after, not by memory.
+// Measured, logits normal with twice unit deviation, in us: 64 rows of 129,280 in fp32 (5 at the copy
+// rate) with temperature alone 31, top-k 50 32, top-p 0.9 69, and with min-p 0.02 54; 200 rows of
+// 32,003 in bf16 25; one row of 129,280 11, 13 with top-k 50, 28 with top-p.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -88,8 +88,7 @@ struct Shared {
   float least;
   int bin, listed, gathered;
   unsigned long long inside;               // with a border found: what is in its bin and above
-  unsigned sorted[kFew];                   // and with units: the keys and ids of the order
-  int sorted_ids[kFew];
+  unsigned sorted[kFew];                   // and with units: their keys in falling order
   unsigned low[kWarps], high[kWarps];
 };
 
@@ -229,6 +228,45 @@ __device__ __forceinline__ unsigned long long ceil_div(unsigned long long x, uns
   while (q * u < x) ++q;
   while (q && (q - 1) * u >= x) --q;
   return q;
+}
+// Sorts m <= kFew different values in shared memory, the largest first. All threads of the CTA together.
+// Up to 128 by counting, a warp for each value in turn, what is larger; above bitonic, with zeros
+// behind them (a warp's 32 pairs are among 64 neighbours where they are 32 or less apart). Top-k of
+// 50, one row: 14.3 us by counting, 16.8 bitonic; of 200 26.7 and 20.7; of 500 81 and 28.
+__device__ __forceinline__ void sort_down(unsigned long long* v, int m, unsigned long long* counted) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  int n = 2;
+  while (n < m) n *= 2;
+  if (t >= m && t < n) v[t] = 0ull;
+  __syncthreads();
+  if (m <= 128) {
+    unsigned long long mine[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine[e] = 32 * e + lane < m ? v[32 * e + lane] : 0ull;
+    for (int i = warp; i < m; i += kWarps) {
+      const unsigned long long x = v[i];
+      int larger = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) larger += __popc(__ballot_sync(0xffffffffu, mine[e] > x));
+      if (lane == 0) counted[larger] = x;
+    }
+    __syncthreads();
+    if (t < m) v[t] = counted[t];
+    __syncthreads();
+    return;
+  }
+  for (int size = 2; size <= n; size *= 2) {
+    for (int apart = size / 2; apart > 0; apart /= 2) {
+      if (t < n / 2) {
+        const int i = 2 * t - (t & (apart - 1)), j = i + apart;
+        const unsigned long long x = v[i], y = v[j];
+        if ((x < y) == ((i & size) == 0)) v[i] = y, v[j] = x;
+      }
+      if (apart > 32 || (apart == 1 && size > 32)) __syncthreads();
+      else __syncwarp();
+    }
+  }
+  __syncthreads();
 }
 // Adds u to a bin's sum in two words.
 __device__ __forceinline__ void bin_add(Shared& sh, int at, unsigned long long u) {
@@ -660,25 +698,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     }
     return __umul64hi(u64, total);
   };
-  // Top-k, top-p, min-p and the draw among the few tokens in sh.keys and sh.ids, by this CTA: ranks and
-  // masses before a token by comparing it with all others.
+  // Top-k, top-p, min-p and the draw among the few tokens in sh.keys and sh.ids, by this CTA: sorted by
+  // their logits, then what is kept by ids.
   auto finish = [&] {
     const int m = min(sh.gathered, kFew);
-    const unsigned key = tid < m ? sh.keys[tid] : 0u;
-    const int id = tid < m ? sh.ids[tid] : 0;
-    if (tid < m) {   // in falling order, of equal logits the lowest ids first
-      int before = 0;
-      for (int j = 0; j < m; ++j) {
-        const unsigned other = sh.keys[j];
-        before += other > key || (other == key && sh.ids[j] < id) ? 1 : 0;
-      }
-      sh.sorted[before] = key;
-      sh.sorted_ids[before] = id;
-    }
-    __syncthreads();
+    unsigned long long* const order = sh.upto;
+    // in falling order, of equal logits the lowest ids first
+    if (tid < m) order[tid] = (unsigned long long)sh.keys[tid] << 32 | ~(unsigned)sh.ids[tid];
+    sort_down(order, m, order + kFew);
     const int first = min(k, m);   // top-k's
-    const unsigned my_key = tid < first ? sh.sorted[tid] : 0u;
-    const int my_id = tid < first ? sh.sorted_ids[tid] : 0;
+    const unsigned my_key = tid < first ? (unsigned)(order[tid] >> 32) : 0u;
+    const unsigned not_id = tid < first ? (unsigned)order[tid] : 0u;
     const unsigned long long mine = tid < first ? row.units(from_key(my_key)) : 0ull;
     const unsigned long long to = block_upto(mine, sh.warp_mass);
     if (tid == kThreads - 1) sh.above = to;
@@ -692,12 +722,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if (tid == kThreads - 1) sh.inside = total_to;
     __syncthreads();
     const unsigned long long total = sh.inside, place = place_of(total);
-    if (!kept) return;
-    unsigned long long from = 0;   // of the kept tokens with lower ids
-    for (int j = 0; j < first; ++j) from += sh.sorted_ids[j] < my_id ? sh.units[j] : 0ull;
-    if (place < from || place >= from + mine) return;
-    p.out[b] = my_id;
-    if (p.prob) p.prob[b] = row.share(from_key(my_key), total);
+    // by their ids; what is not kept has no weight
+    if (tid < first) order[tid] = (unsigned long long)not_id << 32 | tid;
+    sh.sorted[tid] = my_key;
+    sort_down(order, first, order + kFew);
+    const unsigned long long my = tid < first ? order[tid] : 0ull;
+    const int from = (int)(unsigned)my;   // where it was among the sorted
+    const unsigned long long weight = tid < first ? sh.units[from] : 0ull;
+    const unsigned long long upto = block_upto(weight, sh.warp_mass);
+    if (place < upto - weight || place >= upto) return;
+    p.out[b] = (int)~(unsigned)(my >> 32);
+    if (p.prob) p.prob[b] = row.share(from_key(sh.sorted[from]), total);
   };
   Border border{0u, ~0ull};
   unsigned long long own = 0, own_ties = 0;
@@ -888,9 +923,9 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   while ((1 << bits) < p.V) ++bits;
   a.scale = 62 - bits < 45 ? 62 - bits : 45;
   // CTAs per row: as many as give each 16k tokens, so that two fit an SM (64 rows of 129,280: eight
-  // 33.5 us, four 37 to 42, two 46), and for few rows more, down to 1024 tokens (one row of 32,003:
-  // eight 9 us, two 14; one of 129,280 eight 11.5, one 80). Where the rows fill the GPU, more only
-  // add exchanges: 512 rows of 4000 with one 22 us, with two 33; 200 of 32,003 with two 27, four 39.
+  // 31 us, four and two a fifth to a half more), and for few rows more, down to 1024 tokens (one row of 32,003:
+  // eight 8 us, two 14; one of 129,280 eight 11, one 80). Where the rows fill the GPU, more only
+  // add exchanges: 512 rows of 4000 with one 18.5 us, with two 33; 200 of 32,003 with two 25, four 39.
   int C = 1;
   while (C < kMaxCluster && p.V > 16384 * C) C *= 2;
   while (C < kMaxCluster && p.V > 1024 * C && (int64_t)p.B * C < 2 * device_sm_count()) C *= 2;
