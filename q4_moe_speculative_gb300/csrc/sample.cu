@@ -922,10 +922,11 @@ cudaError_t launch_sample(const SampleProblem& p, cudaStream_t s) {
   int bits = 0;
   while ((1 << bits) < p.V) ++bits;
   a.scale = 62 - bits < 45 ? 62 - bits : 45;
-  // CTAs per row: as many as give each 16k tokens, so that two fit an SM (64 rows of 129,280: eight
-  // 31 us, four and two a fifth to a half more), and for few rows more, down to 1024 tokens (one row of 32,003:
-  // eight 8 us, two 14; one of 129,280 eight 11, one 80). Where the rows fill the GPU, more only
-  // add exchanges: 512 rows of 4000 with one 18.5 us, with two 33; 200 of 32,003 with two 25, four 39.
+  // CTAs per row: as many as give each 16k tokens, so that two fit an SM (64 rows of 129,280 with
+  // top-p: eight 69 us, four 78, two 93; with temperature alone 31, 30, 33), and for few rows more, down
+  // to 1024 tokens (one row of 129,280: eight 11 us, two 33; four of 32,003: eight 8, two 11). Where
+  // the rows fill the GPU, more only add exchanges: 512 rows of 4000 with one 18.5 us, with two 30;
+  // 200 of 32,003 with two 25, four 32.
   int C = 1;
   while (C < kMaxCluster && p.V > 16384 * C) C *= 2;
   while (C < kMaxCluster && p.V > 1024 * C && (int64_t)p.B * C < 2 * device_sm_count()) C *= 2;
