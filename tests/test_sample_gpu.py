@@ -198,6 +198,31 @@ def test_weights_are_as_close_as_they_are_said_to_be(T):
         assert bool((got == token).all())
 
 
+def test_many_rows_of_a_small_vocabulary():
+    # one token of weight per row, found whatever the row; then 70,000 rows of three
+    B = 70_000
+    at = torch.arange(B, device=DEV) % 3
+    z = torch.full((B, 3), float("-inf"), device=DEV)
+    z[torch.arange(B, device=DEV), at] = 1.0
+    u = torch.rand(B, generator=torch.Generator().manual_seed(8), dtype=torch.float64).to(DEV)
+    for kw in ({}, dict(top_k=2), dict(top_p=0.5), dict(min_p=0.5)):
+        got, prob = dsm.sample(z, u, **kw)
+        assert torch.equal(got, at.int()) and bool((prob == 1).all())
+
+
+@pytest.mark.parametrize("k", [100, 128, 129, 200, 400, 511, 512, 513])
+def test_every_way_to_finish_a_top_k(k):
+    # kept tokens compared, sorted or counted in bins, with equal logits among them
+    g = torch.Generator()
+    g.manual_seed(k)
+    z = (torch.randn(24, 5000, generator=g) * 8).round().div(8).to(DEV)
+    z[:, :300] = torch.randn(24, 300, generator=g).to(DEV) + 4
+    u = torch.rand(24, generator=g, dtype=torch.float64).to(DEV)
+    check(z, u, k=k)
+    check(z, u, k=k, p=0.8, T=1.5)
+    check(z, u, k=k, p=0.9, mp=0.05)
+
+
 def test_frequencies_follow_the_distribution():
     # 200,000 draws of one row: each token's count within 6 standard deviations
     z = torch.randn(200, generator=torch.Generator().manual_seed(6)) * 1.5
