@@ -4,7 +4,7 @@
 // A row belongs to a cluster of CTAs (up to 8), each of which keeps its part of the logits in shared
 // memory, so that they are read from memory once; what the CTAs have to agree on goes through
 // distributed shared memory. Without top-k and top-p every weight is taken once, for its warp's sum;
-// the draw finds the CTA, the warp and the thread that it falls to.
+// the draw finds the CTA, the warp, the round of 128 tokens and the lane that it falls to.
 //
 // Masses are integers: weight exp((l - max) / T) in units of 2^-scale, the scale such that a
 // vocabulary's sum fits 63 bits. Sums of integers do not depend on their order, so the borders and
@@ -16,9 +16,8 @@
 // top_p), the border is found by counts or masses per bin: first 1024 bins of equal width in
 // (max - l) / T, which spread a vocabulary's logits (with 2048 only one CTA fits an SM), then the
 // border bin's tokens, which one CTA gathers, by their keys (logits as ordered integers) in 1024
-// bins, until a bin is one key. Of the tokens with the border's logit the lowest
-// ids are kept. Up to 512 tokens that top-k keeps are finished by one CTA without further
-// exchanges.
+// bins, until a bin is one key. Of the tokens with the border's logit the lowest ids are kept. Up to
+// 512 tokens that top-k keeps are finished by one CTA without further exchanges.
 //
 // Bound by instruction issue while weights are taken (about 50 per token with its bin, a quarter to a
 // half of the time) and by the latency of what the CTAs exchange before and after, not by memory.
@@ -222,11 +221,11 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long total,
   }
   return (hi << (64 - s) | lo >> s) + (lo & ((1ull << s) - 1) ? 1 : 0);
 }
-// The smallest q with q u >= x, for q below 2^25.
+// The smallest q with q u >= x, for q below 2^25 (the estimate is off by less than 32).
 __device__ __forceinline__ unsigned long long ceil_div(unsigned long long x, unsigned long long u) {
   unsigned long long q = (unsigned long long)__fdividef((float)x, (float)u);   // off by a few
-  while (q * u < x) ++q;
-  while (q && (q - 1) * u >= x) --q;
+  for (int i = 0; i < 32 && q * u < x; ++i) ++q;
+  for (int i = 0; i < 32 && q && (q - 1) * u >= x; ++i) --q;
   return q;
 }
 // Sorts m <= kFew different values in shared memory, the largest first. All threads of the CTA together.
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if constexpr (kStaged) return stage[i];
     if (i >= n) return kNegInf;
     const float l = widen(from[i]);
-    return endless ? (l == INFINITY ? 0.f : kNegInf) : l;
+    return endless ? (l == INFINITY ? 0.f : kNegInf) : fminf(l, top);   // (read anew: never above)
   };
   Row row;
   row.top = top;
@@ -397,10 +396,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if (min_p > 0.f) {
       const double less = sh.less;
       auto enough = [&](float l) { return (double)l - (double)top >= less; };
-      least = fminf(top, __double2float_ru((double)top + less));
-      while (least < top && !enough(least)) least = from_key(key_of(least) + 1);
-      while (least > kNegInf && enough(from_key(key_of(least) - 1)))
-        least = from_key(key_of(least) - 1);
+      // its key: not below `lo`, at most `hi`; mostly the first guess, else in growing steps, since
+      // near 0 more logits than there is time for can have one difference in fp64
+      const unsigned first = key_of(kNegInf), last = key_of(top);
+      unsigned hi = key_of(fminf(top, __double2float_ru((double)top + less))), lo = hi, step = 1;
+      if (enough(from_key(hi))) {
+        while (hi > first) {
+          lo = hi - first > step ? hi - step : first;
+          if (!enough(from_key(lo))) break;
+          hi = lo;
+          step *= 2;
+        }
+      } else {
+        do {
+          lo = hi;
+          hi = last - hi > step ? hi + step : last;
+          step *= 2;
+        } while (hi < last && !enough(from_key(hi)));
+      }
+      while (hi > lo + 1) {   // lo is not enough
+        const unsigned middle = lo + (hi - lo) / 2;
+        if (enough(from_key(middle))) hi = middle;
+        else lo = middle;
+      }
+      least = from_key(hi);
     }
     sh.least = least;
   }
@@ -849,7 +868,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       (lane < kWarps ? sh.warp_mass[lane] : 0ull) +
       (min(tied_to, border.ties) - min(tied_to - warp_tied, border.ties)) * each;
   const unsigned long long mass_to = start + warp_upto(warp_mass, lane);
-  const int w = __ffs(__ballot_sync(0xffffffffu, target < mass_to)) - 1;   // (there is one)
+  const unsigned crossing = __ballot_sync(0xffffffffu, target < mass_to);
+  const int w = crossing ? __ffs(crossing) - 1 : kWarps - 1;   // (there is one)
   unsigned long long at = __shfl_sync(0xffffffffu, mass_to - warp_mass, w);
   unsigned long long tied = __shfl_sync(0xffffffffu, tied_to - warp_tied, w);
   // four neighbouring tokens of a round: their weights above the border, and which are at it
@@ -889,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     const unsigned long long m_to = at + warp_upto(m, lane);
     const unsigned found = __ballot_sync(0xffffffffu, target < m_to);
     const int last = found ? __ffs(found) - 1 : 31;
-    r = r0 + last;
+    r = min(r0 + last, rounds - 1);
     at = __shfl_sync(0xffffffffu, found ? m_to - m : m_to, last);
     tied = __shfl_sync(0xffffffffu, found ? t_to - t : t_to, last);
     if (found) break;

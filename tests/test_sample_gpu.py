@@ -198,6 +198,22 @@ def test_weights_are_as_close_as_they_are_said_to_be(T):
         assert bool((got == token).all())
 
 
+@pytest.mark.parametrize("T,mp,top", [
+    (1.634910225868225, 0.6227176189422607, 0.7743950486183167),
+    (1.8739752769470215, 0.31074097752571106, 2.190294027328491), (1.0, 0.5, 0.6931472), (2.0, 0.1, 1.0)])
+def test_min_p_borders_near_a_logit_of_zero(T, mp, top):
+    # max + T log(min_p) is 0 but for a rounding of fp64, so that hundreds of millions of logits around 0
+    # have the border's difference (the first two); what is clearly above or below is decided
+    row = [top, 1e-3, -1e-3, 1e-12, -1e-12, -5.0, 0.25, -0.25]
+    z = torch.tensor([row] * 9, device=DEV)
+    u = torch.tensor([0.0, 0.2, 0.4, 0.5, 0.6, 0.7, 0.8, 0.9, 1 - 2.0 ** -53], dtype=torch.float64, device=DEV)
+    z[:, 3:5] = -9.0
+    check(z, u, T=T, mp=mp)
+    z[:, 3:5] = torch.tensor([1e-12, -1e-12])
+    got, prob = dsm.sample(z, u, temperature=T, min_p=mp)
+    assert set(got.tolist()) <= {0, 1, 3, 4, 6} | ({2, 7} if top == 1.0 else set())
+
+
 def test_many_rows_of_a_small_vocabulary():
     # one token of weight per row, found whatever the row; then 70,000 rows of three
     B = 70_000
