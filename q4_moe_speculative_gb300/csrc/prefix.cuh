@@ -102,7 +102,7 @@ struct Walk {
     skip(a);
     for (;;) {   // the prefix
       const int64_t n = head_places(a, T) * a.own.c.heads;
-      if (pos < start + n) break;
+      if (pos < start + n || pos == end) break;
       start += n;
       skip(a);
     }
@@ -119,6 +119,7 @@ struct Walk {
       len = p < a.P ? prefix_len(a, p) : 0;
       T = token_tiles(len);
     } while (T == 0 && p < a.P);
+    if (p >= a.P) end = pos;   // (it is, unless the lengths change under the kernel)
   }
   __device__ __forceinline__ bool next(const PrefixArgs& a, Run* r) {
     while (pos < end) {
