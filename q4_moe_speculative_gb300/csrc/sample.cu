@@ -274,6 +274,15 @@ __device__ __forceinline__ void bin_add(Shared& sh, int at, unsigned long long u
   if (up) atomicAdd(&sh.hi[at], up);
 }
 
+// The two halves of a cluster barrier, here to show that every CTA of the cluster has started: before
+// that none may access another's shared memory.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 template <bool kBf16, bool kStaged>
 __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) float stage_mem[];
@@ -283,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int b = blockIdx.x / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  cluster_arrive();   // (waited for behind the logits' loads)
   const int v0 = min(p.V, rank * a.chunk), n = min(p.V, v0 + a.chunk) - v0;
   for (int i = tid; i < kRoots; i += kThreads) {
     const unsigned long long c = a.coarse[i >> 5], f = a.fine[i & 31];
@@ -361,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.warp_top[w]);
+  cluster_wait();
   if (tid < C) *cluster.map_shared_rank(&sh.top[rank], tid) = top;
   cluster.sync();
   for (int c = 0; c < C; ++c) top = fmaxf(top, sh.top[c]);

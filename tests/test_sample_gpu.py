@@ -274,6 +274,17 @@ def test_no_rows_streams_and_replays():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("V", [1025, 2049, 4097, 8193])
+def test_clusters_whose_ctas_have_little_to_load(V):
+    # the CTAs of a row exchange their largest logits as soon as they can, call behind call
+    z, u = inputs(3, V, torch.bfloat16, seed=V)
+    want = [check(z, u, **kw) for kw in (dict(), dict(k=40), dict(p=0.9))]
+    got = [[dsm.sample(z[i % 3:], u[i % 3:], top_k=k, top_p=p)[0] for k, p in ((0, 1.0), (40, 1.0), (0, 0.9))]
+           for i in range(60)]
+    for i, each in enumerate(got):
+        assert [t.tolist() for t in each] == [w[i % 3:] for w in want]
+
+
 def test_verify_sample_and_sample_agree_on_a_row():
     # the bonus token of a step of one row is a draw from the whole distribution
     z, u = inputs(30, 3000, torch.float32, seed=10)
