@@ -48,7 +48,7 @@ struct Tc {
   // warp 0 issues the MMAs, the next bring tiles, then softmax from a multiple of four on
   static constexpr int kFirst = (1 + kBringers + 3) / 4 * 128;
   static constexpr int kThreads = kFirst + kScore;
-  static constexpr int kSmall = 5120 + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
+  static constexpr int kSmall = 6144 + (kQ8 ? kInfo * 2 * kTok * 4 : 0);
   static constexpr int kQ = kRows * 64 * 4;             // of a stream: its queries, then its sums
   static constexpr int kSmem = 1024 + kSmall + 2 * kQ + 2 * kRing * kMat;
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA has an SM's tensor memory");
@@ -62,9 +62,10 @@ struct Small {
   int abort;
   unsigned runs[kInfo];       // which pages of a tile are there
   int row_at[kPagedMaxRows];  // where a row's values start in a sequence's queries
+  Run run[2][4];              // [stream][32 rows]: what their two warps work on
   float top[2][2][2][kRows];  // [tile parity][stream][half of the columns]: largest scores
 };
-static_assert(sizeof(Small) <= 5120, "in front of the tiles");
+static_assert(sizeof(Small) <= 6144, "in front of the tiles");
 
 __device__ __forceinline__ void ld32(uint32_t at, float (&v)[32]) {
   uint32_t r[32];
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   const uint32_t pad = (1024u - (smem_at(smem_raw) & 1023u)) & 1023u;
   uint8_t* const base = smem_raw + pad;
   Small& sh = *reinterpret_cast<Small*>(base);
-  float* const sScale = reinterpret_cast<float*>(base + 5120);   // Q8: [kInfo][2][tokens]
+  float* const sScale = reinterpret_cast<float*>(base + 6144);   // Q8: [kInfo][2][tokens]
   uint8_t* const sQ = base + T::kSmall;                          // [2][halves][rows][128 B]
   uint8_t* const sK = sQ + 2 * T::kQ;                            // [ring][halves][tokens][128 B]
   uint8_t* const sV = sK + kRing * T::kMat;
@@ -224,7 +225,10 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     // score)
     const float fk = fabsf(o.scale_log2);
     const uint32_t flip = o.scale_log2 < 0.f ? 0x80008000u : 0u;
-    // a barrier of the two warps: whether both are alive
+    // A barrier of the two warps: whether both are alive. It has no limit, so neither may leave the other
+    // there: what they do next is the same for both, since the runs come from one of them (their own
+    // walks could differ if the lengths changed under the kernel), and a warp that has given up says
+    // so here, at the next meeting, and not by staying away.
     auto together = [&](bool alive) {
       int gone;
       asm volatile(
@@ -236,8 +240,15 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       return !gone;
     };
     uint32_t jobs = 0, runs = 0, tile0 = 0;   // before this run; tiles of the CTA
-    bool alive = true;
-    while (alive && walk.next(a, &run)) {
+    bool alive = true;   // the same for both warps, but between a wait and the next meeting
+    for (;;) {
+      if (half == 0) {
+        if (!alive || !walk.next(a, &run)) run.t1 = 0;   // no more
+        if (lane == 0) sh.run[w][quad] = run;
+      }
+      together(true);
+      run = sh.run[w][quad];
+      if (run.t1 == 0) break;
       const int n = run.t1 - run.t0, count = run.w == 2 ? n : (n + 1 - w) / 2;   // tiles of the stream
       const int row0 = (run.u * 2 + (run.w == 2 ? w : 0)) * kRows;
       if (count > 0) {
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           if (m >= o.M) m -= o.M, ++seq;
         }
         // (the sums of the run before have left the room)
-        if (runs) alive = wait(&sh.qfree[w], (runs - 1) & 1);
+        if (runs) alive = __all_sync(0xffffffffu, wait(&sh.qfree[w], (runs - 1) & 1));
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
           uint4 x = in[it];
@@ -279,11 +290,11 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       }
       // ref: a score from which 2^(factor (score - ref)) is taken; norm: this thread's part of the sum
       float ref = kNothing, norm = 0.f;
-      for (int i = 0; i < count && alive; ++i, ++jobs) {
+      for (int i = 0; i < count; ++i, ++jobs) {
         const int nt = run.w == 2 ? i : 2 * i + w;   // of the run
         const uint32_t tile = tile0 + nt;            // of the CTA
         const int slot = tile % kInfo, t0 = (run.t0 + nt) * kTok + half * kCols;
-        alive = wait(&sh.info[slot], (tile / kInfo) & 1) && wait(&sh.sfull[w], jobs & 1);
+        alive = alive && wait(&sh.info[slot], (tile / kInfo) & 1) && wait(&sh.sfull[w], jobs & 1);
         alive = __all_sync(0xffffffffu, alive);
         sm100::tc_fence_after();
         volatile unsigned* const known = sh.runs;

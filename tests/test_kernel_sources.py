@@ -26,3 +26,21 @@ def test_sampling_touches_other_ctas_only_when_they_have_started():
     assert 0 <= arrive < wait < first
     # every thread of the cluster comes past both
     assert "return" not in re.sub(r"return l == l[^;]*;", "", body[:wait])
+
+
+def test_no_warp_of_the_shared_prefix_kernel_is_left_in_a_barrier():
+    # Softmax warps meet in pairs in barriers without a limit, so both of a pair have to come to each:
+    # their runs come from one place, and how a wait ended is agreed on by the lanes and then by the pair.
+    # No other role has such barriers.
+    body = code_of("prefix_tc.cu", "k_prefix_tc")
+    at = body.index("if (tid >= T::kFirst)")
+    softmax, others = body[at:].split("} else if (warp > 0", 1)
+    others = others[:others.rindex("__syncthreads()")]
+    assert not re.search(r"barrier\.cta|bar\.sync|__syncthreads", others)
+    assert softmax.count("walk.next") == 1
+    assert re.search(r"if \(half == 0\) \{\s*if \(!alive \|\| !walk\.next\(a, &run\)\) run\.t1 = 0;", softmax)
+    # a vote of the warp in the statement or right behind it, and a meeting before the result is used
+    for found in re.finditer(r"(?<!= )\bwait\(&", softmax):
+        start = softmax.rfind(";", 0, found.start())
+        assert "__all_sync" in softmax[start:softmax.index(";", found.end()) + 60]
+    assert not re.search(r"for \([^)]*&& alive", softmax)
