@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           page = next;
         }
       }
-      if (*abort_flag && teller)   // copies in flight end (bounded) before the CTA does
+      if (teller)   // copies in flight end (bounded) before the CTA does, whoever gives up and when
         for (int j = told - kInfo < 0 ? 0 : told - kInfo; j < told; ++j)
           sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
     } else {
@@ -622,9 +622,9 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             page = prefix_page(a, run.p, (t + 1) * kTok + lane * pt, run.len);
         }
       }
-      if (*abort_flag)   // copies in flight end (bounded) before the CTA does
-        for (int j = done - kRing < 0 ? 0 : done - kRing; j < done; ++j)
-          sm100::mbar_wait(&full[j % kRing], (j / kRing) & 1, kWaitPolls);
+      // copies in flight end (bounded) before the CTA does, whoever gives up and when
+      for (int j = done - kRing < 0 ? 0 : done - kRing; j < done; ++j)
+        sm100::mbar_wait(&full[j % kRing], (j / kRing) & 1, kWaitPolls);
     }
   } else if (warp == 0) {
     // --------------------------------------------------------------------------- MMAs ----

@@ -44,3 +44,13 @@ def test_no_warp_of_the_shared_prefix_kernel_is_left_in_a_barrier():
         start = softmax.rfind(";", 0, found.start())
         assert "__all_sync" in softmax[start:softmax.index(";", found.end()) + 60]
     assert not re.search(r"for \([^)]*&& alive", softmax)
+
+
+def test_copies_in_flight_end_before_the_cta_of_a_shared_prefix():
+    # a warp that brings tiles may be done before another gives up: it waits for its last copies always
+    body = code_of("prefix_tc.cu", "k_prefix_tc")
+    bring = body[body.index("} else if (warp > 0"):body.index("} else if (warp == 0)")]
+    waits = [m.start() for m in re.finditer(r"for \(int j = (told|done) - kI?[nR]\w+ < 0", bring)]
+    assert len(waits) == 2
+    for at in waits:
+        assert "abort" not in bring[bring.rindex(";", 0, at):at]
