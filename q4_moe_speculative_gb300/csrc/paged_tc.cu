@@ -712,13 +712,12 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
           page = a.table[(int64_t)cur.b * a.max_pages + (t >> a.c.page_shift)];
       }
     }
-    if (*abort_flag) {   // copies in flight end (bounded) before the CTA does
-      for (int j = done - ring < 0 ? 0 : done - ring; j < done; ++j)
-        sm100::mbar_wait(&full[j % ring], (j / ring) & 1, kWaitPolls);
-      if (!values)
-        for (int j = done - kInfo < 0 ? 0 : done - kInfo; j < done; ++j)
-          sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
-    }
+    // copies in flight end (bounded) before the CTA does, whoever gives up and when
+    for (int j = done - ring < 0 ? 0 : done - ring; j < done; ++j)
+      sm100::mbar_wait(&full[j % ring], (j / ring) & 1, kWaitPolls);
+    if (!values)
+      for (int j = done - kInfo < 0 ? 0 : done - kInfo; j < done; ++j)
+        sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
   } else if (warp == T::kMmaWarp) {
     // ---------------------------------------------------------------- MMAs of the scores ---
     // (the whole warp walks the loop, so that descriptors stay in uniform registers; one lane

@@ -54,3 +54,12 @@ def test_copies_in_flight_end_before_the_cta_of_a_shared_prefix():
     assert len(waits) == 2
     for at in waits:
         assert "abort" not in bring[bring.rindex(";", 0, at):at]
+
+
+def test_copies_in_flight_end_before_the_cta_of_a_paged_cache():
+    body = code_of("paged_tc.cu", "k_paged_tc")
+    bring = body[body.index("bulk_copy("):body.index("} else if (warp == T::kMmaWarp)")]
+    waits = [m.start() for m in re.finditer(r"for \(int j = done - (ring|kInfo) < 0", bring)]
+    assert len(waits) == 2
+    for at in waits:
+        assert "abort" not in bring[bring.rindex(";", 0, at):at]
