@@ -27,7 +27,27 @@ struct PagedArgs {
   int* span;        // [B][key heads][2]: the CTAs that begin and end a (sequence, head)
   int grid;         // CTAs that share the tiles
   bool pieces;      // all results are left as sums in the workspace, for another kernel's join
+  unsigned long long* ready;   // (pieces) in the workspace's header: see began()
+  unsigned long long call;     // (pieces) a number of this call's, never 0
 };
+
+// For the grid behind this one (PagedArgs::pieces), which may start now. That grid reads what the caller
+// gives, but nothing of this one, so it need not wait for this one's end; yet what the grids before
+// wrote is promised to be visible only to a grid that has waited itself, or to one that acquires
+// what a thread released that had. So the call's number is released here, behind this grid's wait, and
+// the next one waits after all if it does not find it (given_is_there). By one thread of a CTA.
+__device__ __forceinline__ void began(const PagedArgs& a) {
+  if (blockIdx.x == 0)
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.ready), "l"(a.call) : "memory");
+  pdl_trigger();
+}
+// Whether it is released. (The last kernel of a call takes it back, so that a replay of a captured call
+// does not find its predecessor's; a workspace may hold anything at first, but hardly this number.)
+__device__ __forceinline__ bool given_is_there(const PagedArgs& a) {
+  unsigned long long found;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(found) : "l"(a.ready) : "memory");
+  return found == a.call;
+}
 
 // Where a CTA leaves its sums of a (sequence, key head): slot 0 when the run began before this CTA,
 // slot 1 when it begins here and goes on in the next; `all` of it: behind those of the CTAs
@@ -49,7 +69,7 @@ constexpr int kTcMaxRows = 128;
 cudaError_t launch_tc(const PagedArgs& p, int D, cudaStream_t s);
 
 // paged_attn.cu: the kernel of a call alone, every (sequence, key head) left as pieces in the
-// workspace (of pieces_workspace() bytes, the status word first) for the caller's join. *args: what
+// workspace (of pieces_workspace() bytes, the header first) for the caller's join. *args: what
 // the kernel was given.
 size_t pieces_workspace(const PagedAttnProblem& p);
 cudaError_t launch_pieces(const PagedAttnProblem& p, uint8_t* ws, cudaStream_t s, PagedArgs* args);

@@ -30,6 +30,8 @@
 // off by 2^-8, and a result by 1.4 times its own rounding, for 52 instead of 60 us below. Its
 // bound is the issue of instructions: 4 sequences x 8 heads of 8k tokens, 64 rows, 60 us for 132
 // MB of bf16 as for 68 MB of Q8.
+#include <atomic>
+#include <chrono>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(256, 1) k_paged(const __grid_constant__ PagedA
   pdl_wait();
 
   if (blockIdx.x == 0 && tid == 0) *a.status = 0u;
-  if (a.pieces && tid == 0) pdl_trigger();   // (the next kernel reads nothing of this one)
+  if (a.pieces && tid == 0) began(a);
   Cursor cur{};
   const int n = cta_run(a, blockIdx.x, lane, &cur);   // tiles of this CTA
   if (n == 0) return;
@@ -716,6 +718,15 @@ cudaError_t run_pieces(const PagedAttnProblem& p, bool pieces, uint8_t* ws, cuda
   a.part_o = reinterpret_cast<float*>(ws + pl.po);
   a.grid = pl.grid;
   a.pieces = pieces;
+  if (pieces) {
+    // numbers that a workspace's first contents do not hold, from a start that differs from run to run
+    static std::atomic<unsigned long long> calls{
+        (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() *
+        0x9E3779B97F4A7C15ull};
+    a.ready = reinterpret_cast<unsigned long long*>(ws) + 1;   // behind the status word
+    do a.call = calls.fetch_add(1, std::memory_order_relaxed);
+    while (a.call == 0);
+  }
   if (pl.kernel == Kernel::kFew) return launch_few(a, D, s);
   if (pl.kernel == Kernel::kTensor) return launch_tc(a, D, s);
   return with_rows(a.M, [&](auto mt) {

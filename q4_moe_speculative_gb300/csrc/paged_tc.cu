@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &v_map : &k_map) : "memory");
   pdl_wait();
   if (blockIdx.x == 0 && tid == 0) *a.status = 0u;
-  if (a.pieces && tid == 0) pdl_trigger();   // (the next kernel reads nothing of this one)
+  if (a.pieces && tid == 0) began(a);
 
   Cursor cur{};
   const int n = cta_run(a, blockIdx.x, lane, &cur);   // tiles of this CTA

@@ -32,17 +32,14 @@ __global__ void __launch_bounds__(256, kWarps == 1 ? 6 : 4) k_prefix_join(const 
   const unsigned hq = row % o.Hq, br = row / o.Hq, h = hq / o.G;
   const unsigned b = br / o.R, m = br % o.R * o.G + hq % o.G;
   uint16_t* const dst = o.out + row64 * D + V * lane;
-  // (what the caller gives is there already: the kernels before began their dependents after
-  // their own wait, or wait for nothing that these two read)
-  const int own_len = o.lengths[b];
-
   // the pieces of the prefix: of the CTAs that share the row's unit, one or two (its streams) of each
   const unsigned p = b / a.per, mp = (b % a.per) * o.M + m, u = mp / (2 * kRows);
   const int w = unit_tiles(a, u), subs = w == 2 ? 1 : 2;
   const int sub0 = w == 2 ? mp / kRows % 2 : 0;
   const int unit = (p * o.c.heads + h) * a.units + u;
-  const int prefix_tokens = prefix_len(a, p);
   pdl_wait();
+  if (row64 == 0 && lane == 0) *o.ready = 0ull;   // (no prefix kernel of this call looks any more)
+  const int own_len = o.lengths[b], prefix_tokens = prefix_len(a, p);
   const int2 first = __ldcg(reinterpret_cast<const int2*>(a.span) + unit);
   // and those of its own tokens
   const unsigned bh = b * o.c.heads + h;

@@ -60,6 +60,7 @@ struct Small {
   uint64_t qfree[2], info[kInfo], vedge, end;
   uint32_t tmem;
   int abort;
+  bool given;                 // what the caller gives is visible
   unsigned runs[kInfo];       // which pages of a tile are there
   int row_at[kPagedMaxRows];  // where a row's values start in a sequence's queries
   Run run[2][4];              // [stream][32 rows]: what their two warps work on
@@ -174,14 +175,12 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     sh.abort = 0;
     sm100::fence_mbar_init();
   }
-  // (No wait for the kernel of the own tokens before this one: it began the dependents only after its
-  // own wait, and this one uses nothing that it writes. The join needs both: waited for at the end.)
-  const int lane_len = lane < a.P ? prefix_len(a, lane) : 0;
   if (tid < o.M) sh.row_at[tid] = (tid / o.G * o.Hq + tid % o.G) * D;
   if (warp == 0) {
     sm100::tmem_alloc(&sh.tmem, 512);
     sm100::tmem_relinquish();
   }
+  if (tid == 32) sh.given = given_is_there(o);
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
@@ -191,6 +190,11 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
   if (!kQ8 && tid < 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &v_map : &k_map) : "memory");
   pdl_trigger();
+  // (Of the kernel of the own tokens before this one nothing is used but that it had waited for those
+  // before it. The join needs both: waited for at the end.)
+  if (!sh.given) pdl_wait();
+  fence_async_global();
+  const int lane_len = lane < a.P ? prefix_len(a, lane) : 0;
 
   volatile int* const abort_flag = &sh.abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {

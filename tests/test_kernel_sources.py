@@ -3,6 +3,8 @@ for before it touches memory that is not its own."""
 import re
 from pathlib import Path
 
+import pytest
+
 CSRC = Path(__file__).resolve().parents[1] / "q4_moe_speculative_gb300" / "csrc"
 
 
@@ -63,3 +65,31 @@ def test_copies_in_flight_end_before_the_cta_of_a_paged_cache():
     assert len(waits) == 2
     for at in waits:
         assert "abort" not in bring[bring.rindex(";", 0, at):at]
+
+
+READS = r"lengths\[|prefix_len\(|prefix_page\(|__ldg\(|__ldcg\(|\bp\.[xu]\b|o\.q\b|table\[|logits"
+
+
+@pytest.mark.parametrize("name,kernel", [("prefix_tc.cu", "k_prefix_tc"), ("prefix.cu", "k_prefix_join"),
+                                         ("norm.cu", "k_block_norm"), ("sample.cu", "k_sample")])
+def test_nothing_is_read_before_the_wait_for_earlier_kernels(name, kernel):
+    # griddepcontrol.wait is what makes the results of the kernels before visible, to the grid that
+    # executes it; that a grid in between has waited for them is not promised to be enough, unless what
+    # that grid released behind its wait has been acquired
+    body = code_of(name, kernel)
+    before = body[:body.index("pdl_wait()")]
+    assert not re.search(READS, before)
+
+
+def test_the_shared_prefix_kernel_waits_unless_it_has_acquired():
+    body = code_of("prefix_tc.cu", "k_prefix_tc")
+    acquired = body.index("sh.given = given_is_there(o);")
+    everyone = body.index("__syncthreads();", acquired)
+    assert everyone < body.index("if (!sh.given) pdl_wait();\n  fence_async_global();")
+    assert body.rindex("pdl_wait()") > body.rindex("mbar_wait")      # and for the join's sake at the end
+    for name, kernel in (("paged_attn.cu", "k_paged"), ("paged_few.cu", "k_paged_few"),
+                         ("paged_tc.cu", "k_paged_tc")):
+        text = re.sub(r"//[^\n]*", "", (CSRC / name).read_text())
+        assert text.count("pdl_trigger") == (1 if name == "paged_attn.cu" else 0)     # (its join's)
+        assert re.search(r"pdl_wait\(\);\s*if \(blockIdx\.x == 0 && tid == 0\) \*a\.status = 0u;\s*"
+                         r"if \(a\.pieces && tid == 0\) began\(a\);", text), kernel

@@ -339,3 +339,29 @@ def test_pages_beyond_32_bits(q8):
     move = lambda t: torch.where(t >= 0, at[t.clamp(min=0).long()], -1).to(torch.int32)  # noqa: E731
     got = dsm.prefix_attention(q, dsm.PagedCache(*far), move(ptable), plens, move(table), lens)
     assert torch.equal(got, want)
+
+
+def test_inputs_written_right_before_the_call():
+    # kernels that write queries, cache, tables and lengths, and the call behind them without a pause,
+    # eager and captured in turn on one workspace: each sees what was written last
+    problems = [problem([640, 90], [40, 3, 17, 64], 2, 8, 2, 128, 32, False, seed=s) for s in range(4)]
+    want = [dsm.prefix_attention(*p) for p in problems]
+    q, cache, *rest = problem([640, 90], [40, 3, 17, 64], 2, 8, 2, 128, 32, False, seed=9)
+    ws, out = torch.empty(64 << 20, dtype=torch.uint8, device=DEV), torch.empty_like(q)
+    into = [q, cache.k, cache.v, *rest]
+    graph = torch.cuda.CUDAGraph()
+    call = lambda: dsm.prefix_attention(q, cache, *rest, out=out, workspace=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call()
+    got = []
+    for i in range(40):
+        p = problems[i * 7 % 4]
+        for to, x in zip(into, (p[0], p[1].k, p[1].v, *p[2:])):
+            to.copy_(x)
+        graph.replay() if i % 3 else call()
+        got.append(out.clone())
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i * 7 % 4]), i
+    assert dsm.workspace_status(ws) == 0 and not ws[8:16].any()
