@@ -31,7 +31,12 @@ namespace dsmoe {
 namespace prefix {
 
 constexpr int kInfo = 8;                  // tiles whose pages and scales are at hand
-constexpr uint32_t kWaitPolls = 1u << 20;
+// Polls of a wait: of one role for another (a test's build has fewer, so that they run out), and of the
+// last ones, for copies and products in flight.
+#ifndef DS_PREFIX_WAIT_POLLS
+#define DS_PREFIX_WAIT_POLLS (1u << 20)
+#endif
+constexpr uint32_t kWaitPolls = DS_PREFIX_WAIT_POLLS, kEndPolls = 1u << 20;
 constexpr int kStream = 256;              // softmax threads of a stream: two per row
 constexpr int kScore = 2 * kStream;
 // Reference of a row that has seen no token yet: the least finite value, so that any score that
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       }
       if (teller)   // copies in flight end (bounded) before the CTA does, whoever gives up and when
         for (int j = told - kInfo < 0 ? 0 : told - kInfo; j < told; ++j)
-          sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kWaitPolls);
+          sm100::mbar_wait(&sh.info[j % kInfo], (j / kInfo) & 1, kEndPolls);
     } else {
       uint64_t* const full = values ? sh.vfull : sh.kfull;
       uint64_t* const free_bar = values ? sh.vfree : sh.kfree;
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
             const uint32_t edge_par = edges++ & 1;
             alive = wait(&sh.vedge, edge_par);
             if (!(alive = __all_sync(0xffffffffu, alive))) {   // (no full[] counts these copies)
-              sm100::mbar_wait(&sh.vedge, edge_par, kWaitPolls);
+              sm100::mbar_wait(&sh.vedge, edge_par, kEndPolls);
               break;
             }
             for (int r = lane; r < kTok; r += 32) {
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
       }
       // copies in flight end (bounded) before the CTA does, whoever gives up and when
       for (int j = done - kRing < 0 ? 0 : done - kRing; j < done; ++j)
-        sm100::mbar_wait(&full[j % kRing], (j / kRing) & 1, kWaitPolls);
+        sm100::mbar_wait(&full[j % kRing], (j / kRing) & 1, kEndPolls);
     }
   } else if (warp == 0) {
     // --------------------------------------------------------------------------- MMAs ----
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     // MMAs issued but maybe not observed complete: wait (bounded) before TMEM is freed
     if (leader) sm100::mma_commit(&sh.end);
     __syncwarp();
-    sm100::mbar_wait(&sh.end, 0, kWaitPolls);
+    sm100::mbar_wait(&sh.end, 0, kEndPolls);
   }
   __syncwarp();
   pdl_wait();
