@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   // floor(u * total), u in units of 2^-64: drawn is the first token beyond it
   auto place_of = [&](unsigned long long total) {
     unsigned long long u64 = 0;
-    if (u >= 1.0) u64 = ~0ull;
+    if (u >= 1.0) u64 = ~0ull << 11;   // the last value below 1: 1 - 2^-53
     else if (u > 0x1p-1000) {
       const unsigned long long bits = (unsigned long long)__double_as_longlong(u);
       const int shift = (int)(bits >> 52) - 1011;   // of the mantissa

@@ -291,3 +291,14 @@ def test_verify_sample_and_sample_agree_on_a_row():
     a, _ = dsm.sample(z, u, temperature=0.8)
     b, n = dsm.verify_sample(z[:, None].contiguous(), float(np.float32(0.8)), None, None, None, u[:, None].contiguous())
     assert torch.equal(a, b[:, 0]) and bool((n == 1).all())
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=1 << 16), dict(top_p=0.9999999), dict(min_p=1e-12)])
+def test_uniforms_beyond_the_end_are_the_last_one(kw):
+    # 2^17 - 1 tokens of weight 1 and a last one of 2^-37 or less of it, 2^-54 of the mass: above the last
+    # uniform below 1, which leaves 2^-53, and not to be drawn at 1 and beyond either
+    z = torch.zeros(4, 1 << 17, device=DEV)
+    z[:, -1] = -37 * math.log(2)
+    u = torch.tensor([1 - 2.0 ** -53, 1.0, 7.0, float("inf")], dtype=torch.float64, device=DEV)
+    got = dsm.sample(z, u, **kw)[0].tolist()
+    assert got == [got[0]] * 4 and (got[0] == (1 << 17) - 2 or kw.get("top_p") or kw.get("top_k"))
