@@ -624,8 +624,9 @@ ds_status ds_block_norm(const ds_block_norm_args* args, void* x_out, uint16_t* h
  * below 1 when not below it. top_p NaN is 1, min_p NaN is 0, and m - l_i beyond the range of fp32
  * is w_i = 0.
  * Decisions are taken in integers: w in units of 2^-s, s = 45 up to a vocabulary of 2^17 and one
- * less for each doubling, off by half a unit and 2^-35 relative; their sums are exact. A border or
- * a draw closer than that to a 64-bit evaluation's may go the other way.
+ * less for each doubling, off by half a unit and 2^-35 relative (temperatures above 2^100, where
+ * fp32's smallest values take part: 2^-16); their sums are exact. A border or a draw closer than that
+ * to a 64-bit evaluation's may go the other way.
  * Limits: 0 <= n_rows <= 2^20 (0 enqueues nothing), 1 <= n_vocab <= 2^24, row stride >= n_vocab
  * and at most 2^31.
  * ---------------------------------------------------------------------------------- */

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f;
   const float per_log2 = __fdiv_rn(kLog2e, T);
   const float per_log2_low =
-      T < 0x1p64f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-per_log2, T, kLog2e), kLog2eLow), T) : 0.f;
+      T < INFINITY ? __fdiv_rn(__fadd_rn(__fmaf_rn(-per_log2, T, kLog2e), kLog2eLow), T) : 0.f;
   if (tid == kThreads - 1)   // (fp64: one thread, beside the loads)
     sh.less = min_p > 0.f && min_p < 1.f ? (double)T * log((double)min_p) : 0.0;
   const Raw* const from = static_cast<const Raw*>(p.logits) + (int64_t)b * p.stride + v0;

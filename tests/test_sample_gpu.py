@@ -302,3 +302,20 @@ def test_uniforms_beyond_the_end_are_the_last_one(kw):
     u = torch.tensor([1 - 2.0 ** -53, 1.0, 7.0, float("inf")], dtype=torch.float64, device=DEV)
     got = dsm.sample(z, u, **kw)[0].tolist()
     assert got == [got[0]] * 4 and (got[0] == (1 << 17) - 2 or kw.get("top_p") or kw.get("top_k"))
+
+
+@pytest.mark.parametrize("T", [3.3e19, 1.7e25, 7.7e28, 1.2e30])
+def test_weights_at_high_temperatures(T):
+    # as test_weights_are_as_close_as_they_are_said_to_be, with logits of the temperature's size
+    g = torch.Generator()
+    g.manual_seed(5)
+    t32 = float(np.float32(T))
+    diff = (torch.rand(2000, generator=g).double() * 6.2 + 1e-3) * t32
+    top = torch.randn(2000, generator=g) * 3 * t32
+    z = torch.stack([(top.double() - diff).float(), top], 1).to(DEV)
+    d = (z[:, 0].double() - z[:, 1].double()).cpu().numpy().astype(np.longdouble)
+    w = np.exp(d / np.longdouble(t32))
+    share = (w / (1 + w)).astype(np.float64)
+    for side, token in ((1 - 2.0 ** -34, 0), (1 + 2.0 ** -34, 1)):
+        got, _ = dsm.sample(z, torch.from_numpy(share * side).to(DEV), temperature=T)
+        assert bool((got == token).all()), int((got != token).sum())
