@@ -449,9 +449,10 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
         const float other = sh.top[jobs & 1][w][half ^ 1][mine];
         norm = half ? __fadd_rn(other, norm) : __fadd_rn(norm, other);
         const int64_t at = (unit_piece(a, run.p, run.h, run.u, blockIdx.x) * 2 + w) * a.rows + mine;
+        // (never -infinity where there is a sum, of NaN scores for instance: the join leaves those out)
         if (half == 0 && row0 + mine < a.MP)
           *reinterpret_cast<float2*>(a.part_ml + 2 * at) =
-              make_float2(norm == 0.f ? kNegInf : __fmul_rn(ref, fk), norm);
+              make_float2(norm == 0.f ? kNegInf : fmaxf(__fmul_rn(ref, fk), kNothing), norm);
         if (count > 0) {
           alive = __all_sync(0xffffffffu, wait(&sh.odone[w], runs & 1));
           ++runs;

@@ -365,3 +365,25 @@ def test_inputs_written_right_before_the_call():
     for i, x in enumerate(got):
         assert torch.equal(x, want[i * 7 % 4]), i
     assert dsm.workspace_status(ws) == 0 and not ws[8:16].any()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("scale", [None, 0.5, 1.0, 2.5, -1.0, 0.0])
+def test_what_is_no_number_among_queries_and_keys_shows(scale, q8):
+    # a row with a query that is NaN, and rows all of whose prefix's scores are, at scales on both sides of
+    # where the smallest fp32 value times the factor is infinite
+    def make():
+        return problem([200, 150], [5, 9, 3, 4], 2, 4, 2, 128, 16, q8, seed=9)
+    q, *rest = make()
+    clean = dsm.prefix_attention(q, *rest, scale=scale)
+    q[1, 0, 2, 17] = float("nan")
+    got = dsm.prefix_attention(q, *rest, scale=scale)
+    assert bool(got[1, 0, 2].isnan().all())
+    got[1, 0, 2] = clean[1, 0, 2]
+    assert torch.equal(got, clean)
+    q, cache, ptable, *rest = make()
+    for page in ptable[1, :10].tolist():
+        (cache.k_scale if q8 else cache.k)[page, 1] = float("nan")     # one key head
+    got = dsm.prefix_attention(q, cache, ptable, *rest, scale=scale)
+    assert bool(got[2:, :, 2:].isnan().all())
+    assert torch.equal(got[:2], clean[:2]) and torch.equal(got[2:, :, :2], clean[2:, :, :2])
