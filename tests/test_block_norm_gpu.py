@@ -167,3 +167,23 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     want = dsm.block_norm(x, y, weight=w)
     assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(1, 8), (6, 4096), (700, 320), (400, 1032), (310, 9000)])
+def test_the_norm_alone_leaves_its_input(T, H, dtype):
+    x, w = rows(T, H, dtype, 1, 3.0), vec(H, 3)
+    before = x.clone()
+    got = dsm.block_norm(x, weight=w, eps=EPS)
+    assert got[0] is x and torch.equal(x, before)
+    check(x, weight=w, got=got)
+
+
+@pytest.mark.parametrize("T,H", [(5, 64), (9, 520), (300, 4096), (170, 12296)])
+def test_outputs_that_swap_the_inputs_places(T, H):
+    # x_out in y's place and h_out in x's, both of which are read in the same pass
+    x, y, w, p = rows(T, H, seed=1), rows(T, H, seed=2), vec(H, 3), vec(H, 4)
+    want = dsm.block_norm(x, y, weight=w, post_weight=p)
+    got = dsm.block_norm(x, y, weight=w, post_weight=p, x_out=y, h_out=x)
+    assert got[0] is y and got[1] is x
+    assert torch.equal(y, want[0]) and torch.equal(x, want[1])

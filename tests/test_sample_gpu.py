@@ -319,3 +319,20 @@ def test_weights_at_high_temperatures(T):
     for side, token in ((1 - 2.0 ** -34, 0), (1 + 2.0 ** -34, 1)):
         got, _ = dsm.sample(z, torch.from_numpy(share * side).to(DEV), temperature=T)
         assert bool((got == token).all()), int((got != token).sum())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,V", [(2, 311_232), (2, 311_300), (3, 400_003)])
+def test_vocabularies_around_what_shared_memory_holds(B, V, dtype):
+    # the largest of which a CTA keeps its part, and ones that are read again and again: masked tokens,
+    # NaN, infinities, equal logits at the border
+    z, u = inputs(B, V, dtype, seed=V)
+    for kw in (dict(), dict(k=40), dict(k=5000, p=0.9), dict(T=1.3, p=0.9), dict(mp=0.05), dict(T=0.0)):
+        check(z, u, **kw)
+    z[:, ::2] = -float("inf")
+    z[:, 1::6] = float("nan")
+    z[0] = (z[0] * 2).round() / 2
+    for kw in (dict(k=700), dict(p=0.7), dict(p=0.9, mp=0.02)):
+        check(z, u, **kw)
+    z[1, 70::1000] = float("inf")
+    assert check(z, u, k=3)[1] % 1000 == 70 and check(z, u, p=0.5)[1] % 1000 == 70
