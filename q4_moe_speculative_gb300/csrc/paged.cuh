@@ -36,6 +36,7 @@ struct PagedArgs {
 // wrote is promised to be visible only to a grid that has waited itself, or to one that acquires
 // what a thread released that had. So the call's number is released here, behind this grid's wait, and
 // the next one waits after all if it does not find it (given_is_there). By one thread of a CTA.
+// (Waiting always: 64 x 6 rows after 16k tokens 129.5 us against 124.5, 4 x 1 after 1000 19.9 against 17.4.)
 __device__ __forceinline__ void began(const PagedArgs& a) {
   if (blockIdx.x == 0)
     asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.ready), "l"(a.call) : "memory");

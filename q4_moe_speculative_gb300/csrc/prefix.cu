@@ -5,8 +5,9 @@
 // their maxima, normalisers and sums in the workspace (paged_attn.cu). k_prefix_tc (prefix_tc.cu) does
 // the same for the rows of all of a prefix's sequences together over its tokens. k_prefix_join
 // merges both per row, in a fixed order. The second starts as the first's CTAs leave, the third as the
-// second's do. Measured: 64 sequences x 6 rows, 32 heads on 8, after 16k tokens 133 us, of which the
-// second 105; after 128 tokens 30 (14, 8 and 8); 16 x 1 rows, 16 heads on one, after 100k 34 us.
+// second's do. Measured: 64 sequences x 6 rows, 32 heads on 8, with up to 512 tokens of their own after
+// 16k 136 us, of which the second 109; with 6 after 16k 123, after 128 30 (14, 8 and 8); 16 x 1
+// rows, 16 heads on one, after 100k 35 us.
 #include "prefix.cuh"
 
 namespace dsmoe {

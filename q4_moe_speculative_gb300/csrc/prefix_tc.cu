@@ -19,10 +19,11 @@
 //
 // Bound by the tensor cores in bf16: three products of 128 x 128 x 128 per 128 tokens and row tile.
 // Measured, 1536 rows of 8 heads, D = 128: 6.0 us per 1024 tokens, 82% of the measured rate; over 16k
-// tokens 105 us with its beginning (5 us to the first scores) and end. Q8: 8.9 us per 1024 tokens,
-// bound by instruction issue (58 M warp instructions against 33 M in bf16 for 8k tokens: widening and
+// tokens 109 us with its beginning (5 us to the first scores) and end. Q8: 9.0 us per 1024 tokens,
+// bound by instruction issue (59 M warp instructions against 33 M in bf16 for 8k tokens: widening and
 // the scales) and the order widen, score, weigh, add; three widening warps took 1.6 times as long.
-// D = 64: 16k tokens with the other kernels 105 us, bound by the softmax.
+// D = 64: 16k tokens with the other kernels 103 us, in Q8 140; half the products per score, so the
+// softmax's instructions weigh twice as much against them (not profiled).
 #include <type_traits>
 
 #include "prefix.cuh"
@@ -237,7 +238,8 @@ __global__ void __launch_bounds__(Tc<D, kQ8>::kThreads, 1)
     // A barrier of the two warps: whether both are alive. It has no limit, so neither may leave the other
     // there: what they do next is the same for both, since the runs come from one of them (their own
     // walks could differ if the lengths changed under the kernel), and a warp that has given up says
-    // so here, at the next meeting, and not by staying away.
+    // so here, at the next meeting, and not by staying away. (Meeting at an mbarrier with a limit
+    // instead: 126.9 us against 124.2 for 1536 rows of 8 heads after 16k tokens.)
     auto together = [&](bool alive) {
       int gone;
       asm volatile(
