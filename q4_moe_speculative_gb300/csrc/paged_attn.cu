@@ -691,6 +691,16 @@ Plan make_plan(const PagedAttnProblem& p, bool pieces) {
   return pl;
 }
 
+// A number for PagedArgs::call: one that a workspace's first contents do not hold, so from a start that
+// differs from run to run.
+unsigned long long next_call() {
+  static std::atomic<unsigned long long> calls{
+      (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() *
+      0x9E3779B97F4A7C15ull};
+  const unsigned long long n = calls.fetch_add(1, std::memory_order_relaxed);
+  return n ? n : calls.fetch_add(1, std::memory_order_relaxed);
+}
+
 // The kernel of the runs; *args: what it was given.
 template <int D, bool kQ8>
 cudaError_t run_pieces(const PagedAttnProblem& p, bool pieces, uint8_t* ws, cudaStream_t s,
@@ -719,13 +729,8 @@ cudaError_t run_pieces(const PagedAttnProblem& p, bool pieces, uint8_t* ws, cuda
   a.grid = pl.grid;
   a.pieces = pieces;
   if (pieces) {
-    // numbers that a workspace's first contents do not hold, from a start that differs from run to run
-    static std::atomic<unsigned long long> calls{
-        (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() *
-        0x9E3779B97F4A7C15ull};
     a.ready = reinterpret_cast<unsigned long long*>(ws) + 1;   // behind the status word
-    do a.call = calls.fetch_add(1, std::memory_order_relaxed);
-    while (a.call == 0);
+    a.call = next_call();
   }
   if (pl.kernel == Kernel::kFew) return launch_few(a, D, s);
   if (pl.kernel == Kernel::kTensor) return launch_tc(a, D, s);
